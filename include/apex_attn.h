@@ -349,6 +349,173 @@ apex_status apex_attn_decode_noalloc(const void *q, const void *k_cache, const v
  */
 apex_status apex_attn_rope_reserve(int max_pos, int d_h, float rope_base);
 
+/* ======================================================================
+ * Operators over a cache of rotated keys.
+ *
+ * The entry points below work on caches whose keys were rotated before they
+ * were stored ("pre-rotated": apex_attn_rope_keys or apex_attn_rope), so a
+ * cache row need not sit at the index of its position.  Lengths, positions and
+ * masks are device arrays and may change between replays of a captured graph;
+ * nothing is read back to the host.  Supported row lengths of the attention
+ * entry points: (d_qk, d_v) = (64, 64), (128, 128) or, for decoupled rows
+ * [content | rope part], (192, 128).  None of them allocates device memory
+ * once the device's first call of the library has been made.
+ * ====================================================================== */
+
+/* Pair layouts of apex_attn_rope. */
+enum {
+    APEX_ROPE_INTERLEAVED = 0, /* pairs (2i, 2i+1): the layout of every other entry point */
+    APEX_ROPE_HALF = 1         /* pairs (i, i + d_rot/2)                                  */
+};
+
+/* Options of apex_attn_rope; all zeros: interleaved, the whole row, base 10000. */
+typedef struct apex_rope_options {
+    int layout;           /* APEX_ROPE_INTERLEAVED or APEX_ROPE_HALF                     */
+    int rot_start;        /* first rotated entry of a row                                */
+    int d_rot;            /* rotated entries (even); 0: all from rot_start on            */
+    int inverse;          /* non-zero: rotate by -angle (the gradient of the rotation)   */
+    float rope_base;      /* base b of theta_i = b^(-2i/d_rot); 0 means 10000            */
+    float linear_scale;   /* positions divided by this (> 0); 0 means 1                  */
+    float yarn_scale;     /* YaRN factor s as in apex_attn_options; <= 1: none           */
+    float yarn_beta_fast; /* 0: 32                                                       */
+    float yarn_beta_slow; /* 0: 1                                                        */
+} apex_rope_options;
+
+/* One tensor of apex_attn_rope: rows of consecutive entries at in + b * in_b +
+ * h * in_h + s * in_s (strides in elements, any order), written to out likewise.
+ * out may be in with the same strides; otherwise the two must not overlap. */
+typedef struct apex_rope_tensor {
+    const void *in;
+    void *out;
+    int n_heads;
+    int d_row; /* entries per row */
+    long long in_b, in_h, in_s;
+    long long out_b, out_h, out_s;
+} apex_rope_tensor;
+
+/*
+ * Rotary positions: rows of q and k turned by their tokens' positions, and v
+ * copied beside them.  For every token (b, s) at m = positions[b * pos_stride + s]
+ * and every pair (x, y) of a row's rotated part, i = 0 .. d_rot/2 - 1,
+ *   (x, y) -> (x cos(m theta_i) - y sin(m theta_i), x sin(m theta_i) + y cos(m theta_i))
+ * (Part 1 §4.2-§4.4; YaRN's theta_i of Part 1 §5.3-§5.4), in fp32, rounded once to
+ * bf16; the other entries are copied.  Positions are any int32, negative ones
+ * included: the angle is reduced exactly, in 64-bit fractions of a turn, so no
+ * table is read or grown.
+ *
+ *   q, k, v     tensors (either may be NULL, not all three); q and k need
+ *               rot_start + d_rot <= d_row; v's rows are copied unchanged
+ *   positions   [B, S] int32, device (pos_stride elements between sequences, 0: shared)
+ *   row0        NULL, or [B] int32, device: token s of k and of v is written at
+ *               row row0[b] + s of out (instead of s), e.g. appended to a cache;
+ *               rows outside [0, out_rows) are not written
+ *   out_rows    rows of k's and v's out (with row0)
+ *
+ * 1 <= B, S <= 2^24 with B * S < 2^31, d_row <= 1024, d_rot <= 512.  Any strides
+ * and element alignment are taken; 16-byte aligned rows with d_rot (half layout:
+ * d_rot / 2), rot_start and d_row multiples of 8 run 16 bytes at a time.
+ * The YaRN temperature (0.1 ln s + 1) is not applied: it belongs to the scores'
+ * scale.
+ */
+apex_status apex_attn_rope(const apex_rope_tensor *q, const apex_rope_tensor *k, const apex_rope_tensor *v, int B,
+                           int S, const int *positions, long long pos_stride, const int *row0, int out_rows,
+                           const apex_rope_options *opt, apex_stream_t stream);
+
+/*
+ * Attention of a tree of T drafted tokens per sequence over a cache: every
+ * drafted token sees the sequence's cached keys and its own ancestors among the
+ * drafts, whose keys and values already sit behind them in the cache.
+ *
+ *   q         [B, H_q,  T,     d_qk] bf16, read   (rotated)
+ *   k_cache   [B, H_kv, S_cap, d_qk] bf16, read   (rotated; rows lens[b] + u: the drafts)
+ *   v_cache   [B, H_kv, S_cap, d_v]  bf16, read
+ *   out       [B, H_q,  T,     d_v]  bf16, written
+ *   lens      [B] int32, device: cached keys before the drafts (taken as
+ *             clamped to [0, S_cap]; rows at or past S_cap are not visible)
+ *   tree_mask NULL (draft t sees the drafts u <= t), or uint64, device: bit u of
+ *             tree_mask[b * mask_stride + t] set <=> draft t sees draft u
+ *             (mask_stride 0: one tree for the batch)
+ *   positions NULL (draft t at lens[b] + t), or [B, T] int32, device; used with a
+ *             window only; a position below lens[b] counts as lens[b]
+ *   window    <= 0: none; > 0: cached key j is at position j, draft u at its own,
+ *             and a key is seen only if (position of t) - (its position) < window
+ *   scale     factor of the scores, > 0; 0: 1 / sqrt(d_qk)
+ *   workspace at least apex_attn_tree_workspace_bytes(...) bytes, 16-byte aligned,
+ *             owned by the caller, not read before written; calls that may run at
+ *             the same time need one each
+ *
+ * 1 <= T <= 64, 1 <= B <= 65536; G = H_q / H_kv as for the other entry points.  A
+ * row that sees no key gives zeros.  Cache rows that no draft of the sequence
+ * sees (past the drafts, before every window, masked in the whole tree) may hold
+ * anything, infinities and NaN included; the values of the others must be finite.
+ * Softmax statistics and sums are fp32; the weights are rounded to bf16 for the
+ * tensor cores.
+ */
+apex_status apex_attn_tree_decode(const void *q, const void *k_cache, const void *v_cache, void *out, int B, int H_q,
+                                  int H_kv, int T, int S_cap, int d_qk, int d_v, const int *lens,
+                                  const uint64_t *tree_mask, long long mask_stride, const int *positions, int window,
+                                  float scale, void *workspace, size_t workspace_bytes, apex_stream_t stream);
+
+/* Bytes of workspace apex_attn_tree_decode needs; 0 when the sizes are invalid.  Host-only. */
+size_t apex_attn_tree_workspace_bytes(int B, int H_q, int H_kv, int T, int S_cap, int d_qk, int d_v);
+
+/*
+ * Decode (one query per sequence) over a cache of rotated keys that also adds
+ * each cached row's attention weight to a running sum:
+ *   out[b,h]      = sum_j p[b,h,j] v[b,g,j],   p = softmax over j < lens[b]
+ *   acc[b,g,j]   += sum of p[b,h,j] over the G query heads h of KV head g, j < lens[b]
+ *
+ *   q       [B, H_q,  1,     d_qk] bf16, read (rotated)
+ *   k_cache [B, H_kv, S_cap, d_qk] bf16, v_cache [B, H_kv, S_cap, d_v] bf16, read
+ *   out     [B, H_q,  1,     d_v]  bf16, written
+ *   lens    [B] int32, device (taken as clamped to [0, S_cap]); 0 gives zeros
+ *   acc     [B, H_kv, S_cap] fp32, read and written up to lens[b]; rows behind stay
+ *   scale   as for apex_attn_tree_decode
+ *   workspace at least apex_attn_decode_weights_workspace_bytes(...) bytes, as above
+ *
+ * Cache rows at or past lens[b] may hold anything.  The sums are made in a fixed
+ * order: equal inputs give equal bits.
+ */
+apex_status apex_attn_decode_weights(const void *q, const void *k_cache, const void *v_cache, void *out, int B,
+                                     int H_q, int H_kv, int S_cap, int d_qk, int d_v, const int *lens, float *acc,
+                                     float scale, void *workspace, size_t workspace_bytes, apex_stream_t stream);
+
+/* Bytes of workspace apex_attn_decode_weights needs; 0 when the sizes are invalid.  Host-only. */
+size_t apex_attn_decode_weights_workspace_bytes(int B, int H_q, int H_kv, int S_cap, int d_qk, int d_v);
+
+/*
+ * Cut every (sequence, KV head) of a cache down to `budget` rows, by position and
+ * accumulated attention weight.  Of the rows j < lens[b] it keeps those at
+ * positions < n_sink or >= next_pos[b] - n_recent first and then those with the
+ * largest acc (ties, and more such positions than the budget: the lowest row; NaN
+ * counts as the least weight).  Kept rows below `budget` stay where they are;
+ * kept rows at or past it move, in ascending order, into the freed rows below it,
+ * in ascending order: attention over rotated keys does not depend on the order of
+ * the rows, and so only rows that must move do.  A sequence of lens[b] <= budget
+ * keeps everything in place.
+ *
+ *   k_cache [B, H_kv, S_cap, d_k], v_cache [B, H_kv, S_cap, d_v] bf16, moved in place;
+ *           rows at or past min(lens[b], budget) are left as they were
+ *   acc, positions      [B, H_kv, S_cap] fp32 / int32, read; positions NULL: row j is
+ *                       at position j
+ *   acc_out, positions_out  the same shapes, written whole, in the new row order, with
+ *                       0 and -1 from row min(lens[b], budget) on; must not overlap
+ *                       acc, positions
+ *   lens, next_pos      [B] int32; next_pos NULL: lens
+ *   lens_out            [B] int32, written: min(lens[b], budget); may be lens
+ *   budget >= 1, n_sink, n_recent >= 0, n_sink + n_recent <= budget
+ *   workspace           at least apex_attn_evict_workspace_bytes(...) bytes, as above
+ *
+ * d_k and d_v: multiples of 8 up to 1024.
+ */
+apex_status apex_attn_evict(void *k_cache, void *v_cache, int B, int H_kv, int S_cap, int d_k, int d_v,
+                            const float *acc, const int *positions, const int *lens, const int *next_pos, int budget,
+                            int n_sink, int n_recent, float *acc_out, int *positions_out, int *lens_out,
+                            void *workspace, size_t workspace_bytes, apex_stream_t stream);
+
+/* Bytes of workspace apex_attn_evict needs; 0 when the sizes are invalid.  Host-only. */
+size_t apex_attn_evict_workspace_bytes(int B, int H_kv, int S_cap, int budget);
+
 /*
  * Read and clear the current device's status word, after synchronising the
  * device.  APEX_OK when no kernel recorded a problem since the last call;

@@ -11,8 +11,7 @@
 #include <mutex>
 #include <vector>
 
-#include "../../include/apex_attn.h"
-#include "kernel_params.h"
+#include "host_common.h"
 
 namespace apex {
 
@@ -30,16 +29,6 @@ uint64_t wait_timeout_ns()
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxSeq = 1 << 24;
-
-// RoPE frequency parameters: base and the YaRN scaling (s <= 1: none).
-struct RopeFreq {
-    float base, yarn_s, beta_fast, beta_slow;
-    bool operator==(const RopeFreq &o) const
-    {
-        return base == o.base && yarn_s == o.yarn_s && beta_fast == o.beta_fast && beta_slow == o.beta_slow;
-    }
-};
 
 struct RopeTable {
     int d_h;
@@ -89,6 +78,8 @@ apex_status init_device(DeviceState &st, int dev)
     return APEX_OK;
 }
 
+}  // namespace
+
 // Part 1, §4.3: theta_i = base^(-2i/d_h); with YaRN (Part 1, §5.3-§5.4) the
 // pair's wavelength 2 pi / theta_i decides: below beta_fast it is kept, above
 // beta_slow * s it is divided by s, in between divided by t s + 1 - t with
@@ -104,6 +95,8 @@ double rope_frequency(int i, int d_h, const RopeFreq &f)
     t = t < 0.0 ? 0.0 : (t > 1.0 ? 1.0 : t);
     return theta / (t * s + (1.0 - t));
 }
+
+namespace {
 
 // Part 1, §5.5: the YaRN attention temperature multiplied into the scores.
 double score_temperature(const RopeFreq &f) { return f.yarn_s > 1.f ? 0.1 * log((double)f.yarn_s) + 1.0 : 1.0; }
@@ -153,7 +146,8 @@ apex_status get_table(DeviceState &st, int d_h, const RopeFreq &f, int need, Rop
     return APEX_OK;
 }
 
-// Options -> frequency parameters, with the documented defaults; false when invalid.
+}  // namespace
+
 bool freq_of(const apex_attn_options &o, RopeFreq *f)
 {
     f->base = o.rope_base == 0.f ? 10000.f : o.rope_base;
@@ -167,6 +161,8 @@ bool freq_of(const apex_attn_options &o, RopeFreq *f)
         return false;
     return true;
 }
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
@@ -183,8 +179,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
     return fn;
 }
 
-// 3-D bf16 map over a dense [outer][rows][d_h] tensor, 128-byte swizzle, box
-// {64 dims, box_rows, box_outer}; out-of-range elements read as zero.
+}  // namespace
+
 bool make_map(CUtensorMap *m, const void *base, int d_h, int rows, int outer, int box_rows, int box_outer)
 {
     auto enc = tensor_map_encoder();
@@ -198,6 +194,8 @@ bool make_map(CUtensorMap *m, const void *base, int d_h, int rows, int outer, in
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 // 4-D bf16 map over the output [units][G][S_q][128] of the CTA-pair prefill,
 // box {64, min(P, 32), max(1, 32 / P), 1} with P = 128 / G (the 32 M-tile rows of
@@ -216,10 +214,6 @@ bool make_out_map(CUtensorMap *m, void *base, int S_q, int G, int units)
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool supported_group(int G) { return G == 1 || G == 2 || G == 4 || G == 8 || G == 16; }
 
 apex_status check_common(int B, int H_q, int H_kv, int S_k, int d_h, float base)
 {
@@ -241,6 +235,22 @@ DeviceState *current_state(int *dev_out)
     *dev_out = dev;
     return &g_state[dev];
 }
+
+}  // namespace
+
+DeviceScope::DeviceScope() : status(APEX_ERR_CUDA)
+{
+    int dev;
+    DeviceState *st = current_state(&dev);
+    if (!st) return;
+    lock = std::unique_lock<std::mutex>(st->mu);
+    status = init_device(*st, dev);
+    if (status != APEX_OK) return;
+    sm_count = st->sm_count;
+    wait = WaitCtl{st->status, wait_timeout_ns()};
+}
+
+namespace {
 
 // --- decode split choice: the KV range of each (b, kv-head) unit is cut into
 // n_split splits of whole 64-key stages; pick the count that minimises the

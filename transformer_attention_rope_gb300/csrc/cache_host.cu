@@ -1,0 +1,308 @@
+// cache_host.cu -- entry points of include/apex_attn.h that work on caches of
+// rotated keys: argument checks, workspace layout and launches.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "cache_attn.h"
+#include "evict.h"
+#include "host_common.h"
+#include "rope.h"
+
+namespace apex {
+namespace {
+
+bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// ----------------------------------------------------------------- rope
+
+// theta_i / 2 pi as 0.64 fixed-point fractions of a turn.  The last few parameter
+// sets are kept, as the tables of the other entry points are: 64 pow() calls take
+// longer than launching a small rotation.
+struct TurnSet {
+    RopeFreq f;
+    float linear;
+    int d_rot;  // 0: empty
+    uint64_t turns[kRopeMaxPairs];
+};
+
+void turns_of(const RopeFreq &f, float linear, int d_rot, uint64_t *out)
+{
+    static std::mutex mu;
+    static TurnSet sets[8];
+    static int next = 0;
+    std::lock_guard<std::mutex> lk(mu);
+    for (const TurnSet &t : sets)
+        if (t.d_rot == d_rot && t.f == f && t.linear == linear) {
+            memcpy(out, t.turns, sizeof(uint64_t) * (d_rot / 2));
+            return;
+        }
+    TurnSet &t = sets[next];
+    next = (next + 1) % 8;
+    t.f = f;
+    t.linear = linear;
+    t.d_rot = d_rot;
+    for (int i = 0; i < d_rot / 2; ++i) {
+        // whole turns per position do not change the angle
+        const double turn = fmod(rope_frequency(i, d_rot, f) / linear / 6.283185307179586476925, 1.0);
+        t.turns[i] = (uint64_t)ldexp(turn, 64);
+    }
+    memcpy(out, t.turns, sizeof(uint64_t) * (d_rot / 2));
+}
+
+bool rope_tensor_ok(const apex_rope_tensor *t)
+{
+    return t->in && t->out && t->n_heads > 0 && t->d_row > 0 && aligned(t->in, 2) && aligned(t->out, 2);
+}
+
+bool rows_of_16_bytes(const apex_rope_tensor *t)
+{
+    const long long strides = t->in_b | t->in_h | t->in_s | t->out_b | t->out_h | t->out_s;
+    return aligned16(t->in) && aligned16(t->out) && t->d_row % 8 == 0 && strides % 8 == 0;
+}
+
+}  // namespace
+}  // namespace apex
+
+using namespace apex;
+
+extern "C" {
+
+apex_status apex_attn_rope(const apex_rope_tensor *q, const apex_rope_tensor *k, const apex_rope_tensor *v, int B,
+                           int S, const int *positions, long long pos_stride, const int *row0, int out_rows,
+                           const apex_rope_options *opt, apex_stream_t stream)
+{
+    if (!opt || !positions || (!q && !k && !v)) return APEX_ERR_INVALID_ARG;
+    if (!aligned(positions, 4) || (row0 && !aligned(row0, 4))) return APEX_ERR_INVALID_ARG;
+    if (B <= 0 || S <= 0 || pos_stride < 0 || (row0 && out_rows <= 0)) return APEX_ERR_INVALID_ARG;
+    if (opt->layout != APEX_ROPE_INTERLEAVED && opt->layout != APEX_ROPE_HALF) return APEX_ERR_INVALID_ARG;
+    if (opt->rot_start < 0 || opt->d_rot < 0 || opt->d_rot % 2 != 0) return APEX_ERR_INVALID_ARG;
+    apex_attn_options fo;
+    memset(&fo, 0, sizeof fo);
+    fo.rope_base = opt->rope_base;
+    fo.yarn_scale = opt->yarn_scale;
+    fo.yarn_beta_fast = opt->yarn_beta_fast;
+    fo.yarn_beta_slow = opt->yarn_beta_slow;
+    RopeFreq f;
+    if (!freq_of(fo, &f)) return APEX_ERR_INVALID_ARG;
+    const float linear = opt->linear_scale == 0.f ? 1.f : opt->linear_scale;
+    if (!(linear > 0.f) || !isfinite(linear)) return APEX_ERR_INVALID_ARG;
+    if (B > kMaxSeq || S > kMaxSeq || (long long)B * S >= (1ll << 31)) return APEX_ERR_UNSUPPORTED;
+
+    const apex_rope_tensor *in[3] = {q, k, v};
+    int d_rot = opt->d_rot;
+    for (int i = 0; i < 3; ++i) {
+        if (!in[i]) continue;
+        if (!rope_tensor_ok(in[i])) return APEX_ERR_INVALID_ARG;
+        if (i == 2) continue;
+        const int room = in[i]->d_row - opt->rot_start;
+        if (d_rot == 0) d_rot = room;  // the whole row from rot_start on
+        if (d_rot <= 0 || d_rot > room || d_rot % 2 != 0) return APEX_ERR_INVALID_ARG;
+        if (opt->d_rot == 0 && d_rot != room) return APEX_ERR_INVALID_ARG;  // q and k disagree
+    }
+    for (int i = 0; i < 3; ++i)
+        if (in[i] && (in[i]->d_row > 1024 || in[i]->n_heads > (1 << 20))) return APEX_ERR_UNSUPPORTED;
+    if (d_rot > 2 * kRopeMaxPairs) return APEX_ERR_UNSUPPORTED;
+    if (d_rot == 0) d_rot = 2;  // values alone: nothing turns
+
+    RopeParams p;
+    memset(&p, 0, sizeof p);
+    const bool half = opt->layout == APEX_ROPE_HALF;
+    bool wide = opt->rot_start % 8 == 0 && (half ? d_rot / 2 : d_rot) % 8 == 0;
+    int heads = 0, nt = 0, width = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (!in[i]) continue;
+        RopeTensor &t = p.t[nt++];
+        t = RopeTensor{static_cast<const uint16_t *>(in[i]->in), static_cast<uint16_t *>(in[i]->out),
+                       in[i]->in_b, in[i]->in_h, in[i]->in_s, in[i]->out_b, in[i]->out_h, in[i]->out_s,
+                       in[i]->d_row, i != 2, i != 0};
+        wide = wide && rows_of_16_bytes(in[i]);
+        heads += in[i]->n_heads;
+        width = std::max(width, in[i]->d_row);
+    }
+    p.positions = positions;
+    p.pos_stride = pos_stride;
+    p.row0 = row0;
+    p.out_rows = out_rows;
+    p.B = B;
+    p.S = S;
+    p.rot_start = opt->rot_start;
+    p.d_rot = d_rot;
+    p.half = half;
+    p.sign = opt->inverse ? -1.f : 1.f;
+    turns_of(f, linear, d_rot, p.turns);
+
+    int sm_count = 0, dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return APEX_ERR_CUDA;
+    // Heads per group: up to 8 share the sines of a unit; fewer when the tokens alone
+    // do not fill the GPU, down to one head a thread.
+    const long long units = (long long)B * S * (wide ? width / 8 : width);
+    const long long bx = (units + kRopeThreads - 1) / kRopeThreads;
+    const long long target = 4ll * sm_count;
+    int per = (int)std::min<long long>(8, std::max<long long>(1, bx * heads / target));
+    per = std::max(per, (heads + kRopeMaxGroups - 4) / (kRopeMaxGroups - 3));
+    for (int i = 0, k = 0; i < 3; ++i) {
+        if (!in[i]) continue;
+        for (int h = 0; h < in[i]->n_heads; h += per)
+            p.groups[p.n_groups++] = RopeGroup{k, h, std::min(per, in[i]->n_heads - h)};
+        ++k;
+    }
+    const int kind = !wide ? kRopePairs : half ? kRopeHalf : kRopeInterleaved;
+    const int grid_x = (int)std::min<long long>(bx, 1 << 20);
+    if (launch_rope(p, kind, grid_x, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return APEX_ERR_CUDA;
+    return APEX_OK;
+}
+
+// ----------------------------------------------------------------- eviction
+
+size_t apex_attn_evict_workspace_bytes(int B, int H_kv, int S_cap, int budget)
+{
+    if (B <= 0 || H_kv <= 0 || S_cap <= 0 || budget <= 0 || S_cap > kMaxSeq) return 0;
+    if ((long long)B * H_kv > (1 << 24)) return 0;
+    return evict_workspace(B * H_kv, S_cap, budget).bytes;
+}
+
+apex_status apex_attn_evict(void *k_cache, void *v_cache, int B, int H_kv, int S_cap, int d_k, int d_v,
+                            const float *acc, const int *positions, const int *lens, const int *next_pos, int budget,
+                            int n_sink, int n_recent, float *acc_out, int *positions_out, int *lens_out,
+                            void *workspace, size_t workspace_bytes, apex_stream_t stream)
+{
+    if (!k_cache || !v_cache || !acc || !lens || !acc_out || !positions_out || !lens_out || !workspace)
+        return APEX_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(acc) || !aligned16(positions) || !aligned(lens, 4) ||
+        !aligned(next_pos, 4) || !aligned16(acc_out) || !aligned16(positions_out) || !aligned(lens_out, 4) ||
+        !aligned16(workspace))
+        return APEX_ERR_INVALID_ARG;
+    if (B <= 0 || H_kv <= 0 || S_cap <= 0 || d_k <= 0 || d_v <= 0) return APEX_ERR_INVALID_ARG;
+    if (budget <= 0 || n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > budget) return APEX_ERR_INVALID_ARG;
+    if (acc_out == acc || positions_out == positions) return APEX_ERR_INVALID_ARG;
+    if (S_cap > kMaxSeq || (long long)B * H_kv > (1 << 24)) return APEX_ERR_UNSUPPORTED;
+    if (d_k % 8 != 0 || d_v % 8 != 0 || d_k > 1024 || d_v > 1024) return APEX_ERR_UNSUPPORTED;
+    const EvictWorkspace w = evict_workspace(B * H_kv, S_cap, budget);
+    if (workspace_bytes < w.bytes) return APEX_ERR_INVALID_ARG;
+    EvictParams p;
+    memset(&p, 0, sizeof p);
+    p.k = static_cast<uint4 *>(k_cache);
+    p.v = static_cast<uint4 *>(v_cache);
+    p.ck = d_k / 8;
+    p.cv = d_v / 8;
+    p.acc = acc;
+    p.positions = positions;
+    p.lens = lens;
+    p.next_pos = next_pos ? next_pos : lens;
+    p.acc_out = acc_out;
+    p.positions_out = positions_out;
+    p.lens_out = lens_out;
+    p.moved = reinterpret_cast<int *>(workspace);
+    p.holes = reinterpret_cast<int *>(static_cast<char *>(workspace) + w.holes);
+    p.sources = reinterpret_cast<int *>(static_cast<char *>(workspace) + w.sources);
+    p.cap = w.cap;
+    p.B = B;
+    p.H_kv = H_kv;
+    p.S_cap = S_cap;
+    p.budget = budget;
+    p.n_sink = n_sink;
+    p.n_recent = n_recent;
+    int sm_count = 0, dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return APEX_ERR_CUDA;
+    if (launch_evict(p, sm_count, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return APEX_ERR_CUDA;
+    return APEX_OK;
+}
+
+// ----------------------------------------------------------------- attention over a cache of rotated keys
+
+static apex_status check_cache_attn(int B, int H_q, int H_kv, int T, int S_cap, int d_qk, int d_v)
+{
+    if (B <= 0 || H_q <= 0 || H_kv <= 0 || T <= 0 || S_cap <= 0 || d_qk <= 0 || d_v <= 0) return APEX_ERR_INVALID_ARG;
+    if (H_q % H_kv != 0) return APEX_ERR_INVALID_ARG;
+    if (T > kTreeMaxDrafts || S_cap > kMaxSeq || B > 65536) return APEX_ERR_UNSUPPORTED;
+    if (!((d_qk == 64 && d_v == 64) || (d_qk == 128 && d_v == 128) || (d_qk == 192 && d_v == 128)))
+        return APEX_ERR_UNSUPPORTED;
+    if (!supported_group(H_q / H_kv)) return APEX_ERR_UNSUPPORTED;
+    if ((long long)B * H_q > (1 << 24) || (long long)B * H_kv * (long long)S_cap > (1ll << 40))
+        return APEX_ERR_UNSUPPORTED;
+    return APEX_OK;
+}
+
+static apex_status cache_attn(const void *q, const void *k_cache, const void *v_cache, void *out, int B, int H_q,
+                              int H_kv, int T, int S_cap, int d_qk, int d_v, const int *lens,
+                              const uint64_t *tree_mask, long long mask_stride, const int *positions, int window,
+                              float *acc, bool weights, float scale, void *workspace, size_t workspace_bytes,
+                              apex_stream_t stream)
+{
+    if (!q || !k_cache || !v_cache || !out || !lens || !workspace || (weights && !acc)) return APEX_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace) ||
+        !aligned(lens, 4) || !aligned(tree_mask, 8) || !aligned(positions, 4) || !aligned(acc, 4))
+        return APEX_ERR_INVALID_ARG;
+    if (!isfinite(scale) || scale < 0.f || mask_stride < 0) return APEX_ERR_INVALID_ARG;
+    apex_status s = check_cache_attn(B, H_q, H_kv, T, S_cap, d_qk, d_v);
+    if (s != APEX_OK) return s;
+    const CacheAttnWorkspace w = cache_attn_workspace(B, H_q, H_kv, T, S_cap, d_v, weights);
+    if (workspace_bytes < w.bytes) return APEX_ERR_INVALID_ARG;
+    DeviceScope dev;
+    if (dev.status != APEX_OK) return dev.status;
+    CacheAttnParams p;
+    memset(&p, 0, sizeof p);
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(k_cache);
+    p.v = static_cast<const uint16_t *>(v_cache);
+    p.out = static_cast<uint16_t *>(out);
+    p.B = B;
+    p.H_q = H_q;
+    p.H_kv = H_kv;
+    p.G = H_q / H_kv;
+    p.T = T;
+    p.S_cap = S_cap;
+    p.d_qk = d_qk;
+    p.d_v = d_v;
+    p.lens = lens;
+    p.tree_mask = tree_mask;
+    p.mask_stride = mask_stride;
+    p.positions = positions;
+    p.window = window > 0 ? window : 0;
+    p.drafts = weights ? 0 : T;
+    p.acc = acc;
+    p.scale_log2 = (float)(1.4426950408889634 * (scale == 0.f ? 1.0 / sqrt((double)d_qk) : (double)scale));
+    p.wait = dev.wait;
+    cache_attn_bind(p, w, workspace);
+    if (launch_cache_attn(p, dev.sm_count, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return APEX_ERR_CUDA;
+    return APEX_OK;
+}
+
+size_t apex_attn_tree_workspace_bytes(int B, int H_q, int H_kv, int T, int S_cap, int d_qk, int d_v)
+{
+    if (check_cache_attn(B, H_q, H_kv, T, S_cap, d_qk, d_v) != APEX_OK) return 0;
+    return cache_attn_workspace(B, H_q, H_kv, T, S_cap, d_v, false).bytes;
+}
+
+size_t apex_attn_decode_weights_workspace_bytes(int B, int H_q, int H_kv, int S_cap, int d_qk, int d_v)
+{
+    if (check_cache_attn(B, H_q, H_kv, 1, S_cap, d_qk, d_v) != APEX_OK) return 0;
+    return cache_attn_workspace(B, H_q, H_kv, 1, S_cap, d_v, true).bytes;
+}
+
+apex_status apex_attn_tree_decode(const void *q, const void *k_cache, const void *v_cache, void *out, int B, int H_q,
+                                  int H_kv, int T, int S_cap, int d_qk, int d_v, const int *lens,
+                                  const uint64_t *tree_mask, long long mask_stride, const int *positions, int window,
+                                  float scale, void *workspace, size_t workspace_bytes, apex_stream_t stream)
+{
+    return cache_attn(q, k_cache, v_cache, out, B, H_q, H_kv, T, S_cap, d_qk, d_v, lens, tree_mask, mask_stride,
+                      positions, window, nullptr, false, scale, workspace, workspace_bytes, stream);
+}
+
+apex_status apex_attn_decode_weights(const void *q, const void *k_cache, const void *v_cache, void *out, int B,
+                                     int H_q, int H_kv, int S_cap, int d_qk, int d_v, const int *lens, float *acc,
+                                     float scale, void *workspace, size_t workspace_bytes, apex_stream_t stream)
+{
+    return cache_attn(q, k_cache, v_cache, out, B, H_q, H_kv, 1, S_cap, d_qk, d_v, lens, nullptr, 0, nullptr, 0, acc,
+                      true, scale, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
