@@ -6,17 +6,18 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kernel_params.h"
 
 namespace apex {
 
-constexpr int kTreeMaxDrafts = 64;  // one mask word per draft
+constexpr int kTreeMaxDrafts = 64;    // one mask word per draft
+constexpr int kCacheTileKeys = 128;   // keys per tile
+constexpr int kCacheMaxCtas = 160;    // CTAs that may hold partial results
 
 struct CacheAttnParams {
-    const uint16_t *q;  // [B, H_q, T, d_qk]
-    const uint16_t *k;  // [B, H_kv, S_cap, d_qk]
-    const uint16_t *v;  // [B, H_kv, S_cap, d_v]
-    uint16_t *out;      // [B, H_q, T, d_v]
+    uint16_t *out;  // [B, H_q, T, d_v]
     int B, H_q, H_kv, G, T, S_cap, d_qk, d_v;
     const int *lens;
     const uint64_t *tree_mask;
@@ -27,25 +28,67 @@ struct CacheAttnParams {
     float *acc;  // [B, H_kv, S_cap], or NULL
     float scale_log2;
     WaitCtl wait;
-    float *lse;  // [B*H_q] log2 of the softmax denominators (with acc)
+    int R;          // query rows of a KV head, G * T
+    int group;      // rows of a row group (one or two M tiles)
+    int n_groups;   // row groups of a KV head
+    int rows_cap;   // rows of a partial result, min(R, group)
+    // workspace
+    float *ws_o;    // [2 * kCacheMaxCtas][rows_cap][d_v] partial outputs (unnormalised)
+    float2 *ws_ml;  // [2 * kCacheMaxCtas][rows_cap]      their (max in log2 units, sum)
+    int2 *units;    // [B * H_kv * n_groups]              first and last CTA of each unit
+    float *lse;     // [B * H_q]                          log2 of the softmax denominators (with acc)
+    float *scores;  // [B * H_q][S_pad]                   scores (with acc)
+    int S_pad;
 };
+
+// Rows of a KV head's queries (G heads x T drafts) are worked on in groups of one or
+// two 128-row M tiles.
+inline int cache_attn_group(int R) { return R <= 128 ? 128 : 256; }
 
 struct CacheAttnWorkspace {
-    size_t bytes;
+    size_t ml, units, lse, scores, bytes;
+    int rows_cap, n_groups, S_pad;
 };
 
-inline CacheAttnWorkspace cache_attn_workspace(int B, int H_q, int, int T, int, int, bool weights)
+inline CacheAttnWorkspace cache_attn_workspace(int B, int H_q, int H_kv, int T, int S_cap, int d_v, bool weights)
 {
     CacheAttnWorkspace w;
-    w.bytes = weights ? ((size_t)B * H_q * T * sizeof(float) + 255) & ~size_t(255) : 256;
+    const int R = H_q / H_kv * T, group = cache_attn_group(R);
+    w.rows_cap = std::min(R, group);
+    w.n_groups = (R + group - 1) / group;
+    w.S_pad = (S_cap + kCacheTileKeys - 1) / kCacheTileKeys * kCacheTileKeys;
+    auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+    const size_t slots = (size_t)2 * kCacheMaxCtas * w.rows_cap;
+    w.ml = up(slots * d_v * sizeof(float));
+    w.units = w.ml + up(slots * sizeof(float2));
+    w.lse = w.units + up((size_t)B * H_kv * w.n_groups * sizeof(int2));
+    w.scores = w.lse + (weights ? up((size_t)B * H_q * sizeof(float)) : 0);
+    w.bytes = w.scores + (weights ? up((size_t)B * H_q * w.S_pad * sizeof(float)) : 0);
     return w;
 }
 
-inline void cache_attn_bind(CacheAttnParams &p, const CacheAttnWorkspace &, void *workspace)
+inline void cache_attn_bind(CacheAttnParams &p, const CacheAttnWorkspace &w, void *workspace)
 {
-    p.lse = static_cast<float *>(workspace);
+    char *base = static_cast<char *>(workspace);
+    p.R = p.G * p.T;
+    p.group = cache_attn_group(p.R);
+    p.n_groups = w.n_groups;
+    p.rows_cap = w.rows_cap;
+    p.S_pad = w.S_pad;
+    p.ws_o = reinterpret_cast<float *>(base);
+    p.ws_ml = reinterpret_cast<float2 *>(base + w.ml);
+    p.units = reinterpret_cast<int2 *>(base + w.units);
+    p.lse = reinterpret_cast<float *>(base + w.lse);
+    p.scores = reinterpret_cast<float *>(base + w.scores);
 }
 
-cudaError_t launch_cache_attn(const CacheAttnParams &p, int sm_count, cudaStream_t stream);
+struct CacheAttnLaunch {
+    // 3-D maps, boxes of 128 rows x 64 entries, 128-byte swizzle: q as [B*H_kv][R][d_qk]
+    // (the rows of a KV head's query heads are adjacent), k and v [B*H_kv][S_cap][d]
+    CUtensorMap tm_q, tm_k, tm_v;
+    CacheAttnParams p;
+};
+
+cudaError_t launch_cache_attn(const CacheAttnLaunch &L, int sm_count, cudaStream_t stream);
 
 }  // namespace apex

@@ -247,11 +247,9 @@ static apex_status cache_attn(const void *q, const void *k_cache, const void *v_
     if (workspace_bytes < w.bytes) return APEX_ERR_INVALID_ARG;
     DeviceScope dev;
     if (dev.status != APEX_OK) return dev.status;
-    CacheAttnParams p;
-    memset(&p, 0, sizeof p);
-    p.q = static_cast<const uint16_t *>(q);
-    p.k = static_cast<const uint16_t *>(k_cache);
-    p.v = static_cast<const uint16_t *>(v_cache);
+    CacheAttnLaunch L;
+    memset(&L, 0, sizeof L);
+    CacheAttnParams &p = L.p;
     p.out = static_cast<uint16_t *>(out);
     p.B = B;
     p.H_q = H_q;
@@ -271,7 +269,10 @@ static apex_status cache_attn(const void *q, const void *k_cache, const void *v_
     p.scale_log2 = (float)(1.4426950408889634 * (scale == 0.f ? 1.0 / sqrt((double)d_qk) : (double)scale));
     p.wait = dev.wait;
     cache_attn_bind(p, w, workspace);
-    if (launch_cache_attn(p, dev.sm_count, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    if (!make_map(&L.tm_q, q, d_qk, p.R, B * H_kv, 128, 1) || !make_map(&L.tm_k, k_cache, d_qk, S_cap, B * H_kv, 128, 1) ||
+        !make_map(&L.tm_v, v_cache, d_v, S_cap, B * H_kv, 128, 1))
+        return APEX_ERR_CUDA;
+    if (launch_cache_attn(L, dev.sm_count, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return APEX_ERR_CUDA;
     return APEX_OK;
 }
