@@ -493,6 +493,7 @@ EVICT = [  # H, d_k, d_v, S_cap, lens, budget, n_sink, n_recent
     (1, 192, 128, 5000, [5000, 4097], 513, 4, 64),       # two CTAs a row set
     (2, 64, 64, 9001, [9001, 4500], 1000, 0, 1000),      # nothing but the newest
     (1, 8, 8, 40000, [40000], 3000, 7, 0),               # eight CTAs
+    (1, 8, 8, 400000, [399999], 100000, 3, 9000),        # more rows than shared memory holds
     (3, 128, 128, 600, [-4, 600, 9999], 599, 0, 0),      # one row goes
     (1, 128, 128, 300, [300], 1, 1, 0),
     (1, 128, 128, 64, [64], 100, 4, 4),                  # budget past the capacity
@@ -541,8 +542,8 @@ def test_evict_more_forced_rows_than_budget():
 
 
 @pytest.mark.gpu
-def test_evict_again_and_in_place_lengths():
-    """A second cut with the first one's outputs as inputs, lengths updated in place."""
+def test_evict_again():
+    """A second cut with the first one's outputs as inputs."""
     dev = _gpu()
     g = _gen(dev, 13)
     k, v = _normal(g, dev, 2, 2, 700, 128), _normal(g, dev, 2, 2, 700, 128)
@@ -550,11 +551,13 @@ def test_evict_again_and_in_place_lengths():
     ln = torch.tensor([700, 650], dtype=torch.int32, device=dev)
     nxt = ln.clone()
     want = _evict_ref(k, v, acc, [700, 650], 300, 4, 50, None, None)
-    a, p, n = apex.evict(k, v, acc, ln, 300, n_sink=4, n_recent=50, lens_out=ln)
-    assert n is ln and ln.tolist() == [300, 300]
+    a, p, n = apex.evict(k, v, acc, ln, 300, n_sink=4, n_recent=50)
+    assert n.tolist() == [300, 300] and ln.tolist() == [700, 650]
     want = _evict_ref(want[0], want[1], want[2], [300, 300], 120, 4, 50, want[3], nxt.tolist())
-    a, p, n = apex.evict(k, v, a, ln, 120, n_sink=4, n_recent=50, positions=p, next_pos=nxt, lens_out=ln)
-    assert ln.tolist() == [120, 120] and torch.equal(p.cpu(), want[3]) and torch.equal(a.double().cpu(), want[2])
+    n2 = torch.empty_like(n)
+    a, p, out = apex.evict(k, v, a, n, 120, n_sink=4, n_recent=50, positions=p, next_pos=nxt, lens_out=n2)
+    assert out is n2 and n2.tolist() == [120, 120]
+    assert torch.equal(p.cpu(), want[3]) and torch.equal(a.double().cpu(), want[2])
     assert torch.equal(k.cpu(), want[0]) and torch.equal(v.cpu(), want[1])
 
 
@@ -787,14 +790,14 @@ def test_decode_weights_refuses(lib, o, code):
 
 
 EVICT_ARGS = dict(k=P, v=P, B=1, H=2, cap=64, dk=128, dv=128, acc=P, pos=None, lens=P, nxt=None, budget=16, sink=0,
-                  recent=0, acc_out=2 * P, pos_out=2 * P, lens_out=P, ws=P, n=1 << 40)
+                  recent=0, acc_out=2 * P, pos_out=2 * P, lens_out=2 * P, ws=P, n=1 << 40)
 
 
 @pytest.mark.parametrize("o,code", [
     (dict(k=None), BAD), (dict(v=None), BAD), (dict(acc=None), BAD), (dict(lens=None), BAD), (dict(acc_out=None), BAD),
     (dict(pos_out=None), BAD), (dict(lens_out=None), BAD), (dict(ws=None), BAD), (dict(k=P + 8), BAD),
     (dict(pos=P + 4), BAD), (dict(lens=P + 2), BAD), (dict(nxt=P + 2), BAD), (dict(acc_out=P), BAD),
-    (dict(pos=2 * P), BAD), (dict(B=0), BAD), (dict(H=-1), BAD), (dict(cap=0), BAD), (dict(budget=0), BAD),
+    (dict(pos=2 * P), BAD), (dict(lens_out=P), BAD), (dict(nxt=2 * P), BAD), (dict(B=0), BAD), (dict(H=-1), BAD), (dict(cap=0), BAD), (dict(budget=0), BAD),
     (dict(sink=-1), BAD), (dict(recent=-1), BAD), (dict(sink=10, recent=7), BAD), (dict(dk=0), BAD),
     (dict(dk=100), UNSUPPORTED), (dict(dv=2048), UNSUPPORTED), (dict(cap=(1 << 24) + 1), UNSUPPORTED),
     (dict(n=15), BAD),

@@ -24,7 +24,9 @@ Over caches of rotated keys (int32 lengths and positions on the device; the tens
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 import threading
 
 __all__ = [
@@ -46,6 +48,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libapex_attn.so")
 _lock = threading.Lock()
 _lib = None
+_torch = None  # the torch module, once a call over caches of rotated keys has needed it
 
 APEX_OK = 0
 _STATUS_NAMES = {0: "APEX_OK", 1: "APEX_ERR_INVALID_ARG", 2: "APEX_ERR_UNSUPPORTED", 3: "APEX_ERR_CUDA",
@@ -88,6 +91,8 @@ def library_path() -> str:
 def load_library():
     """Load the CUDA library; raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -122,8 +127,9 @@ def load_library():
             lib.apex_attn_rope_keys.restype = i32
             lib.apex_attn_mla_rope_keys.argtypes = [vp, vp] + [i32] * 5 + [ctypes.c_longlong] * 2 + [op, vp]
             lib.apex_attn_mla_rope_keys.restype = i32
-            i64, rt = ctypes.c_longlong, ctypes.POINTER(RopeTensor)
-            lib.apex_attn_rope.argtypes = [rt, rt, rt, i32, i32, vp, i64, vp, i32, ctypes.POINTER(RopeOptions), vp]
+            i64 = ctypes.c_longlong
+            # the structs by address: byref(...) or their bytes
+            lib.apex_attn_rope.argtypes = [vp, vp, vp, i32, i32, vp, i64, vp, i32, vp, vp]
             lib.apex_attn_rope.restype = i32
             lib.apex_attn_tree_decode.argtypes = [vp] * 4 + [i32] * 7 + [vp, vp, i64, vp, i32, f32, vp, sz, vp]
             lib.apex_attn_tree_decode.restype = i32
@@ -231,7 +237,7 @@ def apex_attn_mla_rope_keys(k_in, k_out, n_heads, n_pos, d_h, d_r, pos0, in_head
 
 
 def apex_attn_rope(q, k, v, B, S, positions, pos_stride, row0, out_rows, opt, stream) -> int:
-    ref = [ctypes.byref(t) if t is not None else None for t in (q, k, v, opt)]
+    ref = [ctypes.byref(t) if isinstance(t, ctypes.Structure) else t for t in (q, k, v, opt)]
     return load_library().apex_attn_rope(ref[0], ref[1], ref[2], B, S, positions, pos_stride, row0, out_rows, ref[3],
                                          stream)
 
@@ -518,70 +524,113 @@ def mla_rope_keys(k, d_r: int, *, pos0: int = 0, out=None, rope_base: float = 10
 
 
 # ------------------------------------------------------------------ over caches of rotated keys
-def _check_on(t, name, like, dtype, shape):
-    """A contiguous tensor of this dtype and shape on the device of `like`."""
+# A decode step makes several of these calls, each a few microseconds on the device, so
+# the checks of a call that is right are kept short; _refuse says what is wrong otherwise.
+def _load_torch():
+    global _torch
     import torch
+    _torch = torch
+    return torch
+
+
+def _refuse(t, name, dtype, shape, device):
+    torch = _torch
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError("%s must be a CUDA %s tensor" % (name, str(dtype).replace("torch.", "")))
-    if t.device != like.device:
+    if t.get_device() != device:
         raise ValueError("%s is on another device than the other tensors" % name)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous tensor of shape %s" % (name, tuple(shape)))
+    raise ValueError("%s must be a contiguous tensor of shape %s" % (name, tuple(shape)))
+
+
+def _fit(t, name, dtype, shape, device):
+    """Address of a contiguous tensor of this dtype and shape on CUDA device `device` (>= 0)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, device)
+
+
+def _rows4(t, name):
+    """Shape of a 4-D bf16 CUDA tensor."""
+    torch = _torch
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda:
+        raise TypeError("%s must be a CUDA bf16 tensor" % name)
+    shape = t.shape
+    if len(shape) != 4:
+        raise ValueError("%s must be a 4-D tensor" % name)
+    return shape
 
 
 class _Launch:
-    """The device of a tensor made current, and the stream to launch on: the one
-    given, else that device's current stream.  Scratch taken from torch's allocator
-    is kept until the stream is done with it."""
+    """`device` made current, and the stream to launch on: the one given, else the
+    device's current stream."""
+    __slots__ = ("device", "stream", "handle", "guard")
 
-    def __init__(self, like, stream):
-        import torch
-        self.device = like.device
-        self.guard = torch.cuda.device(like.device)
-        self.given = stream
-        if stream is not None and stream.device != like.device:
-            raise ValueError("stream and tensors are on different devices")
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guard = device, stream, None
+        if stream is None:
+            self.handle = _torch._C._cuda_getCurrentRawStream(device)
+        else:
+            if stream.device_index != device:
+                raise ValueError("stream and tensors are on different devices")
+            self.handle = stream.cuda_stream
+        if _torch._C._cuda_getDevice() != device:
+            self.guard = _torch.cuda.device(device)
+            self.guard.__enter__()
 
-    def __enter__(self):
-        import torch
-        self.guard.__enter__()
-        self.stream = self.given if self.given is not None else torch.cuda.current_stream()
-        self.handle = self.stream.cuda_stream
-        return self
+    def leave(self):
+        if self.guard is not None:
+            self.guard.__exit__(None, None, None)
 
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+    def new(self, like, shape, dtype):
+        """A tensor from torch's allocator, kept until the stream is done with it."""
+        t = _torch.empty(shape, dtype=dtype, device=like.device)
+        if self.stream is not None:
+            t.record_stream(self.stream)
+        return t
 
-    def workspace(self, given, need):
-        """(pointer, bytes) of the caller's workspace, or of scratch of `need` bytes."""
-        import torch
+    def workspace(self, given, like, need):
         if given is None:
-            given = torch.empty(max(int(need), 16), dtype=torch.uint8, device=self.device)
-            if self.given is not None:
-                given.record_stream(self.stream)
-        elif not given.is_cuda or given.device != self.device or not given.is_contiguous():
+            return self.new(like, need if need > 16 else 16, _torch.uint8)
+        if not given.is_cuda or given.get_device() != self.device or not given.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the device of the other tensors")
-        return given.data_ptr(), given.numel() * given.element_size()
+        return given
 
 
-def _done(status, what):
-    if status != APEX_OK:
-        raise ApexError(status, what)
+# apex_rope_tensor and apex_rope_options as bytes: quicker to make than ctypes structs
+_ROPE_TENSOR = struct.Struct("@PPiiqqqqqq")
+_ROPE_OPTIONS = struct.Struct("@iiiifffff")
+assert _ROPE_TENSOR.size == ctypes.sizeof(RopeTensor) and _ROPE_OPTIONS.size == ctypes.sizeof(RopeOptions)
+_rope_options = functools.lru_cache(maxsize=64)(_ROPE_OPTIONS.pack)
 
 
-def _rope_rows(x, out, name, like):
-    import torch
-    for t, n in ((x, name), (out, name + "_out")):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
-            raise TypeError("%s must be a CUDA bf16 tensor" % n)
-        if t.device != like.device:
-            raise ValueError("%s is on another device than the other tensors" % n)
-        if t.dim() != 4 or (t.shape[-1] > 1 and t.stride(-1) != 1):
-            raise ValueError("%s must be a 4-D tensor whose last dimension is contiguous" % n)
-    if any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):
+def _rope_rows(x, out, name, B, S, into, device):
+    """apex_rope_tensor of a tensor and its output, as bytes."""
+    bf16 = _torch.bfloat16
+    try:
+        known = x.dtype is bf16 and out.dtype is bf16 and x.get_device() == device == out.get_device()
+    except AttributeError:
+        known = False
+    if not known:
+        _rows4(x, name)
+        _rows4(out, name + "_out")
+        raise ValueError("%s or %s_out is on another device than q" % (name, name))
+    xs, to = x.shape, out.shape
+    if len(xs) != 4 or len(to) != 4:
+        raise ValueError("%s and %s_out must be 4-D tensors" % (name, name))
+    if xs[0] != B or xs[2] != S:
+        raise ValueError("%s must have the batch and length of q" % name)
+    if (to != xs and not into) or to[0] != B or to[1] != xs[1] or to[3] != xs[3]:
+        raise ValueError("%s_out does not fit %s" % (name, name))
+    xb, xh, xr, xe = x.stride()
+    ob, oh, orow, oe = out.stride()
+    if (xe != 1 or oe != 1) and xs[3] > 1:
+        raise ValueError("the last dimension of %s and %s_out must be contiguous" % (name, name))
+    if (ob == 0 and B > 1) or (oh == 0 and to[1] > 1) or (orow == 0 and to[2] > 1):
         raise ValueError("%s_out repeats its elements" % name)
-    return RopeTensor(x.data_ptr(), out.data_ptr(), x.shape[1], x.shape[3], x.stride(0), x.stride(1), x.stride(2),
-                      out.stride(0), out.stride(1), out.stride(2))
+    return _ROPE_TENSOR.pack(x.data_ptr(), out.data_ptr(), xs[1], xs[3], xb, xh, xr, ob, oh, orow)
 
 
 def rope(q, k=None, v=None, *, positions, layout: str = "interleaved", rot_start: int = 0, d_rot=None,
@@ -596,64 +645,63 @@ def rope(q, k=None, v=None, *, positions, layout: str = "interleaved", rot_start
     q_out, k_out, v_out: outputs of any strides, the inputs themselves among them; else new
     contiguous tensors.  row0 [B] int32: token s of k and v goes to row row0[b] + s of k_out
     and v_out (caches [B,H_kv,S_cap,d]); rows outside them are dropped, the others untouched."""
-    import torch
-    if layout not in ("interleaved", "half"):
+    torch = _torch or _load_torch()
+    if layout != "interleaved" and layout != "half":
         raise ValueError("layout must be 'interleaved' or 'half'")
-    if v is not None and k is None:
-        raise ValueError("v goes with k")
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a 4-D tensor")
-    B, _, S, _ = q.shape
-    tensors, outs, out_rows = [], [], 0
-    for x, o, name in ((q, q_out, "q"), (k, k_out, "k"), (v, v_out, "v")):
-        if x is None:
-            if o is not None:
-                raise ValueError("%s_out without %s" % (name, name))
-            continue
-        if o is None:
-            if row0 is not None and name != "q":
-                raise ValueError("row0 needs %s_out" % name)
-            o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        tensors.append(_rope_rows(x, o, name, q))
-        if x.shape[0] != B or x.shape[2] != S:
-            raise ValueError("%s must have the batch and length of q" % name)
-        into = row0 is not None and name != "q"
-        if o.shape[:2] != x.shape[:2] or o.shape[3] != x.shape[3] or (o.shape[2] != S and not into):
-            raise ValueError("%s_out does not fit %s" % (name, name))
-        if into:
-            if out_rows not in (0, o.shape[2]):
-                raise ValueError("k_out and v_out must have the same number of rows")
-            out_rows = o.shape[2]
-        outs.append(o)
-    _check_on(positions, "positions", q, torch.int32, (S,) if positions.dim() == 1 else (B, S))
-    if row0 is not None:
-        _check_on(row0, "row0", q, torch.int32, (B,))
-    opt = RopeOptions(1 if layout == "half" else 0, int(rot_start), 0 if d_rot is None else int(d_rot),
-                      1 if inverse else 0, float(rope_base), float(linear_scale), float(yarn_scale),
-                      float(yarn_beta_fast), float(yarn_beta_slow))
-    if d_rot is not None and int(d_rot) <= 0:
+    if d_rot is None:
+        d_rot = 0
+    elif d_rot <= 0:
         raise ValueError("d_rot must be positive")
-    with _Launch(q, stream) as at:
-        tensors += [None] * (3 - len(tensors))
-        _done(apex_attn_rope(tensors[0], tensors[1], tensors[2], B, S, positions.data_ptr(),
-                             S if positions.dim() == 2 else 0, row0.data_ptr() if row0 is not None else None,
-                             out_rows, opt, at.handle), "apex_attn_rope")
-    return outs[0] if len(outs) == 1 else tuple(outs)
+    if k is None and (v is not None or k_out is not None) or v is None and v_out is not None:
+        raise ValueError("k_out goes with k, and v and v_out with k")
+    B, _, S, _ = _rows4(q, "q")
+    device = q.get_device()
+    opt = _rope_options(1 if layout == "half" else 0, rot_start, d_rot, 1 if inverse else 0, rope_base, linear_scale,
+                        yarn_scale, yarn_beta_fast, yarn_beta_slow)
+    at = _Launch(device, stream)
+    try:
+        pos = _fit(positions, "positions", torch.int32, (S,) if positions.dim() == 1 else (B, S), device)
+        if q_out is None:
+            q_out = at.new(q, q.shape, torch.bfloat16)
+        tq, tk, tv = _rope_rows(q, q_out, "q", B, S, False, device), None, None
+        into, rows, start = row0 is not None, 0, None
+        if into:
+            if k is None or k_out is None or (v is not None and v_out is None):
+                raise ValueError("row0 needs k_out, and v_out where there is a v")
+            start, rows = _fit(row0, "row0", torch.int32, (B,), device), k_out.shape[2]
+            if v is not None and v_out.shape[2] != rows:
+                raise ValueError("k_out and v_out must have the same number of rows")
+        if k is not None:
+            if k_out is None:
+                k_out = at.new(k, k.shape, torch.bfloat16)
+            tk = _rope_rows(k, k_out, "k", B, S, into, device)
+        if v is not None:
+            if v_out is None:
+                v_out = at.new(v, v.shape, torch.bfloat16)
+            tv = _rope_rows(v, v_out, "v", B, S, into, device)
+        status = (_lib or load_library()).apex_attn_rope(tq, tk, tv, B, S, pos, S if positions.dim() == 2 else 0,
+                                                         start, rows, opt, at.handle)
+        if status:
+            raise ApexError(status, "apex_attn_rope")
+    finally:
+        at.leave()
+    return q_out if k is None else (q_out, k_out) if v is None else (q_out, k_out, v_out)
 
 
 def _cache_shapes(q, k_cache, v_cache):
-    for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check(t, n, 4)
-    B, H_q, T, d_qk = q.shape
-    _, H_kv, S_cap, d_v = v_cache.shape
-    if tuple(k_cache.shape) != (B, H_kv, S_cap, d_qk) or v_cache.shape[0] != B:
-        raise ValueError("k_cache / v_cache must be [B, H_kv, S_cap, d] with the batch and row length of q")
-    if k_cache.device != q.device or v_cache.device != q.device:
-        raise ValueError("q, k_cache and v_cache must be on one device")
-    return B, H_q, T, d_qk, H_kv, S_cap, d_v
+    """Sizes of queries and caches, their device and addresses."""
+    torch = _torch
+    B, H_q, T, d_qk = _rows4(q, "q")
+    _, H_kv, S_cap, d_v = _rows4(v_cache, "v_cache")
+    device = q.get_device()
+    return (B, H_q, T, d_qk, H_kv, S_cap, d_v, device, _fit(q, "q", torch.bfloat16, (B, H_q, T, d_qk), device),
+            _fit(k_cache, "k_cache", torch.bfloat16, (B, H_kv, S_cap, d_qk), device),
+            _fit(v_cache, "v_cache", torch.bfloat16, (B, H_kv, S_cap, d_v), device))
 
 
+@functools.lru_cache(maxsize=256)
 def tree_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_v=None) -> int:
+    """Workspace bytes of tree_decode for these sizes (0: invalid; see apex_attn_tree_workspace_bytes)."""
     return int(apex_attn_tree_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_qk if d_v is None else d_v))
 
 
@@ -665,29 +713,38 @@ def tree_decode(q, k_cache, v_cache, lens, *, tree_mask=None, positions=None, wi
 
     tree_mask [B,T] or [T] int64: bit u of word t set when draft t sees draft u (None: u <= t);
     positions [B,T] int32: the drafts' positions, for a window (None: lens[b] + t)."""
-    import torch
-    B, H_q, T, d_qk, H_kv, S_cap, d_v = _cache_shapes(q, k_cache, v_cache)
-    _check_on(lens, "lens", q, torch.int32, (B,))
+    torch = _torch or _load_torch()
+    B, H_q, T, d_qk, H_kv, S_cap, d_v, device, pq, pk, pv = _cache_shapes(q, k_cache, v_cache)
+    plens = _fit(lens, "lens", torch.int32, (B,), device)
+    pmask = ppos = None
+    stride = 0
     if tree_mask is not None:
-        _check_on(tree_mask, "tree_mask", q, torch.int64, (T,) if tree_mask.dim() == 1 else (B, T))
+        one = tree_mask.dim() == 1
+        pmask = _fit(tree_mask, "tree_mask", torch.int64, (T,) if one else (B, T), device)
+        stride = 0 if one else T
     if positions is not None:
-        _check_on(positions, "positions", q, torch.int32, (B, T))
-    with _Launch(q, stream) as at:
+        ppos = _fit(positions, "positions", torch.int32, (B, T), device)
+    at = _Launch(device, stream)
+    try:
         if out is None:
-            out = torch.empty((B, H_q, T, d_v), dtype=torch.bfloat16, device=q.device)
-        _check_on(out, "out", q, torch.bfloat16, (B, H_q, T, d_v))
-        ws, ws_bytes = at.workspace(workspace, tree_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_v))
-        _done(apex_attn_tree_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q,
-                                    H_kv, T, S_cap, d_qk, d_v, lens.data_ptr(),
-                                    tree_mask.data_ptr() if tree_mask is not None else None,
-                                    T if tree_mask is not None and tree_mask.dim() == 2 else 0,
-                                    positions.data_ptr() if positions is not None else None, int(window),
-                                    0.0 if scale is None else float(scale), ws, ws_bytes, at.handle),
-              "apex_attn_tree_decode")
+            out = at.new(q, (B, H_q, T, d_v), torch.bfloat16)
+            pout = out.data_ptr()
+        else:
+            pout = _fit(out, "out", torch.bfloat16, (B, H_q, T, d_v), device)
+        ws = at.workspace(workspace, q, tree_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_v))
+        status = (_lib or load_library()).apex_attn_tree_decode(
+            pq, pk, pv, pout, B, H_q, H_kv, T, S_cap, d_qk, d_v, plens, pmask, stride, ppos, window,
+            0.0 if scale is None else scale, ws.data_ptr(), ws.nbytes, at.handle)
+        if status:
+            raise ApexError(status, "apex_attn_tree_decode")
+    finally:
+        at.leave()
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def decode_weights_workspace_bytes(B, H_q, H_kv, S_cap, d_qk, d_v=None) -> int:
+    """Workspace bytes of decode_weights for these sizes (0: invalid)."""
     return int(apex_attn_decode_weights_workspace_bytes(B, H_q, H_kv, S_cap, d_qk, d_qk if d_v is None else d_v))
 
 
@@ -695,25 +752,33 @@ def decode_weights(q, k_cache, v_cache, lens, acc, *, scale=None, out=None, work
     """Decode over a cache of rotated keys that adds each row's attention weight to acc. q [B,H_q,1,d_qk]
     (rotated), caches [B,H_kv,S_cap,d_qk] / [B,H_kv,S_cap,d_v], lens [B] int32, acc [B,H_kv,S_cap] fp32
     (changed in place, up to lens[b]) -> out [B,H_q,1,d_v]."""
-    import torch
-    B, H_q, T, d_qk, H_kv, S_cap, d_v = _cache_shapes(q, k_cache, v_cache)
+    torch = _torch or _load_torch()
+    B, H_q, T, d_qk, H_kv, S_cap, d_v, device, pq, pk, pv = _cache_shapes(q, k_cache, v_cache)
     if T != 1:
         raise ValueError("decode_weights takes one query per sequence")
-    _check_on(lens, "lens", q, torch.int32, (B,))
-    _check_on(acc, "acc", q, torch.float32, (B, H_kv, S_cap))
-    with _Launch(q, stream) as at:
+    plens = _fit(lens, "lens", torch.int32, (B,), device)
+    pacc = _fit(acc, "acc", torch.float32, (B, H_kv, S_cap), device)
+    at = _Launch(device, stream)
+    try:
         if out is None:
-            out = torch.empty((B, H_q, 1, d_v), dtype=torch.bfloat16, device=q.device)
-        _check_on(out, "out", q, torch.bfloat16, (B, H_q, 1, d_v))
-        ws, ws_bytes = at.workspace(workspace, decode_weights_workspace_bytes(B, H_q, H_kv, S_cap, d_qk, d_v))
-        _done(apex_attn_decode_weights(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q,
-                                       H_kv, S_cap, d_qk, d_v, lens.data_ptr(), acc.data_ptr(),
-                                       0.0 if scale is None else float(scale), ws, ws_bytes, at.handle),
-              "apex_attn_decode_weights")
+            out = at.new(q, (B, H_q, 1, d_v), torch.bfloat16)
+            pout = out.data_ptr()
+        else:
+            pout = _fit(out, "out", torch.bfloat16, (B, H_q, 1, d_v), device)
+        ws = at.workspace(workspace, q, decode_weights_workspace_bytes(B, H_q, H_kv, S_cap, d_qk, d_v))
+        status = (_lib or load_library()).apex_attn_decode_weights(
+            pq, pk, pv, pout, B, H_q, H_kv, S_cap, d_qk, d_v, plens, pacc, 0.0 if scale is None else scale,
+            ws.data_ptr(), ws.nbytes, at.handle)
+        if status:
+            raise ApexError(status, "apex_attn_decode_weights")
+    finally:
+        at.leave()
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def evict_workspace_bytes(B, H_kv, S_cap, budget) -> int:
+    """Workspace bytes of evict for these sizes (0: invalid)."""
     return int(apex_attn_evict_workspace_bytes(B, H_kv, S_cap, budget))
 
 
@@ -723,34 +788,33 @@ def evict(k_cache, v_cache, acc, lens, budget: int, *, n_sink: int = 0, n_recent
     positions, then the largest acc. caches [B,H_kv,S_cap,d], acc [B,H_kv,S_cap] fp32, lens [B] int32,
     positions [B,H_kv,S_cap] int32 (None: the row index), next_pos [B] int32 (None: lens)
     -> (acc_out, positions_out, lens_out), in the new order of rows."""
-    import torch
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check(t, n, 4)
-    B, H_kv, S_cap, d_k = k_cache.shape
-    d_v = v_cache.shape[-1]
-    if tuple(v_cache.shape[:3]) != (B, H_kv, S_cap) or v_cache.device != k_cache.device:
-        raise ValueError("k_cache and v_cache must hold the same rows on one device")
-    at_rows = (B, H_kv, S_cap)
-    _check_on(acc, "acc", k_cache, torch.float32, at_rows)
-    _check_on(lens, "lens", k_cache, torch.int32, (B,))
-    if positions is not None:
-        _check_on(positions, "positions", k_cache, torch.int32, at_rows)
-    if next_pos is not None:
-        _check_on(next_pos, "next_pos", k_cache, torch.int32, (B,))
-    with _Launch(k_cache, stream) as at:
+    torch = _torch or _load_torch()
+    B, H_kv, S_cap, d_k = _rows4(k_cache, "k_cache")
+    d_v = _rows4(v_cache, "v_cache")[3]
+    device = k_cache.get_device()
+    rows = (B, H_kv, S_cap)
+    i32, f32 = torch.int32, torch.float32
+    pk = _fit(k_cache, "k_cache", torch.bfloat16, (B, H_kv, S_cap, d_k), device)
+    pv = _fit(v_cache, "v_cache", torch.bfloat16, (B, H_kv, S_cap, d_v), device)
+    pacc = _fit(acc, "acc", f32, rows, device)
+    plens = _fit(lens, "lens", i32, (B,), device)
+    ppos = None if positions is None else _fit(positions, "positions", i32, rows, device)
+    pnext = None if next_pos is None else _fit(next_pos, "next_pos", i32, (B,), device)
+    at = _Launch(device, stream)
+    try:
         if acc_out is None:
-            acc_out = torch.empty_like(acc)
+            acc_out = at.new(acc, rows, f32)
         if positions_out is None:
-            positions_out = torch.empty(at_rows, dtype=torch.int32, device=k_cache.device)
+            positions_out = at.new(lens, rows, i32)
         if lens_out is None:
-            lens_out = torch.empty_like(lens)
-        _check_on(acc_out, "acc_out", k_cache, torch.float32, at_rows)
-        _check_on(positions_out, "positions_out", k_cache, torch.int32, at_rows)
-        _check_on(lens_out, "lens_out", k_cache, torch.int32, (B,))
-        ws, ws_bytes = at.workspace(workspace, evict_workspace_bytes(B, H_kv, S_cap, int(budget)))
-        _done(apex_attn_evict(k_cache.data_ptr(), v_cache.data_ptr(), B, H_kv, S_cap, d_k, d_v, acc.data_ptr(),
-                              positions.data_ptr() if positions is not None else None, lens.data_ptr(),
-                              next_pos.data_ptr() if next_pos is not None else None, int(budget), int(n_sink),
-                              int(n_recent), acc_out.data_ptr(), positions_out.data_ptr(), lens_out.data_ptr(), ws,
-                              ws_bytes, at.handle), "apex_attn_evict")
+            lens_out = at.new(lens, (B,), i32)
+        ws = at.workspace(workspace, acc, evict_workspace_bytes(B, H_kv, S_cap, budget))
+        status = (_lib or load_library()).apex_attn_evict(
+            pk, pv, B, H_kv, S_cap, d_k, d_v, pacc, ppos, plens, pnext, budget, n_sink, n_recent,
+            _fit(acc_out, "acc_out", f32, rows, device), _fit(positions_out, "positions_out", i32, rows, device),
+            _fit(lens_out, "lens_out", i32, (B,), device), ws.data_ptr(), ws.nbytes, at.handle)
+        if status:
+            raise ApexError(status, "apex_attn_evict")
+    finally:
+        at.leave()
     return acc_out, positions_out, lens_out

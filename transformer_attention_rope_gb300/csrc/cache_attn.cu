@@ -93,8 +93,8 @@ __device__ __forceinline__ void make_sched(const CacheAttnParams &p, Sched *out)
     const int lane = threadIdx.x & 31;
     const int per_b = p.H_kv * p.n_groups;
     long long total = 0;
+    Seq s;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        Seq s;
         s.tiles = 0;
         if (b0 + lane < p.B) s.load(p, b0 + lane);
         total += __reduce_add_sync(0xffffffffu, s.tiles);
@@ -110,9 +110,10 @@ __device__ __forceinline__ void make_sched(const CacheAttnParams &p, Sched *out)
     if (r.left > 0) {
         long long before = 0;  // tiles of the sequences before b0
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            Seq s;
-            s.tiles = 0;
-            if (b0 + lane < p.B) s.load(p, b0 + lane);
+            if (p.B > 32) {  // else the lanes still hold the lengths
+                s.tiles = 0;
+                if (b0 + lane < p.B) s.load(p, b0 + lane);
+            }
             int incl = s.tiles;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -271,6 +272,11 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
         fence_mbarrier_init();
     }
     if (warp == C::kWarpMma) tmem_alloc(sb + C::kTmemSlot, 512);
+    if (warp == C::kWarpTma && lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
     // launched as a programmatic dependent: nothing in global memory is touched
     // before the stream's previous kernel is done
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -287,9 +293,6 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
     if (warp == C::kWarpTma) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
-            tma_prefetch_desc(&tm_q);
-            tma_prefetch_desc(&tm_k);
-            tma_prefetch_desc(&tm_v);
             // a cache that one row group reads is streamed once: its lines go first from L2
             uint64_t policy;
             if (p.n_groups == 1)
@@ -436,6 +439,8 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
                 }
             }
         }
+        // every product of this CTA is issued: the joining kernel's launch may overlap the rest
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     } else if ((warp & 3) < live_warps(warp >> 2)) {
         // ------------------------------------------------------------ softmax + epilogue
         const int t = warp >> 2;
@@ -587,45 +592,74 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining partial results
+// max and sum of a row of a cut unit over its fragments, and the shift of this lane's
+// fragment c0 + lane: the fragments of unit u are the last of CTA c0 (slot 2 c0 + 1),
+// then the first of each CTA up to c1 (slots 2 c).
+struct RowParts {
+    const CacheAttnParams &p;
+    int c0, n, rc;
+    __device__ __forceinline__ size_t at(int i) const
+    {
+        return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * p.rows_cap + rc;
+    }
+    // log2 of the sum of all fragments, relative to the maximum M
+    __device__ __forceinline__ void stats(int lane, float &M, float &L, float2 &mine) const
+    {
+        mine = make_float2(-INFINITY, 0.f);
+        if (lane < n) mine = p.ws_ml[at(lane)];
+        M = mine.x;
+        for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, p.ws_ml[at(i)].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        L = mine.x == -INFINITY ? 0.f : exp2f(mine.x - M) * mine.y;
+        for (int i = lane + 32; i < n; i += 32) {
+            const float2 v = p.ws_ml[at(i)];
+            L += v.x == -INFINITY ? 0.f : exp2f(v.x - M) * v.y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    }
+};
+
+template <int E>
+struct Vec;
+template <>
+struct Vec<2> {
+    float2 v;
+    __device__ __forceinline__ float at(int e) const { return e ? v.y : v.x; }
+};
+template <>
+struct Vec<4> {
+    float4 v;
+    __device__ __forceinline__ float at(int e) const { return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w; }
+};
+
 // One row of a cut unit: W warps share its fragments, then their sums are added.
-// Fragments of unit u: the last of CTA c0 (slot 2 c0 + 1), then the first of the CTAs
-// up to c1 (slots 2 c).
 template <int DV, int W>
-__global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p, int n_units)
+__device__ __forceinline__ void join_row(const CacheAttnParams &p, int n_units, float (*sh)[DV])
 {
     constexpr int E = DV / 32;  // entries per lane
-    constexpr int kRows = 8 / W;
-    __shared__ float sh[W > 1 ? 8 : 1][DV];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * kRows + warp / W;
+    const long long row = (long long)blockIdx.x * (8 / W) + warp / W;
     const int unit = (int)(row / p.rows_cap), rc = (int)(row % p.rows_cap);
     const int r = unit < n_units ? unit % p.n_groups * p.group + rc : p.R;
     if (r >= p.R) return;  // the whole block when W = 8
     const int2 c = p.units[unit];
     if (c.x == c.y) return;
-    auto part = [&](int cta) { return (size_t)(2 * cta + (cta == c.x ? 1 : 0)) * p.rows_cap + rc; };
-    float M = -INFINITY;
-    for (int i = c.x + lane; i <= c.y; i += 32) M = fmaxf(M, p.ws_ml[part(i)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f;
-    for (int i = c.x + lane; i <= c.y; i += 32) {
-        const float2 v = p.ws_ml[part(i)];
-        L += (v.x == -INFINITY) ? 0.f : exp2f(v.x - M) * v.y;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const RowParts parts{p, c.x, c.y - c.x + 1, rc};
+    float M, L;
+    float2 mine;
+    parts.stats(lane, M, L, mine);
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-    for (int i = c.x + warp % W; i <= c.y; i += W) {
-        const float m = p.ws_ml[part(i)].x;
+    for (int i = warp % W; i < parts.n; i += W) {
+        const Vec<E> o = *reinterpret_cast<const Vec<E> *>(p.ws_o + parts.at(i) * DV + lane * E);
+        const float m = i < 32 ? __shfl_sync(0xffffffffu, mine.x, i & 31) : p.ws_ml[parts.at(i)].x;
         const float w = (m == -INFINITY) ? 0.f : exp2f(m - M);
-        const float *o = p.ws_o + part(i) * DV + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += w * o[e];
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, o.at(e), acc[e]);
     }
     if (W > 1) {
 #pragma unroll
@@ -637,31 +671,77 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
             for (int e = 0; e < E; ++e) acc[e] += sh[w][lane * E + e];
     }
     const float inv = (L > 0.f) ? 1.f / L : 0.f;
-    const size_t at = (size_t)(unit / p.n_groups) * p.R + r;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + at * DV + lane * E);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + ((size_t)(unit / p.n_groups) * p.R + r) * DV + lane * E);
 #pragma unroll
     for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (p.acc && lane == 0) p.lse[at] = M + log2f(L);
 }
 
-// ---------------------------------------------------------------- accumulated weights
-// acc[b, g, j] += sum over the heads of g of 2^(scale score - lse), heads in order.
-__global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnParams p)
+// acc[b, g, j] += sum over the heads of g of 2^(scale score - lse), heads in order:
+// a block takes 1024 keys of a (sequence, KV head), a thread four neighbours.
+constexpr int kWeightKeys = 1024;
+__device__ __forceinline__ void add_weights(const CacheAttnParams &p, long long block, int chunks, float *lse)
 {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = (int)(block / chunks);
+    const int j0 = (int)(block % chunks) * kWeightKeys;
+    const int len = min(max(p.lens[unit / p.H_kv], 0), p.S_cap);
+    if (j0 >= len) return;
+    const int2 c = p.units[unit];
+    const int j = j0 + 4 * threadIdx.x;
+    const float *s = p.scores + (size_t)unit * p.G * p.S_pad + j;
+    for (int g = warp; g < p.G; g += 8) {
+        float x;
+        if (c.x == c.y) {
+            x = p.lse[(size_t)unit * p.G + g];
+        } else {
+            const RowParts parts{p, c.x, c.y - c.x + 1, g};
+            float M, L;
+            float2 mine;
+            parts.stats(lane, M, L, mine);
+            x = M + log2f(L);
+        }
+        if (lane == 0) lse[g] = x;
+    }
+    __syncthreads();
+    if (j >= len) return;
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int g = 0; g < p.G; ++g) {
+        // exp2f: weights below 2^-126 are kept, as the sums of a long service need them
+        const float4 x = *reinterpret_cast<const float4 *>(s + (size_t)g * p.S_pad);
+        w[0] += exp2f(fmaf(x.x, p.scale_log2, -lse[g]));
+        w[1] += exp2f(fmaf(x.y, p.scale_log2, -lse[g]));
+        w[2] += exp2f(fmaf(x.z, p.scale_log2, -lse[g]));
+        w[3] += exp2f(fmaf(x.w, p.scale_log2, -lse[g]));
+    }
+    float *acc = p.acc + (size_t)unit * p.S_cap + j;
+    if (j + 4 <= len && (reinterpret_cast<uintptr_t>(acc) & 15) == 0) {
+        float4 a = *reinterpret_cast<float4 *>(acc);
+        a.x += w[0];
+        a.y += w[1];
+        a.z += w[2];
+        a.w += w[3];
+        *reinterpret_cast<float4 *>(acc) = a;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (j + e < len) acc[e] += w[e];
+    }
+}
+
+// The first blocks join rows; with WEIGHTS the others add weights, each from its own
+// join of the statistics.
+template <int DV, int W, bool WEIGHTS>
+__global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p, int n_units, int join_blocks,
+                                                         int chunks)
+{
+    __shared__ float sh[W > 1 ? 8 : 1][DV];
     __shared__ float lse[16];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const size_t unit = blockIdx.x;
-    const int len = min(max(p.lens[unit / p.H_kv], 0), p.S_cap);
-    if (threadIdx.x < p.G) lse[threadIdx.x] = p.lse[unit * p.G + threadIdx.x];
-    __syncthreads();
-    const float *s = p.scores + unit * p.G * p.S_pad;
-    float *acc = p.acc + unit * p.S_cap;
-    for (int j = blockIdx.y * 256 + threadIdx.x; j < len; j += gridDim.y * 256) {
-        float w = 0.f;
-        // exp2f: weights below 2^-126 are kept, as the sums of a long service need them
-        for (int g = 0; g < p.G; ++g) w += exp2f(fmaf(s[(size_t)g * p.S_pad + j], p.scale_log2, -lse[g]));
-        acc[j] += w;
-    }
+    if (!WEIGHTS || blockIdx.x < join_blocks)
+        join_row<DV, W>(p, n_units, sh);
+    else
+        add_weights(p, blockIdx.x - join_blocks, chunks, lse);
 }
 
 template <int DQK, int DV, int MT, bool WEIGHTS>
@@ -681,14 +761,27 @@ cudaError_t launch_d(const CacheAttnLaunch &L, int grid, cudaStream_t stream)
     return L.p.group == 128 ? launch_t<DQK, DV, 1, false>(L, grid, stream) : launch_t<DQK, DV, 2, false>(L, grid, stream);
 }
 
-template <int DV>
-cudaError_t launch_join(const CacheAttnParams &p, int grid, cudaStream_t stream)
+template <int DV, int W>
+cudaError_t launch_join_w(const CacheAttnParams &p, cudaStream_t stream)
 {
     const int n_units = p.B * p.H_kv * p.n_groups;
     const long long rows = (long long)n_units * p.rows_cap;
+    const int join_blocks = (int)((rows + 8 / W - 1) / (8 / W));
+    const int chunks = (p.S_cap + kWeightKeys - 1) / kWeightKeys;
+    if (!p.acc)
+        return launch_dependent(cache_join_kernel<DV, W, false>, join_blocks, 256, 0, stream, p, n_units, join_blocks, 0);
+    const long long blocks = join_blocks + (long long)n_units * chunks;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    return launch_dependent(cache_join_kernel<DV, W, true>, (int)blocks, 256, 0, stream, p, n_units, join_blocks,
+                            chunks);
+}
+
+template <int DV>
+cudaError_t launch_join(const CacheAttnParams &p, int grid, cudaStream_t stream)
+{
     // few units: each is cut into many fragments, which then share a block
-    if (4ll * n_units <= grid) return launch_dependent(cache_join_kernel<DV, 8>, (int)rows, 256, 0, stream, p, n_units);
-    return launch_dependent(cache_join_kernel<DV, 1>, (int)((rows + 7) / 8), 256, 0, stream, p, n_units);
+    if (4ll * p.B * p.H_kv * p.n_groups <= grid) return launch_join_w<DV, 8>(p, stream);
+    return launch_join_w<DV, 1>(p, stream);
 }
 
 }  // namespace
@@ -696,25 +789,12 @@ cudaError_t launch_join(const CacheAttnParams &p, int grid, cudaStream_t stream)
 cudaError_t launch_cache_attn(const CacheAttnLaunch &L, int sm_count, cudaStream_t stream)
 {
     const CacheAttnParams &p = L.p;
-    const long long most = (long long)p.B * p.H_kv * p.n_groups * ((p.S_cap + kKeys - 1) / kKeys);
-    const int grid = (int)std::min<long long>(std::min(sm_count, kCacheMaxCtas), most);
+    const int grid = std::min(sm_count, cache_attn_ctas(p.B, p.H_kv, p.n_groups, p.S_cap));
     cudaError_t err = p.d_qk == 64    ? launch_d<64, 64>(L, grid, stream)
                       : p.d_qk == 128 ? launch_d<128, 128>(L, grid, stream)
                                       : launch_d<192, 128>(L, grid, stream);
     if (err != cudaSuccess) return err;
-    err = p.d_v == 64 ? launch_join<64>(p, grid, stream) : launch_join<128>(p, grid, stream);
-    if (err != cudaSuccess || !p.acc) return err;
-    const int units = p.B * p.H_kv;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(units, std::min(std::max(1, 8 * sm_count / units), (p.S_cap + 255) / 256));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_weights_kernel, p);
+    return p.d_v == 64 ? launch_join<64>(p, grid, stream) : launch_join<128>(p, grid, stream);
 }
 
 }  // namespace apex

@@ -33,8 +33,8 @@ struct CacheAttnParams {
     int n_groups;   // row groups of a KV head
     int rows_cap;   // rows of a partial result, min(R, group)
     // workspace
-    float *ws_o;    // [2 * kCacheMaxCtas][rows_cap][d_v] partial outputs (unnormalised)
-    float2 *ws_ml;  // [2 * kCacheMaxCtas][rows_cap]      their (max in log2 units, sum)
+    float *ws_o;    // [2 * CTAs][rows_cap][d_v]          partial outputs (unnormalised)
+    float2 *ws_ml;  // [2 * CTAs][rows_cap]               their (max in log2 units, sum)
     int2 *units;    // [B * H_kv * n_groups]              first and last CTA of each unit
     float *lse;     // [B * H_q]                          log2 of the softmax denominators (with acc)
     float *scores;  // [B * H_q][S_pad]                   scores (with acc)
@@ -44,6 +44,13 @@ struct CacheAttnParams {
 // Rows of a KV head's queries (G heads x T drafts) are worked on in groups of one or
 // two 128-row M tiles.
 inline int cache_attn_group(int R) { return R <= 128 ? 128 : 256; }
+
+// Most CTAs a call can use: one per tile, kCacheMaxCtas at most.
+inline int cache_attn_ctas(int B, int H_kv, int n_groups, int S_cap)
+{
+    const long long tiles = (long long)B * H_kv * n_groups * ((S_cap + kCacheTileKeys - 1) / kCacheTileKeys);
+    return (int)std::min<long long>(kCacheMaxCtas, tiles);
+}
 
 struct CacheAttnWorkspace {
     size_t ml, units, lse, scores, bytes;
@@ -58,7 +65,7 @@ inline CacheAttnWorkspace cache_attn_workspace(int B, int H_q, int H_kv, int T, 
     w.n_groups = (R + group - 1) / group;
     w.S_pad = (S_cap + kCacheTileKeys - 1) / kCacheTileKeys * kCacheTileKeys;
     auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
-    const size_t slots = (size_t)2 * kCacheMaxCtas * w.rows_cap;
+    const size_t slots = (size_t)2 * cache_attn_ctas(B, H_kv, w.n_groups, S_cap) * w.rows_cap;
     w.ml = up(slots * d_v * sizeof(float));
     w.units = w.ml + up(slots * sizeof(float2));
     w.lse = w.units + up((size_t)B * H_kv * w.n_groups * sizeof(int2));

@@ -179,7 +179,8 @@ apex_status apex_attn_evict(void *k_cache, void *v_cache, int B, int H_kv, int S
         return APEX_ERR_INVALID_ARG;
     if (B <= 0 || H_kv <= 0 || S_cap <= 0 || d_k <= 0 || d_v <= 0) return APEX_ERR_INVALID_ARG;
     if (budget <= 0 || n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > budget) return APEX_ERR_INVALID_ARG;
-    if (acc_out == acc || positions_out == positions) return APEX_ERR_INVALID_ARG;
+    if (acc_out == acc || positions_out == positions || lens_out == lens || lens_out == next_pos)
+        return APEX_ERR_INVALID_ARG;
     if (S_cap > kMaxSeq || (long long)B * H_kv > (1 << 24)) return APEX_ERR_UNSUPPORTED;
     if (d_k % 8 != 0 || d_v % 8 != 0 || d_k > 1024 || d_v > 1024) return APEX_ERR_UNSUPPORTED;
     const EvictWorkspace w = evict_workspace(B * H_kv, S_cap, budget);
@@ -197,8 +198,7 @@ apex_status apex_attn_evict(void *k_cache, void *v_cache, int B, int H_kv, int S
     p.acc_out = acc_out;
     p.positions_out = positions_out;
     p.lens_out = lens_out;
-    p.moved = reinterpret_cast<int *>(workspace);
-    p.holes = reinterpret_cast<int *>(static_cast<char *>(workspace) + w.holes);
+    p.holes = reinterpret_cast<int *>(workspace);
     p.sources = reinterpret_cast<int *>(static_cast<char *>(workspace) + w.sources);
     p.cap = w.cap;
     p.B = B;

@@ -18,14 +18,13 @@ struct EvictParams {
     float *acc_out;
     int *positions_out;
     int *lens_out;
-    int *moved;             // [B*H_kv] rows to move
     int *holes, *sources;   // [B*H_kv][cap] destination and source rows, ascending
     int cap;
     int B, H_kv, S_cap, budget, n_sink, n_recent;
 };
 
 struct EvictWorkspace {
-    size_t holes, sources, bytes;
+    size_t sources, bytes;
     int cap;
 };
 
@@ -35,10 +34,8 @@ inline EvictWorkspace evict_workspace(int units, int S_cap, int budget)
     EvictWorkspace w;
     w.cap = std::max(0, std::min(budget, S_cap - budget));
     auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
-    const size_t list = up((size_t)units * w.cap * sizeof(int));
-    w.holes = up((size_t)units * sizeof(int));
-    w.sources = w.holes + list;
-    w.bytes = w.sources + list;
+    w.sources = up((size_t)units * w.cap * sizeof(int));
+    w.bytes = std::max<size_t>(256, 2 * w.sources);
     return w;
 }
 
