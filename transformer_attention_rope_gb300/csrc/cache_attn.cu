@@ -634,16 +634,25 @@ struct Vec<4> {
     __device__ __forceinline__ float at(int e) const { return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w; }
 };
 
-// One row of a cut unit: W warps share its fragments, then their sums are added.
-template <int DV, int W>
-__device__ __forceinline__ void join_row(const CacheAttnParams &p, int n_units, float (*sh)[DV])
+template <int E>
+__device__ __forceinline__ void store_row(uint16_t *out, int lane, const float (&acc)[E], float L)
+{
+    const float inv = (L > 0.f) ? 1.f / L : 0.f;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(out) + lane * (E / 2);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+}
+
+// One row of a cut unit to a block: its 8 warps share the fragments (few units, cut
+// into many).
+template <int DV>
+__device__ __forceinline__ void join_many(const CacheAttnParams &p, int n_units, float (*sh)[DV])
 {
     constexpr int E = DV / 32;  // entries per lane
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * (8 / W) + warp / W;
-    const int unit = (int)(row / p.rows_cap), rc = (int)(row % p.rows_cap);
-    const int r = unit < n_units ? unit % p.n_groups * p.group + rc : p.R;
-    if (r >= p.R) return;  // the whole block when W = 8
+    const int unit = blockIdx.x / p.rows_cap, rc = blockIdx.x % p.rows_cap;
+    const int r = unit % p.n_groups * p.group + rc;
+    if (r >= p.R) return;
     const int2 c = p.units[unit];
     if (c.x == c.y) return;
     const RowParts parts{p, c.x, c.y - c.x + 1, rc};
@@ -654,26 +663,75 @@ __device__ __forceinline__ void join_row(const CacheAttnParams &p, int n_units, 
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-    for (int i = warp % W; i < parts.n; i += W) {
+    for (int i = warp; i < parts.n; i += 8) {
         const Vec<E> o = *reinterpret_cast<const Vec<E> *>(p.ws_o + parts.at(i) * DV + lane * E);
         const float m = i < 32 ? __shfl_sync(0xffffffffu, mine.x, i & 31) : p.ws_ml[parts.at(i)].x;
         const float w = (m == -INFINITY) ? 0.f : exp2f(m - M);
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(w, o.at(e), acc[e]);
     }
-    if (W > 1) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = acc[e];
-        __syncthreads();
-        if (warp > 0) return;
-        for (int w = 1; w < W; ++w)
+    for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 1; w < 8; ++w)
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += sh[w][lane * E + e];
+        for (int e = 0; e < E; ++e) acc[e] += sh[w][lane * E + e];
+    store_row<E>(p.out + ((size_t)(unit / p.n_groups) * p.R + r) * DV, lane, acc, L);
+}
+
+// 32 rows of a cut unit to a block, 4 to a warp (many units, cut into a few fragments
+// each): lanes 8 k .. 8 k + 7 hold the statistics of row k's fragments, eight at a time.
+template <int DV>
+__device__ __forceinline__ void join_few(const CacheAttnParams &p, int row_blocks)
+{
+    constexpr int E = DV / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = blockIdx.x / row_blocks, rc0 = blockIdx.x % row_blocks * 32 + 4 * warp;
+    const int r0 = unit % p.n_groups * p.group + rc0;
+    const int rows = min(4, min(p.R - r0, p.rows_cap - rc0));
+    if (rows <= 0) return;
+    const int2 c = p.units[unit];
+    if (c.x == c.y) return;
+    const int n = c.y - c.x + 1;
+    const RowParts stat{p, c.x, n, rc0 + min(lane >> 3, rows - 1)};  // this lane's row, for the statistics
+    float M = -INFINITY;
+    for (int i = lane & 7; i < n; i += 8) M = fmaxf(M, p.ws_ml[stat.at(i)].x);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    float acc[4][E];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 8) {
+        float w = 0.f;
+        if (i0 + (lane & 7) < n) {
+            const float2 v = p.ws_ml[stat.at(i0 + (lane & 7))];
+            w = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
+            L += w * v.y;
+        }
+#pragma unroll 2
+        for (int i = i0; i < min(i0 + 8, n); ++i) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const RowParts part{p, c.x, n, rc0 + min(k, rows - 1)};
+                const Vec<E> o = *reinterpret_cast<const Vec<E> *>(p.ws_o + part.at(i) * DV + lane * E);
+                const float wk = __shfl_sync(0xffffffffu, w, 8 * k + i - i0);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[k][e] = fmaf(wk, o.at(e), acc[k][e]);
+            }
+        }
     }
-    const float inv = (L > 0.f) ? 1.f / L : 0.f;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + ((size_t)(unit / p.n_groups) * p.R + r) * DV + lane * E);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const size_t out0 = (size_t)(unit / p.n_groups) * p.R + r0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float Lk = __shfl_sync(0xffffffffu, L, 8 * k);
+        if (k < rows) store_row<E>(p.out + (out0 + k) * DV, lane, acc[k], Lk);
+    }
 }
 
 // acc[b, g, j] += sum over the heads of g of 2^(scale score - lse), heads in order:
@@ -731,17 +789,23 @@ __device__ __forceinline__ void add_weights(const CacheAttnParams &p, long long 
 
 // The first blocks join rows; with WEIGHTS the others add weights, each from its own
 // join of the statistics.
-template <int DV, int W, bool WEIGHTS>
+template <int DV, bool MANY, bool WEIGHTS>
 __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p, int n_units, int join_blocks,
-                                                         int chunks)
+                                                         int row_blocks, int chunks)
 {
-    __shared__ float sh[W > 1 ? 8 : 1][DV];
+    __shared__ float sh[MANY ? 8 : 1][DV];
     __shared__ float lse[16];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!WEIGHTS || blockIdx.x < join_blocks)
-        join_row<DV, W>(p, n_units, sh);
-    else
+    // the next kernel's launch may overlap this one (it waits for it before it reads)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!WEIGHTS || blockIdx.x < join_blocks) {
+        if (MANY)
+            join_many<DV>(p, n_units, sh);
+        else
+            join_few<DV>(p, row_blocks);
+    } else {
         add_weights(p, blockIdx.x - join_blocks, chunks, lse);
+    }
 }
 
 template <int DQK, int DV, int MT, bool WEIGHTS>
@@ -761,27 +825,28 @@ cudaError_t launch_d(const CacheAttnLaunch &L, int grid, cudaStream_t stream)
     return L.p.group == 128 ? launch_t<DQK, DV, 1, false>(L, grid, stream) : launch_t<DQK, DV, 2, false>(L, grid, stream);
 }
 
-template <int DV, int W>
-cudaError_t launch_join_w(const CacheAttnParams &p, cudaStream_t stream)
+template <int DV, bool MANY>
+cudaError_t launch_join_t(const CacheAttnParams &p, cudaStream_t stream)
 {
     const int n_units = p.B * p.H_kv * p.n_groups;
-    const long long rows = (long long)n_units * p.rows_cap;
-    const int join_blocks = (int)((rows + 8 / W - 1) / (8 / W));
+    const int row_blocks = MANY ? p.rows_cap : (p.rows_cap + 31) / 32;
+    const long long join_blocks = (long long)n_units * row_blocks;
     const int chunks = (p.S_cap + kWeightKeys - 1) / kWeightKeys;
-    if (!p.acc)
-        return launch_dependent(cache_join_kernel<DV, W, false>, join_blocks, 256, 0, stream, p, n_units, join_blocks, 0);
-    const long long blocks = join_blocks + (long long)n_units * chunks;
+    const long long blocks = join_blocks + (p.acc ? (long long)n_units * chunks : 0);
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    return launch_dependent(cache_join_kernel<DV, W, true>, (int)blocks, 256, 0, stream, p, n_units, join_blocks,
-                            chunks);
+    if (p.acc)
+        return launch_dependent(cache_join_kernel<DV, MANY, true>, (int)blocks, 256, 0, stream, p, n_units,
+                                (int)join_blocks, row_blocks, chunks);
+    return launch_dependent(cache_join_kernel<DV, MANY, false>, (int)blocks, 256, 0, stream, p, n_units,
+                            (int)join_blocks, row_blocks, chunks);
 }
 
 template <int DV>
 cudaError_t launch_join(const CacheAttnParams &p, int grid, cudaStream_t stream)
 {
     // few units: each is cut into many fragments, which then share a block
-    if (4ll * p.B * p.H_kv * p.n_groups <= grid) return launch_join_w<DV, 8>(p, stream);
-    return launch_join_w<DV, 1>(p, stream);
+    return 4ll * p.B * p.H_kv * p.n_groups <= grid ? launch_join_t<DV, true>(p, stream)
+                                                   : launch_join_t<DV, false>(p, stream);
 }
 
 }  // namespace
