@@ -690,13 +690,20 @@ def rope(q, k=None, v=None, *, positions, layout: str = "interleaved", rot_start
 
 def _cache_shapes(q, k_cache, v_cache):
     """Sizes of queries and caches, their device and addresses."""
-    torch = _torch
-    B, H_q, T, d_qk = _rows4(q, "q")
-    _, H_kv, S_cap, d_v = _rows4(v_cache, "v_cache")
-    device = q.get_device()
-    return (B, H_q, T, d_qk, H_kv, S_cap, d_v, device, _fit(q, "q", torch.bfloat16, (B, H_q, T, d_qk), device),
-            _fit(k_cache, "k_cache", torch.bfloat16, (B, H_kv, S_cap, d_qk), device),
-            _fit(v_cache, "v_cache", torch.bfloat16, (B, H_kv, S_cap, d_v), device))
+    bf16 = _torch.bfloat16
+    try:
+        B, H_q, T, d_qk = q.shape
+        _, H_kv, S_cap, d_v = v_cache.shape
+        device = q.get_device()
+    except (AttributeError, ValueError):
+        device = -1
+    if device < 0:
+        _rows4(q, "q")
+        _rows4(v_cache, "v_cache")
+        raise ValueError("q and v_cache must be 4-D CUDA tensors")
+    return (B, H_q, T, d_qk, H_kv, S_cap, d_v, device, _fit(q, "q", bf16, (B, H_q, T, d_qk), device),
+            _fit(k_cache, "k_cache", bf16, (B, H_kv, S_cap, d_qk), device),
+            _fit(v_cache, "v_cache", bf16, (B, H_kv, S_cap, d_v), device))
 
 
 @functools.lru_cache(maxsize=256)

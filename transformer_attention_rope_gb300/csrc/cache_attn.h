@@ -14,7 +14,7 @@ namespace apex {
 
 constexpr int kTreeMaxDrafts = 64;    // one mask word per draft
 constexpr int kCacheTileKeys = 128;   // keys per tile
-constexpr int kCacheMaxCtas = 160;    // CTAs that may hold partial results
+constexpr int kCacheMaxCtas = 160;    // CTAs of a call at most
 
 struct CacheAttnParams {
     uint16_t *out;  // [B, H_q, T, d_v]
@@ -29,27 +29,37 @@ struct CacheAttnParams {
     float scale_log2;
     WaitCtl wait;
     int R;          // query rows of a KV head, G * T
-    int group;      // rows of a row group (one or two M tiles)
+    int group;      // rows of a row group
     int n_groups;   // row groups of a KV head
     int rows_cap;   // rows of a partial result, min(R, group)
     // workspace
-    float *ws_o;    // [2 * CTAs][rows_cap][d_v]          partial outputs (unnormalised)
-    float2 *ws_ml;  // [2 * CTAs][rows_cap]               their (max in log2 units, sum)
-    int2 *units;    // [B * H_kv * n_groups]              first and last CTA of each unit
+    float *ws_o;    // [2 * shares][d_v / 4][rows_cap][4] partial outputs (unnormalised)
+    float2 *ws_ml;  // [2 * shares][rows_cap]             their (max in log2 units, sum)
+    int2 *units;    // [B * H_kv * n_groups]              first and last share of each unit
     float *lse;     // [B * H_q]                          log2 of the softmax denominators (with acc)
     float *scores;  // [B * H_q][S_pad]                   scores (with acc)
     int S_pad;
 };
 
-// Rows of a KV head's queries (G heads x T drafts) are worked on in groups of one or
-// two 128-row M tiles.
-inline int cache_attn_group(int R) { return R <= 128 ? 128 : 256; }
+// Which kernel, by the rows R = G * T of a KV head's queries.  Up to 128 rows: one M tile
+// on one CTA, bound by the cache's bytes.  More: pairs of CTAs that share each K/V tile,
+// with one M tile each up to 256 rows and two from there on, as the tensor cores read the
+// tile from shared memory once for both CTAs; d_v = 64, whose halves of a V tile would be
+// narrower than the 128-byte swizzle, stays on one CTA with two M tiles.
+inline bool cache_attn_pairs(int R, int d_v) { return R > 128 && d_v == 128; }
+inline int cache_attn_group(int R, int d_v) { return R <= 128 ? 128 : (R <= 256 || d_v != 128) ? 256 : 512; }
 
-// Most CTAs a call can use: one per tile, kCacheMaxCtas at most.
-inline int cache_attn_ctas(int B, int H_kv, int n_groups, int S_cap)
+// What starting a unit costs in the schedule, in tiles: the pipeline fills and drains once
+// more.  32 caches of 100 to 2000 keys, 4 drafts, 32/8 heads: 45.5 us counting 0, 33.9 at 1,
+// 31.0 at 2, 31.3 at 3; a tree of 64 on 128/8 heads, 4 x 8192 keys: 105.5, 102.3, 101.1, 102.0;
+// 8 long caches are indifferent.
+constexpr int kCacheUnitCost = 2;
+
+// Most shares of a call: one per tile, one per CTA or pair at most.
+inline int cache_attn_shares(int B, int H_kv, int n_groups, int S_cap, bool pairs)
 {
     const long long tiles = (long long)B * H_kv * n_groups * ((S_cap + kCacheTileKeys - 1) / kCacheTileKeys);
-    return (int)std::min<long long>(kCacheMaxCtas, tiles);
+    return (int)std::min<long long>(pairs ? kCacheMaxCtas / 2 : kCacheMaxCtas, tiles);
 }
 
 struct CacheAttnWorkspace {
@@ -60,12 +70,12 @@ struct CacheAttnWorkspace {
 inline CacheAttnWorkspace cache_attn_workspace(int B, int H_q, int H_kv, int T, int S_cap, int d_v, bool weights)
 {
     CacheAttnWorkspace w;
-    const int R = H_q / H_kv * T, group = cache_attn_group(R);
+    const int R = H_q / H_kv * T, group = cache_attn_group(R, d_v);
     w.rows_cap = std::min(R, group);
     w.n_groups = (R + group - 1) / group;
     w.S_pad = (S_cap + kCacheTileKeys - 1) / kCacheTileKeys * kCacheTileKeys;
     auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
-    const size_t slots = (size_t)2 * cache_attn_ctas(B, H_kv, w.n_groups, S_cap) * w.rows_cap;
+    const size_t slots = (size_t)2 * cache_attn_shares(B, H_kv, w.n_groups, S_cap, cache_attn_pairs(R, d_v)) * w.rows_cap;
     w.ml = up(slots * d_v * sizeof(float));
     w.units = w.ml + up(slots * sizeof(float2));
     w.lse = w.units + up((size_t)B * H_kv * w.n_groups * sizeof(int2));
@@ -78,7 +88,7 @@ inline void cache_attn_bind(CacheAttnParams &p, const CacheAttnWorkspace &w, voi
 {
     char *base = static_cast<char *>(workspace);
     p.R = p.G * p.T;
-    p.group = cache_attn_group(p.R);
+    p.group = cache_attn_group(p.R, p.d_v);
     p.n_groups = w.n_groups;
     p.rows_cap = w.rows_cap;
     p.S_pad = w.S_pad;
@@ -90,12 +100,15 @@ inline void cache_attn_bind(CacheAttnParams &p, const CacheAttnWorkspace &w, voi
 }
 
 struct CacheAttnLaunch {
-    // 3-D maps, boxes of 128 rows x 64 entries, 128-byte swizzle: q as [B*H_kv][R][d_qk]
-    // (the rows of a KV head's query heads are adjacent), k and v [B*H_kv][S_cap][d]
+    // 3-D maps, boxes of 128 rows x 64 entries (k on pairs: 64 x 64), 128-byte swizzle: q as
+    // [B*H_kv][R][d_qk] (the rows of a KV head's query heads are adjacent), k and v
+    // [B*H_kv][S_cap][d]
     CUtensorMap tm_q, tm_k, tm_v;
     CacheAttnParams p;
 };
 
 cudaError_t launch_cache_attn(const CacheAttnLaunch &L, int sm_count, cudaStream_t stream);
+// the attention kernel on CTA pairs alone (the caller joins)
+cudaError_t launch_cache_pair(const CacheAttnLaunch &L, int pairs, cudaStream_t stream);
 
 }  // namespace apex

@@ -269,7 +269,7 @@ static apex_status cache_attn(const void *q, const void *k_cache, const void *v_
     p.scale_log2 = (float)(1.4426950408889634 * (scale == 0.f ? 1.0 / sqrt((double)d_qk) : (double)scale));
     p.wait = dev.wait;
     cache_attn_bind(p, w, workspace);
-    if (!make_map(&L.tm_q, q, d_qk, p.R, B * H_kv, 128, 1) || !make_map(&L.tm_k, k_cache, d_qk, S_cap, B * H_kv, 128, 1) ||
+    if (!make_map(&L.tm_q, q, d_qk, p.R, B * H_kv, 128, 1) || !make_map(&L.tm_k, k_cache, d_qk, S_cap, B * H_kv, cache_attn_pairs(p.R, d_v) ? 64 : 128, 1) ||
         !make_map(&L.tm_v, v_cache, d_v, S_cap, B * H_kv, 128, 1))
         return APEX_ERR_CUDA;
     if (launch_cache_attn(L, dev.sm_count, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)

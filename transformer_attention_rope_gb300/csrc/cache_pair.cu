@@ -1,0 +1,390 @@
+// cache_pair.cu -- attention of drafted trees with more than 128 query rows per KV head
+// on CTA pairs (tcgen05 cta_group::2), value rows of 128 entries, query and key rows of
+// 128 or 192.  What is computed and how the work is dealt out: cache_attn.cuh.
+//
+// On one CTA such a tree is bound by shared memory: a 128 x 128 product reads its A and
+// B operands at the rate the tensor cores use them.  Here S_t = Q_t K^T and O_t += P_t V
+// are M = 256 products over both CTAs (M tile 2 t of the row group on the leader, 2 t + 1
+// on its peer) and B is split between the two shared memories: each CTA loads 64 of a
+// tile's 128 keys of K and 64 of the 128 entries of V, so every K/V byte crosses L2 once
+// for 256 (MT = 1) or 512 (MT = 2) rows and the operand traffic of B halves.
+//
+// Warps per CTA: 4 softmax warps per M tile, then a TMA warp (K and V), an MMA warp (the
+// leader's issues, both allocate TMEM), a warp that loads the queries, waits for what has
+// landed here, mends V tiles and tells the leader, and an idle one.  The leader's MMA
+// thread waits on its own barriers, which the peer reaches by remote arrivals; commits
+// are multicast, so everybody waits on local barriers.  With MT = 1 S has two buffers:
+// the product of the next tile runs under this tile's softmax.
+#include <math.h>
+
+#include "cache_attn.cuh"
+
+namespace apex {
+namespace {
+
+constexpr int DV = 128;
+constexpr int kKeys = kCacheTileKeys;
+constexpr int kQBox = 128 * 128;   // [128 rows][64 entries]
+constexpr int kKBox = 64 * 128;    // [64 keys][64 entries]
+constexpr int kVTile = 128 * 128;  // 128 keys x this CTA's 64 entries
+
+template <int DQK, int MT>
+struct PairCfg {
+    static constexpr int kThreads = 128 * MT + 128;
+    static constexpr int kWarpTma = 4 * MT, kWarpMma = 4 * MT + 1, kWarpReady = 4 * MT + 2;
+    // Two softmax warpgroups need more registers than an even split of 64 K gives: the
+    // block is launched with kLaunchRegs a thread, which setmaxnreg redistributes.
+    static constexpr int kLaunchRegs = 168, kRegsSoftmax = 200, kRegsCtl = 104;
+    static_assert(2 * kRegsSoftmax + kRegsCtl <= 3 * kLaunchRegs, "register split");
+    static constexpr int kBoxes = DQK / 64;
+    static constexpr int kQTile = kBoxes * kQBox, kKTile = kBoxes * kKBox;
+    static constexpr int kStage = kKTile + kVTile;  // K and V of a tile share a stage
+    static constexpr int kStages = DQK == 128 ? (MT == 1 ? 6 : 5) : (MT == 1 ? 4 : 3);
+    static constexpr int kQOff = 0;
+    static constexpr int kStageOff = MT * kQTile;
+    static constexpr int kBarOff = kStageOff + kStages * kStage;
+    static constexpr int kBarQFull = 0;                       // local TMA
+    static constexpr int kBarQReady = 1;                      // leader: both CTAs
+    static constexpr int kBarQEmpty = 2;                      // multicast commit
+    static constexpr int kBarSFull = 3;                       // [2] multicast commit, per S buffer
+    static constexpr int kBarPReady = 5;                      // [2] leader: live softmax warps, per S buffer
+    static constexpr int kBarPV = 7;                          // [2] multicast commit, a phase per tile (MT = 1) or fragment
+    static constexpr int kBarOEmpty = 9;                      // [2] leader: live softmax warps, one phase per fragment
+    static constexpr int kBarFull = 11;                       // [stages] local TMA
+    static constexpr int kBarReady = kBarFull + kStages;      // [stages] leader: both CTAs
+    static constexpr int kBarEmpty = kBarReady + kStages;     // [stages] multicast commit
+    static constexpr int kNumBars = kBarEmpty + kStages;
+    static constexpr int kSched = kBarOff + kNumBars * 8;
+    static constexpr int kTmemSlot = kSched + 48;
+    static constexpr int kSmemBytes = kTmemSlot + 16 + 1024;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t col_s(int s) { return 128u * s; }
+__device__ __forceinline__ uint32_t col_o(int t) { return 256u + 128u * t; }
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrive on the barrier at the same shared-memory offset in the leader CTA.
+__device__ __forceinline__ void arrive_leader(uint32_t local_bar)
+{
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_bar), "r"(0));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+
+__device__ __forceinline__ void commit_pair(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Bounded wait; after one time-out of the CTA (abort flag) later waits that do not
+// complete at once give up at their first timer check, so a broken pipeline drains in
+// about one time-out.
+__device__ __forceinline__ void pair_wait(uint32_t bar, uint32_t parity, const WaitCtl &wc, volatile uint32_t *abort)
+{
+    if (mbar_try_wait(bar, parity)) return;
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return;
+        if ((n & 255u) == 0) {
+            if (*abort) return;
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) {
+                t0 = now;
+            } else if (now - t0 > wc.timeout_ns) {
+                *abort = 1u;
+                report_status(wc.status, kStatusWaitTimeout);
+                return;
+            }
+        }
+    }
+}
+
+template <int DQK, int MT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kThreads, 1)
+    cache_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CacheAttnParams p)
+{
+    using C = PairCfg<DQK, MT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem =
+        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int share = blockIdx.x >> 1, shares = gridDim.x >> 1;
+    auto bar = [&](int i) -> uint32_t { return sb + C::kBarOff + 8 * i; };
+    volatile uint32_t *abort = reinterpret_cast<volatile uint32_t *>(smem + C::kTmemSlot + 4);
+    // softmax warps that hold rows of M tile T of the row group
+    auto live_warps = [&](int T) { return max(0, min(4, (p.rows_cap - 128 * T + 31) / 32)); };
+
+    if (threadIdx.x == 0) {
+        *abort = 0u;
+        mbar_init(bar(C::kBarQFull), 1);
+        mbar_init(bar(C::kBarQReady), 2);
+        mbar_init(bar(C::kBarQEmpty), 1);
+        for (int s = 0; s < 2; ++s) {
+            const int t = MT == 2 ? s : 0;
+            mbar_init(bar(C::kBarSFull + s), 1);
+            mbar_init(bar(C::kBarPReady + s), live_warps(2 * t) + live_warps(2 * t + 1));
+            mbar_init(bar(C::kBarPV + s), 1);
+            mbar_init(bar(C::kBarOEmpty + s), live_warps(2 * t) + live_warps(2 * t + 1));
+        }
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(bar(C::kBarFull + s), 1);
+            mbar_init(bar(C::kBarReady + s), 2);
+            mbar_init(bar(C::kBarEmpty + s), 1);
+        }
+        fence_mbarrier_init();
+    }
+    if (warp == C::kWarpMma) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + C::kTmemSlot),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (warp == C::kWarpTma && lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    // launched as a programmatic dependent: nothing in global memory is touched
+    // before the stream's previous kernel is done
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Sched *sched = reinterpret_cast<Sched *>(smem + C::kSched);
+    if (warp == C::kWarpTma) make_sched(p, share, shares, sched);
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();  // both CTAs' barriers initialised, TMEM allocated, schedules made
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::kTmemSlot);
+
+    Walk walk(p, *sched);
+    Frag f;
+    if (MT == 2 && warp >= C::kWarpTma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsCtl));
+    if (warp == C::kWarpTma) {
+        // ------------------------------------------------------------ K and V (both CTAs, a half each)
+        if (lane == 0) {
+            // a cache that one row group reads is streamed once: its lines go first from L2
+            uint64_t policy;
+            if (p.n_groups == 1)
+                asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+            else
+                asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+            int g = 0;  // tiles so far
+            while (walk.next(p, f)) {
+                const int kv = f.b * p.H_kv + f.hk;
+                if (f.head && rank == 0) p.units[f.unit] = make_int2(share, f.last);
+                for (int j = 0; j < f.n; ++j, ++g) {
+                    const int key0 = kKeys * (f.first + j);
+                    const int st = g % C::kStages;
+                    const uint32_t at = sb + C::kStageOff + st * C::kStage;
+                    pair_wait(bar(C::kBarEmpty + st), ((g / C::kStages) & 1) ^ 1, p.wait, abort);
+                    mbar_arrive_expect_tx(bar(C::kBarFull + st), C::kStage);
+#pragma unroll
+                    for (int bx = 0; bx < C::kBoxes; ++bx)
+                        tma_load_3d_policy(at + bx * kKBox, &tm_k, bar(C::kBarFull + st), 64 * bx, key0 + 64 * rank, kv,
+                                           policy);
+                    tma_load_3d_policy(at + C::kKTile, &tm_v, bar(C::kBarFull + st), 64 * rank, key0, kv, policy);
+                }
+            }
+        }
+    } else if (warp == C::kWarpReady) {
+        // ------------------------------------------------------------ queries, mended V tiles, word to the leader
+        int g = 0;
+        for (int fi = 0; walk.next(p, f); ++fi) {
+            if (lane == 0) {
+                pair_wait(bar(C::kBarQEmpty), (fi & 1) ^ 1, p.wait, abort);
+                mbar_arrive_expect_tx(bar(C::kBarQFull), MT * C::kQTile);
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int bx = 0; bx < C::kBoxes; ++bx)
+                        tma_load_3d(sb + C::kQOff + t * C::kQTile + bx * kQBox, &tm_q, bar(C::kBarQFull), 64 * bx,
+                                    f.group * p.group + 128 * (2 * t + rank), f.b * p.H_kv + f.hk);
+            }
+            __syncwarp();
+            pair_wait(bar(C::kBarQFull), fi & 1, p.wait, abort);
+            if (lane == 0) arrive_leader(bar(C::kBarQReady));
+            Mend mend;
+            for (int j = 0; j < f.n; ++j, ++g) {
+                const int st = g % C::kStages;
+                pair_wait(bar(C::kBarFull + st), (g / C::kStages) & 1, p.wait, abort);
+                mend_v<1>(p, f, mend, kKeys * (f.first + j), smem + C::kStageOff + st * C::kStage + C::kKTile);
+                __syncwarp();
+                if (lane == 0) arrive_leader(bar(C::kBarReady + st));
+            }
+        }
+    } else if (warp == C::kWarpMma) {
+        // ------------------------------------------------------------ MMA issuer (leader)
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t idesc_qk = idesc_bf16_f32(256, kKeys, false);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(256, DV, true);
+            // the empty asm keeps a descriptor's base a runtime value, stepped by its
+            // address field, instead of one live register pair per tile and stage
+            auto desc_base = [&](uint32_t addr, uint32_t lbo) -> uint64_t {
+                uint64_t d = smem_desc_sw128(addr, lbo, 1024);
+                asm volatile("" : "+l"(d));
+                return d;
+            };
+            auto issue_qk = [&](int t, int s, int st) {
+                const uint64_t da = desc_base(sb + C::kQOff + t * C::kQTile, 16);
+                const uint64_t db = desc_base(sb + C::kStageOff + st * C::kStage, 16);
+#pragma unroll
+                for (int i = 0; i < DQK / 16; ++i)
+                    mma_ss_pair(tmem + col_s(s), da + (uint64_t)(((i >> 2) * kQBox + (i & 3) * 32) >> 4),
+                                db + (uint64_t)(((i >> 2) * kKBox + (i & 3) * 32) >> 4), idesc_qk, i > 0 ? 1u : 0u);
+                commit_pair(bar(C::kBarSFull + s));
+            };
+            auto issue_pv = [&](int t, int s, int st, bool acc) {
+                const uint64_t dv = desc_base(sb + C::kStageOff + st * C::kStage + C::kKTile, kQBox);
+#pragma unroll
+                for (int i = 0; i < kKeys / 16; ++i)
+                    mma_ts_pair(tmem + col_o(t), tmem + col_s(s) + 8 * i, dv + (uint64_t)(i * 2048 >> 4), idesc_pv,
+                                (acc || i > 0) ? 1u : 0u);
+            };
+            int g = 0;
+            for (int fi = 0; walk.next(p, f); ++fi) {
+                pair_wait(bar(C::kBarQReady), fi & 1, p.wait, abort);
+                pair_wait(bar(C::kBarReady + g % C::kStages), (g / C::kStages) & 1, p.wait, abort);
+                tc_fence_after();
+                for (int t = 0; t < MT; ++t) issue_qk(t, MT == 2 ? t : (g & 1), g % C::kStages);
+                if (f.n == 1) commit_pair(bar(C::kBarQEmpty));
+                for (int j = 0; j < f.n; ++j, ++g) {
+                    const int st = g % C::kStages, st1 = (g + 1) % C::kStages;
+                    const bool nxt = j + 1 < f.n;
+                    if (MT == 1 && nxt) {
+                        pair_wait(bar(C::kBarReady + st1), ((g + 1) / C::kStages) & 1, p.wait, abort);
+                        tc_fence_after();
+                        issue_qk(0, (g + 1) & 1, st1);
+                        if (j + 2 == f.n) commit_pair(bar(C::kBarQEmpty));
+                    }
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        const int s = MT == 2 ? t : (g & 1);
+                        pair_wait(bar(C::kBarPReady + s), (MT == 2 ? g : g >> 1) & 1, p.wait, abort);
+                        if (j == 0) pair_wait(bar(C::kBarOEmpty + t), (fi & 1) ^ 1, p.wait, abort);
+                        tc_fence_after();
+                        issue_pv(t, s, st, j > 0);
+                        if (MT == 1 || !nxt) commit_pair(bar(C::kBarPV + t));
+                        if (t == MT - 1) commit_pair(bar(C::kBarEmpty + st));
+                        if (MT == 2 && nxt) {
+                            if (t == 0) {
+                                pair_wait(bar(C::kBarReady + st1), ((g + 1) / C::kStages) & 1, p.wait, abort);
+                                tc_fence_after();
+                            }
+                            issue_qk(t, t, st1);
+                            if (t == 1 && j + 2 == f.n) commit_pair(bar(C::kBarQEmpty));
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        // every product of this pair is issued: the joining kernel's launch may overlap the rest
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    } else if (warp < C::kWarpTma) {
+        // ------------------------------------------------------------ softmax + epilogue (both CTAs)
+        if (MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+        const int t = warp >> 2;
+        const int T = 2 * t + rank;            // M tile of the row group
+        const int i = (warp & 3) * 32 + lane;  // its row == TMEM lane
+        if ((warp & 3) < live_warps(T)) {
+            const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+            const uint32_t o_addr = lane_base + col_o(t);
+            int g = 0;
+            for (int fi = 0; walk.next(p, f); ++fi) {
+                const int r = f.group * p.group + 128 * T + i;  // row of the KV head
+                const bool row_ok = r < p.R;                    // padding rows of the last M tile
+                int lo;
+                const uint64_t drafts = draft_sight(p, f.b, row_ok ? r % p.T : 0, f.s.len, f.s.total, lo);
+                float m_run = -INFINITY, l_run = 0.f;
+                for (int j = 0; j < f.n; ++j, ++g) {
+                    const int s = MT == 2 ? t : (g & 1);
+                    pair_wait(bar(C::kBarSFull + s), (MT == 2 ? g : g >> 1) & 1, p.wait, abort);
+                    tc_fence_after();
+                    // O's product of tile g - 1 must be done before O is touched.  With one S buffer a
+                    // tile these scores follow it; with two it is waited for, in every tile, so
+                    // that no phase of its barrier is skipped.
+                    softmax_tile<DV, false>(
+                        p, lane_base + col_s(s), o_addr, kKeys * (f.first + j), lo, f.s.len, drafts, m_run, l_run,
+                        nullptr,
+                        [&] { if (MT == 1 && g > 0) pair_wait(bar(C::kBarPV + t), (g - 1) & 1, p.wait, abort); });
+                    __syncwarp();
+                    if (lane == 0) arrive_leader(bar(C::kBarPReady + s));
+                }
+                pair_wait(bar(C::kBarPV + t), (MT == 1 ? g - 1 : fi) & 1, p.wait, abort);
+                tc_fence_after();
+                write_row<DV, false>(p, o_addr, f.head && f.tail, row_ok, (size_t)(f.b * p.H_kv + f.hk) * p.R + r,
+                                     2 * share + (f.head ? 1 : 0), 128 * T + i, m_run, l_run);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader(bar(C::kBarOEmpty + t));
+            }
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();  // every product of the pair has completed and every remote arrival has landed
+    if (warp == C::kWarpMma) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+template <int DQK, int MT>
+cudaError_t launch_t(const CacheAttnLaunch &L, int pairs, cudaStream_t stream)
+{
+    using C = PairCfg<DQK, MT>;
+    auto kernel = cache_pair_kernel<DQK, MT>;
+    static KernelSetup setup;
+    const cudaError_t err = setup(kernel, C::kSmemBytes, MT == 2 ? C::kLaunchRegs : 0);
+    if (err != cudaSuccess) return err;
+    return launch_dependent(kernel, 2 * pairs, C::kThreads, C::kSmemBytes, stream, L.tm_q, L.tm_k, L.tm_v, L.p);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_pair(const CacheAttnLaunch &L, int pairs, cudaStream_t stream)
+{
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    if (L.p.d_qk == 128) return L.p.group == 256 ? launch_t<128, 1>(L, pairs, stream) : launch_t<128, 2>(L, pairs, stream);
+    return L.p.group == 256 ? launch_t<192, 1>(L, pairs, stream) : launch_t<192, 2>(L, pairs, stream);
+}
+
+}  // namespace apex
