@@ -285,9 +285,9 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining partial results
-// max and sum of a row of a cut unit over its fragments, and the shift of this lane's
-// fragment c0 + lane: the fragments of unit u are the last of share c0 (slot 2 c0 + 1),
-// then the first of each CTA up to c1 (slots 2 c).
+// max and sum of a row of a cut unit over its fragments, by a warp.  The fragments of a
+// unit are the last of share c0 (slot 2 c0 + 1), then the first of each share up to c1
+// (slots 2 c).
 struct RowParts {
     const CacheAttnParams &p;
     int c0, n, rc;
@@ -295,10 +295,9 @@ struct RowParts {
     {
         return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * p.rows_cap + rc;
     }
-    // log2 of the sum of all fragments, relative to the maximum M
-    __device__ __forceinline__ void stats(int lane, float &M, float &L, float2 &mine) const
+    __device__ __forceinline__ void stats(int lane, float &M, float &L) const
     {
-        mine = make_float2(-INFINITY, 0.f);
+        float2 mine = make_float2(-INFINITY, 0.f);
         if (lane < n) mine = p.ws_ml[at(lane)];
         M = mine.x;
         for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, p.ws_ml[at(i)].x);
@@ -333,24 +332,43 @@ __device__ __forceinline__ void join_rows(const CacheAttnParams &p, int blocks_p
     float M = -INFINITY, L = 0.f, acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    if (ok) {
-#pragma unroll 4
-        for (int i = first; i < n; i += SPLIT) M = fmaxf(M, p.ws_ml[slot(i) + rc].x);
-#pragma unroll 2
-        for (int i = first; i < n; i += SPLIT) {
-            const float2 ml = p.ws_ml[slot(i) + rc];
-            const float4 *o = reinterpret_cast<const float4 *>(p.ws_o + slot(i) * DV) + (size_t)2 * chunk * p.rows_cap + rc;
-            const float4 a = o[0], b = o[p.rows_cap];
-            const float w = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M);
-            L = fmaf(w, ml.y, L);
-            acc[0] = fmaf(w, a.x, acc[0]);
-            acc[1] = fmaf(w, a.y, acc[1]);
-            acc[2] = fmaf(w, a.z, acc[2]);
-            acc[3] = fmaf(w, a.w, acc[3]);
-            acc[4] = fmaf(w, b.x, acc[4]);
-            acc[5] = fmaf(w, b.y, acc[5]);
-            acc[6] = fmaf(w, b.z, acc[6]);
-            acc[7] = fmaf(w, b.w, acc[7]);
+    // four fragments in flight: one round trip for their statistics and outputs
+    for (int i0 = first; ok && i0 < n; i0 += 4 * SPLIT) {
+        float2 ml[4];
+        float4 a[4], b[4];
+        float top = M;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + q * SPLIT;
+            ml[q] = make_float2(-INFINITY, 0.f);
+            if (i < n) {
+                const float4 *o =
+                    reinterpret_cast<const float4 *>(p.ws_o + slot(i) * DV) + (size_t)2 * chunk * p.rows_cap + rc;
+                ml[q] = p.ws_ml[slot(i) + rc];
+                a[q] = o[0];
+                b[q] = o[p.rows_cap];
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) top = fmaxf(top, ml[q].x);
+        const float keep = (M == -INFINITY) ? 0.f : exp2f(M - top);
+        M = top;
+        L *= keep;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= keep;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (ml[q].x == -INFINITY) continue;  // nothing seen, or no such fragment
+            const float w = exp2f(ml[q].x - M);
+            L = fmaf(w, ml[q].y, L);
+            acc[0] = fmaf(w, a[q].x, acc[0]);
+            acc[1] = fmaf(w, a[q].y, acc[1]);
+            acc[2] = fmaf(w, a[q].z, acc[2]);
+            acc[3] = fmaf(w, a[q].w, acc[3]);
+            acc[4] = fmaf(w, b[q].x, acc[4]);
+            acc[5] = fmaf(w, b[q].y, acc[5]);
+            acc[6] = fmaf(w, b[q].z, acc[6]);
+            acc[7] = fmaf(w, b[q].w, acc[7]);
         }
     }
     if (SPLIT > 1) {
@@ -383,40 +401,54 @@ __device__ __forceinline__ void join_rows(const CacheAttnParams &p, int blocks_p
 // acc[b, g, j] += sum over the heads of g of 2^(scale score - lse), heads in order:
 // a block takes 1024 keys of a (sequence, KV head), a thread four neighbours.
 constexpr int kWeightKeys = 1024;
+constexpr int kWeightHeads = 4;  // heads whose scores are in flight
 __device__ __forceinline__ void add_weights(const CacheAttnParams &p, long long block, int chunks, float *lse)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = (int)(block / chunks);
     const int j0 = (int)(block % chunks) * kWeightKeys;
+    const int j = j0 + 4 * threadIdx.x;
+    const float *s = p.scores + (size_t)unit * p.G * p.S_pad + j;
+    // the first heads' scores are under way before the statistics that they wait for
+    float4 x[kWeightHeads];
+#pragma unroll
+    for (int g = 0; g < kWeightHeads; ++g) {
+        x[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (g < p.G && j < p.S_pad) x[g] = *reinterpret_cast<const float4 *>(s + (size_t)g * p.S_pad);
+    }
     const int len = min(max(p.lens[unit / p.H_kv], 0), p.S_cap);
     if (j0 >= len) return;
     const int2 c = p.units[unit];
-    const int j = j0 + 4 * threadIdx.x;
-    const float *s = p.scores + (size_t)unit * p.G * p.S_pad + j;
     for (int g = warp; g < p.G; g += 8) {
-        float x;
+        float at;
         if (c.x == c.y) {
-            x = p.lse[(size_t)unit * p.G + g];
+            at = p.lse[(size_t)unit * p.G + g];
         } else {
             const RowParts parts{p, c.x, c.y - c.x + 1, g};
             float M, L;
-            float2 mine;
-            parts.stats(lane, M, L, mine);
-            x = M + log2f(L);
+            parts.stats(lane, M, L);
+            at = M + log2f(L);
         }
-        if (lane == 0) lse[g] = x;
+        if (lane == 0) lse[g] = at;
     }
     __syncthreads();
     if (j >= len) return;
     float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int g = 0; g < p.G; ++g) {
-        // exp2f: weights below 2^-126 are kept, as the sums of a long service need them
-        const float4 x = *reinterpret_cast<const float4 *>(s + (size_t)g * p.S_pad);
-        w[0] += exp2f(fmaf(x.x, p.scale_log2, -lse[g]));
-        w[1] += exp2f(fmaf(x.y, p.scale_log2, -lse[g]));
-        w[2] += exp2f(fmaf(x.z, p.scale_log2, -lse[g]));
-        w[3] += exp2f(fmaf(x.w, p.scale_log2, -lse[g]));
+    for (int g0 = 0; g0 < p.G; g0 += kWeightHeads) {
+#pragma unroll
+        for (int g = 0; g < kWeightHeads; ++g)
+            if (g0 + g < p.G) {
+                // exp2f: weights below 2^-126 are kept, as the sums of a long service need them
+                const float at = lse[g0 + g];
+                w[0] += exp2f(fmaf(x[g].x, p.scale_log2, -at));
+                w[1] += exp2f(fmaf(x[g].y, p.scale_log2, -at));
+                w[2] += exp2f(fmaf(x[g].z, p.scale_log2, -at));
+                w[3] += exp2f(fmaf(x[g].w, p.scale_log2, -at));
+            }
+#pragma unroll
+        for (int g = 0; g < kWeightHeads; ++g)
+            if (g0 + kWeightHeads + g < p.G)
+                x[g] = *reinterpret_cast<const float4 *>(s + (size_t)(g0 + kWeightHeads + g) * p.S_pad);
     }
     float *acc = p.acc + (size_t)unit * p.S_cap + j;
     if (j + 4 <= len && (reinterpret_cast<uintptr_t>(acc) & 15) == 0) {
