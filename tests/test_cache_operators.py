@@ -561,6 +561,48 @@ def test_evict_again():
     assert torch.equal(k.cpu(), want[0]) and torch.equal(v.cpu(), want[1])
 
 
+@pytest.mark.gpu
+def test_rows_past_32_bit_offsets():
+    """One sequence of the longest cache, 2 heads of 2^24 rows of 64: entries past 2^31."""
+    dev = _gpu()
+    if torch.cuda.mem_get_info(dev)[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    cap, T, H = 1 << 24, 3, 2
+    n = cap - T - 2
+    g = _gen(dev, 60)
+    kc, vc = (torch.full((1, H, cap, 64), float("nan"), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    seen = 500
+    kc[:, :, n - seen:n], vc[:, :, n - seen:n] = _normal(g, dev, 1, H, seen, 64), _normal(g, dev, 1, H, seen, 64)
+    q, k, v = _normal(g, dev, 1, 4, T, 64), _normal(g, dev, 1, H, T, 64), _normal(g, dev, 1, H, T, 64)
+    lens = torch.tensor([n], dtype=torch.int32, device=dev)
+    at = (lens[:, None] + torch.arange(T, device=dev, dtype=torch.int32)).contiguous()
+    qr, _, _ = apex.rope(q, k, v, positions=at, k_out=kc, v_out=vc, row0=lens)
+    _rope_close(kc[:, :, n:n + T], *_rope_ref(k, at))
+    assert torch.equal(vc[:, :, n:n + T], v) and torch.isnan(vc[:, :, n + T:].float()).all()
+    got = apex.tree_decode(qr, kc, vc, lens, window=seen)
+    # the same rows as a short cache: a window of `seen` counts positions alike
+    lo = n - seen
+    ref, tol, _, _ = _attn_ref(qr, kc[:, :, lo:n + T], vc[:, :, lo:n + T], [seen], True, window=seen)
+    _close(got, ref, tol)
+    # keep eight rows, the heaviest at the end of the cache
+    acc = torch.zeros(1, H, cap, device=dev)
+    acc[:, :, n - 5:n] = 1.0 + torch.arange(5, device=dev)
+    last_k, last_v = kc[:, :, n - 5:n].clone(), vc[:, :, n - 5:n].clone()
+    a, p, m = apex.evict(kc, vc, acc, lens, 8, n_sink=3)
+    assert m.tolist() == [8]
+    assert p[..., :8].tolist() == [[[0, 1, 2] + list(range(n - 5, n))] * H] and (p[..., 8:] == -1).all()
+    assert torch.equal(a[..., :8].cpu(), torch.tensor([0.0] * 3 + [1, 2, 3, 4, 5]).expand(1, H, 8))
+    assert torch.equal(kc[:, :, 3:8], last_k) and torch.equal(vc[:, :, 3:8], last_v)
+    # every weight of a row of equal keys is 1 / n
+    kc[:, :, :n] = 0
+    vc[:, :, :n] = 0
+    vc[:, :, n - 1] = 1.0
+    acc.zero_()
+    out = apex.decode_weights(qr[:, :, :1].contiguous(), kc, vc, lens, acc)
+    assert ((acc[..., :n].double() - 2.0 / n).abs() <= 2.0 / n * 2.0 ** -11).all() and (acc[..., n:] == 0).all()
+    assert ((out.double() - 1.0 / n).abs() <= 1.0 / n * 2 * U).all()
+
+
 # ------------------------------------------------------------------------------------------------- together
 def _served(dev, seed, dk, dv, layout):
     """A bounded cache served for a few steps, each checked against the formulas on the same inputs."""
@@ -790,14 +832,14 @@ def test_decode_weights_refuses(lib, o, code):
 
 
 EVICT_ARGS = dict(k=P, v=P, B=1, H=2, cap=64, dk=128, dv=128, acc=P, pos=None, lens=P, nxt=None, budget=16, sink=0,
-                  recent=0, acc_out=2 * P, pos_out=2 * P, lens_out=2 * P, ws=P, n=1 << 40)
+                  recent=0, acc_out=2 * P, pos_out=4 * P, lens_out=2 * P, ws=P, n=1 << 40)
 
 
 @pytest.mark.parametrize("o,code", [
     (dict(k=None), BAD), (dict(v=None), BAD), (dict(acc=None), BAD), (dict(lens=None), BAD), (dict(acc_out=None), BAD),
     (dict(pos_out=None), BAD), (dict(lens_out=None), BAD), (dict(ws=None), BAD), (dict(k=P + 8), BAD),
     (dict(pos=P + 4), BAD), (dict(lens=P + 2), BAD), (dict(nxt=P + 2), BAD), (dict(acc_out=P), BAD),
-    (dict(pos=2 * P), BAD), (dict(lens_out=P), BAD), (dict(nxt=2 * P), BAD), (dict(B=0), BAD), (dict(H=-1), BAD), (dict(cap=0), BAD), (dict(budget=0), BAD),
+    (dict(acc_out=P + 496), BAD), (dict(pos=2 * P), BAD), (dict(pos=4 * P - 16), BAD), (dict(pos_out=2 * P), BAD), (dict(lens_out=P), BAD), (dict(nxt=2 * P), BAD), (dict(B=0), BAD), (dict(H=-1), BAD), (dict(cap=0), BAD), (dict(budget=0), BAD),
     (dict(sink=-1), BAD), (dict(recent=-1), BAD), (dict(sink=10, recent=7), BAD), (dict(dk=0), BAD),
     (dict(dk=100), UNSUPPORTED), (dict(dv=2048), UNSUPPORTED), (dict(cap=(1 << 24) + 1), UNSUPPORTED),
     (dict(n=15), BAD),

@@ -229,8 +229,6 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
                 }
             }
         }
-        // every product of this CTA is issued: the joining kernel's launch may overlap the rest
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     } else if ((warp & 3) < live_warps(warp >> 2)) {
         // ------------------------------------------------------------ softmax + epilogue
         const int t = warp >> 2;
@@ -474,8 +472,6 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
     __shared__ float sh[SPLIT > 1 ? SPLIT : 1][10][32];
     __shared__ float lse[16];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // the next kernel's launch may overlap this one (it waits for it before it reads)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!WEIGHTS || blockIdx.x < join_blocks)
         join_rows<DV, SPLIT>(p, blocks_per_unit, sh);
     else
@@ -498,15 +494,14 @@ cudaError_t launch_join_t(const CacheAttnParams &p, cudaStream_t stream)
 {
     const int n_units = p.B * p.H_kv * p.n_groups;
     const int per_unit = (p.rows_cap * (DV / 8) + 256 / SPLIT - 1) / (256 / SPLIT);
-    const long long join_blocks = (long long)n_units * per_unit;
+    // below 2^31 blocks: B * H_q <= 2^24 and B * H_kv * S_cap <= 2^40
+    const int join_blocks = n_units * per_unit;
     const int chunks = (p.S_cap + kWeightKeys - 1) / kWeightKeys;
-    const long long blocks = join_blocks + (p.acc ? (long long)n_units * chunks : 0);
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     if (p.acc)
-        return launch_dependent(cache_join_kernel<DV, SPLIT, true>, (int)blocks, 256, 0, stream, p, (int)join_blocks,
-                                per_unit, chunks);
-    return launch_dependent(cache_join_kernel<DV, SPLIT, false>, (int)blocks, 256, 0, stream, p, (int)join_blocks,
-                            per_unit, chunks);
+        return launch_dependent(cache_join_kernel<DV, SPLIT, true>, join_blocks + n_units * chunks, 256, 0, stream, p,
+                                join_blocks, per_unit, chunks);
+    return launch_dependent(cache_join_kernel<DV, SPLIT, false>, join_blocks, 256, 0, stream, p, join_blocks, per_unit,
+                            chunks);
 }
 
 template <int DV>

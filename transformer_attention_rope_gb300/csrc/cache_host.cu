@@ -16,6 +16,13 @@ namespace {
 
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// Whether [a, a + n) and [b, b + n) share a byte (b may be NULL: no).
+bool overlap(const void *a, const void *b, size_t n)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return b && (x < y ? y - x : x - y) < n;
+}
+
 // ----------------------------------------------------------------- rope
 
 // theta_i / 2 pi as 0.64 fixed-point fractions of a turn.  The last few parameter
@@ -179,9 +186,14 @@ apex_status apex_attn_evict(void *k_cache, void *v_cache, int B, int H_kv, int S
         return APEX_ERR_INVALID_ARG;
     if (B <= 0 || H_kv <= 0 || S_cap <= 0 || d_k <= 0 || d_v <= 0) return APEX_ERR_INVALID_ARG;
     if (budget <= 0 || n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > budget) return APEX_ERR_INVALID_ARG;
-    if (acc_out == acc || positions_out == positions || lens_out == lens || lens_out == next_pos)
-        return APEX_ERR_INVALID_ARG;
     if (S_cap > kMaxSeq || (long long)B * H_kv > (1 << 24)) return APEX_ERR_UNSUPPORTED;
+    // every CTA reads its inputs while others already write: no output may lie on an input
+    const size_t row_bytes = (size_t)B * H_kv * S_cap * 4, seq_bytes = (size_t)B * 4;
+    if (overlap(acc_out, acc, row_bytes) || overlap(positions_out, positions, row_bytes) ||
+        overlap(acc_out, positions, row_bytes) || overlap(positions_out, acc, row_bytes) ||
+        overlap(acc_out, positions_out, row_bytes) || overlap(lens_out, lens, seq_bytes) ||
+        overlap(lens_out, next_pos, seq_bytes))
+        return APEX_ERR_INVALID_ARG;
     if (d_k % 8 != 0 || d_v % 8 != 0 || d_k > 1024 || d_v > 1024) return APEX_ERR_UNSUPPORTED;
     const EvictWorkspace w = evict_workspace(B * H_kv, S_cap, budget);
     if (workspace_bytes < w.bytes) return APEX_ERR_INVALID_ARG;
@@ -247,6 +259,7 @@ static apex_status cache_attn(const void *q, const void *k_cache, const void *v_
     if (workspace_bytes < w.bytes) return APEX_ERR_INVALID_ARG;
     DeviceScope dev;
     if (dev.status != APEX_OK) return dev.status;
+    if (cache_attn_pairs(H_q / H_kv * T, d_v) && dev.sm_count < 2) return APEX_ERR_UNSUPPORTED;
     CacheAttnLaunch L;
     memset(&L, 0, sizeof L);
     CacheAttnParams &p = L.p;

@@ -314,9 +314,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                 }
             }
         }
-        __syncwarp();
-        // every product of this pair is issued: the joining kernel's launch may overlap the rest
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     } else if (warp < C::kWarpTma) {
         // ------------------------------------------------------------ softmax + epilogue (both CTAs)
         if (MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
@@ -382,7 +379,6 @@ cudaError_t launch_t(const CacheAttnLaunch &L, int pairs, cudaStream_t stream)
 
 cudaError_t launch_cache_pair(const CacheAttnLaunch &L, int pairs, cudaStream_t stream)
 {
-    if (pairs < 1) return cudaErrorInvalidConfiguration;
     if (L.p.d_qk == 128) return L.p.group == 256 ? launch_t<128, 1>(L, pairs, stream) : launch_t<128, 2>(L, pairs, stream);
     return L.p.group == 256 ? launch_t<192, 1>(L, pairs, stream) : launch_t<192, 2>(L, pairs, stream);
 }
