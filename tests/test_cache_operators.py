@@ -373,11 +373,13 @@ def test_tree_decode_scale(scale):
 
 
 @pytest.mark.gpu
-def test_tree_decode_rising_scores():
+@pytest.mark.parametrize("Hq,Hkv,T,dk,dv", [(8, 2, 4, 64, 64), (16, 1, 20, 64, 64), (8, 2, 4, 128, 128),
+                                            (16, 1, 10, 128, 128), (16, 1, 40, 128, 128), (16, 1, 33, 192, 128)])
+def test_tree_decode_rising_scores(Hq, Hkv, T, dk, dv):
     """Scores that keep rising along the keys: the running maximum is raised in every tile."""
     dev = _gpu()
-    n, T = 1500, 4
-    q, k, v, ln = _attn_inputs(dev, 5, 8, 2, T, 64, 64, n + T, [n])
+    n = 1500
+    q, k, v, ln = _attn_inputs(dev, 5, Hq, Hkv, T, dk, dv, n + T, [n])
     q[..., 0], k[..., 0] = 8.0, torch.linspace(-60, 60, n + T, device=dev).to(torch.bfloat16)
     got = apex.tree_decode(q, k, v, ln)
     ref, tol, _, _ = _attn_ref(q, k, v, [n], True)
@@ -385,6 +387,53 @@ def test_tree_decode_rising_scores():
     k[..., 0] = -k[..., 0]
     ref, tol, _, _ = _attn_ref(q, k, v, [n], True)
     _close(apex.tree_decode(q, k, v, ln), ref, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,T,d,cap", [(33, 4, 2, 3, 64, 300), (70, 8, 2, 5, 128, 700), (300, 4, 1, 1, 64, 140),
+                                              (40, 16, 1, 17, 128, 400), (1, 8, 8, 4, 128, 40000)])
+def test_many_and_long_sequences(B, Hq, Hkv, T, d, cap):
+    """More sequences than a warp's lanes hold, shares that end in the middle of units, one long sequence."""
+    dev = _gpu()
+    lens = torch.randint(0, cap - T + 1, (B,), generator=torch.Generator().manual_seed(B)).tolist()
+    lens[-1] = cap - T
+    q, k, v, ln = _attn_inputs(dev, B, Hq, Hkv, T, d, d, cap, lens)
+    mask, _ = _tree(B, B, T, lens)
+    ref, tol, _, _ = _attn_ref(q, k, v, lens, True, mask)
+    _close(apex.tree_decode(q, k, v, ln, tree_mask=mask.to(dev)), ref, tol)
+    q1 = q[:, :, :1].contiguous()
+    acc = torch.zeros(B, Hkv, cap, device=dev)
+    ref, tol, w, wtol = _attn_ref(q1, k, v, lens, False)
+    _close(apex.decode_weights(q1, k, v, ln, acc), ref, tol)
+    _close(acc, w, wtol + 2.0 ** -23 * w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(40))
+def test_random_configurations(seed):
+    """Seeded draws over head groups, rows, lengths, windows and trees, on every kernel."""
+    dev = _gpu()
+    r = torch.Generator().manual_seed(1000 + seed)
+
+    def pick(*xs):
+        return xs[int(torch.randint(0, len(xs), (1,), generator=r))]
+
+    def log(lo, hi):
+        return int(round(math.exp(math.log(lo) + float(torch.rand(1, generator=r)) * (math.log(hi) - math.log(lo)))))
+
+    G, Hkv, B, T = pick(1, 2, 4, 8, 16), pick(1, 2, 3), pick(1, 2, 5), log(1, 64)
+    dk, dv = pick((64, 64), (128, 128), (192, 128))
+    cap = T + log(1, 3000)
+    lens = torch.randint(0, cap - T + 1, (B,), generator=r).tolist()
+    window = pick(0, 0, log(1, 1000))
+    q, k, v, ln = _attn_inputs(dev, seed, G * Hkv, Hkv, T, dk, dv, cap, lens)
+    mask, pos = _tree(seed, B, T, lens)
+    if pick(0, 1):  # some drafts see nothing of the tree, not even themselves
+        mask[:, ::3] = 0
+    ref, tol, _, _ = _attn_ref(q, k, v, lens, True, mask, pos, window)
+    got = apex.tree_decode(q, k, v, ln, tree_mask=mask.to(dev), positions=pos.to(dev), window=window)
+    _close(got, ref, tol)
+    assert apex.apex_attn_device_status() == 0
 
 
 WEIGHTS = [  # Hq, Hkv, d_qk, d_v, S_cap, lens
