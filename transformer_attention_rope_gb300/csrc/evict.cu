@@ -170,6 +170,9 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
             cut |= sh.digit << shift;
             want -= sh.above;
             all_ties = sh.equal == want;
+            // every row with this prefix stays: the digits below it do not matter (for weights
+            // that differ, usually after three of four)
+            if (all_ties) break;
         }
         ties = want;
     }
