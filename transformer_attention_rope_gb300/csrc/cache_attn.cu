@@ -513,12 +513,16 @@ cudaError_t launch_join(const CacheAttnParams &p, int shares, cudaStream_t strea
 
 }  // namespace
 
-cudaError_t launch_cache_attn(const CacheAttnLaunch &L, int sm_count, cudaStream_t stream)
+cudaError_t launch_cache_attn(CacheAttnLaunch &L, int sm_count, cudaStream_t stream)
 {
-    const CacheAttnParams &p = L.p;
+    CacheAttnParams &p = L.p;
     const bool pairs = cache_attn_pairs(p.R, p.d_v);
-    const int shares = std::min(pairs ? sm_count / 2 : sm_count,
-                                cache_attn_shares(p.B, p.H_kv, p.n_groups, p.S_cap, pairs));
+    const int n_units = p.B * p.H_kv * p.n_groups, room = pairs ? sm_count / 2 : sm_count;
+    int shares = std::min(room, cache_attn_shares(p.B, p.H_kv, p.n_groups, p.S_cap, pairs));
+    // keys that a unit can reach: a window bounds them, the drafts and a tile's slack beside it
+    const int reach = p.window > 0 ? (int)std::min<long long>(p.S_cap, (long long)p.window + p.drafts + kKeys) : p.S_cap;
+    p.whole = !p.acc && cache_attn_whole(n_units, reach, room);
+    if (p.whole) shares = std::min(shares, n_units);
     cudaError_t err;
     if (pairs)
         err = launch_cache_pair(L, shares, stream);
@@ -531,7 +535,7 @@ cudaError_t launch_cache_attn(const CacheAttnLaunch &L, int sm_count, cudaStream
     else
         err = p.acc ? launch_t<192, 128, 1, true>(L, shares, stream) : launch_t<192, 128, 1, false>(L, shares, stream);
     if (err != cudaSuccess) return err;
-    if (p.S_cap <= kKeys && !p.acc) return cudaSuccess;  // one tile a unit: nothing is ever cut
+    if (p.whole) return cudaSuccess;
     return p.d_v == 64 ? launch_join<64>(p, shares, stream) : launch_join<128>(p, shares, stream);
 }
 

@@ -59,7 +59,7 @@ struct KernelSetup {
 // number of tiles (one at least, so that every unit writes its output).
 struct Seq {
     int len, total, tile0, tiles;
-    int cost;  // of a unit in the schedule: its tiles and kCacheUnitCost for its start
+    int cost;  // of a unit in the schedule: its tiles and kCacheUnitCost for its start; 1 when units stay whole
     __device__ __forceinline__ void load(const CacheAttnParams &p, int b)
     {
         len = min(max(__ldg(p.lens + b), 0), p.S_cap);
@@ -67,7 +67,7 @@ struct Seq {
         const int lo = p.window > 0 ? max(0, len - p.window + 1) : 0;
         tile0 = lo / kCacheTileKeys;
         tiles = max(1, (total + kCacheTileKeys - 1) / kCacheTileKeys - tile0);
-        cost = tiles + kCacheUnitCost;
+        cost = p.whole ? 1 : tiles + kCacheUnitCost;
     }
 };
 
@@ -153,7 +153,8 @@ struct Walk {
             if (fresh) seq.load(p, s.b);
             fresh = false;
             const int n = min(seq.cost - s.off, s.left);  // cost of this unit in the share
-            const int t0 = max(0, s.off - kCacheUnitCost), t1 = max(0, s.off + n - kCacheUnitCost);
+            const int t0 = p.whole ? 0 : max(0, s.off - kCacheUnitCost);
+            const int t1 = p.whole ? seq.tiles : max(0, s.off + n - kCacheUnitCost);
             f.s = seq;
             f.b = s.b;
             f.hk = s.unit / p.n_groups;

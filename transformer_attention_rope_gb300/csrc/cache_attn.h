@@ -32,6 +32,7 @@ struct CacheAttnParams {
     int group;      // rows of a row group
     int n_groups;   // row groups of a KV head
     int rows_cap;   // rows of a partial result, min(R, group)
+    int whole;      // units are not cut: nothing to join
     // workspace
     float *ws_o;    // [2 * shares][d_v / 4][rows_cap][4] partial outputs (unnormalised)
     float2 *ws_ml;  // [2 * shares][rows_cap]             their (max in log2 units, sum)
@@ -60,6 +61,21 @@ inline int cache_attn_shares(int B, int H_kv, int n_groups, int S_cap, bool pair
 {
     const long long tiles = (long long)B * H_kv * n_groups * ((S_cap + kCacheTileKeys - 1) / kCacheTileKeys);
     return (int)std::min<long long>(pairs ? kCacheMaxCtas / 2 : kCacheMaxCtas, tiles);
+}
+
+// Whether short caches are better not cut: without cuts the joining kernel is not
+// launched, which is worth about 3.5 tiles, but the CTAs' loads are less even.  Judged on
+// full caches; past 6 tiles a ragged batch could lose more than that.  Measured cut / whole
+// at d = 128, 32/8 heads, 4 drafts: 1 cache of 376 keys 8.6 / 7.8 us, of 504 8.7 / 8.8, of
+// 632 8.9 / 9.7; 8 caches of 504 keys 11.1 / 9.7; 32 of 248 14.8 / 12.4, of 760 24.2 / 21.2;
+// 640 rows, 4 caches of 480 keys on pairs 22.7 / 16.3.
+inline bool cache_attn_whole(long long units, int keys, int shares)
+{
+    const long long tiles = (keys + kCacheTileKeys - 1) / kCacheTileKeys, cost = tiles + kCacheUnitCost;
+    if (tiles == 1) return true;
+    const long long rounds = (units + shares - 1) / shares;
+    const long long cut = std::max<long long>(1 + kCacheUnitCost, units * cost / shares);
+    return tiles <= 6 && 2 * rounds * cost <= 2 * cut + 7;
 }
 
 struct CacheAttnWorkspace {
@@ -107,7 +123,8 @@ struct CacheAttnLaunch {
     CacheAttnParams p;
 };
 
-cudaError_t launch_cache_attn(const CacheAttnLaunch &L, int sm_count, cudaStream_t stream);
+// chooses the kernel and how the work is cut (L.p.whole), launches it and what joins it
+cudaError_t launch_cache_attn(CacheAttnLaunch &L, int sm_count, cudaStream_t stream);
 // the attention kernel on CTA pairs alone (the caller joins)
 cudaError_t launch_cache_pair(const CacheAttnLaunch &L, int pairs, cudaStream_t stream);
 
