@@ -151,39 +151,33 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
             }
         }
     } else if (warp == C::kWarpMma) {
-        // ------------------------------------------------------------ MMA issuer (lane 0; the warp mends V tiles)
+        // ------------------------------------------------------------ MMA issuer, which also mends V tiles
         constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kKeys, false);
         constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV, true);
-        // the empty asm keeps a descriptor's base a runtime value, stepped by its
-        // address field, instead of one live register pair per tile and stage
-        auto desc_base = [&](uint32_t addr, uint32_t lbo) -> uint64_t {
-            uint64_t d = smem_desc_sw128(addr, lbo, 1024);
-            asm volatile("" : "+l"(d));
-            return d;
+        const bool one = elect_one();
+        auto commit = [&](int i) {
+            if (one) tc_commit(bar(i));
         };
         auto issue_qk = [&](int t, int s, int ks) {
-            if (lane == 0) {
-                const uint64_t da = desc_base(sb + C::kQOff + t * C::kQTile, 16);
-                const uint64_t db = desc_base(sb + C::kKOff + ks * C::kKTile, 16);
+            const uint64_t da = smem_desc_sw128(sb + C::kQOff + t * C::kQTile, 16, 1024);
+            const uint64_t db = smem_desc_sw128(sb + C::kKOff + ks * C::kKTile, 16, 1024);
+            if (one) {
 #pragma unroll
                 for (int i = 0; i < DQK / 16; ++i) {
                     const uint64_t off = ((i >> 2) * kBox + (i & 3) * 32) >> 4;
                     umma_ss(tmem + C::col_s(s), da + off, db + off, idesc_qk, i > 0 ? 1u : 0u);
                 }
-                tc_commit(bar(C::kBarSFull + s));
             }
+            commit(C::kBarSFull + s);
         };
         auto issue_pv = [&](int t, int s, int vs, bool acc) {
-            if (lane == 0) {
-                const uint64_t dv = desc_base(sb + C::kVOff + vs * C::kVTile, kBox);
+            const uint64_t dv = smem_desc_sw128(sb + C::kVOff + vs * C::kVTile, kBox, 1024);
+            if (one) {
 #pragma unroll
                 for (int i = 0; i < kKeys / 16; ++i)
                     umma_ts(tmem + C::col_o(t), tmem + C::col_s(s) + 8 * i, dv + (uint64_t)(i * 2048 >> 4), idesc_pv,
                             (acc || i > 0) ? 1u : 0u);
             }
-        };
-        auto commit = [&](int i) {
-            if (lane == 0) tc_commit(bar(i));
         };
         int g = 0;
         for (int fi = 0; walk.next(p, f); ++fi) {

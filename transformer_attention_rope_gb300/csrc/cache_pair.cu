@@ -251,31 +251,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
         }
     } else if (warp == C::kWarpMma) {
         // ------------------------------------------------------------ MMA issuer (leader)
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             constexpr uint32_t idesc_qk = idesc_bf16_f32(256, kKeys, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(256, DV, true);
-            // the empty asm keeps a descriptor's base a runtime value, stepped by its
-            // address field, instead of one live register pair per tile and stage
-            auto desc_base = [&](uint32_t addr, uint32_t lbo) -> uint64_t {
-                uint64_t d = smem_desc_sw128(addr, lbo, 1024);
-                asm volatile("" : "+l"(d));
-                return d;
+            const bool one = elect_one();
+            auto commit = [&](int i) {
+                if (one) commit_pair(bar(i));
             };
             auto issue_qk = [&](int t, int s, int st) {
-                const uint64_t da = desc_base(sb + C::kQOff + t * C::kQTile, 16);
-                const uint64_t db = desc_base(sb + C::kStageOff + st * C::kStage, 16);
+                const uint64_t da = smem_desc_sw128(sb + C::kQOff + t * C::kQTile, 16, 1024);
+                const uint64_t db = smem_desc_sw128(sb + C::kStageOff + st * C::kStage, 16, 1024);
+                if (one) {
 #pragma unroll
-                for (int i = 0; i < DQK / 16; ++i)
-                    mma_ss_pair(tmem + col_s(s), da + (uint64_t)(((i >> 2) * kQBox + (i & 3) * 32) >> 4),
-                                db + (uint64_t)(((i >> 2) * kKBox + (i & 3) * 32) >> 4), idesc_qk, i > 0 ? 1u : 0u);
-                commit_pair(bar(C::kBarSFull + s));
+                    for (int i = 0; i < DQK / 16; ++i)
+                        mma_ss_pair(tmem + col_s(s), da + (uint64_t)(((i >> 2) * kQBox + (i & 3) * 32) >> 4),
+                                    db + (uint64_t)(((i >> 2) * kKBox + (i & 3) * 32) >> 4), idesc_qk, i > 0 ? 1u : 0u);
+                }
+                commit(C::kBarSFull + s);
             };
             auto issue_pv = [&](int t, int s, int st, bool acc) {
-                const uint64_t dv = desc_base(sb + C::kStageOff + st * C::kStage + C::kKTile, kQBox);
+                const uint64_t dv = smem_desc_sw128(sb + C::kStageOff + st * C::kStage + C::kKTile, kQBox, 1024);
+                if (one) {
 #pragma unroll
-                for (int i = 0; i < kKeys / 16; ++i)
-                    mma_ts_pair(tmem + col_o(t), tmem + col_s(s) + 8 * i, dv + (uint64_t)(i * 2048 >> 4), idesc_pv,
-                                (acc || i > 0) ? 1u : 0u);
+                    for (int i = 0; i < kKeys / 16; ++i)
+                        mma_ts_pair(tmem + col_o(t), tmem + col_s(s) + 8 * i, dv + (uint64_t)(i * 2048 >> 4), idesc_pv,
+                                    (acc || i > 0) ? 1u : 0u);
+                }
             };
             int g = 0;
             for (int fi = 0; walk.next(p, f); ++fi) {
@@ -283,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                 pair_wait(bar(C::kBarReady + g % C::kStages), (g / C::kStages) & 1, p.wait, abort);
                 tc_fence_after();
                 for (int t = 0; t < MT; ++t) issue_qk(t, MT == 2 ? t : (g & 1), g % C::kStages);
-                if (f.n == 1) commit_pair(bar(C::kBarQEmpty));
+                if (f.n == 1) commit(C::kBarQEmpty);
                 for (int j = 0; j < f.n; ++j, ++g) {
                     const int st = g % C::kStages, st1 = (g + 1) % C::kStages;
                     const bool nxt = j + 1 < f.n;
@@ -291,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                         pair_wait(bar(C::kBarReady + st1), ((g + 1) / C::kStages) & 1, p.wait, abort);
                         tc_fence_after();
                         issue_qk(0, (g + 1) & 1, st1);
-                        if (j + 2 == f.n) commit_pair(bar(C::kBarQEmpty));
+                        if (j + 2 == f.n) commit(C::kBarQEmpty);
                     }
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
@@ -300,15 +301,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                         if (j == 0) pair_wait(bar(C::kBarOEmpty + t), (fi & 1) ^ 1, p.wait, abort);
                         tc_fence_after();
                         issue_pv(t, s, st, j > 0);
-                        if (MT == 1 || !nxt) commit_pair(bar(C::kBarPV + t));
-                        if (t == MT - 1) commit_pair(bar(C::kBarEmpty + st));
+                        if (MT == 1 || !nxt) commit(C::kBarPV + t);
+                        if (t == MT - 1) commit(C::kBarEmpty + st);
                         if (MT == 2 && nxt) {
                             if (t == 0) {
                                 pair_wait(bar(C::kBarReady + st1), ((g + 1) / C::kStages) & 1, p.wait, abort);
                                 tc_fence_after();
                             }
                             issue_qk(t, t, st1);
-                            if (t == 1 && j + 2 == f.n) commit_pair(bar(C::kBarQEmpty));
+                            if (t == 1 && j + 2 == f.n) commit(C::kBarQEmpty);
                         }
                     }
                 }
