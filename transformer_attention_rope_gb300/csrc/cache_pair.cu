@@ -9,12 +9,17 @@
 // tile's 128 keys of K and 64 of the 128 entries of V, so every K/V byte crosses L2 once
 // for 256 (MT = 1) or 512 (MT = 2) rows and the operand traffic of B halves.
 //
-// Warps per CTA: 4 softmax warps per M tile, then a TMA warp (K and V), an MMA warp (the
+// Warps per CTA: two softmax warpgroups, then a TMA warp (K and V), an MMA warp (the
 // leader's issues, both allocate TMEM), a warp that loads the queries, waits for what has
-// landed here, mends V tiles and tells the leader, and an idle one.  The leader's MMA
-// thread waits on its own barriers, which the peer reaches by remote arrivals; commits
-// are multicast, so everybody waits on local barriers.  With MT = 1 S has two buffers:
-// the product of the next tile runs under this tile's softmax.
+// landed here, mends V tiles and tells the leader, and an idle one.  The leader's MMA warp
+// waits on its own barriers, which the peer reaches by remote arrivals; commits are
+// multicast, so everybody waits on local barriers.
+//
+// Softmax: one warpgroup needs about 1 us for the 128 x 128 scores of a tile, the products
+// half of that.  With MT = 2 each warpgroup has its own M tile.  With MT = 1 both work on
+// the same rows, on every other key tile, each with its own S, running maximum, sum and O;
+// the two results are joined when a fragment ends (both warpgroups reach the same TMEM
+// lanes), each warpgroup writing half of the columns.
 #include <math.h>
 
 #include "cache_attn.cuh"
@@ -30,8 +35,8 @@ constexpr int kVTile = 128 * 128;  // 128 keys x this CTA's 64 entries
 
 template <int DQK, int MT>
 struct PairCfg {
-    static constexpr int kThreads = 128 * MT + 128;
-    static constexpr int kWarpTma = 4 * MT, kWarpMma = 4 * MT + 1, kWarpReady = 4 * MT + 2;
+    static constexpr int kThreads = 3 * 128;
+    static constexpr int kWarpTma = 8, kWarpMma = 9, kWarpReady = 10;
     // Two softmax warpgroups need more registers than an even split of 64 K gives: the
     // block is launched with kLaunchRegs a thread, which setmaxnreg redistributes.
     static constexpr int kLaunchRegs = 168, kRegsSoftmax = 200, kRegsCtl = 104;
@@ -39,7 +44,7 @@ struct PairCfg {
     static constexpr int kBoxes = DQK / 64;
     static constexpr int kQTile = kBoxes * kQBox, kKTile = kBoxes * kKBox;
     static constexpr int kStage = kKTile + kVTile;  // K and V of a tile share a stage
-    static constexpr int kStages = DQK == 128 ? (MT == 1 ? 6 : 5) : (MT == 1 ? 4 : 3);
+    static constexpr int kStages = DQK == 128 ? 5 : (MT == 1 ? 4 : 3);
     static constexpr int kQOff = 0;
     static constexpr int kStageOff = MT * kQTile;
     static constexpr int kBarOff = kStageOff + kStages * kStage;
@@ -48,15 +53,16 @@ struct PairCfg {
     static constexpr int kBarQEmpty = 2;                      // multicast commit
     static constexpr int kBarSFull = 3;                       // [2] multicast commit, per S buffer
     static constexpr int kBarPReady = 5;                      // [2] leader: live softmax warps, per S buffer
-    static constexpr int kBarPV = 7;                          // [2] multicast commit, a phase per tile (MT = 1) or fragment
-    static constexpr int kBarOEmpty = 9;                      // [2] leader: live softmax warps, one phase per fragment
+    static constexpr int kBarPV = 7;                          // [2] multicast commit, per O: its last product of a fragment
+    static constexpr int kBarOEmpty = 9;                      // [MT] leader: live softmax warps, one phase per fragment
     static constexpr int kBarFull = 11;                       // [stages] local TMA
     static constexpr int kBarReady = kBarFull + kStages;      // [stages] leader: both CTAs
     static constexpr int kBarEmpty = kBarReady + kStages;     // [stages] multicast commit
     static constexpr int kNumBars = kBarEmpty + kStages;
     static constexpr int kSched = kBarOff + kNumBars * 8;
     static constexpr int kTmemSlot = kSched + 48;
-    static constexpr int kSmemBytes = kTmemSlot + 16 + 1024;
+    static constexpr int kStatsOff = kTmemSlot + 16;          // MT = 1: [2 fragments][2 warpgroups][128] (max, sum)
+    static constexpr int kSmemBytes = kStatsOff + (MT == 1 ? 4096 : 0) + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -134,6 +140,41 @@ __device__ __forceinline__ void pair_wait(uint32_t bar, uint32_t parity, const W
     }
 }
 
+// Columns [c0, c0 + 64) of a row from both warpgroups' outputs, w0 O_0 + w1 O_1 (a weight of
+// zero: that O may hold anything), finished or as a part of a cut unit's result.
+__device__ __forceinline__ void join_half(const CacheAttnParams &p, uint32_t lane_cols, float w0, float w1, bool whole,
+                                          bool row_ok, size_t row, int slot, int rc, int c0, float M, float L)
+{
+    const float inv = !whole ? 1.f : (L == 0.f) ? 0.f : 1.f / L;
+    if (row_ok && !whole && c0 == 0) p.ws_ml[(size_t)slot * p.rows_cap + rc] = make_float2(M, L);
+    uint4 *dst16 = reinterpret_cast<uint4 *>(p.out + row * DV + c0);
+    float4 *dst32 = reinterpret_cast<float4 *>(p.ws_o + (size_t)slot * p.rows_cap * DV) + (size_t)(c0 / 4) * p.rows_cap + rc;
+    w0 *= inv;
+    w1 *= inv;
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+        uint32_t a[16], b[16];
+        tmem_ld16(lane_cols + col_o(0) + 16 * ch, a);
+        tmem_ld16(lane_cols + col_o(1) + 16 * ch, b);
+        tmem_wait_ld();
+        float o[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            o[e] = (w0 == 0.f ? 0.f : w0 * __uint_as_float(a[e])) + (w1 == 0.f ? 0.f : w1 * __uint_as_float(b[e]));
+        if (row_ok && whole) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                dst16[2 * ch + q] =
+                    make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
+                               pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
+        } else if (row_ok) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                dst32[(size_t)(4 * ch + q) * p.rows_cap] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
+    }
+}
+
 template <int DQK, int MT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kThreads, 1)
     cache_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -158,11 +199,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
         mbar_init(bar(C::kBarQReady), 2);
         mbar_init(bar(C::kBarQEmpty), 1);
         for (int s = 0; s < 2; ++s) {
-            const int t = MT == 2 ? s : 0;
+            const int t = MT == 2 ? s : 0, live = live_warps(2 * t) + live_warps(2 * t + 1);
             mbar_init(bar(C::kBarSFull + s), 1);
-            mbar_init(bar(C::kBarPReady + s), live_warps(2 * t) + live_warps(2 * t + 1));
+            mbar_init(bar(C::kBarPReady + s), live);
             mbar_init(bar(C::kBarPV + s), 1);
-            mbar_init(bar(C::kBarOEmpty + s), live_warps(2 * t) + live_warps(2 * t + 1));
+            mbar_init(bar(C::kBarOEmpty + s), MT == 2 ? live : 2 * live);
         }
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(bar(C::kBarFull + s), 1);
@@ -195,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
 
     Walk walk(p, *sched);
     Frag f;
-    if (MT == 2 && warp >= C::kWarpTma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsCtl));
+    if (warp >= C::kWarpTma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsCtl));
     if (warp == C::kWarpTma) {
         // ------------------------------------------------------------ K and V (both CTAs, a half each)
         if (lane == 0) {
@@ -300,8 +341,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                         pair_wait(bar(C::kBarPReady + s), (MT == 2 ? g : g >> 1) & 1, p.wait, abort);
                         if (j == 0) pair_wait(bar(C::kBarOEmpty + t), (fi & 1) ^ 1, p.wait, abort);
                         tc_fence_after();
-                        issue_pv(t, s, st, j > 0);
-                        if (MT == 1 || !nxt) commit(C::kBarPV + t);
+                        // MT = 1: O s takes every other tile of the fragment
+                        issue_pv(s, s, st, j >= (MT == 2 ? 1 : 2));
+                        if (j + (MT == 2 ? 1 : 2) >= f.n) commit(C::kBarPV + s);
                         if (t == MT - 1) commit(C::kBarEmpty + st);
                         if (MT == 2 && nxt) {
                             if (t == 0) {
@@ -317,14 +359,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
         }
     } else if (warp < C::kWarpTma) {
         // ------------------------------------------------------------ softmax + epilogue (both CTAs)
-        if (MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
         const int t = warp >> 2;
-        const int T = 2 * t + rank;            // M tile of the row group
-        const int i = (warp & 3) * 32 + lane;  // its row == TMEM lane
+        const int T = MT == 2 ? 2 * t + rank : rank;  // M tile of the row group
+        const int i = (warp & 3) * 32 + lane;         // its row == TMEM lane
         if ((warp & 3) < live_warps(T)) {
             const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-            const uint32_t o_addr = lane_base + col_o(t);
-            int g = 0;
+            const uint32_t s_addr = lane_base + col_s(t), o_addr = lane_base + col_o(t);
+            int g = 0;   // tiles so far
+            int mine = 0;  // MT = 1: fragments so far that held a tile of this warpgroup
             for (int fi = 0; walk.next(p, f); ++fi) {
                 const int r = f.group * p.group + 128 * T + i;  // row of the KV head
                 const bool row_ok = r < p.R;                    // padding rows of the last M tile
@@ -332,26 +375,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                 const uint64_t drafts = draft_sight(p, f.b, row_ok ? r % p.T : 0, f.s.len, f.s.total, lo);
                 float m_run = -INFINITY, l_run = 0.f;
                 for (int j = 0; j < f.n; ++j, ++g) {
-                    const int s = MT == 2 ? t : (g & 1);
-                    pair_wait(bar(C::kBarSFull + s), (MT == 2 ? g : g >> 1) & 1, p.wait, abort);
+                    if (MT == 1 && (g & 1) != t) continue;
+                    pair_wait(bar(C::kBarSFull + t), (MT == 2 ? g : g >> 1) & 1, p.wait, abort);
                     tc_fence_after();
-                    // O's product of tile g - 1 must be done before O is touched.  With one S buffer a
-                    // tile these scores follow it; with two it is waited for, in every tile, so
-                    // that no phase of its barrier is skipped.
-                    softmax_tile<DV, false>(
-                        p, lane_base + col_s(s), o_addr, kKeys * (f.first + j), lo, f.s.len, drafts, m_run, l_run,
-                        nullptr,
-                        [&] { if (MT == 1 && g > 0) pair_wait(bar(C::kBarPV + t), (g - 1) & 1, p.wait, abort); });
+                    // O's last product came before the product that made these scores: O may be touched
+                    softmax_tile<DV, false>(p, s_addr, o_addr, kKeys * (f.first + j), lo, f.s.len, drafts, m_run, l_run,
+                                            nullptr, [] {});
                     __syncwarp();
-                    if (lane == 0) arrive_leader(bar(C::kBarPReady + s));
+                    if (lane == 0) arrive_leader(bar(C::kBarPReady + t));
                 }
-                pair_wait(bar(C::kBarPV + t), (MT == 1 ? g - 1 : fi) & 1, p.wait, abort);
-                tc_fence_after();
-                write_row<DV, false>(p, o_addr, f.head && f.tail, row_ok, (size_t)(f.b * p.H_kv + f.hk) * p.R + r,
-                                     2 * share + (f.head ? 1 : 0), 128 * T + i, m_run, l_run);
+                const bool whole = f.head && f.tail;
+                const size_t row = (size_t)(f.b * p.H_kv + f.hk) * p.R + r;
+                const int slot = 2 * share + (f.head ? 1 : 0), rc = 128 * T + i;
+                if (MT == 2) {
+                    pair_wait(bar(C::kBarPV + t), fi & 1, p.wait, abort);
+                    tc_fence_after();
+                    write_row<DV, false>(p, o_addr, whole, row_ok, row, slot, rc, m_run, l_run);
+                } else {
+                    if (f.n > 1 || ((g - 1) & 1) == t) {
+                        pair_wait(bar(C::kBarPV + t), mine & 1, p.wait, abort);
+                        ++mine;
+                    }
+                    float2 *stats = reinterpret_cast<float2 *>(smem + C::kStatsOff) + 256 * (fi & 1);
+                    stats[128 * t + i] = make_float2(m_run, l_run);
+                    tc_fence_before();
+                    named_bar_sync(1, 64 * live_warps(T));  // both warpgroups are done with the fragment's tiles
+                    tc_fence_after();
+                    const float2 other = stats[128 * (t ^ 1) + i];
+                    const float M = fmaxf(m_run, other.x);
+                    const float ws = m_run == -INFINITY ? 0.f : fast_exp2(m_run - M);
+                    const float wo = other.x == -INFINITY ? 0.f : fast_exp2(other.x - M);
+                    const float L = ws * l_run + wo * other.y;
+                    join_half(p, lane_base + 64 * t, t == 0 ? ws : wo, t == 0 ? wo : ws, whole, row_ok, row, slot, rc,
+                              64 * t, M, L);
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_leader(bar(C::kBarOEmpty + t));
+                if (lane == 0) arrive_leader(bar(C::kBarOEmpty + (MT == 2 ? t : 0)));
             }
         }
     }
@@ -371,7 +431,7 @@ cudaError_t launch_t(const CacheAttnLaunch &L, int pairs, cudaStream_t stream)
     using C = PairCfg<DQK, MT>;
     auto kernel = cache_pair_kernel<DQK, MT>;
     static KernelSetup setup;
-    const cudaError_t err = setup(kernel, C::kSmemBytes, MT == 2 ? C::kLaunchRegs : 0);
+    const cudaError_t err = setup(kernel, C::kSmemBytes, C::kLaunchRegs);
     if (err != cudaSuccess) return err;
     return launch_dependent(kernel, 2 * pairs, C::kThreads, C::kSmemBytes, stream, L.tm_q, L.tm_k, L.tm_v, L.p);
 }
