@@ -75,7 +75,7 @@ struct Seq {
     int cost;  // of a unit in the schedule: its tiles and kCacheUnitCost for its start; 1 when units stay whole
     __device__ __forceinline__ void load(const CacheAttnParams &p, int b)
     {
-        len = min(max(__ldg(p.lens + b), 0), p.S_cap);
+        len = min(max(p.lens[b], 0), p.S_cap);
         total = min(len + p.drafts, p.S_cap);
         const int lo = p.window > 0 ? max(0, len - p.window + 1) : 0;
         tile0 = lo / kCacheTileKeys;
