@@ -401,13 +401,17 @@ __device__ __forceinline__ void add_weights(const CacheAttnParams &p, long long 
     const int j0 = (int)(block % chunks) * kWeightKeys;
     const int j = j0 + 4 * threadIdx.x;
     const float *s = p.scores + (size_t)unit * p.G * p.S_pad + j;
-    // the first heads' scores are under way before the statistics that they wait for
+    // the first heads' scores and the sums are under way before the statistics that they wait for
     float4 x[kWeightHeads];
 #pragma unroll
     for (int g = 0; g < kWeightHeads; ++g) {
         x[g] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (g < p.G && j < p.S_pad) x[g] = *reinterpret_cast<const float4 *>(s + (size_t)g * p.S_pad);
     }
+    float *acc = p.acc + (size_t)unit * p.S_cap + j;
+    const bool wide = (reinterpret_cast<uintptr_t>(acc) & 15) == 0;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (wide && j + 4 <= p.S_cap) sum = *reinterpret_cast<const float4 *>(acc);
     const int len = min(max(p.lens[unit / p.H_kv], 0), p.S_cap);
     if (j0 >= len) return;
     const int2 c = p.units[unit];
@@ -442,14 +446,8 @@ __device__ __forceinline__ void add_weights(const CacheAttnParams &p, long long 
             if (g0 + kWeightHeads + g < p.G)
                 x[g] = *reinterpret_cast<const float4 *>(s + (size_t)(g0 + kWeightHeads + g) * p.S_pad);
     }
-    float *acc = p.acc + (size_t)unit * p.S_cap + j;
-    if (j + 4 <= len && (reinterpret_cast<uintptr_t>(acc) & 15) == 0) {
-        float4 a = *reinterpret_cast<float4 *>(acc);
-        a.x += w[0];
-        a.y += w[1];
-        a.z += w[2];
-        a.w += w[3];
-        *reinterpret_cast<float4 *>(acc) = a;
+    if (wide && j + 4 <= len) {
+        *reinterpret_cast<float4 *>(acc) = make_float4(sum.x + w[0], sum.y + w[1], sum.z + w[2], sum.w + w[3]);
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
