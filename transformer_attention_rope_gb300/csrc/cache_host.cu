@@ -146,7 +146,8 @@ apex_status apex_attn_rope(const apex_rope_tensor *q, const apex_rope_tensor *k,
         cudaDeviceGetAttribute(&sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return APEX_ERR_CUDA;
     // Heads per group: up to 8 share the sines of a unit; fewer when the tokens alone
-    // do not fill the GPU, down to one head a thread.
+    // do not fill the GPU, down to one head a thread.  8191 tokens of 136 heads: 130 us with 8,
+    // 149 with 4; 128 tokens of 48: 3.6 us with 1, 4.1 with 8; one token: 2.4 and 2.9.
     const long long units = (long long)B * S * (wide ? width / 8 : width);
     const long long bx = (units + kRopeThreads - 1) / kRopeThreads;
     const long long target = 4ll * sm_count;

@@ -14,6 +14,10 @@
 // position into its hole.  Sources and holes never meet, so the copies need no order
 // among themselves, and a cache slightly over its budget moves only the few rows
 // that are past it.
+//
+// Bound: latency of the search, about 2 us a digit and 4 for the two walks, then HBM for
+// the moves.  64 caches of 4224 rows cut to 4096: 12 us; 32 of 32768 rows cut to 4096 with
+// 110 MB moved: 38 us, 20 of them the moves at 5.5 TB/s.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
@@ -70,7 +74,8 @@ __device__ __forceinline__ void before_warp(Shared &sh, uint32_t c0, uint32_t c1
 
 // chunk: rows of a CTA; seg: rows of a warp, a multiple of 32 (chunk <= kWarps * seg).
 // ONE: seg <= kBlock, the rows are read once and kept; else they are read again, from
-// L2, in each of the six walks over them.
+// L2, in each of the six walks over them (64 caches of 4224 rows 12.0 us kept, 14.9 read
+// again; 32 of 32768 rows 37.8 and 41.6).
 template <bool ONE>
 __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p, int chunk, int seg)
 {

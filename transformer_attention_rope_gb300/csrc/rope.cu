@@ -11,7 +11,9 @@
 // A thread owns one unit of a token's row and walks over heads, so the sines and
 // cosines of the unit (4 or 8 pairs) are computed once per head group; a unit is
 // one 16-byte chunk (interleaved), or the two 16-byte chunks whose elements pair up
-// (half layout).  The bound is HBM: every row is read and written once.
+// (half layout).  The bound is HBM: every row is read and written once.  8191 tokens of
+// 128 + 8 heads of 192 entries (856 MB): 130 us, 6.6 TB/s; one token of 32 + 8 heads with its
+// key and value appended: 2.4 us.
 #include "device_common.cuh"
 #include "rope.h"
 
@@ -128,7 +130,8 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_consta
 }
 
 // The same for rows whose parts, strides or alignment do not fit 16-byte chunks: a
-// thread owns one pair, or one copied entry, and reads and writes 2 bytes at a time.
+// thread owns one pair, or one copied entry, and reads and writes 2 bytes at a time
+// (395 us on the 8191 tokens above, where the other kernel takes 130).
 __global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const __grid_constant__ RopeParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
