@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
                 // that no phase of its barrier is skipped.
                 softmax_tile<DV, WEIGHTS>(
                     p, s_addr, o_addr, key0, lo, f.s.len, drafts, m_run, l_run, row_ok ? scores : nullptr,
-                    [&] { if (MT == 1 && g > 0) mbar_wait(bar(C::kBarPV + t), (g - 1) & 1, p.wait); });
+                    [&] { if (MT == 1 && g > 0) mbar_wait(bar(C::kBarPV + t), (g - 1) & 1, p.wait); }, [] {});
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::kBarPReady + s));
             }

@@ -295,10 +295,10 @@ __device__ __forceinline__ void mend_v(const CacheAttnParams &p, const Frag &f, 
 // the sum of weights so far.  O (at o_addr) is rescaled only when the maximum grew by more
 // than 2^8: the final O / l does not depend on the reference point.  scores: where the
 // row's scores are kept, or NULL; wait_pv: waits until O may be touched.
-template <int DV, bool WEIGHTS, typename WaitPV>
+template <int DV, bool WEIGHTS, typename WaitPV, typename Half>
 __device__ __forceinline__ void softmax_tile(const CacheAttnParams &p, uint32_t s_addr, uint32_t o_addr, int key0,
                                              int lo, int len, uint64_t drafts, float &m_run, float &l_run,
-                                             float *scores, WaitPV wait_pv)
+                                             float *scores, WaitPV wait_pv, Half half_done)
 {
     uint32_t v[128];
 #pragma unroll
@@ -366,6 +366,7 @@ __device__ __forceinline__ void softmax_tile(const CacheAttnParams &p, uint32_t 
             pk[e2] = pack_bf16x2(p0, p1);  // the tensor cores take bf16; the sum keeps fp32
         }
         tmem_st16(s_addr + 16 * q4, pk);
+        if (q4 == 1) half_done();
     }
     {
         float a0, a1;

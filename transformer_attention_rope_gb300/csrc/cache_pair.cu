@@ -60,7 +60,8 @@ struct PairCfg {
     static constexpr int kBarPReady = 5;                      // [2] leader: live softmax warps, per S buffer
     static constexpr int kBarPV = 7;                          // [2] multicast commit, per O: its last product of a fragment
     static constexpr int kBarOEmpty = 9;                      // [MT] leader: live softmax warps, one phase per fragment
-    static constexpr int kBarFull = 11;                       // [stages] local TMA
+    static constexpr int kBarPHalf = 11;                      // [2] leader: the same, the first 64 keys' weights
+    static constexpr int kBarFull = 13;                       // [stages] local TMA
     static constexpr int kBarReady = kBarFull + kStages;      // [stages] leader: both CTAs
     static constexpr int kBarEmpty = kBarReady + kStages;     // [stages] multicast commit
     static constexpr int kNumBars = kBarEmpty + kStages;
@@ -207,6 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
             const int t = MT == 2 ? s : 0, live = live_warps(2 * t) + live_warps(2 * t + 1);
             mbar_init(bar(C::kBarSFull + s), 1);
             mbar_init(bar(C::kBarPReady + s), live);
+            mbar_init(bar(C::kBarPHalf + s), live);
             mbar_init(bar(C::kBarPV + s), 1);
             mbar_init(bar(C::kBarOEmpty + s), MT == 2 ? live : 2 * live);
         }
@@ -315,13 +317,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                 }
                 commit(C::kBarSFull + s);
             };
-            auto issue_pv = [&](int t, int s, int st, bool acc) {
-                const uint64_t dv = smem_desc_sw128(sb + C::kStageOff + st * C::kStage + C::kKTile, kQBox, 1024);
+            // half h of the tile's keys: the first can start while the softmax still works on the second
+            auto issue_pv = [&](int o, int s, int st, int h, bool acc) {
+                const uint64_t dv =
+                    smem_desc_sw128(sb + C::kStageOff + st * C::kStage + C::kKTile + h * 8192, kQBox, 1024);
                 if (one) {
 #pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i)
-                        mma_ts_pair(tmem + col_o(t), tmem + col_s(s) + 8 * i, dv + (uint64_t)(i * 2048 >> 4), idesc_pv,
-                                    (acc || i > 0) ? 1u : 0u);
+                    for (int i = 0; i < kKeys / 32; ++i)
+                        mma_ts_pair(tmem + col_o(o), tmem + col_s(s) + 32 * h + 8 * i, dv + (uint64_t)(i * 2048 >> 4),
+                                    idesc_pv, (acc || i > 0) ? 1u : 0u);
                 }
             };
             int g = 0;
@@ -343,11 +347,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
                         const int s = MT == 2 ? t : (g & 1);
-                        pair_wait(bar(C::kBarPReady + s), (MT == 2 ? g : g >> 1) & 1, p.wait, abort);
+                        const uint32_t ph = (MT == 2 ? g : g >> 1) & 1;
+                        pair_wait(bar(C::kBarPHalf + s), ph, p.wait, abort);
                         if (j == 0) pair_wait(bar(C::kBarOEmpty + t), (fi & 1) ^ 1, p.wait, abort);
                         tc_fence_after();
                         // MT = 1: O s takes every other tile of the fragment
-                        issue_pv(s, s, st, j >= (MT == 2 ? 1 : 2));
+                        issue_pv(s, s, st, 0, j >= (MT == 2 ? 1 : 2));
+                        pair_wait(bar(C::kBarPReady + s), ph, p.wait, abort);
+                        tc_fence_after();
+                        issue_pv(s, s, st, 1, true);
                         if (j + (MT == 2 ? 1 : 2) >= f.n) commit(C::kBarPV + s);
                         if (t == MT - 1) commit(C::kBarEmpty + st);
                         if (MT == 2 && nxt) {
@@ -385,7 +393,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                     tc_fence_after();
                     // O's last product came before the product that made these scores: O may be touched
                     softmax_tile<DV, false>(p, s_addr, o_addr, kKeys * (f.first + j), lo, f.s.len, drafts, m_run, l_run,
-                                            nullptr, [] {});
+                                            nullptr, [] {}, [&] {
+                                                tmem_wait_st();
+                                                tc_fence_before();
+                                                __syncwarp();
+                                                if (lane == 0) arrive_leader(bar(C::kBarPHalf + t));
+                                            });
                     __syncwarp();
                     if (lane == 0) arrive_leader(bar(C::kBarPReady + t));
                 }
