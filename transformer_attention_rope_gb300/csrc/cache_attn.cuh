@@ -294,7 +294,8 @@ __device__ __forceinline__ void mend_v(const CacheAttnParams &p, const Frag &f, 
 // the scores, relative to a running maximum in log2 units; m_run, l_run: that maximum and
 // the sum of weights so far.  O (at o_addr) is rescaled only when the maximum grew by more
 // than 2^8: the final O / l does not depend on the reference point.  scores: where the
-// row's scores are kept, or NULL; wait_pv: waits until O may be touched.
+// row's scores are kept, or NULL; wait_pv: waits until O may be touched;
+// half_done: called once the first 64 keys' weights are stored.
 template <int DV, bool WEIGHTS, typename WaitPV, typename Half>
 __device__ __forceinline__ void softmax_tile(const CacheAttnParams &p, uint32_t s_addr, uint32_t o_addr, int key0,
                                              int lo, int len, uint64_t drafts, float &m_run, float &l_run,

@@ -45,7 +45,7 @@ struct CacheAttnParams {
 // Which kernel, by the rows R = G * T of a KV head's queries.  Up to 128 rows: one M tile
 // on one CTA, bound by the cache's bytes.  More: pairs of CTAs that share each K/V tile,
 // with one M tile each up to 256 rows and two from there on, as the tensor cores read the
-// tile from shared memory once for both CTAs (256 rows, 8 x 8000 keys: 59 us on pairs, 72 on
+// tile from shared memory once for both CTAs (256 rows, 8 x 8000 keys: 57 us on pairs, 72 on
 // single CTAs with two M tiles; 1024 rows, 4 x 8192 keys: 99 and 107); d_v = 64, whose halves of a V tile would be
 // narrower than the 128-byte swizzle, stays on one CTA with two M tiles.
 inline bool cache_attn_pairs(int R, int d_v) { return R > 128 && d_v == 128; }

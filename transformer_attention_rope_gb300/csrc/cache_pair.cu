@@ -22,9 +22,9 @@
 // lanes), each warpgroup writing half of the columns.
 //
 // Bound: the softmax beside the products from 257 rows on -- 64 drafts on 128/8 heads over
-// 4 x 32768 keys 341 us, 1.61 PFLOP/s; over 4 x 4100 to 8192 keys 84 us with cut units
-// joined -- and HBM with the products below that: 256 rows over 8 x 8000 keys 59 us, 4.4
-// TB/s (65 us with one warpgroup).
+// 4 x 32768 keys 341 us, 1.61 PFLOP/s; over 4 x 4100 to 8192 keys 81 us with cut units
+// joined (84 before O += P V started on half a tile) -- and HBM with the products below
+// that: 256 rows over 8 x 8000 keys 57 us, 4.6 TB/s (65 us with one warpgroup).
 #include <math.h>
 
 #include "cache_attn.cuh"
