@@ -429,7 +429,7 @@ apex_status apex_attn_rope(const apex_rope_tensor *q, const apex_rope_tensor *k,
  *   q         [B, H_q,  T,     d_qk] bf16, read   (rotated)
  *   k_cache   [B, H_kv, S_cap, d_qk] bf16, read   (rotated; rows lens[b] + u: the drafts)
  *   v_cache   [B, H_kv, S_cap, d_v]  bf16, read
- *   out       [B, H_q,  T,     d_v]  bf16, written
+ *   out       [B, H_q,  T,     d_v]  bf16, written (must not overlap q or the caches)
  *   lens      [B] int32, device: cached keys before the drafts (taken as
  *             clamped to [0, S_cap]; rows at or past S_cap are not visible)
  *   tree_mask NULL (draft t sees the drafts u <= t), or uint64, device: bit u of
@@ -467,7 +467,7 @@ size_t apex_attn_tree_workspace_bytes(int B, int H_q, int H_kv, int T, int S_cap
  *
  *   q       [B, H_q,  1,     d_qk] bf16, read (rotated)
  *   k_cache [B, H_kv, S_cap, d_qk] bf16, v_cache [B, H_kv, S_cap, d_v] bf16, read
- *   out     [B, H_q,  1,     d_v]  bf16, written
+ *   out     [B, H_q,  1,     d_v]  bf16, written (must not overlap q or the caches)
  *   lens    [B] int32, device (taken as clamped to [0, S_cap]); 0 gives zeros
  *   acc     [B, H_kv, S_cap] fp32, read and written up to lens[b]; rows behind stay
  *   scale   as for apex_attn_tree_decode

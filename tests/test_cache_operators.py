@@ -91,6 +91,8 @@ ROPE = [  # B, S, Hq, Hkv, d, options
     (2, 40, 8, 2, 128, dict(yarn=16.0, fast=8.0, slow=2.0, half=True)),
     (1, 3, 40, 40, 256, dict(half=True)),
     (1, 2, 200, 100, 64, {}),                            # more heads than head groups
+    (1, 3, 2, 1, 1024, dict(d_rot=512, half=True, rot_start=256)),  # the widest row
+    (2, 2, 1, 1, 1024, dict(d_rot=510)),
 ]
 
 
@@ -409,6 +411,42 @@ def test_many_and_long_sequences(B, Hq, Hkv, T, d, cap):
 
 
 @pytest.mark.gpu
+def test_thousands_of_short_sequences():
+    dev = _gpu()
+    B, T, cap = 5000, 2, 5
+    lens = torch.randint(0, cap - T + 1, (B,), generator=torch.Generator().manual_seed(4)).to(torch.int32).to(dev)
+    g = _gen(dev, 70)
+    q, k, v = _normal(g, dev, B, 2, T, 64), _normal(g, dev, B, 1, cap, 64), _normal(g, dev, B, 1, cap, 64)
+    got = apex.tree_decode(q, k, v, lens)
+    some = [0, 1, 77, 2499, 4095, 4096, 4998, 4999]
+    ref, tol, _, _ = _attn_ref(q[some], k[some], v[some], lens[some].tolist(), True)
+    _close(got[some], ref, tol)
+    one = torch.arange(cap, device=dev) < (lens + T)[:, None]  # every row of a unit sums its weights to one
+    ones = torch.where(one[:, None, :, None], 1.0, float("nan")).to(torch.bfloat16).expand(B, 1, cap, 64).contiguous()
+    out = apex.tree_decode(q, k, ones, lens)
+    assert ((out.float() - 1).abs() <= 2 * U).all()
+    acc = torch.rand(B, 1, cap, generator=g, device=dev)
+    a, p, n = apex.evict(k, v, acc, lens + T, 3)
+    assert torch.equal(n, (lens + T).clamp(max=3))
+    kept = torch.where(one, acc[:, 0], -1.0).sort(-1, descending=True).values[:, :3].clamp(min=0).sort(-1).values
+    assert torch.equal(a[:, 0, :3].sort(-1).values, kept) and (a[:, 0, 3:] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,T,d", [(4, 3, 128), (16, 12, 128), (16, 40, 128), (16, 12, 64)])
+def test_a_query_that_is_not_finite_stays_alone(Hq, T, d):
+    dev = _gpu()
+    q, k, v, ln = _attn_inputs(dev, 80, Hq, 1, T, d, d, 800, [700])
+    q[0, 1, 1, 5] = float("nan")
+    got = apex.tree_decode(q, k, v, ln)
+    assert torch.isnan(got[0, 1, 1]).all()
+    q[0, 1, 1, 5] = 0.0
+    ref, tol, _, _ = _attn_ref(q, k, v, [700], True)
+    got[0, 1, 1] = ref[0, 1, 1].to(torch.bfloat16)
+    _close(got, ref, tol)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("seed", range(40))
 def test_random_configurations(seed):
     """Seeded draws over head groups, rows, lengths, windows and trees, on every kernel."""
@@ -496,6 +534,31 @@ def test_decode_weights_equals_tree_of_one_and_decode():
     dec = apex.decode(q, k, v, 1199, keys_prerotated=True)
     _close(apex.decode_weights(qr, k, v, ln, torch.zeros(2, 8, 1200, device=dev)).float() - dec.float() + ref.float(),
            ref, 3 * tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,d_r,window,yarn", [(64, 0, 0, 1.0), (128, 0, 100, 1.0), (128, 0, 0, 16.0), (128, 64, 0, 1.0)])
+def test_rope_and_tree_are_the_causal_block(d, d_r, window, yarn):
+    """Queries and keys rotated by rope, a chain of drafts over them: the last rows of the block's
+    prefill by the oracle, at the block's tolerance (Q and K rounded after the rotation)."""
+    import oracle
+    from transformer_attention_rope_gb300 import inputs
+    dev = _gpu()
+    B, Hq, Hkv, S, T = 2, 8, 2, 400, 12
+    q, k, v = inputs.make_qkv(B, Hq, Hkv, T, S, d, 77, **({"d_r": d_r} if d_r else {}))
+    how = dict(rot_start=d, d_rot=d_r) if d_r else {}
+    at = torch.arange(S, dtype=torch.int32, device=dev)
+    qr = apex.rope(q.to(dev), positions=at[S - T:], yarn_scale=yarn, **how)
+    kr = apex.rope(k.to(dev), positions=at, yarn_scale=yarn, **how)
+    scale = (0.1 * math.log(yarn) + 1.0) / math.sqrt(d + d_r) if yarn > 1 else None
+    got = apex.tree_decode(qr, kr, v.to(dev), torch.full((B,), S - T, dtype=torch.int32, device=dev), window=window,
+                           scale=scale)
+    if d_r:
+        ref = oracle.mla_attn(q, k, v, d_r, window=window, q_pos0=S - T)
+    else:
+        ref = oracle.attn(q, k, v, window=window, q_pos0=S - T, **({"yarn_s": yarn} if yarn > 1 else {}))
+    e = (got.double().cpu() - torch.as_tensor(ref)).abs()
+    assert e.max() <= 2e-2 and e.mean() <= 2e-3, (float(e.max()), float(e.mean()))
 
 
 # ------------------------------------------------------------------------------------------------- eviction

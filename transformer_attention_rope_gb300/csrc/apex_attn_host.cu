@@ -243,7 +243,11 @@ DeviceScope::DeviceScope() : status(APEX_ERR_CUDA)
     int dev;
     DeviceState *st = current_state(&dev);
     if (!st) return;
-    lock = std::unique_lock<std::mutex>(st->mu);
+    try {
+        lock = std::unique_lock<std::mutex>(st->mu);
+    } catch (...) {
+        return;  // no exception passes a C entry point
+    }
     status = init_device(*st, dev);
     if (status != APEX_OK) return;
     sm_count = st->sm_count;

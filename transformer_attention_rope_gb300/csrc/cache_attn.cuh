@@ -378,6 +378,13 @@ __device__ __forceinline__ void softmax_tile(const CacheAttnParams &p, uint32_t 
     tc_fence_before();
 }
 
+// A row's maximum once its tiles are done: -inf says that it saw nothing, which a row whose
+// scores are all NaN (a sum that is not zero) did not.
+__device__ __forceinline__ float row_max(float m_run, float l_run)
+{
+    return (m_run == -INFINITY && !(l_run == 0.f)) ? 0.f : m_run;
+}
+
 // The finished row (index `row` over all query rows), or its part of a cut unit's result:
 // row rc of the slot.  Partial outputs lie four entries at a time, rows adjacent, so that
 // the lanes' rows are written and read side by side.
@@ -386,7 +393,7 @@ __device__ __forceinline__ void write_row(const CacheAttnParams &p, uint32_t o_a
                                           size_t row, int slot, int rc, float m_run, float l_run)
 {
     const float inv = (l_run > 0.f) ? 1.f / l_run : 0.f;
-    if (row_ok && !whole) p.ws_ml[(size_t)slot * p.rows_cap + rc] = make_float2(m_run, l_run);
+    if (row_ok && !whole) p.ws_ml[(size_t)slot * p.rows_cap + rc] = make_float2(row_max(m_run, l_run), l_run);
     if (WEIGHTS && row_ok && whole) p.lse[row] = m_run + log2f(l_run);
     uint4 *dst16 = reinterpret_cast<uint4 *>(p.out + row * DV);
     uint4 *dst32 = reinterpret_cast<uint4 *>(p.ws_o + (size_t)slot * p.rows_cap * DV) + rc;

@@ -35,16 +35,21 @@ struct TurnSet {
     uint64_t turns[kRopeMaxPairs];
 };
 
-void turns_of(const RopeFreq &f, float linear, int d_rot, uint64_t *out)
+bool turns_of(const RopeFreq &f, float linear, int d_rot, uint64_t *out)
 {
     static std::mutex mu;
     static TurnSet sets[8];
     static int next = 0;
-    std::lock_guard<std::mutex> lk(mu);
+    std::unique_lock<std::mutex> lk(mu, std::defer_lock);
+    try {
+        lk.lock();
+    } catch (...) {
+        return false;  // no exception passes a C entry point
+    }
     for (const TurnSet &t : sets)
         if (t.d_rot == d_rot && t.f == f && t.linear == linear) {
             memcpy(out, t.turns, sizeof(uint64_t) * (d_rot / 2));
-            return;
+            return true;
         }
     TurnSet &t = sets[next];
     next = (next + 1) % 8;
@@ -57,6 +62,7 @@ void turns_of(const RopeFreq &f, float linear, int d_rot, uint64_t *out)
         t.turns[i] = (uint64_t)ldexp(turn, 64);
     }
     memcpy(out, t.turns, sizeof(uint64_t) * (d_rot / 2));
+    return true;
 }
 
 bool rope_tensor_ok(const apex_rope_tensor *t)
@@ -139,7 +145,7 @@ apex_status apex_attn_rope(const apex_rope_tensor *q, const apex_rope_tensor *k,
     p.d_rot = d_rot;
     p.half = half;
     p.sign = opt->inverse ? -1.f : 1.f;
-    turns_of(f, linear, d_rot, p.turns);
+    if (!turns_of(f, linear, d_rot, p.turns)) return APEX_ERR_CUDA;
 
     int sm_count = 0, dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -22,7 +22,7 @@
 // lanes), each warpgroup writing half of the columns.
 //
 // Bound: the softmax beside the products from 257 rows on -- 64 drafts on 128/8 heads over
-// 4 x 32768 keys 341 us, 1.61 PFLOP/s; over 4 x 4100 to 8192 keys 81 us with cut units
+// 4 x 32768 keys 330 us, 1.67 PFLOP/s; over 4 x 4100 to 8192 keys 81 us with cut units
 // joined (84 before O += P V started on half a tile) -- and HBM with the products below
 // that: 256 rows over 8 x 8000 keys 57 us, 4.6 TB/s (65 us with one warpgroup).
 #include <math.h>
@@ -414,6 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                         pair_wait(bar(C::kBarPV + t), mine & 1, p.wait, abort);
                         ++mine;
                     }
+                    m_run = row_max(m_run, l_run);
                     float2 *stats = reinterpret_cast<float2 *>(smem + C::kStatsOff) + 256 * (fi & 1);
                     stats[128 * t + i] = make_float2(m_run, l_run);
                     tc_fence_before();
