@@ -16,7 +16,7 @@
 // that are past it.
 //
 // Bound: latency of the search, about 2 us a digit and 4 for the two walks, then HBM for
-// the moves.  64 caches of 4224 rows cut to 4096: 12 us; 32 of 32768 rows cut to 4096 with
+// the moves.  64 caches of 4224 rows cut to 4096: 12.5 us; 32 of 32768 rows cut to 4096 with
 // 110 MB moved: 38 us, 20 of them the moves at 5.5 TB/s.
 #include <cooperative_groups.h>
 
@@ -41,6 +41,7 @@ struct Shared {
     uint32_t inbox[2][kMaxCluster][256];       // those of the whole cluster, by turns
     uint32_t warp[2][kWarps];
     uint32_t digit, above, equal;
+    int len, next;      // of the sequence, in the first CTA
     uint32_t count[2];  // this CTA's ties, then its holes and sources, for the cluster
 };
 
@@ -75,7 +76,7 @@ __device__ __forceinline__ void before_warp(Shared &sh, uint32_t c0, uint32_t c1
 // chunk: rows of a CTA; seg: rows of a warp, a multiple of 32 (chunk <= kWarps * seg).
 // ONE: seg <= kBlock, the rows are read once and kept; else they are read again, from
 // L2, in each of the six walks over them (64 caches of 4224 rows 12.0 us kept, 14.9 read
-// again; 32 of 32768 rows 37.8 and 41.6).
+// again, before one CTA read the length for all; 32 of 32768 rows 37.8 and 41.6).
 template <bool ONE>
 __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p, int chunk, int seg)
 {
@@ -87,13 +88,9 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < 4 * 256; i += kThreads) (&sh.hist[0][0])[i] = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int n = min(max(p.lens[b], 0), p.S_cap);
-    const int next = p.next_pos[b];
     const int lo = min(rank * chunk, p.S_cap), hi = min(lo + chunk, p.S_cap);
     const int wlo = min(lo + warp * seg, hi), whi = min(wlo + seg, hi);  // this warp's rows
-    const int wend = min(whi, n);                                       // those that hold a key
     const size_t base = (size_t)unit * p.S_cap;
-    const int out_len = min(n, p.budget);
 
     float w[kItems];
     int pos[kItems];
@@ -103,14 +100,11 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
             const int j = j0 + 32 * e + lane;
             w[e] = 0.f;
             pos[e] = j;
-            if (j < wend) {
+            if (j < whi) {
                 w[e] = p.acc[base + j];
                 if (p.positions) pos[e] = p.positions[base + j];
             }
         }
-    };
-    auto key = [&](int e) -> uint32_t {
-        return (pos[e] < p.n_sink || (long long)pos[e] >= (long long)next - p.n_recent) ? kMust : weight_key(w[e]);
     };
     // visit(j0) for the blocks of this warp's rows, in order
     auto blocks = [&](auto &&visit) {
@@ -125,11 +119,25 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
     };
     if (ONE) load(wlo);
 
+    // One CTA reads the length, so that the whole cluster walks the same path through its
+    // barriers; the rows are under way meanwhile.
+    if (rank == 0 && tid == 0) {
+        sh.len = p.lens[b];
+        sh.next = p.next_pos[b];
+    }
+    cluster.sync();  // every CTA runs, and its counts are clear
+    const int n = min(max(*cluster.map_shared_rank(&sh.len, 0), 0), p.S_cap);
+    const int next = *cluster.map_shared_rank(&sh.next, 0);
+    const int wend = min(whi, n);  // this warp's rows that hold a key
+    const int out_len = min(n, p.budget);
+    auto key = [&](int e) -> uint32_t {
+        return (pos[e] < p.n_sink || (long long)pos[e] >= (long long)next - p.n_recent) ? kMust : weight_key(w[e]);
+    };
+
     uint32_t cut = 0;      // the budget-th largest key
     uint32_t ties = 0;     // rows equal to it that are kept
     bool all_ties = true;  // every row equal to it is kept
     if (n > p.budget) {    // the same for the whole cluster
-        cluster.sync();    // every CTA of the cluster runs, and hist is clear
         uint32_t want = p.budget;  // rows to take from those that match the prefix
 #pragma unroll
         for (int pass = 0; pass < 4; ++pass) {
