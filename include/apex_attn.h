@@ -467,7 +467,7 @@ size_t apex_attn_tree_workspace_bytes(int B, int H_q, int H_kv, int T, int S_cap
  *
  *   q       [B, H_q,  1,     d_qk] bf16, read (rotated)
  *   k_cache [B, H_kv, S_cap, d_qk] bf16, v_cache [B, H_kv, S_cap, d_v] bf16, read
- *   out     [B, H_q,  1,     d_v]  bf16, written (must not overlap q or the caches)
+ *   out     [B, H_q,  1,     d_v]  bf16, written (must not overlap q, the caches or acc)
  *   lens    [B] int32, device (taken as clamped to [0, S_cap]); 0 gives zeros
  *   acc     [B, H_kv, S_cap] fp32, read and written up to lens[b]; rows behind stay
  *   scale   as for apex_attn_tree_decode

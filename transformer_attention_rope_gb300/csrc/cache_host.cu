@@ -16,11 +16,11 @@ namespace {
 
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Whether [a, a + n) and [b, b + n) share a byte (b may be NULL: no).
-bool overlap(const void *a, const void *b, size_t n)
+// Whether na bytes at a and nb at b share one (b may be NULL: no).
+bool overlap(const void *a, size_t na, const void *b, size_t nb)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return b && (x < y ? y - x : x - y) < n;
+    return b && (x < y ? y - x < na : x - y < nb);
 }
 
 // ----------------------------------------------------------------- rope
@@ -196,10 +196,10 @@ apex_status apex_attn_evict(void *k_cache, void *v_cache, int B, int H_kv, int S
     if (S_cap > kMaxSeq || (long long)B * H_kv > (1 << 24)) return APEX_ERR_UNSUPPORTED;
     // every CTA reads its inputs while others already write: no output may lie on an input
     const size_t row_bytes = (size_t)B * H_kv * S_cap * 4, seq_bytes = (size_t)B * 4;
-    if (overlap(acc_out, acc, row_bytes) || overlap(positions_out, positions, row_bytes) ||
-        overlap(acc_out, positions, row_bytes) || overlap(positions_out, acc, row_bytes) ||
-        overlap(acc_out, positions_out, row_bytes) || overlap(lens_out, lens, seq_bytes) ||
-        overlap(lens_out, next_pos, seq_bytes))
+    auto same_rows = [&](const void *a, const void *b) { return overlap(a, row_bytes, b, row_bytes); };
+    if (same_rows(acc_out, acc) || same_rows(positions_out, positions) || same_rows(acc_out, positions) ||
+        same_rows(positions_out, acc) || same_rows(acc_out, positions_out) ||
+        overlap(lens_out, seq_bytes, lens, seq_bytes) || overlap(lens_out, seq_bytes, next_pos, seq_bytes))
         return APEX_ERR_INVALID_ARG;
     if (d_k % 8 != 0 || d_v % 8 != 0 || d_k > 1024 || d_v > 1024) return APEX_ERR_UNSUPPORTED;
     const EvictWorkspace w = evict_workspace(B * H_kv, S_cap, budget);
@@ -262,6 +262,11 @@ static apex_status cache_attn(const void *q, const void *k_cache, const void *v_
     if (!isfinite(scale) || scale < 0.f || mask_stride < 0) return APEX_ERR_INVALID_ARG;
     apex_status s = check_cache_attn(B, H_q, H_kv, T, S_cap, d_qk, d_v);
     if (s != APEX_OK) return s;
+    // a CTA writes its rows while others still read theirs
+    const size_t rows = (size_t)B * H_q * T, keys = (size_t)B * H_kv * S_cap;
+    if (overlap(out, 2 * rows * d_v, q, 2 * rows * d_qk) || overlap(out, 2 * rows * d_v, k_cache, 2 * keys * d_qk) ||
+        overlap(out, 2 * rows * d_v, v_cache, 2 * keys * d_v) || (acc && overlap(out, 2 * rows * d_v, acc, 4 * keys)))
+        return APEX_ERR_INVALID_ARG;
     const CacheAttnWorkspace w = cache_attn_workspace(B, H_q, H_kv, T, S_cap, d_v, weights);
     if (workspace_bytes < w.bytes) return APEX_ERR_INVALID_ARG;
     DeviceScope dev;
