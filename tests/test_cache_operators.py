@@ -825,6 +825,43 @@ def test_two_streams_with_their_own_workspaces():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("op", ["rope", "tree", "weights", "evict"])
+def test_memory_freed_on_the_current_stream_is_not_written_from_another(op):
+    """A block freed while its stream still has a write to it ahead goes to that stream's next
+    tensor only: a call on another stream takes its output and workspace elsewhere."""
+    dev = _gpu()
+    q, k, v, ln = _attn_inputs(dev, 31, 8, 2, 1, 128, 128, 600, [600, 20])
+    acc, pos = torch.rand(2, 2, 600, device=dev), torch.zeros(2, 1, dtype=torch.int32, device=dev)
+    s = torch.cuda.Stream(dev)
+    own = [(acc.clone(), k.clone(), v.clone()) for _ in range(2)]  # what calls change
+
+    def call(stream):
+        a, kc, vc = own.pop()
+        if op == "rope":
+            return apex.rope(q, positions=pos, stream=stream)
+        if op == "tree":
+            return apex.tree_decode(q, k, v, ln, stream=stream)
+        if op == "weights":
+            return apex.decode_weights(q, k, v, ln, a, stream=stream)
+        return apex.evict(kc, vc, a, ln, 500, stream=stream)[0]
+
+    want = call(None)
+    sizes = [want.numel() * want.element_size(), apex.tree_workspace_bytes(2, 8, 2, 1, 600, 128),
+             apex.decode_weights_workspace_bytes(2, 8, 2, 600, 128), apex.evict_workspace_bytes(2, 2, 600, 500)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(int(1e8))
+    late = [torch.full((n,), 0xFF, dtype=torch.uint8, device=dev) for n in sizes for _ in range(4)]
+    taken = {t.data_ptr() for t in late}
+    del late
+    got = call(s)
+    assert got.data_ptr() not in taken
+    s.synchronize()
+    held = got.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(held, want)
+
+
+@pytest.mark.gpu
 def test_outputs_and_workspaces_stay_within_their_bounds():
     dev = _gpu()
     pad = 4096
@@ -905,7 +942,7 @@ def test_rope_refuses_rows_that_disagree(lib):
     assert apex.apex_attn_rope(_tensor(), _tensor(d_row=64), None, 1, 1, P, 1, None, 0, apex.RopeOptions(), None) == BAD
 
 
-ATTN_ARGS = dict(q=P, k=P, v=P, out=P, B=1, H_q=8, H_kv=2, T=4, S_cap=64, d_qk=128, d_v=128, lens=P, mask=None,
+ATTN_ARGS = dict(q=P, k=P, v=P, out=8 * P, B=1, H_q=8, H_kv=2, T=4, S_cap=64, d_qk=128, d_v=128, lens=P, mask=None,
                  stride=0, positions=None, window=0, scale=0.0, ws=P, n=1 << 40)
 
 
@@ -918,6 +955,8 @@ ATTN_ARGS = dict(q=P, k=P, v=P, out=P, B=1, H_q=8, H_kv=2, T=4, S_cap=64, d_qk=1
     (dict(B=65537), UNSUPPORTED), (dict(d_qk=64), UNSUPPORTED), (dict(d_qk=192, d_v=192), UNSUPPORTED),
     (dict(H_q=6), UNSUPPORTED), (dict(H_q=64), UNSUPPORTED), (dict(scale=float("inf")), BAD),
     (dict(scale=float("nan")), BAD), (dict(scale=-0.3), BAD), (dict(n=15), BAD),
+    # outputs (8192 bytes) on the queries, on the keys (32768 bytes), on the values
+    (dict(q=8 * P), BAD), (dict(q=8 * P + 8176), BAD), (dict(k=8 * P - 32752), BAD), (dict(v=8 * P + 16), BAD),
 ])
 def test_tree_decode_refuses(lib, o, code):
     a = dict(ATTN_ARGS)
@@ -933,7 +972,7 @@ def test_tree_decode_refuses(lib, o, code):
 @pytest.mark.parametrize("o,code", [
     (dict(acc=None), BAD), (dict(acc=P + 2), BAD), (dict(q=None), BAD), (dict(lens=None), BAD), (dict(B=0), BAD),
     (dict(H_kv=3), BAD), (dict(d_v=64), UNSUPPORTED), (dict(H_q=10), UNSUPPORTED), (dict(n=15), BAD),
-    (dict(scale=float("-inf")), BAD),
+    (dict(scale=float("-inf")), BAD), (dict(q=8 * P - 2032), BAD), (dict(acc=8 * P - 508), BAD),
 ])
 def test_decode_weights_refuses(lib, o, code):
     a = dict(ATTN_ARGS, acc=P)

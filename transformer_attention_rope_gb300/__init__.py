@@ -585,10 +585,14 @@ class _Launch:
             self.guard.__exit__(None, None, None)
 
     def new(self, like, shape, dtype):
-        """A tensor from torch's allocator, kept until the stream is done with it."""
-        t = _torch.empty(shape, dtype=dtype, device=like.device)
-        if self.stream is not None:
-            t.record_stream(self.stream)
+        """A tensor from torch's allocator: the launch stream's memory, as that of the current
+        one may still be in use there, kept until the current stream is done with it too."""
+        if self.stream is None:
+            return _torch.empty(shape, dtype=dtype, device=like.device)
+        now = _torch.cuda.current_stream(self.device)
+        with _torch.cuda.stream(self.stream):
+            t = _torch.empty(shape, dtype=dtype, device=like.device)
+        t.record_stream(now)
         return t
 
     def workspace(self, given, like, need):
