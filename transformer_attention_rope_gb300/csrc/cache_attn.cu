@@ -186,13 +186,13 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
         };
         int g = 0;
         for (int fi = 0; walk.next(p, f); ++fi) {
-            Mend mend;
             mbar_wait(bar(C::kBarQFull), fi & 1, p.wait);
             mbar_wait(bar(C::kBarKFull + g % C::kKStages), (g / C::kKStages) & 1, p.wait);
             tc_fence_after();
             for (int t = 0; t < MT; ++t) issue_qk(t, MT == 2 ? t : (g & 1), g % C::kKStages);
             commit(C::kBarKEmpty + g % C::kKStages);
             if (f.n == 1) commit(C::kBarQEmpty);
+            const Sight some(p, f);
             for (int j = 0; j < f.n; ++j, ++g) {
                 const int ks = (g + 1) % C::kKStages, vs = g % C::kVStages;
                 const bool nxt = j + 1 < f.n;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
                     if (j + 2 == f.n) commit(C::kBarQEmpty);
                 }
                 mbar_wait(bar(C::kBarVFull + vs), (g / C::kVStages) & 1, p.wait);
-                mend_v<C::kVBoxes>(p, f, mend, kKeys * (f.first + j), smem + C::kVOff + vs * C::kVTile);
+                mend_v<C::kVBoxes>(f, some, kKeys * (f.first + j), smem + C::kVOff + vs * C::kVTile);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     const int s = MT == 2 ? t : (g & 1);

@@ -253,30 +253,37 @@ __device__ __forceinline__ void tma_load_3d_policy(uint32_t dst, const CUtensorM
         : "memory");
 }
 
-// Zero the rows of a V tile in shared memory (NB boxes of [128 keys][64 entries]) whose
-// key no row of the unit sees; by one warp.  `any`: the drafts that some row sees, filled
-// on first use.
-struct Mend {
+// What some row of a unit sees: the drafts in `any` and the cached keys from `lo` on -- the
+// first that any draft's window reaches, which is past len - window + 1 when every draft's
+// position is past len.  Made once a fragment by one warp, while its first tile is on the way.
+struct Sight {
     uint64_t any;
-    bool known;
-    __device__ __forceinline__ Mend() : any(0), known(false) {}
+    int lo;
+    __device__ __forceinline__ Sight(const CacheAttnParams &p, const Frag &f) : any(0), lo(0)
+    {
+        // keys that every row sees, but for a window and the drafts
+        if (p.drafts == 0 || (p.window == 0 && kCacheTileKeys * (f.first + f.n) <= f.s.len)) return;
+        int first = f.s.len;
+        for (int t = threadIdx.x & 31; t < p.T; t += 32) {
+            int from;
+            any |= draft_sight(p, f.b, t, f.s.len, f.s.total, from);
+            first = min(first, from);
+        }
+        any = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)any) |
+              ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32);
+        lo = __reduce_min_sync(0xffffffffu, first);
+    }
 };
+
+// Zero the rows of a V tile in shared memory (NB boxes of [128 keys][64 entries]) whose
+// key no row of the unit sees; by one warp.
 template <int NB>
-__device__ __forceinline__ void mend_v(const CacheAttnParams &p, const Frag &f, Mend &m, int key0, uint8_t *tile)
+__device__ __forceinline__ void mend_v(const Frag &f, const Sight &some, int key0, uint8_t *tile)
 {
     const int lane = threadIdx.x & 31;
-    const int lo_all = p.window > 0 ? max(0, f.s.len - p.window + 1) : 0;
-    if (key0 >= lo_all && key0 + kCacheTileKeys <= f.s.len) return;
-    if (!m.known) {
-        int lo;
-        m.any = 0;
-        for (int t = lane; t < p.T && p.drafts; t += 32) m.any |= draft_sight(p, f.b, t, f.s.len, f.s.total, lo);
-        m.any = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)m.any) |
-                ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(m.any >> 32)) << 32);
-        m.known = true;
-    }
+    if (key0 >= some.lo && key0 + kCacheTileKeys <= f.s.len) return;
     uint32_t w[4];
-    sight_words(w, key0, lo_all, f.s.len, m.any);
+    sight_words(w, key0, some.lo, f.s.len, some.any);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (!((w[i] >> lane) & 1))

@@ -286,13 +286,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                                     f.group * p.group + 128 * (2 * t + rank), f.b * p.H_kv + f.hk);
             }
             __syncwarp();
+            const Sight some(p, f);
             pair_wait(bar(C::kBarQFull), fi & 1, p.wait, abort);
             if (lane == 0) arrive_leader(bar(C::kBarQReady));
-            Mend mend;
             for (int j = 0; j < f.n; ++j, ++g) {
                 const int st = g % C::kStages;
                 pair_wait(bar(C::kBarFull + st), (g / C::kStages) & 1, p.wait, abort);
-                mend_v<1>(p, f, mend, kKeys * (f.first + j), smem + C::kStageOff + st * C::kStage + C::kKTile);
+                mend_v<1>(f, some, kKeys * (f.first + j), smem + C::kStageOff + st * C::kStage + C::kKTile);
                 __syncwarp();
                 if (lane == 0) arrive_leader(bar(C::kBarReady + st));
             }
