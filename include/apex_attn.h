@@ -383,7 +383,10 @@ typedef struct apex_rope_options {
 
 /* One tensor of apex_attn_rope: rows of consecutive entries at in + b * in_b +
  * h * in_h + s * in_s (strides in elements, any order), written to out likewise.
- * out may be in with the same strides; otherwise the two must not overlap. */
+ * out may be in with the same strides (of k and v only without row0).  Otherwise no
+ * out may share an element with any in or other out of the call, the rows up to
+ * out_rows counted whole with row0, nor hold an element twice; views that interleave in
+ * one buffer do not. */
 typedef struct apex_rope_tensor {
     const void *in;
     void *out;

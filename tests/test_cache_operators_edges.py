@@ -56,3 +56,167 @@ def test_tree_decode_rows_before_every_window_may_hold_anything(Hq, Hkv, T, dk, 
     ref, tol, _, _ = _attn_ref(q, k, v, lens, True, mask, pos, window)
     _close(got, ref, tol)
     assert apex.apex_attn_device_status() == 0
+
+
+# ------------------------------------------------------------------------------------------------- rope: outputs on inputs
+@pytest.fixture(scope="module")
+def lib():
+    try:
+        return apex.load_library()
+    except RuntimeError:
+        pytest.skip("library not built")
+
+
+P = 1 << 20  # an aligned address that a refused call never touches
+BAD = 1
+
+
+def _rows(at, out, heads, d, strides, out_strides=None):
+    return apex.RopeTensor(at, out, heads, d, *strides, *(out_strides or strides))
+
+
+def _rope_status(q, k=None, v=None, B=2, S=4, row0=None, out_rows=0):
+    return apex.apex_attn_rope(q, k, v, B, S, P, S, row0, out_rows, apex.RopeOptions(), None)
+
+
+DENSE = (2 * 4 * 64, 4 * 64, 64)       # [2, 2, 4, 64]
+CACHE = (2 * 32 * 64, 32 * 64, 64)     # rows of [2, 2, 32, 64]
+
+
+@pytest.mark.parametrize("what", ["shifted by a row", "shifted by an entry", "transposed", "q on k", "k on v's input",
+                                  "one output for both", "in place with row0", "rows of the cache itself",
+                                  "v on the queries", "an output over itself", "one head's rows again"])
+def test_rope_refuses_outputs_that_other_threads_still_read(lib, what):
+    """One thread would write a row that another has not read, or has written."""
+    q = _rows(P, 2 * P, 2, 64, DENSE)
+    k = _rows(4 * P, 8 * P, 2, 64, DENSE, CACHE)
+    v = _rows(5 * P, 16 * P, 2, 64, DENSE, CACHE)
+    more = dict(row0=P, out_rows=32)
+    if what == "shifted by a row":
+        q, k, v, more = _rows(P, P + 2 * 64, 2, 64, DENSE), None, None, {}
+    elif what == "shifted by an entry":
+        q, k, v, more = _rows(P, P + 2, 2, 64, DENSE), None, None, {}
+    elif what == "transposed":
+        q, k, v, more = _rows(P, P, 2, 64, DENSE, (2 * 4 * 64, 64, 2 * 64)), None, None, {}
+    elif what == "q on k":
+        q.out = 4 * P + 2 * 1023  # the last entry of k
+    elif what == "k on v's input":
+        k.out = 5 * P
+    elif what == "one output for both":
+        v.out = 8 * P + 2 * 32 * 64
+    elif what == "in place with row0":
+        k = _rows(4 * P, 4 * P, 2, 64, DENSE)
+        more = dict(row0=P, out_rows=4)
+    elif what == "rows of the cache itself":
+        k = _rows(8 * P + 2 * 10 * 64, 8 * P, 2, 64, CACHE)
+    elif what == "v on the queries":
+        v.out = P
+    elif what == "an output over itself":
+        q, k, v, more = _rows(P, 2 * P, 2, 64, DENSE, (2 * 4 * 64, 32, 64)), None, None, {}
+    else:
+        q, k, v, more = _rows(P, 2 * P, 2, 64, DENSE, (2 * 4 * 64, 0, 64)), None, None, {}
+    assert _rope_status(q, k, v, **more) == BAD
+
+
+def test_rope_refuses_exactly_the_outputs_that_share_elements(lib):
+    """Random small layouts against their elements, listed one by one."""
+    if torch.cuda.is_available():
+        pytest.skip("calls that pass the checks would run on addresses that hold nothing")
+    import itertools
+    import random
+    r = random.Random(5)
+
+    def elements(at, heads, d, strides, S):
+        return [at // 2 + b * strides[0] + h * strides[1] + s * strides[2] + e
+                for b, h, s, e in itertools.product(range(2), range(heads), range(S), range(d))]
+
+    def layout(heads, d, S):
+        sizes, step, strides = [(0, 2), (1, heads), (2, S)], d, [0, 0, 0]
+        r.shuffle(sizes)
+        for i, n in sizes:
+            step += r.choice([0, 0, 0, d, 2 * d, 1, -1])
+            strides[i] = step * r.choice([1, 1, 1, 1, -1])
+            step *= n
+        return tuple(strides)
+
+    counts = [0, 0]
+    for trial in range(3000):
+        S, row0 = r.randint(1, 4), r.random() < 0.4
+        rows = S + r.randint(0, 3) if row0 else S
+        tensors = []
+        for i in range(3):
+            heads, d = r.randint(1, 3), r.choice([2, 4])
+            a = layout(heads, d, S)
+            o = a if r.random() < 0.5 else layout(heads, d, rows)
+            at = P + 2 * r.randint(0, 300)
+            tensors.append((at, at if r.random() < 0.3 else P + 2 * r.randint(0, 300), heads, d, a, o))
+        tensors = [t if r.random() < 0.7 else None for t in tensors]
+        if tensors[0] and tensors[1] and tensors[0][3] != tensors[1][3] or not any(tensors):
+            continue
+        ins = [t and elements(t[0], t[2], t[3], t[4], S) for t in tensors]
+        outs = [t and elements(t[1], t[2], t[3], t[5], rows if row0 and i else S) for i, t in enumerate(tensors)]
+        bad = False
+        for i, t in enumerate(tensors):
+            if not t:
+                continue
+            bad |= len(set(outs[i])) < len(outs[i])
+            bad |= any(set(outs[i]) & set(outs[k]) for k in range(i) if tensors[k])
+            for k in range(3):
+                if tensors[k] and not (k == i and outs[i] == ins[i] and not (row0 and i)):
+                    bad |= bool(set(outs[i]) & set(ins[k]))
+        args = [t and _rows(t[0], t[1], t[2], t[3], t[4], t[5]) for t in tensors]
+        status = _rope_status(*args, S=S, row0=P if row0 else None, out_rows=rows)
+        assert (status == BAD) == bad, (trial, tensors, S, row0, rows)
+        counts[bad] += 1
+    assert min(counts) > 200, counts
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("pad", [0, 1, 8])
+def test_rope_turns_the_parts_of_one_projection_in_place(half, pad):
+    """q and k interleaved in one buffer with v, both in place: their spans overlap, their elements do not."""
+    from test_cache_operators import _gen, _normal, _rope_close, _rope_ref
+    dev = _gpu()
+    g = _gen(dev, 90 + pad)
+    B, S, Hq, Hkv, d = 2, 9, 6, 2, 64
+    fused = _normal(g, dev, B, S, (Hq + 2 * Hkv) * d + pad)
+    before = fused.clone()
+    part = lambda x, a, n: x[..., a * d:(a + n) * d].view(B, S, n, d).transpose(1, 2)
+    q, k, v = part(fused, 0, Hq), part(fused, Hq, Hkv), part(fused, Hq + Hkv, Hkv)
+    pos = torch.randint(0, 999, (B, S), generator=g, device=dev, dtype=torch.int32)
+    how = dict(positions=pos, layout="half" if half else "interleaved")
+    q2, k2, v2 = apex.rope(q, k, v, q_out=q, k_out=k, **how)
+    assert q2 is q and k2 is k and torch.equal(v2, part(before, Hq + Hkv, Hkv))
+    for x, a, n in ((q, 0, Hq), (k, Hq, Hkv)):
+        _rope_close(x, *_rope_ref(part(before, a, n), pos, half=half))
+    assert torch.equal(fused[..., (Hq + Hkv) * d:], before[..., (Hq + Hkv) * d:])
+    with pytest.raises(apex.ApexError):
+        apex.rope(q, k, positions=pos, q_out=q, k_out=q[:, :Hkv])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("order", ["b s kv h", "b h s kv", "s b kv h", "kv b h s"])
+def test_rope_appends_to_caches_that_share_a_buffer(order):
+    """Keys and values side by side in one buffer, in any order of dimensions."""
+    from test_cache_operators import _gen, _normal, _rope_close, _rope_ref
+    dev = _gpu()
+    g = _gen(dev, 95)
+    size = dict(b=2, h=3, s=40, kv=2)
+    names = order.split()
+    buf = _normal(g, dev, *[size[n] for n in names], 64)
+    view = buf.permute(*[names.index(n) for n in ("kv", "b", "h", "s")], 4)
+    kc, vc = view[0], view[1]
+    before = kc.clone(), vc.clone()
+    S, row0 = 5, [0, 37]  # the second loses its last two rows
+    q, k, v = (_normal(g, dev, 2, h, S, 64) for h in (6, 3, 3))
+    pos = torch.randint(0, 999, (2, S), generator=g, device=dev, dtype=torch.int32)
+    apex.rope(q, k, v, positions=pos, k_out=kc, v_out=vc, row0=torch.tensor(row0, dtype=torch.int32, device=dev))
+    want, slack = _rope_ref(k, pos)
+    for b, r in enumerate(row0):
+        n = min(S, 40 - r)
+        _rope_close(kc[b, :, r:r + n], want[b, :, :n], slack[b, :, :n])
+        assert torch.equal(vc[b, :, r:r + n], v[b, :, :n])
+        for c, old in zip((kc, vc), before):
+            c[b, :, r:r + n] = old[b, :, r:r + n]
+    assert torch.equal(kc, before[0]) and torch.equal(vc, before[1])

@@ -646,9 +646,10 @@ def rope(q, k=None, v=None, *, positions, layout: str = "interleaved", rot_start
 
     layout: "interleaved" pairs (2i, 2i+1) or "half" pairs (i, i + d_rot/2) of the d_rot entries
     (None: all) from rot_start on; inverse: the opposite rotation, which is the gradient.
-    q_out, k_out, v_out: outputs of any strides, the inputs themselves among them; else new
-    contiguous tensors.  row0 [B] int32: token s of k and v goes to row row0[b] + s of k_out
-    and v_out (caches [B,H_kv,S_cap,d]); rows outside them are dropped, the others untouched."""
+    q_out, k_out, v_out: outputs of any strides, else new contiguous tensors.  An output may be
+    its own input (with row0: q's only) and must otherwise share no element with any input or
+    other output.  row0 [B] int32: token s of k and v goes to row row0[b] + s of k_out and v_out
+    (caches [B,H_kv,S_cap,d]); rows outside them are dropped, the others untouched."""
     torch = _torch or _load_torch()
     if layout != "interleaved" and layout != "half":
         raise ValueError("layout must be 'interleaved' or 'half'")

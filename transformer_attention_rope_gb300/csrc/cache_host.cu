@@ -70,6 +70,124 @@ bool rope_tensor_ok(const apex_rope_tensor *t)
     return t->in && t->out && t->n_heads > 0 && t->d_row > 0 && aligned(t->in, 2) && aligned(t->out, 2);
 }
 
+// Rows of a tensor: elements at + b * stride[0] + h * stride[1] + s * stride[2] + [0, d).
+struct RowSet {
+    __int128 at;
+    long long stride[3];
+    int count[3], d;
+};
+
+// The span of stride * x over the counts, from its least (negative strides) to its largest.
+void span_of(const RowSet &r, __int128 *lo, __int128 *hi)
+{
+    *lo = r.at;
+    *hi = r.at + r.d - 1;
+    for (int i = 0; i < 3; ++i) (r.stride[i] < 0 ? *lo : *hi) += (__int128)r.stride[i] * (r.count[i] - 1);
+}
+
+// Whether two sets of rows share an element (b == &a: whether two rows of a do).  That is a
+// sum of strides times bounded integers, the differences of the rows' indices, that falls
+// into the rows' lengths: searched from the largest stride down, where sums of the smaller
+// strides leave one or two candidates each in any layout of nested dimensions.  Layouts
+// that would take long to tell count as sharing.
+struct RowSearch {
+    struct Term {
+        __int128 stride, lo, hi;  // stride > 0, times an integer of [lo, hi]
+    } t[6];
+    __int128 least[7], most[7];  // sums of the terms from i on
+    int n = 0, left = 4096;
+    bool self;
+    void add(__int128 stride, __int128 lo, __int128 hi)
+    {
+        if (stride < 0)
+            t[n++] = Term{-stride, -hi, -lo};
+        else
+            t[n++] = Term{stride, lo, hi};
+    }
+    static __int128 floor_div(__int128 a, __int128 b) { return a / b - (a % b < 0 ? 1 : 0); }
+    bool search(int i, __int128 lo, __int128 hi, bool moved)  // a sum of the terms from i on in [lo, hi]
+    {
+        if (i == n) return lo <= 0 && hi >= 0 && (moved || !self);
+        const __int128 from = std::max(t[i].lo, -floor_div(-(lo - most[i + 1]), t[i].stride));
+        const __int128 to = std::min(t[i].hi, floor_div(hi - least[i + 1], t[i].stride));
+        for (__int128 x = from; x <= to; ++x) {
+            if (--left < 0) return true;
+            if (search(i + 1, lo - x * t[i].stride, hi - x * t[i].stride, moved || x != 0)) return true;
+        }
+        return false;
+    }
+};
+
+// Whether every dimension steps over all that the smaller ones reach: no element comes twice.
+bool nested(const RowSet &r)
+{
+    int by[3] = {0, 1, 2};
+    auto step = [&](int i) -> __int128 { return r.stride[i] < 0 ? -(__int128)r.stride[i] : r.stride[i]; };
+    std::sort(by, by + 3, [&](int x, int y) { return step(x) < step(y); });
+    __int128 reach = r.d;
+    for (int i : by) {
+        if (r.count[i] == 1) continue;
+        if (step(i) < reach) return false;
+        reach = step(i) * (r.count[i] - 1) + reach;
+    }
+    return true;
+}
+
+bool share_elements(const RowSet &a, const RowSet &b)
+{
+    RowSearch r;
+    r.self = &a == &b;
+    if (r.self && nested(a)) return false;
+    __int128 a0, a1, b0, b1;
+    span_of(a, &a0, &a1);
+    span_of(b, &b0, &b1);
+    if (a1 < b0 || b1 < a0) return false;
+    for (int i = 0; i < 3; ++i) {
+        const bool one = a.stride[i] == b.stride[i];
+        if (r.self && a.stride[i] == 0 && a.count[i] > 1) return true;
+        if (a.stride[i] != 0 && (one ? a.count[i] + b.count[i] > 2 : a.count[i] > 1))
+            r.add(a.stride[i], one ? 1 - b.count[i] : 0, a.count[i] - 1);
+        if (!one && b.stride[i] != 0 && b.count[i] > 1) r.add(b.stride[i], 1 - b.count[i], 0);
+    }
+    std::sort(r.t, r.t + r.n, [](const RowSearch::Term &x, const RowSearch::Term &y) { return x.stride > y.stride; });
+    r.least[r.n] = r.most[r.n] = 0;
+    for (int i = r.n - 1; i >= 0; --i) {
+        r.least[i] = r.least[i + 1] + r.t[i].stride * r.t[i].lo;
+        r.most[i] = r.most[i + 1] + r.t[i].stride * r.t[i].hi;
+    }
+    const __int128 apart = b.at - a.at;
+    return r.search(0, apart - (a.d - 1), apart + b.d - 1, false);
+}
+
+// Whether the tensors' outputs may be written while other threads still read or write: an
+// output shares no element with an input or another output, but for a tensor turned in
+// place (a thread reads the pairs that it writes; not with row0, which may shift rows).
+bool outputs_apart(const apex_rope_tensor *const (&t)[3], int B, int S, bool row0, int out_rows)
+{
+    RowSet in[3], out[3];
+    for (int i = 0; i < 3; ++i) {
+        if (!t[i]) continue;
+        in[i] = RowSet{(__int128)(reinterpret_cast<uintptr_t>(t[i]->in) / 2), {t[i]->in_b, t[i]->in_h, t[i]->in_s},
+                       {B, t[i]->n_heads, S}, t[i]->d_row};
+        out[i] = RowSet{(__int128)(reinterpret_cast<uintptr_t>(t[i]->out) / 2),
+                        {t[i]->out_b, t[i]->out_h, t[i]->out_s},
+                        {B, t[i]->n_heads, row0 && i > 0 ? out_rows : S}, t[i]->d_row};
+    }
+    for (int i = 0; i < 3; ++i) {
+        if (!t[i]) continue;
+        if (share_elements(out[i], out[i])) return false;
+        for (int k = 0; k < 3; ++k) {
+            if (!t[k]) continue;
+            if (k < i && share_elements(out[i], out[k])) return false;
+            bool in_place = k == i && in[i].at == out[i].at && !(row0 && i > 0);
+            for (int d = 0; d < 3; ++d)
+                in_place = in_place && (in[i].stride[d] == out[i].stride[d] || in[i].count[d] == 1);
+            if (!in_place && share_elements(out[i], in[k])) return false;
+        }
+    }
+    return true;
+}
+
 bool rows_of_16_bytes(const apex_rope_tensor *t)
 {
     const long long strides = t->in_b | t->in_h | t->in_s | t->out_b | t->out_h | t->out_s;
@@ -118,6 +236,7 @@ apex_status apex_attn_rope(const apex_rope_tensor *q, const apex_rope_tensor *k,
     for (int i = 0; i < 3; ++i)
         if (in[i] && (in[i]->d_row > 1024 || in[i]->n_heads > (1 << 20))) return APEX_ERR_UNSUPPORTED;
     if (d_rot > 2 * kRopeMaxPairs) return APEX_ERR_UNSUPPORTED;
+    if (!outputs_apart(in, B, S, row0 != nullptr, out_rows)) return APEX_ERR_INVALID_ARG;
     if (d_rot == 0) d_rot = 2;  // values alone: nothing turns
 
     RopeParams p;
