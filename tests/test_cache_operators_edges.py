@@ -220,3 +220,55 @@ def test_rope_appends_to_caches_that_share_a_buffer(order):
         for c, old in zip((kc, vc), before):
             c[b, :, r:r + n] = old[b, :, r:r + n]
     assert torch.equal(kc, before[0]) and torch.equal(vc, before[1])
+
+
+# ------------------------------------------------------------------------------------------------- rope: which kernel runs
+def _launched(call):
+    """(name, grid) of the kernels that `call` launches."""
+    import json
+    import os
+    import tempfile
+    from torch.profiler import ProfilerActivity, profile
+    call()
+    torch.cuda.synchronize()
+    found = []
+    for _ in range(3):  # a process's first records may be lost
+        with profile(activities=[ProfilerActivity.CPU, ProfilerActivity.CUDA]) as p:
+            call()
+            torch.cuda.synchronize()
+        with tempfile.TemporaryDirectory() as d:
+            at = os.path.join(d, "trace.json")
+            p.export_chrome_trace(at)
+            with open(at) as f:
+                events = json.load(f)["traceEvents"]
+        found = found or [(e["name"], e["args"]["grid"]) for e in events if e.get("cat") == "kernel"]
+    if not found:
+        pytest.skip("no kernel records from the profiler")
+    return found
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("half", [0, 1])
+@pytest.mark.parametrize("d,wide", [(128, True), (72, True), (66, False)])
+def test_rope_of_values_alone(d, wide, half):
+    """Values appended without queries and keys: rows of 16 bytes go 16 bytes at a time."""
+    from test_cache_operators import _gen, _normal
+    dev = _gpu()
+    g = _gen(dev, 97)
+    B, H, S, cap = 2, 3, 5, 20
+    v, vc = _normal(g, dev, B, H, S, d), _normal(g, dev, B, H, cap, d)
+    want = vc.clone()
+    want[0, :, 7:12], want[1, :, 17:20] = v[0], v[1, :, :3]
+    row0 = torch.tensor([7, 17], dtype=torch.int32, device=dev)
+    pos = torch.zeros(S, dtype=torch.int32, device=dev)
+    t = apex.RopeTensor(v.data_ptr(), vc.data_ptr(), H, d, *v.stride()[:3], *vc.stride()[:3])
+    opt = apex.RopeOptions(layout=half)
+
+    def call():
+        assert apex.apex_attn_rope(None, None, t, B, S, pos.data_ptr(), 0, row0.data_ptr(), cap, opt,
+                                   torch.cuda.current_stream(dev).cuda_stream) == 0
+
+    call()
+    assert torch.equal(vc, want)
+    names = [n for n, _ in _launched(call) if "rope" in n]
+    assert len(names) == 1 and ("rope_rows" in names[0]) == wide, names

@@ -237,12 +237,13 @@ apex_status apex_attn_rope(const apex_rope_tensor *q, const apex_rope_tensor *k,
         if (in[i] && (in[i]->d_row > 1024 || in[i]->n_heads > (1 << 20))) return APEX_ERR_UNSUPPORTED;
     if (d_rot > 2 * kRopeMaxPairs) return APEX_ERR_UNSUPPORTED;
     if (!outputs_apart(in, B, S, row0 != nullptr, out_rows)) return APEX_ERR_INVALID_ARG;
-    if (d_rot == 0) d_rot = 2;  // values alone: nothing turns
+    const bool turns = q || k;
+    if (d_rot == 0) d_rot = 2;  // values alone: nothing turns, and no frequency is used
 
     RopeParams p;
     memset(&p, 0, sizeof p);
     const bool half = opt->layout == APEX_ROPE_HALF;
-    bool wide = opt->rot_start % 8 == 0 && (half ? d_rot / 2 : d_rot) % 8 == 0;
+    bool wide = !turns || (opt->rot_start % 8 == 0 && (half ? d_rot / 2 : d_rot) % 8 == 0);
     int heads = 0, nt = 0, width = 0;
     for (int i = 0; i < 3; ++i) {
         if (!in[i]) continue;
