@@ -272,3 +272,20 @@ def test_rope_of_values_alone(d, wide, half):
     assert torch.equal(vc, want)
     names = [n for n, _ in _launched(call) if "rope" in n]
     assert len(names) == 1 and ("rope_rows" in names[0]) == wide, names
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,groups", [(32, 8, 48), (33, 8, 25), (24, 12, 48), (46, 1, 48), (48, 48, 48), (1, 1, 3)])
+def test_rope_of_one_token_spreads_its_heads(Hq, Hkv, groups):
+    """Few tokens: a head of q, k or v to a group as far as groups go, then two, and so on."""
+    from test_cache_operators import _gen, _normal, _rope_close, _rope_ref
+    dev = _gpu()
+    g = _gen(dev, Hq)
+    q, k, v = (_normal(g, dev, 1, h, 1, 128) for h in (Hq, Hkv, Hkv))
+    pos = torch.tensor([4321], dtype=torch.int32, device=dev)
+    got = apex.rope(q, k, v, positions=pos)
+    for x, y in zip((q, k), got):
+        _rope_close(y, *_rope_ref(x, pos[None]))
+    assert torch.equal(got[2], v)
+    grids = [at for n, at in _launched(lambda: apex.rope(q, k, v, positions=pos)) if "rope_rows" in n]
+    assert len(grids) == 1 and grids[0][1] == groups, grids

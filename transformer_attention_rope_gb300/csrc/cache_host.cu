@@ -271,14 +271,25 @@ apex_status apex_attn_rope(const apex_rope_tensor *q, const apex_rope_tensor *k,
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return APEX_ERR_CUDA;
-    // Heads per group: up to 8 share the sines of a unit; fewer when the tokens alone
-    // do not fill the GPU, down to one head a thread.  8191 tokens of 136 heads: 130 us with 8,
-    // 149 with 4; 128 tokens of 48: 3.6 us with 1, 4.1 with 8; one token: 2.4 and 2.9.
+    // Heads per group: a thread's heads share the sines of a unit, but with few tokens one
+    // block an SM is what there is to gain from fewer.  Up to 4 heads, whose loads are in
+    // flight together, and 8 once that many still leave a block for every SM (times with
+    // 1 / 2 / 4 / 8 heads, 32 + 8 + 8 heads of 128, interleaved): one token 2.2 / 2.2 / 2.2 / 2.7 us,
+    // 32 tokens 2.4 / 2.5 / 2.7 / 3.2, 64 tokens 3.2 / 2.5 / 2.7 / 3.2, 8 x 16 tokens
+    // 3.7 / 3.2 / 2.7 / 3.2, 256 tokens 5.6 / 4.0 / 3.6 / 3.3 (half layout 4.2 / 3.6 / 3.2 / 4.1),
+    // 2048 tokens 29 / 16 / 10 / 8; 8191 tokens of 136 heads of 192: 4 heads 149, 8 heads 130.
     const long long units = (long long)B * S * (wide ? width / 8 : width);
     const long long bx = (units + kRopeThreads - 1) / kRopeThreads;
-    const long long target = 4ll * sm_count;
-    int per = (int)std::min<long long>(8, std::max<long long>(1, bx * heads / target));
-    per = std::max(per, (heads + kRopeMaxGroups - 4) / (kRopeMaxGroups - 3));
+    const long long share = (bx * heads + sm_count - 1) / sm_count;
+    int per = share >= 8 ? 8 : (int)std::min<long long>(4, share);
+    auto groups = [&](int n) {  // n heads each
+        int sum = 0;
+        for (int i = 0; i < 3; ++i)
+            if (in[i]) sum += (in[i]->n_heads + n - 1) / n;
+        return sum;
+    };
+    per = std::max(per, heads / kRopeMaxGroups);
+    while (groups(per) > kRopeMaxGroups) ++per;
     for (int i = 0, k = 0; i < 3; ++i) {
         if (!in[i]) continue;
         for (int h = 0; h < in[i]->n_heads; h += per)
