@@ -504,7 +504,8 @@ size_t apex_attn_decode_weights_workspace_bytes(int B, int H_q, int H_kv, int S_
  *   acc_out, positions_out  the same shapes, written whole, in the new row order, with
  *                       0 and -1 from row min(lens[b], budget) on; must not overlap
  *                       acc, positions
- *   lens, next_pos      [B] int32; next_pos NULL: lens
+ *   lens, next_pos      [B] int32; next_pos NULL: lens, or one past the largest of the
+ *                       head's positions where that is more (a cache that was cut before)
  *   lens_out            [B] int32, written: min(lens[b], budget); not lens, not next_pos
  *   budget >= 1, n_sink, n_recent >= 0, n_sink + n_recent <= budget
  *   workspace           at least apex_attn_evict_workspace_bytes(...) bytes, as above

@@ -289,3 +289,65 @@ def test_rope_of_one_token_spreads_its_heads(Hq, Hkv, groups):
     assert torch.equal(got[2], v)
     grids = [at for n, at in _launched(lambda: apex.rope(q, k, v, positions=pos)) if "rope_rows" in n]
     assert len(grids) == 1 and grids[0][1] == groups, grids
+
+
+# ------------------------------------------------------------------------------------------------- evict
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap,lens,budget,sink,recent", [
+    (300, [300, 250, 0], 200, 4, 20), (300, [300, 290], 64, 0, 0), (5000, [5000, 4300], 600, 4, 64),
+    (40000, [40000], 3000, 7, 100)])
+def test_evict_finds_the_newest_position_of_a_cache_that_was_cut_before(cap, lens, budget, sink, recent):
+    """Without next_pos the newest rows are those behind the largest position, not behind the length:
+    positions far past the lengths would all count as new, and the lowest rows stay whatever their weights."""
+    from test_cache_operators import _evict_check, _evict_ref, _gen, _normal
+    dev = _gpu()
+    g = _gen(dev, cap + budget)
+    B, H = len(lens), 2
+    k, v = _normal(g, dev, B, H, cap, 8), _normal(g, dev, B, H, cap, 8)
+    acc = torch.exp(torch.randn(B, H, cap, generator=g, device=dev))
+    pos = (torch.rand(B, H, cap, generator=g, device=dev).argsort(-1) * 3 + cap).to(torch.int32).contiguous()
+    for head in range(H):  # the heads' newest rows differ
+        pos[:, head, ::7] += 5 * head
+    wants = []
+    for head in range(H):
+        own = [int(pos[b, head, :n].max()) + 1 if n else 0 for b, n in enumerate(lens)]
+        one = slice(head, head + 1)
+        wants.append(_evict_ref(k[:, one], v[:, one], acc[:, one], lens, budget, sink, recent, pos[:, one], own))
+    ln = torch.tensor(lens, dtype=torch.int32, device=dev)
+    a, p, n = apex.evict(k, v, acc, ln, budget, n_sink=sink, n_recent=recent, positions=pos)
+    for head in range(H):
+        want = wants[head]
+        assert torch.equal(p[:, head].cpu(), want[3][:, 0]) and n.tolist() == want[4]
+        assert torch.equal(a[:, head].double().cpu(), want[2][:, 0])
+        assert torch.equal(k[:, head].cpu(), want[0][:, 0]) and torch.equal(v[:, head].cpu(), want[1][:, 0])
+    # rows in order, none cut before: the length, as without positions
+    k, v = _normal(g, dev, B, H, cap, 8), _normal(g, dev, B, H, cap, 8)
+    rows = torch.arange(cap, dtype=torch.int32, device=dev).expand(B, H, cap).contiguous()
+    k2, v2 = k.clone(), v.clone()
+    got = apex.evict(k, v, acc, ln, budget, n_sink=sink, n_recent=recent, positions=rows)
+    want = apex.evict(k2, v2, acc, ln, budget, n_sink=sink, n_recent=recent)
+    assert all(torch.equal(x, y) for x, y in zip((*got, k, v), (*want, k2, v2)))
+
+
+@pytest.mark.gpu
+def test_evict_newest_position_at_the_ends_of_the_range():
+    """Positions up to the largest integer, and negative ones alone."""
+    from test_cache_operators import _evict_check, _gen, _normal
+    dev = _gpu()
+    g = _gen(dev, 7)
+    for top in (2 ** 31 - 1, 40, -3):
+        k, v = _normal(g, dev, 1, 1, 60, 8), _normal(g, dev, 1, 1, 60, 8)
+        acc = torch.rand(1, 1, 60, generator=g, device=dev)
+        pos = (top - torch.randperm(60, generator=g, device=dev)).to(torch.int32).view(1, 1, 60)
+        nxt = max(60, top + 1)
+        if nxt < 2 ** 31:
+            _evict_check(dev, k.clone(), v.clone(), acc, [60], 20, 0, 9, pos, [nxt])
+            b = apex.evict(k.clone(), v.clone(), acc, torch.tensor([60], dtype=torch.int32, device=dev), 20,
+                           n_recent=9, positions=pos, next_pos=torch.tensor([nxt], dtype=torch.int32, device=dev))
+        else:  # the same with positions moved down
+            b = apex.evict(k.clone(), v.clone(), acc, torch.tensor([60], dtype=torch.int32, device=dev), 20,
+                           n_recent=9, positions=pos - 1000, next_pos=torch.tensor([nxt - 1000], dtype=torch.int32,
+                                                                                   device=dev))
+            b = (b[0], torch.where(b[1] >= 0, b[1] + 1000, b[1]), b[2])
+        a = apex.evict(k, v, acc, torch.tensor([60], dtype=torch.int32, device=dev), 20, n_recent=9, positions=pos)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))

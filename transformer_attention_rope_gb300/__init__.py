@@ -798,7 +798,8 @@ def evict(k_cache, v_cache, acc, lens, budget: int, *, n_sink: int = 0, n_recent
           next_pos=None, acc_out=None, positions_out=None, lens_out=None, workspace=None, stream=None):
     """Cut each (sequence, KV head) of a cache to `budget` rows, in place: the first n_sink and last n_recent
     positions, then the largest acc. caches [B,H_kv,S_cap,d], acc [B,H_kv,S_cap] fp32, lens [B] int32,
-    positions [B,H_kv,S_cap] int32 (None: the row index), next_pos [B] int32 (None: lens)
+    positions [B,H_kv,S_cap] int32 (None: the row index), next_pos [B] int32 (None: lens, or one past
+    the largest of the head's positions where that is more)
     -> (acc_out, positions_out, lens_out), in the new order of rows."""
     torch = _torch or _load_torch()
     B, H_kv, S_cap, d_k = _rows4(k_cache, "k_cache")

@@ -345,6 +345,7 @@ apex_status apex_attn_evict(void *k_cache, void *v_cache, int B, int H_kv, int S
     p.positions = positions;
     p.lens = lens;
     p.next_pos = next_pos ? next_pos : lens;
+    p.newest = positions && !next_pos;
     p.acc_out = acc_out;
     p.positions_out = positions_out;
     p.lens_out = lens_out;

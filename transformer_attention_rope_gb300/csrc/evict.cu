@@ -19,6 +19,7 @@
 // the moves.  64 caches of 4224 rows cut to 4096: 12.5 us; 32 of 32768 rows cut to 4096 with
 // 110 MB moved: 38 us, 20 of them the moves at 5.5 TB/s.
 #include <cooperative_groups.h>
+#include <limits.h>
 
 #include "device_common.cuh"
 #include "evict.h"
@@ -42,6 +43,7 @@ struct Shared {
     uint32_t warp[2][kWarps];
     uint32_t digit, above, equal;
     int len, next;      // of the sequence, in the first CTA
+    int top[kWarps];    // the largest position of each warp's rows
     uint32_t count[2];  // this CTA's ties, then its holes and sources, for the cluster
 };
 
@@ -127,17 +129,31 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
     }
     cluster.sync();  // every CTA runs, and its counts are clear
     const int n = min(max(*cluster.map_shared_rank(&sh.len, 0), 0), p.S_cap);
-    const int next = *cluster.map_shared_rank(&sh.next, 0);
+    long long next = *cluster.map_shared_rank(&sh.next, 0);
     const int wend = min(whi, n);  // this warp's rows that hold a key
     const int out_len = min(n, p.budget);
     auto key = [&](int e) -> uint32_t {
-        return (pos[e] < p.n_sink || (long long)pos[e] >= (long long)next - p.n_recent) ? kMust : weight_key(w[e]);
+        return (pos[e] < p.n_sink || pos[e] >= next - p.n_recent) ? kMust : weight_key(w[e]);
     };
 
     uint32_t cut = 0;      // the budget-th largest key
     uint32_t ties = 0;     // rows equal to it that are kept
     bool all_ties = true;  // every row equal to it is kept
     if (n > p.budget) {    // the same for the whole cluster
+        if (p.newest) {  // positions without next_pos: one past the largest, lens where that is more
+            int top = INT_MIN;
+            blocks([&](int j0) {
+#pragma unroll
+                for (int e = 0; e < kItems; ++e)
+                    if (j0 + 32 * e + lane < wend) top = max(top, pos[e]);
+            });
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (lane == 0) sh.top[warp] = top;
+            cluster.sync();  // read by every CTA; not written again
+            for (int i = lane; i < cs * kWarps; i += 32)
+                top = max(top, *cluster.map_shared_rank(&sh.top[i % kWarps], i / kWarps));
+            next = max(next, 1ll + __reduce_max_sync(0xffffffffu, top));
+        }
         uint32_t want = p.budget;  // rows to take from those that match the prefix
 #pragma unroll
         for (int pass = 0; pass < 4; ++pass) {

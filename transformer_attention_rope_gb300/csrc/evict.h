@@ -15,6 +15,7 @@ struct EvictParams {
     const float *acc;
     const int *positions;  // NULL: row index
     const int *lens, *next_pos;
+    int newest;  // next_pos holds lens: the rows' positions may be past it
     float *acc_out;
     int *positions_out;
     int *lens_out;
