@@ -351,3 +351,33 @@ def test_evict_newest_position_at_the_ends_of_the_range():
             b = (b[0], torch.where(b[1] >= 0, b[1] + 1000, b[1]), b[2])
         a = apex.evict(k, v, acc, torch.tensor([60], dtype=torch.int32, device=dev), 20, n_recent=9, positions=pos)
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# ------------------------------------------------------------------------------------------------- sizes that do not fit
+@pytest.mark.parametrize("o", [dict(budget=2 ** 32 + 2), dict(budget=2 ** 31), dict(budget=-2 ** 32 + 2),
+                               dict(budget=2, n_sink=2 ** 32), dict(budget=2, n_recent=2 ** 32 + 1)])
+def test_evict_refuses_sizes_that_do_not_fit_an_int(lib, o):
+    """Cut to 32 bits, a budget of 2^32 + 2 would leave two rows of each cache."""
+    x = torch.zeros(1, 2, 3, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        apex.evict(x, x, torch.zeros(1, 2, 3), torch.zeros(1, dtype=torch.int32), **o)
+
+
+@pytest.mark.gpu
+def test_sizes_that_do_not_fit_an_int():
+    dev = _gpu()
+    q, k, v, ln = _attn_inputs(dev, 3, 8, 2, 4, 128, 128, 304, [300, 290])
+    whole = apex.tree_decode(q, k, v, ln)
+    for window in (-5, -2 ** 32 + 7, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 7, 2 ** 63):
+        assert torch.equal(apex.tree_decode(q, k, v, ln, window=window), whole)
+    assert not torch.equal(apex.tree_decode(q, k, v, ln, window=7), whole)
+    acc, kept = torch.rand(2, 2, 304, device=dev), k.clone()
+    with pytest.raises(ValueError):
+        apex.evict(k, v, acc, ln, 2 ** 32 + 4)
+    assert torch.equal(k, kept)
+    pos = torch.zeros(4, dtype=torch.int32, device=dev)
+    for o in (dict(d_rot=2 ** 32 + 64), dict(rot_start=2 ** 32), dict(rot_start=0.5)):
+        with pytest.raises(ValueError):
+            apex.rope(q, positions=pos, **o)
+    with pytest.raises(apex.ApexError):  # an infinity in 32 bits
+        apex.rope(q, positions=pos, rope_base=1e39)

@@ -533,6 +533,9 @@ def _load_torch():
     return torch
 
 
+_INT_MIN, _INT_MAX = -2 ** 31, 2 ** 31 - 1  # of the C interface: ctypes drops what does not fit
+
+
 def _refuse(t, name, dtype, shape, device):
     torch = _torch
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
@@ -628,6 +631,8 @@ def _rope_rows(x, out, name, B, S, into, device):
         raise ValueError("%s must have the batch and length of q" % name)
     if (to != xs and not into) or to[0] != B or to[1] != xs[1] or to[3] != xs[3]:
         raise ValueError("%s_out does not fit %s" % (name, name))
+    if xs[1] > _INT_MAX or xs[3] > _INT_MAX:
+        raise ValueError("%s has more heads or entries than rope takes" % name)
     xb, xh, xr, xe = x.stride()
     ob, oh, orow, oe = out.stride()
     if (xe != 1 or oe != 1) and xs[3] > 1:
@@ -660,9 +665,14 @@ def rope(q, k=None, v=None, *, positions, layout: str = "interleaved", rot_start
     if k is None and (v is not None or k_out is not None) or v is None and v_out is not None:
         raise ValueError("k_out goes with k, and v and v_out with k")
     B, _, S, _ = _rows4(q, "q")
+    if B > _INT_MAX or S > _INT_MAX or k_out is not None and k_out.shape[2] > _INT_MAX:
+        raise ValueError("more sequences, tokens or rows than rope takes")
     device = q.get_device()
-    opt = _rope_options(1 if layout == "half" else 0, rot_start, d_rot, 1 if inverse else 0, rope_base, linear_scale,
-                        yarn_scale, yarn_beta_fast, yarn_beta_slow)
+    try:
+        opt = _rope_options(1 if layout == "half" else 0, rot_start, d_rot, 1 if inverse else 0, rope_base,
+                            linear_scale, yarn_scale, yarn_beta_fast, yarn_beta_slow)
+    except struct.error as e:
+        raise ValueError("rope's options: %s" % e) from None
     at = _Launch(device, stream)
     try:
         pos = _fit(positions, "positions", torch.int32, (S,) if positions.dim() == 1 else (B, S), device)
@@ -728,6 +738,8 @@ def tree_decode(q, k_cache, v_cache, lens, *, tree_mask=None, positions=None, wi
     torch = _torch or _load_torch()
     B, H_q, T, d_qk, H_kv, S_cap, d_v, device, pq, pk, pv = _cache_shapes(q, k_cache, v_cache)
     plens = _fit(lens, "lens", torch.int32, (B,), device)
+    if not 0 < window <= _INT_MAX:  # positions are int32: a wider window is none
+        window = 0
     pmask = ppos = None
     stride = 0
     if tree_mask is not None:
@@ -802,7 +814,12 @@ def evict(k_cache, v_cache, acc, lens, budget: int, *, n_sink: int = 0, n_recent
     the largest of the head's positions where that is more)
     -> (acc_out, positions_out, lens_out), in the new order of rows."""
     torch = _torch or _load_torch()
+    for n, x in (("budget", budget), ("n_sink", n_sink), ("n_recent", n_recent)):
+        if not _INT_MIN <= x <= _INT_MAX:
+            raise ValueError("%s must fit 32 bits" % n)
     B, H_kv, S_cap, d_k = _rows4(k_cache, "k_cache")
+    if B > _INT_MAX or H_kv > _INT_MAX or S_cap > _INT_MAX:
+        raise ValueError("more sequences, heads or rows than evict takes")
     d_v = _rows4(v_cache, "v_cache")[3]
     device = k_cache.get_device()
     rows = (B, H_kv, S_cap)
