@@ -28,6 +28,7 @@
 #include <math.h>
 
 #include "cache_attn.cuh"
+#include "pair_common.cuh"
 
 namespace apex {
 namespace {
@@ -74,77 +75,6 @@ struct PairCfg {
 
 __device__ __forceinline__ uint32_t col_s(int s) { return 128u * s; }
 __device__ __forceinline__ uint32_t col_o(int t) { return 256u + 128u * t; }
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Arrive on the barrier at the same shared-memory offset in the leader CTA.
-__device__ __forceinline__ void arrive_leader(uint32_t local_bar)
-{
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_bar), "r"(0));
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
-}
-
-__device__ __forceinline__ void commit_pair(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                     bar),
-                 "h"((uint16_t)3)
-                 : "memory");
-}
-
-__device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                            uint32_t acc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
-// Bounded wait; after one time-out of the CTA (abort flag) later waits that do not
-// complete at once give up at their first timer check, so a broken pipeline drains in
-// about one time-out.
-__device__ __forceinline__ void pair_wait(uint32_t bar, uint32_t parity, const WaitCtl &wc, volatile uint32_t *abort)
-{
-    if (mbar_try_wait(bar, parity)) return;
-    uint64_t t0 = 0;
-    for (uint32_t n = 1;; ++n) {
-        if (mbar_try_wait(bar, parity)) return;
-        if ((n & 255u) == 0) {
-            if (*abort) return;
-            const uint64_t now = global_timer_ns();
-            if (t0 == 0) {
-                t0 = now;
-            } else if (now - t0 > wc.timeout_ns) {
-                *abort = 1u;
-                report_status(wc.status, kStatusWaitTimeout);
-                return;
-            }
-        }
-    }
-}
 
 // Columns [c0, c0 + 64) of a row from both warpgroups' outputs, w0 O_0 + w1 O_1 (a weight of
 // zero: that O may hold anything), finished or as a part of a cut unit's result.
