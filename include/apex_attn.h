@@ -441,7 +441,9 @@ apex_status apex_attn_rope(const apex_rope_tensor *q, const apex_rope_tensor *k,
  *   positions NULL (draft t at lens[b] + t), or [B, T] int32, device; used with a
  *             window only; a position below lens[b] counts as lens[b]
  *   window    <= 0: none; > 0: cached key j is at position j, draft u at its own,
- *             and a key is seen only if (position of t) - (its position) < window
+ *             and a key is seen only if (position of t) - (its position) < window; not
+ *             for caches whose rows are elsewhere (after apex_attn_evict, or appended
+ *             by apex_attn_rope at rows that are not their positions)
  *   scale     factor of the scores, > 0; 0: 1 / sqrt(d_qk)
  *   workspace at least apex_attn_tree_workspace_bytes(...) bytes, 16-byte aligned,
  *             owned by the caller, not read before written; calls that may run at
@@ -477,7 +479,9 @@ size_t apex_attn_tree_workspace_bytes(int B, int H_q, int H_kv, int T, int S_cap
  *   workspace at least apex_attn_decode_weights_workspace_bytes(...) bytes, as above
  *
  * Cache rows at or past lens[b] may hold anything.  The sums are made in a fixed
- * order: equal inputs give equal bits.
+ * order: equal inputs give equal bits.  Statistics, sums and what is added to acc are
+ * fp32; the weights are rounded to bf16 for out alone, on the tensor cores.  Most of
+ * the workspace holds the scores, 4 bytes for every query head and row of capacity.
  */
 apex_status apex_attn_decode_weights(const void *q, const void *k_cache, const void *v_cache, void *out, int B,
                                      int H_q, int H_kv, int S_cap, int d_qk, int d_v, const int *lens, float *acc,

@@ -734,7 +734,9 @@ def tree_decode(q, k_cache, v_cache, lens, *, tree_mask=None, positions=None, wi
     -> out [B,H_q,T,d_v].
 
     tree_mask [B,T] or [T] int64: bit u of word t set when draft t sees draft u (None: u <= t);
-    positions [B,T] int32: the drafts' positions, for a window (None: lens[b] + t)."""
+    positions [B,T] int32: the drafts' positions, for a window (None: lens[b] + t); cached row j is
+    then at position j, which is not so after evict or an append at other rows.
+    scale: factor of the scores (None or 0: 1 / sqrt(d_qk))."""
     torch = _torch or _load_torch()
     B, H_q, T, d_qk, H_kv, S_cap, d_v, device, pq, pk, pv = _cache_shapes(q, k_cache, v_cache)
     plens = _fit(lens, "lens", torch.int32, (B,), device)
@@ -775,7 +777,9 @@ def decode_weights_workspace_bytes(B, H_q, H_kv, S_cap, d_qk, d_v=None) -> int:
 def decode_weights(q, k_cache, v_cache, lens, acc, *, scale=None, out=None, workspace=None, stream=None):
     """Decode over a cache of rotated keys that adds each row's attention weight to acc. q [B,H_q,1,d_qk]
     (rotated), caches [B,H_kv,S_cap,d_qk] / [B,H_kv,S_cap,d_v], lens [B] int32, acc [B,H_kv,S_cap] fp32
-    (changed in place, up to lens[b]) -> out [B,H_q,1,d_v]."""
+    (changed in place, up to lens[b]) -> out [B,H_q,1,d_v].
+
+    scale: factor of the scores (None or 0: 1 / sqrt(d_qk))."""
     torch = _torch or _load_torch()
     B, H_q, T, d_qk, H_kv, S_cap, d_v, device, pq, pk, pv = _cache_shapes(q, k_cache, v_cache)
     if T != 1:
@@ -812,7 +816,8 @@ def evict(k_cache, v_cache, acc, lens, budget: int, *, n_sink: int = 0, n_recent
     positions, then the largest acc. caches [B,H_kv,S_cap,d], acc [B,H_kv,S_cap] fp32, lens [B] int32,
     positions [B,H_kv,S_cap] int32 (None: the row index), next_pos [B] int32 (None: lens, or one past
     the largest of the head's positions where that is more)
-    -> (acc_out, positions_out, lens_out), in the new order of rows."""
+    -> (acc_out, positions_out, lens_out), in the new order of rows: row j is no longer at position j, so
+    that tree_decode takes no window over the cache from then on."""
     torch = _torch or _load_torch()
     for n, x in (("budget", budget), ("n_sink", n_sink), ("n_recent", n_recent)):
         if not _INT_MIN <= x <= _INT_MAX:

@@ -12,8 +12,11 @@
 //
 // Bound: HBM.  8 caches of 9001 to 32768 keys, 8 drafts, 32/8 heads of 128: 104 us, 6.6 TB/s
 // (a CTA's tile of 64 KB takes 1.3 us, its products 0.5 and its softmax 0.9 beside it); the
-// same with weights kept and added, 12345 to 32768 keys: 122 us.  8 caches of 30000 keys at
-// d = 64: 78 us, 6.3 TB/s.  One cache of 128 keys: 5.5 us.
+// same with weights kept and added, 12345 to 32768 keys: 122 us.  8 caches of 8000 keys of
+// 192 / 128 entries, 128 rows: 57 us, 5.8 TB/s.  8 caches of 30000 keys at d = 64: 78 us,
+// 6.3 TB/s.  One cache of 128 keys: 5.4 to 6.0 us.  With two M tiles at d = 64 the softmax, 0.9 us
+// a tile and M tile beside products of 0.25, bounds: 256 rows over 8 x 30000 keys 136 us (the
+// bytes 73), 1024 rows over 4 x 8192 keys 84 us (the products 36).
 #include <math.h>
 
 #include "cache_attn.cuh"
@@ -505,8 +508,8 @@ template <int DV>
 cudaError_t launch_join(const CacheAttnParams &p, int shares, cudaStream_t stream)
 {
     // Few units: each is cut into many fragments, which the warps of a block then share.  8
-    // units of 9 fragments: 9.3 us a call so, 10.1 with a thread for all fragments; 64 long
-    // units of 2 or 3: 105.8 and 104.0; 64 of 512 rows: 126 and 84.
+    // units of 19 tiles, one or two a CTA: 9.9 us a call so, 12.4 with a thread for all
+    // fragments; 64 long units of 2 or 3 fragments: 162.9 and 160.0; 64 of 512 rows: 120 and 77.
     return 4ll * p.B * p.H_kv * p.n_groups <= shares ? launch_join_t<DV, 8>(p, stream) : launch_join_t<DV, 1>(p, stream);
 }
 

@@ -59,7 +59,7 @@ struct KernelSetup {
 // only the instructions are elected: descriptors are then the same in every lane and stay in
 // the uniform registers that tcgen05.mma takes.  Under `if (lane == 0)` each was moved there
 // anew, about 100 clocks a product: a tree of 64 on 128/8 heads over 4 x 32768 keys took
-// 435 us, now 341 us.
+// 435 us so, and 341 us elected.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t one;
@@ -94,7 +94,10 @@ struct Sched {
     int b, unit, off;     // sequence, unit within it and cost within the unit where the share starts
 };
 
-// One warp: share c of n, cost [total * c / n, total * (c + 1) / n).
+// One warp: share c of n, cost [total * c / n, total * (c + 1) / n).  The lengths are read 32 at
+// a time, and beyond 32 sequences twice, before the first tile: 512 caches of 256 to 512 keys
+// take 1.29 times their bytes and 4096 of them 1.24, but 65536 caches of 8 keys, one KV head,
+// 2.4 ms, nearly all of it here.
 __device__ __forceinline__ void make_sched(const CacheAttnParams &p, int c, int n, Sched *out)
 {
     const int lane = threadIdx.x & 31;

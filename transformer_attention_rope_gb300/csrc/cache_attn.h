@@ -45,16 +45,22 @@ struct CacheAttnParams {
 // Which kernel, by the rows R = G * T of a KV head's queries.  Up to 128 rows: one M tile
 // on one CTA, bound by the cache's bytes.  More: pairs of CTAs that share each K/V tile,
 // with one M tile each up to 256 rows and two from there on, as the tensor cores read the
-// tile from shared memory once for both CTAs (256 rows, 8 x 8000 keys: 57 us on pairs, 72 on
-// single CTAs with two M tiles; 1024 rows, 4 x 8192 keys: 99 and 107); d_v = 64, whose halves of a V tile would be
+// tile from shared memory once for both CTAs.  d_v = 64, whose halves of a V tile would be
 // narrower than the 128-byte swizzle, stays on one CTA with two M tiles.
+// Measured at d = 128 on pairs / on single CTAs with two M tiles (an instance built for the
+// comparison; rows of 192 leave it one stage).  512 rows, 8 x 8000 keys: 90 / 106 us; 1024
+// rows, 4 x 8192: 94 / 108, ragged 4100 to 8192: 76 / 82.  Up to 256 rows neither leads
+// throughout: 32 units (32 caches of 500 to 4000 keys, one KV head) 144 rows 20.2 / 23.7,
+// 256 rows 21.2 / 30.3; 64 units (8 x 8000) 144 rows 54.7 / 50.7, 256 rows 57.2 / 55.7,
+// 8 x 30000 keys 256 rows 172 / 170; 128 units (16 caches of 500 to 4000) 144 rows
+// 47.4 / 37.0, 256 rows 51.4 / 44.8.
 inline bool cache_attn_pairs(int R, int d_v) { return R > 128 && d_v == 128; }
 inline int cache_attn_group(int R, int d_v) { return R <= 128 ? 128 : (R <= 256 || d_v != 128) ? 256 : 512; }
 
 // What starting a unit costs in the schedule, in tiles: the pipeline fills and drains once
-// more.  32 caches of 100 to 2000 keys, 4 drafts, 32/8 heads: 45.5 us counting 0, 33.9 at 1,
-// 31.0 at 2, 31.3 at 3; a tree of 64 on 128/8 heads, 4 x 8192 keys: 105.5, 102.3, 101.1, 102.0;
-// 8 long caches are indifferent.
+// more.  32 caches of 100 to 2000 keys, 4 drafts, 32/8 heads: 36.3 us counting 0, 29.5 at 1,
+// 28.5 at 2, 28.8 at 3; a tree of 64 on 128/8 heads, 4 x 8192 keys: 95.9, 94.6, 94.0, 94.4,
+// 4 x 4100 to 8192: 77.8, 78.7, 76.3, 77.0; 8 long caches are indifferent (102.9 to 103.5).
 constexpr int kCacheUnitCost = 2;
 
 // Most shares of a call: one per tile, one per CTA or pair at most.
@@ -67,9 +73,9 @@ inline int cache_attn_shares(int B, int H_kv, int n_groups, int S_cap, bool pair
 // Whether short caches are better not cut: without cuts the joining kernel is not
 // launched, which is worth about 3.5 tiles, but the CTAs' loads are less even.  Judged on
 // full caches; past 6 tiles a ragged batch could lose more than that.  Measured cut / whole
-// at d = 128, 32/8 heads, 4 drafts: 1 cache of 376 keys 8.6 / 7.8 us, of 504 8.7 / 8.8, of
-// 632 8.9 / 9.7; 8 caches of 504 keys 11.1 / 9.7; 32 of 248 14.8 / 12.4, of 760 24.2 / 21.2;
-// 640 rows, 4 caches of 480 keys on pairs 22.7 / 16.3.
+// at d = 128, 32/8 heads, 4 drafts: 1 cache of 376 keys 8.5 / 7.7 us, of 504 8.6 / 8.5, of
+// 632 8.5 / 9.3; 8 caches of 504 keys 10.8 / 8.7; 32 of 248 14.0 / 11.7, of 760 21.8 / 20.0;
+// 640 rows, 4 caches of 480 keys on pairs 22.6 / 15.9.
 inline bool cache_attn_whole(long long units, int keys, int shares)
 {
     const long long tiles = (keys + kCacheTileKeys - 1) / kCacheTileKeys, cost = tiles + kCacheUnitCost;

@@ -22,9 +22,11 @@
 // lanes), each warpgroup writing half of the columns.
 //
 // Bound: the softmax beside the products from 257 rows on -- 64 drafts on 128/8 heads over
-// 4 x 32768 keys 330 us, 1.67 PFLOP/s; over 4 x 4100 to 8192 keys 81 us with cut units
-// joined (84 before O += P V started on half a tile) -- and HBM with the products below
-// that: 256 rows over 8 x 8000 keys 57 us, 4.6 TB/s (65 us with one warpgroup).
+// 4 x 32768 keys 313 to 330 us, 1.67 to 1.76 PFLOP/s; over 4 x 4100 to 8192 keys 76 to 81 us
+// with cut units joined (84 before O += P V started on half a tile); rows of 192 over 4 x 8192
+// keys 108 us.  Below that the cycle of an S buffer -- product, 1 us of softmax, product --
+// of which there are two: 256 rows over 8 x 8000 keys 57 us, where the bytes take 40 and the
+// products 36 (65 us with one warpgroup); 208 rows of 192 63 us, where the bytes take 50.
 #include <math.h>
 
 #include "cache_attn.cuh"

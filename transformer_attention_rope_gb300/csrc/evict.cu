@@ -16,8 +16,8 @@
 // that are past it.
 //
 // Bound: latency of the search, about 2 us a digit and 4 for the two walks, then HBM for
-// the moves.  64 caches of 4224 rows cut to 4096: 12.5 us; 32 of 32768 rows cut to 4096 with
-// 110 MB moved: 38 us, 20 of them the moves at 5.5 TB/s.
+// the moves.  64 caches of 4224 rows cut to 4096: 12.3 us; 32 of 32768 rows cut to 4096 with
+// 110 MB moved: 37 us, 20 of them the moves at 5.5 TB/s.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -77,8 +77,8 @@ __device__ __forceinline__ void before_warp(Shared &sh, uint32_t c0, uint32_t c1
 
 // chunk: rows of a CTA; seg: rows of a warp, a multiple of 32 (chunk <= kWarps * seg).
 // ONE: seg <= kBlock, the rows are read once and kept; else they are read again, from
-// L2, in each of the six walks over them (64 caches of 4224 rows 12.0 us kept, 14.9 read
-// again, before one CTA read the length for all; 32 of 32768 rows 37.8 and 41.6).
+// L2, in each of the up to eight walks over them (64 caches of 4224 rows 12.3 us kept, 14.3
+// read again; 32 of 32768 rows 37.5 and 40.1).
 template <bool ONE>
 __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p, int chunk, int seg)
 {
@@ -328,8 +328,11 @@ cudaError_t launch_evict(const EvictParams &p, int sm_count, cudaStream_t stream
 {
     const int units = p.B * p.H_kv;
     // Parts of 4096 rows at most, as far as clusters of 8 go; smaller ones, down to 1024
-    // rows, only while every CTA still has an SM of its own (64 caches of 4224 rows: 14.4 us
-    // as 128 CTAs, 17.4 us as 256; 8 caches of 32768 rows: 64 CTAs).
+    // rows, only while every CTA still has an SM of its own.  64 caches of 4224 rows cut to
+    // 4096: 22 us as 64 CTAs, 12.3 as 128, 14.2 as 256; 8 caches of 4096 rows cut to half: 39 us
+    // as 8 CTAs, 18.5 as 32, 16.3 as 64; 32 of 32768 cut to 4096: 106 us in clusters of 2, 59 of
+    // 4, 37.5 of 8.  Where half of the rows go, more CTAs than SMs would move them faster: 64
+    // caches of 8192 rows 63 us as 128 CTAs, 46 as 256; of 2048 rows 18.1 and 19.0.
     int cs = 1;
     auto part = [&](int c) { return (p.S_cap + c - 1) / c; };
     while (cs < kMaxCluster && (part(cs) > 16 * kBlock || (part(cs) > 1024 && (long long)units * cs * 2 <= sm_count)))

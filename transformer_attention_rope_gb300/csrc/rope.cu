@@ -6,7 +6,8 @@
 // m * f_i mod 2^64 is then the angle of position m reduced to one turn -- exactly,
 // for every int32 m of either sign -- and its top 32 bits, as a signed fraction of
 // half a turn, go to sincospi.  theta_i carries the 2^-53 of double precision, so
-// the angle of m = 2^24 is off by under 2^-30 turns.
+// the reduced angle of m = 2^24 is off by under 2^-30 turns; made a float, of 24 bits, it is
+// rounded by up to 2^-26 turns at any m, about 10^-7 of what turns.
 //
 // A thread owns one unit of a token's row and walks over heads, so the sines and
 // cosines of the unit (4 or 8 pairs) are computed once per head group; a unit is
