@@ -381,3 +381,15 @@ def test_sizes_that_do_not_fit_an_int():
             apex.rope(q, positions=pos, **o)
     with pytest.raises(apex.ApexError):  # an infinity in 32 bits
         apex.rope(q, positions=pos, rope_base=1e39)
+
+
+@pytest.mark.gpu
+def test_rope_refuses_outputs_of_other_shapes():
+    dev = _gpu()
+    q, k, v, ln = _attn_inputs(dev, 4, 8, 2, 4, 128, 128, 4, [0, 0])
+    pos = torch.zeros(4, dtype=torch.int32, device=dev)
+    for o in (dict(k_out=k[0, 0]), dict(k_out=k[0, 0], row0=ln), dict(k_out=k[0], row0=ln),
+              dict(v=v, k_out=torch.empty_like(k), v_out=v[0, 0], row0=ln),
+              dict(v=v, k_out=torch.empty_like(k), v_out=torch.empty_like(v)[:, :, :3], row0=ln)):
+        with pytest.raises(ValueError):
+            apex.rope(q, k, positions=pos, **o)

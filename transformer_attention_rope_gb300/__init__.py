@@ -631,8 +631,8 @@ def _rope_rows(x, out, name, B, S, into, device):
         raise ValueError("%s must have the batch and length of q" % name)
     if (to != xs and not into) or to[0] != B or to[1] != xs[1] or to[3] != xs[3]:
         raise ValueError("%s_out does not fit %s" % (name, name))
-    if xs[1] > _INT_MAX or xs[3] > _INT_MAX:
-        raise ValueError("%s has more heads or entries than rope takes" % name)
+    if xs[1] > _INT_MAX or xs[3] > _INT_MAX or to[2] > _INT_MAX:
+        raise ValueError("%s has more heads or entries, or %s_out more rows, than rope takes" % (name, name))
     xb, xh, xr, xe = x.stride()
     ob, oh, orow, oe = out.stride()
     if (xe != 1 or oe != 1) and xs[3] > 1:
@@ -665,8 +665,8 @@ def rope(q, k=None, v=None, *, positions, layout: str = "interleaved", rot_start
     if k is None and (v is not None or k_out is not None) or v is None and v_out is not None:
         raise ValueError("k_out goes with k, and v and v_out with k")
     B, _, S, _ = _rows4(q, "q")
-    if B > _INT_MAX or S > _INT_MAX or k_out is not None and k_out.shape[2] > _INT_MAX:
-        raise ValueError("more sequences, tokens or rows than rope takes")
+    if B > _INT_MAX or S > _INT_MAX:
+        raise ValueError("more sequences or tokens than rope takes")
     device = q.get_device()
     try:
         opt = _rope_options(1 if layout == "half" else 0, rot_start, d_rot, 1 if inverse else 0, rope_base,
@@ -683,9 +683,7 @@ def rope(q, k=None, v=None, *, positions, layout: str = "interleaved", rot_start
         if into:
             if k is None or k_out is None or (v is not None and v_out is None):
                 raise ValueError("row0 needs k_out, and v_out where there is a v")
-            start, rows = _fit(row0, "row0", torch.int32, (B,), device), k_out.shape[2]
-            if v is not None and v_out.shape[2] != rows:
-                raise ValueError("k_out and v_out must have the same number of rows")
+            start = _fit(row0, "row0", torch.int32, (B,), device)
         if k is not None:
             if k_out is None:
                 k_out = at.new(k, k.shape, torch.bfloat16)
@@ -694,6 +692,10 @@ def rope(q, k=None, v=None, *, positions, layout: str = "interleaved", rot_start
             if v_out is None:
                 v_out = at.new(v, v.shape, torch.bfloat16)
             tv = _rope_rows(v, v_out, "v", B, S, into, device)
+        if into:
+            rows = k_out.shape[2]
+            if v is not None and v_out.shape[2] != rows:
+                raise ValueError("k_out and v_out must have the same number of rows")
         status = (_lib or load_library()).apex_attn_rope(tq, tk, tv, B, S, pos, S if positions.dim() == 2 else 0,
                                                          start, rows, opt, at.handle)
         if status:
