@@ -385,8 +385,9 @@ typedef struct apex_rope_options {
  * h * in_h + s * in_s (strides in elements, any order), written to out likewise.
  * out may be in with the same strides (of k and v only without row0).  Otherwise no
  * out may share an element with any in or other out of the call, the rows up to
- * out_rows counted whole with row0, nor hold an element twice; views that interleave in
- * one buffer do not. */
+ * out_rows counted whole with row0, nor hold an element twice.  Views that interleave in
+ * one buffer do not; strides that no nesting of dimensions gives may take too long to tell,
+ * and are refused then. */
 typedef struct apex_rope_tensor {
     const void *in;
     void *out;

@@ -393,3 +393,26 @@ def test_rope_refuses_outputs_of_other_shapes():
               dict(v=v, k_out=torch.empty_like(k), v_out=torch.empty_like(v)[:, :, :3], row0=ln)):
         with pytest.raises(ValueError):
             apex.rope(q, k, positions=pos, **o)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("off,S,per", [(0, 64, None), (1, 1, 1), (1, 64, None), (1, 512, 8)])
+def test_rope_of_some_tokens_spreads_its_heads(off, S, per):
+    """One block an SM where rows go 16 bytes at a time, four where they go 2 bytes at a time, heads in fours or
+    up to eight."""
+    from test_cache_operators import _gen, _normal, _rope_close, _rope_ref
+    dev = _gpu()
+    g = _gen(dev, 70 + S)
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    q, k, v = (_normal(g, dev, 1, S, h * 128 + off)[..., off:].view(1, S, h, 128).transpose(1, 2) for h in (32, 8, 8))
+    pos = torch.arange(S, dtype=torch.int32, device=dev)
+    got = apex.rope(q, k, v, positions=pos)
+    for x, y in zip((q, k), got):
+        _rope_close(y, *_rope_ref(x, pos[None]))
+    assert torch.equal(got[2], v)
+    blocks, room = (S * 128 // 256, 4 * sms) if off else (S * 16 // 256, sms)
+    share = max(1, -(-blocks * 48 // room))
+    want = min(share, 8) if off or share >= 8 else min(share, 4)
+    assert per is None or want == per
+    grids = [at for n, at in _launched(lambda: apex.rope(q, k, v, positions=pos)) if "rope_" in n]
+    assert len(grids) == 1 and grids[0][1] == sum(-(-h // want) for h in (32, 8, 8)), grids

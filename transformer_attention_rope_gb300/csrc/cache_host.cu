@@ -271,17 +271,20 @@ apex_status apex_attn_rope(const apex_rope_tensor *q, const apex_rope_tensor *k,
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return APEX_ERR_CUDA;
-    // Heads per group: a thread's heads share the sines of a unit, but with few tokens one
-    // block an SM is what there is to gain from fewer.  Up to 4 heads, whose loads are in
-    // flight together, and 8 once that many still leave a block for every SM (times with
-    // 1 / 2 / 4 / 8 heads, 32 + 8 + 8 heads of 128, interleaved): one token 2.2 / 2.2 / 2.2 / 2.7 us,
-    // 32 tokens 2.4 / 2.5 / 2.7 / 3.2, 64 tokens 3.2 / 2.5 / 2.7 / 3.2, 8 x 16 tokens
-    // 3.7 / 3.2 / 2.7 / 3.2, 256 tokens 5.6 / 4.0 / 3.6 / 3.3 (half layout 4.2 / 3.6 / 3.2 / 4.1),
-    // 2048 tokens 29 / 16 / 10 / 8; 8191 tokens of 136 heads of 192: 4 heads 149, 8 heads 130.
+    // Heads per group: a thread's heads share the sines of a unit, but with few tokens blocks
+    // for the SMs are what there is to gain from fewer.  16 bytes at a time: up to 4 heads,
+    // whose loads are in flight together, as far as a block for every SM goes, and 8 beyond
+    // (32 + 8 + 8 heads of 128, interleaved, with 1 / 2 / 4 / 8 heads: one token 2.2 / 2.2 / 2.2 /
+    // 2.7 us, 32 tokens 2.4 / 2.5 / 2.7 / 3.2, 64 tokens 3.2 / 2.5 / 2.7 / 3.2, 8 x 16 tokens
+    // 3.7 / 3.2 / 2.7 / 3.2, 256 tokens 5.6 / 4.0 / 3.6 / 3.3 (half layout 4.2 / 3.6 / 3.2 / 4.1), 2048
+    // tokens 29 / 16 / 10 / 8; 8191 tokens of 136 heads of 192: 4 heads 149, 8 heads 130).  2 bytes
+    // at a time, head after head: up to 8 with four blocks an SM (the same: one token 1.9 / 2.1 /
+    // 2.5 / 3.2, 64 tokens 3.9 / 2.9 / 3.0 / 3.5, 128 tokens 5.7 / 4.1 / 3.5 / 3.9, 256 tokens 9.6 / 6.2 /
+    // 4.9 / 4.5).
     const long long units = (long long)B * S * (wide ? width / 8 : width);
     const long long bx = (units + kRopeThreads - 1) / kRopeThreads;
-    const long long share = (bx * heads + sm_count - 1) / sm_count;
-    int per = share >= 8 ? 8 : (int)std::min<long long>(4, share);
+    const long long room = wide ? sm_count : 4ll * sm_count, share = (bx * heads + room - 1) / room;
+    int per = share >= 8 ? 8 : (int)std::min<long long>(wide ? 4 : 8, share);
     auto groups = [&](int n) {  // n heads each
         int sum = 0;
         for (int i = 0; i < 3; ++i)
