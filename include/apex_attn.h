@@ -207,6 +207,33 @@ apex_status apex_attn_mla_fwd_ws(const void *q, const void *k, const void *v, vo
                                  apex_stream_t stream);
 
 /*
+ * Prefill under a sliding window whose first tokens stay visible (sinks):
+ *   visible(m, j) <=> j <= m  and  (m - j < opt->window  or  j < n_sink)
+ * and for everything else apex_attn_fwd_ws (d_r = 0) or apex_attn_mla_fwd_ws (d_r > 0:
+ * q and k rows of d_h + d_r entries): layouts, options (a query inside a prefix sees the
+ * prefix alone), workspaces, supported sizes and errors.  n_sink >= 0; 0, or no window, is
+ * the call without sinks.  A work item visits the key tiles of the sinks and those of its
+ * window, whatever lies between.
+ */
+apex_status apex_attn_sink_fwd(const void *q, const void *k, const void *v, void *out,
+                               int B, int H_q, int H_kv, int S_q, int S_k, int d_h, int d_r, int n_sink,
+                               const apex_attn_options *opt, void *workspace, size_t workspace_bytes,
+                               apex_stream_t stream);
+
+/* Bytes of workspace apex_attn_sink_fwd will use, as apex_attn_fwd_workspace_bytes.  Host-only. */
+size_t apex_attn_sink_fwd_workspace_bytes(int B, int H_q, int H_kv, int S_q, int S_k, int d_h, int d_r, int n_sink,
+                                          const apex_attn_options *opt);
+
+/*
+ * Decode under the same rule: apex_attn_decode_ex (d_r = 0) or apex_attn_mla_decode (d_r > 0)
+ * with the first n_sink keys visible behind opt->window; workspace as for them.
+ */
+apex_status apex_attn_sink_decode(const void *q, const void *k_cache, const void *v_cache, void *out,
+                                  int B, int H_q, int H_kv, int S_k, int d_h, int d_r, int n_sink,
+                                  const apex_attn_options *opt, void *workspace, size_t workspace_bytes,
+                                  apex_stream_t stream);
+
+/*
  * Decode with options: as apex_attn_decode, with window, q_pos and rope_base
  * taken from *opt.  With a prefix and q_pos < P the query sees keys [0, P).
  * The workspace size is apex_attn_decode_workspace_bytes(...) as for
@@ -425,6 +452,59 @@ apex_status apex_attn_rope(const apex_rope_tensor *q, const apex_rope_tensor *k,
                            int S, const int *positions, long long pos_stride, const int *row0, int out_rows,
                            const apex_rope_options *opt, apex_stream_t stream);
 
+/* One tensor of apex_attn_norm_rope or of its gradient: rows of consecutive bf16 entries at
+ * x + b * x_b + h * x_h + s * x_s (strides in elements, any order), the result at out
+ * likewise.  For the gradient dy is that of the result and out receives x's. */
+typedef struct apex_norm_tensor {
+    const void *x;
+    const void *dy;      /* gradient only                                                    */
+    void *out;
+    const void *weight;  /* [d_row], or [n_heads][d_row]; NULL: ones                         */
+    float *dweight;      /* gradient only: the weights' gradient, shaped as they; NULL: none */
+    int n_heads, d_row;
+    int weight_f32;      /* weights are fp32 (0: bf16)                                       */
+    int weight_per_head; /* non-zero: [n_heads][d_row]                                       */
+    long long x_b, x_h, x_s;
+    long long dy_b, dy_h, dy_s;
+    long long out_b, out_h, out_s;
+} apex_norm_tensor;
+
+/*
+ * RMS norm of every query and key head (Part 1 §3) and its rotary position in one pass, with
+ * v copied beside them.  For a row x of d = d_row entries at position m
+ *   y = R_m (x / sqrt(mean(x^2) + eps) * weight)
+ * with R_m the rotation of apex_attn_rope (the whole row is normed, the part that *opt names is
+ * turned), in fp32, rounded once to bf16.  Positions, row0, out_rows, layouts and limits are
+ * those of apex_attn_rope; opt->inverse is not used.  q may not be NULL, k and v may be.
+ *
+ * An out may be its own x with the same strides (of k and v only without row0); otherwise no
+ * out may share an element with any x, weight or other out, nor hold one twice.
+ * d_row <= 1024, n_heads <= 16384, d_rot <= 512; eps >= 0 and finite.  16-byte aligned rows of
+ * up to 256 entries with d_rot (half layout: d_rot / 2), rot_start and d_row multiples of 8 run
+ * 16 bytes at a time.
+ */
+apex_status apex_attn_norm_rope(const apex_norm_tensor *q, const apex_norm_tensor *k, const apex_rope_tensor *v, int B,
+                                int S, const int *positions, long long pos_stride, const int *row0, int out_rows,
+                                const apex_rope_options *opt, float eps, apex_stream_t stream);
+
+/*
+ * Gradients of apex_attn_norm_rope.  With u = x / sqrt(mean(x^2) + eps) and g = R_m^-1 dy
+ *   dx      = (g * weight - u * mean(g * weight * u)) / sqrt(mean(x^2) + eps)   to out, bf16
+ *   dweight = sum of g * u over all rows (of the head, with weights for each), fp32
+ * The sums are made in a fixed order: equal inputs give equal bits.  An out may be its own x
+ * or dy with the same strides.
+ *   workspace at least apex_attn_norm_rope_grad_workspace_bytes(...) bytes, 16-byte aligned,
+ *             owned by the caller, not read before written; calls that may run at the same
+ *             time need one each
+ */
+apex_status apex_attn_norm_rope_grad(const apex_norm_tensor *q, const apex_norm_tensor *k, int B, int S,
+                                     const int *positions, long long pos_stride, const apex_rope_options *opt,
+                                     float eps, void *workspace, size_t workspace_bytes, apex_stream_t stream);
+
+/* Bytes of workspace apex_attn_norm_rope_grad needs (H_kv, d_k: 0 without k); 0 when the sizes are invalid.
+ * Host-only. */
+size_t apex_attn_norm_rope_grad_workspace_bytes(int H_q, int H_kv, int d_q, int d_k);
+
 /*
  * Attention of a tree of T drafted tokens per sequence over a cache: every
  * drafted token sees the sequence's cached keys and its own ancestors among the
@@ -524,6 +604,82 @@ apex_status apex_attn_evict(void *k_cache, void *v_cache, int B, int H_kv, int S
 
 /* Bytes of workspace apex_attn_evict needs; 0 when the sizes are invalid.  Host-only. */
 size_t apex_attn_evict_workspace_bytes(int B, int H_kv, int S_cap, int budget);
+
+/* ======================================================================
+ * Caches held in 4 bits.
+ *
+ * A packed row of d entries is d / 2 bytes of e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives; entry 2i in the low half of byte i) and d / 16 e4m3 scales, one for 16
+ * neighbouring entries.  An entry stands for value * scale * factor, where factor is an fp32
+ * number of the KV head that the caller chooses (> 0 and finite, best a power of two; no array:
+ * 1): e4m3 scales lose precision below 2^-6 and end at 448, so a head's factor should be near
+ * its largest entry / 1000.  Packed tensors are dense, [B, H_kv, S_cap, d / 2] and
+ * [B, H_kv, S_cap, d / 16] bytes, 16-byte aligned.
+ * ====================================================================== */
+
+/* One tensor of apex_attn_append4 and apex_attn_unpack4. */
+typedef struct apex_bits4_tensor {
+    void *rows;          /* bf16 rows at rows + i_b * b + i_h * h + i_s * s (strides in elements); read by
+                            apex_attn_append4, written by apex_attn_unpack4                              */
+    void *bytes;         /* [B, H_kv, S_cap, d / 2]                                                      */
+    void *scales;        /* [B, H_kv, S_cap, d / 16]                                                     */
+    const float *factor; /* [H_kv], device, or NULL: 1                                                   */
+    long long b, h, s;
+    int d;               /* entries of a row: a multiple of 16 up to 512                                 */
+} apex_bits4_tensor;
+
+/*
+ * Append keys and values to a 4-bit cache: row s < S of sequence b goes to row row0[b] + s
+ * (row0 NULL: s); rows outside [0, S_cap) are dropped, the others of the cache untouched.  For
+ * each 16 entries x
+ *   scale = e4m3(max |x| / (6 factor)),  value = e2m1(x / (scale * factor))
+ * rounded to nearest, ties to even, to at most 448 and 6 (with a factor that is no power of two
+ * a quotient within 2^-22 of a tie may go either way); a scale of 0 gives zeros.  16 entries that
+ * hold an infinity or a NaN read as NaN.  The packed tensors share no byte with the rows or with
+ * one another.  B * H_kv * S < 2^31.
+ */
+apex_status apex_attn_append4(const apex_bits4_tensor *k, const apex_bits4_tensor *v, int B, int H_kv, int S, int S_cap,
+                              const int *row0, apex_stream_t stream);
+
+/*
+ * The same rows back as bf16, rounded once (exact for factors that are powers of two); rows
+ * outside [0, S_cap) give zeros.  The rows share no element with the packed tensors or with one
+ * another.
+ */
+apex_status apex_attn_unpack4(const apex_bits4_tensor *k, const apex_bits4_tensor *v, int B, int H_kv, int S, int S_cap,
+                              const int *row0, apex_stream_t stream);
+
+/*
+ * Attention of T new tokens per sequence over a 4-bit cache that holds their own rows too:
+ *   m        = lens[b] + t                    position of token t, and its row of the cache
+ *   out      = sum_j softmax_j(scale <q, k_j>) v_j   over the rows j < S_cap visible from m:
+ *   visible(m, j) <=> j <= m and (window <= 0 or m - j < window or j < n_sink)
+ *
+ *   q         [B, H_q, T, d_qk] bf16, read (rotated)
+ *   k4, k_scale, v4, v_scale  packed tensors, read; keys rotated before they were packed
+ *   out       [B, H_q, T, d_v] bf16, written (must not overlap an input)
+ *   lens      [B] int32, device: rows before the new tokens' (taken as clamped to [0, S_cap])
+ *   n_sink    first rows that stay visible behind a window (>= 0)
+ *   k_factor, v_factor  [H_kv], device, or NULL: 1
+ *   scale     factor of the scores, > 0; 0: 1 / sqrt(d_qk)
+ *   workspace at least apex_attn_decode4_workspace_bytes(...) bytes, 16-byte aligned, owned by
+ *             the caller, not read before written; calls that may run at the same time need
+ *             one each
+ *
+ * Row lengths, groups and limits as for apex_attn_tree_decode (1 <= T <= 64); made for few rows
+ * G * T of a KV head, which are worked on 16 at a time.  A row that sees no key gives zeros.
+ * Cache rows that no token of the sequence sees may hold anything; the values of the others must
+ * be finite.  Queries are held in fp16 relative to their row's largest entry, where entries below
+ * 2^-24 of it lose precision; scores, statistics and sums are fp32, weights are rounded to fp16 for
+ * the tensor cores.  Equal inputs give equal bits.
+ */
+apex_status apex_attn_decode4(const void *q, const void *k4, const void *k_scale, const void *v4, const void *v_scale,
+                              void *out, int B, int H_q, int H_kv, int T, int S_cap, int d_qk, int d_v, const int *lens,
+                              int window, int n_sink, const float *k_factor, const float *v_factor, float scale,
+                              void *workspace, size_t workspace_bytes, apex_stream_t stream);
+
+/* Bytes of workspace apex_attn_decode4 needs; 0 when the sizes are invalid.  Host-only. */
+size_t apex_attn_decode4_workspace_bytes(int B, int H_q, int H_kv, int T, int S_cap, int d_qk, int d_v);
 
 /*
  * Read and clear the current device's status word, after synchronising the

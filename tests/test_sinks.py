@@ -1,0 +1,290 @@
+"""Prefill and decode under a window whose first tokens stay visible, against plain 64-bit attention.
+
+Tolerances (u = 2^-8: half a step of bf16, relative to the value): the rotated queries and keys are
+rounded to bf16, each by u relative, so a score moves by at most e = (2 u + u^2) scale sum |q k| over
+the worst signs; the sum of d such roundings of either sign stays below 6 standard deviations of u / sqrt(3)
+each (a row's largest over n keys: 6 covers n = 2^20), which is what is counted:
+  e = 6 (2 u / sqrt 3) scale sqrt(sum (q k)^2) + d 2^-24 scale sum |q k|;
+numerators and denominators of the weights move by e: 2 e A, A = sum p |v|, in the sum.  Weights are rounded
+to bf16: u A; the result: u |out|; exp2 and sums in fp32: 2^-13 A.
+"""
+import math
+
+import pytest
+import torch
+
+import transformer_attention_rope_gb300 as apex
+
+U = 2.0 ** -8
+
+
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch.device("cuda:0")
+
+
+def _turn(x, pos, d_r, yarn=1.0):
+    """Rows with their last d_r entries turned, interleaved pairs, 64 bits."""
+    x = x.double()
+    theta = []
+    for i in range(d_r // 2):
+        th = 10000.0 ** (-2.0 * i / d_r)
+        if yarn > 1.0:
+            lam = 2 * math.pi / th
+            t = min(1.0, max(0.0, (lam - 1.0) / (yarn - 1.0)))
+            th = th if lam < 32.0 else th / yarn if lam > yarn else th / (t * yarn + 1 - t)
+        theta.append(th)
+    ang = pos.double()[:, None] * torch.tensor(theta, dtype=torch.float64, device=x.device)
+    y = x.clone()
+    a = x.shape[-1] - d_r + 2 * torch.arange(d_r // 2, device=x.device)
+    y[..., a] = x[..., a] * ang.cos() - x[..., a + 1] * ang.sin()
+    y[..., a + 1] = x[..., a] * ang.sin() + x[..., a + 1] * ang.cos()
+    return y
+
+
+def _ref(q, k, v, q0, window, n_sink, d_r=0, prefix=0, yarn=1.0, turned=False):
+    """(out, tolerance)"""
+    B, Hq, S, d = q.shape
+    Hkv, Sk = k.shape[1:3]
+    G = Hq // Hkv
+    dev = q.device
+    d_rot = d_r or d
+    scale = (0.1 * math.log(yarn) + 1 if yarn > 1 else 1) / math.sqrt(d)
+    m = q0 + torch.arange(S, device=dev)
+    j = torch.arange(Sk, device=dev)
+    seen = (j <= m[:, None]) & ((m[:, None] - j < window) | (j < n_sink)) if window > 0 else j <= m[:, None]
+    if prefix:
+        seen = torch.where((m < prefix)[:, None], j < prefix, seen)
+    out = torch.zeros(*q.shape[:3], v.shape[-1], dtype=torch.float64, device=dev)
+    tol = torch.zeros_like(out)
+    for b in range(B):
+        for h in range(Hkv):
+            kk = k[b, h].double() if turned else _turn(k[b, h], j, d_rot, yarn)
+            vv = v[b, h].double()
+            for i in range(h * G, (h + 1) * G):
+                x = _turn(q[b, i], m, d_rot, yarn)
+                s = (x @ kk.T * scale).masked_fill(~seen, -math.inf)
+                p = torch.softmax(s, -1)
+                o, A = p @ vv, p @ vv.abs()
+                e = 12 * U / math.sqrt(3) * scale * ((x * x) @ (kk * kk).T).sqrt() + d * 2.0 ** -24 * scale * (x.abs() @ kk.abs().T)
+                e = e.masked_fill(~seen, 0).amax(-1, keepdim=True)
+                out[b, i] = o
+                tol[b, i] = U * o.abs() + A * (U + 2 * e + 2.0 ** -13)
+    return out, tol
+
+
+def _close(got, ref, tol):
+    err = (got.double() - ref).abs()
+    assert torch.isfinite(err).all()
+    assert (err <= tol).all(), float((err - tol).max())
+
+
+def _inputs(dev, seed, B, Hq, Hkv, S, Sk, d, d_r=0):
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    f = lambda *s: torch.randn(*s, generator=g, device=dev).to(torch.bfloat16)  # noqa: E731
+    return f(B, Hq, S, d + d_r), f(B, Hkv, Sk, d + d_r), f(B, Hkv, Sk, d)
+
+
+FWD = [  # B, Hq, Hkv, S, Sk, d, d_r, window, sinks
+    (1, 4, 2, 128, 128, 64, 0, 16, 4),
+    (1, 4, 2, 700, 700, 64, 0, 100, 1),
+    (2, 8, 8, 513, 700, 64, 0, 64, 130),
+    (1, 8, 2, 1000, 1000, 128, 0, 128, 4),
+    (1, 8, 2, 1000, 1300, 128, 0, 200, 128),
+    (2, 16, 1, 300, 1500, 128, 0, 257, 300),
+    (1, 2, 2, 1100, 1100, 128, 0, 1, 1),
+    (1, 4, 4, 1, 1000, 128, 0, 17, 64),
+    (1, 32, 4, 600, 900, 128, 64, 100, 4),
+    (1, 4, 2, 500, 500, 128, 64, 33, 200),
+    (1, 4, 2, 300, 300, 128, 0, 299, 5000),       # every key is a sink
+    (1, 4, 2, 700, 700, 128, 0, 650, 3),          # sinks within the window's reach for most rows
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("workspace", [None, False])
+@pytest.mark.parametrize("B,Hq,Hkv,S,Sk,d,d_r,window,sinks", FWD)
+def test_prefill_matches_the_formula(B, Hq, Hkv, S, Sk, d, d_r, window, sinks, workspace):
+    dev = _gpu()
+    q, k, v = _inputs(dev, S + Sk, B, Hq, Hkv, S, Sk, d, d_r)
+    how = dict(window=window, n_sink=sinks, q_pos0=Sk - S, workspace=workspace)
+    got = apex.mla_fwd(q, k, v, d_r, **how) if d_r else apex.fwd(q, k, v, **how)
+    _close(got, *_ref(q, k, v, Sk - S, window, sinks, d_r))
+    assert apex.apex_attn_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,d_r", [(64, 0), (128, 0), (128, 64)])
+def test_keys_rotated_once(d, d_r):
+    """The pass that rotates the keys beforehand, and keys that the caller rotated."""
+    dev = _gpu()
+    q, k, v = _inputs(dev, 3, 1, 8, 1, 700, 700, d, d_r)
+    call = (lambda *a, **o: apex.mla_fwd(*a, d_r, **o)) if d_r else apex.fwd
+    need = apex.apex_attn_sink_fwd_workspace_bytes
+    ref = _ref(q, k, v, 0, 90, 10, d_r)
+    turned = apex.mla_rope_keys(k, d_r) if d_r else apex.rope_keys(k)
+    _close(call(q, turned, v, window=90, n_sink=10, keys_prerotated=True), *ref)
+    # long enough for the cost model to choose the pass
+    q, k, v = _inputs(dev, 4, 1, 16, 1, 6000, 6000, d, d_r)
+    opt = apex.Options(window=3000)
+    n = need(1, 16, 1, 6000, 6000, d, d_r, 5, opt)
+    got = call(q, k, v, window=3000, n_sink=5)
+    raw = call(q, k, v, window=3000, n_sink=5, workspace=False)
+    assert n in (0, k.numel() * 2)
+    assert (got.float() - raw.float()).abs().max() <= 2 * U * raw.float().abs().max()
+
+
+@pytest.mark.gpu
+def test_without_a_window_or_sinks_it_is_the_plain_call():
+    dev = _gpu()
+    for d, d_r in ((64, 0), (128, 0), (128, 64)):
+        q, k, v = _inputs(dev, 5, 2, 8, 2, 400, 400, d, d_r)
+        call = (lambda *a, **o: apex.mla_fwd(*a, d_r, **o)) if d_r else apex.fwd
+        one = (lambda *a, **o: apex.mla_decode(*a, 399, d_r, **o)) if d_r else (lambda *a, **o: apex.decode(*a, 399, **o))
+        q1 = q[:, :, -1:].contiguous()
+        assert torch.equal(call(q, k, v, n_sink=7), call(q, k, v))
+        assert torch.equal(call(q, k, v, window=50, n_sink=0), call(q, k, v, window=50))
+        assert torch.equal(one(q1, k, v, n_sink=7), one(q1, k, v))
+        # a window that reaches everything, and one that the sinks fill up
+        want, tol = _ref(q, k, v, 0, 0, 0, d_r)
+        _close(call(q, k, v, window=400, n_sink=7), want, tol)
+        _close(call(q, k, v, window=1, n_sink=400), want, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,d_r", [(64, 0), (128, 0), (128, 64)])
+def test_prefix_and_yarn(d, d_r):
+    dev = _gpu()
+    q, k, v = _inputs(dev, 6, 1, 8, 2, 600, 600, d, d_r)
+    call = (lambda *a, **o: apex.mla_fwd(*a, d_r, **o)) if d_r else apex.fwd
+    got = call(q, k, v, window=70, n_sink=150, prefix_len=40, yarn_scale=16.0)
+    _close(got, *_ref(q, k, v, 0, 70, 150, d_r, prefix=40, yarn=16.0))
+
+
+DECODE = [  # B, Hq, Hkv, Sk, q_pos, d, d_r, window, sinks
+    (1, 4, 2, 1, 0, 64, 0, 16, 4),
+    (3, 8, 8, 700, 699, 64, 0, 100, 1),
+    (2, 32, 8, 3000, 2999, 128, 0, 1024, 4),
+    (2, 32, 8, 3000, 1500, 128, 0, 64, 200),
+    (1, 16, 1, 5000, 4990, 128, 0, 1, 64),
+    (2, 8, 2, 1000, 130, 128, 0, 128, 4),
+    (2, 8, 2, 1000, 999, 128, 64, 100, 65),
+    (1, 4, 2, 900, 899, 128, 0, 300, 900),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("turned", [False, True])
+@pytest.mark.parametrize("B,Hq,Hkv,Sk,at,d,d_r,window,sinks", DECODE)
+def test_decode_matches_the_formula(B, Hq, Hkv, Sk, at, d, d_r, window, sinks, turned):
+    dev = _gpu()
+    q, k, v = _inputs(dev, Sk + at, B, Hq, Hkv, 1, Sk, d, d_r)
+    if turned:
+        k = apex.mla_rope_keys(k, d_r) if d_r else apex.rope_keys(k)
+    how = dict(window=window, n_sink=sinks, keys_prerotated=turned)
+    got = apex.mla_decode(q, k, v, at, d_r, **how) if d_r else apex.decode(q, k, v, at, **how)
+    ref = _ref(q, k, v, at, window, sinks, d_r, turned=turned)
+    err = (got.double() - ref[0]).abs()
+    assert (err <= ref[1]).all(), float((err - ref[1]).max())
+
+
+@pytest.mark.gpu
+def test_prompt_then_tokens():
+    """Chunks of a prompt and then single tokens give the rows of one call over all."""
+    dev = _gpu()
+    S, window, sinks = 700, 150, 6
+    q, k, v = _inputs(dev, 8, 2, 8, 2, S, S, 128)
+    ref, tol = _ref(q, k, v, 0, window, sinks)
+    _close(apex.fwd(q, k, v, window=window, n_sink=sinks), ref, tol)
+    for lo, hi in ((0, 300), (300, 301), (301, 650)):
+        got = apex.fwd(q[:, :, lo:hi].contiguous(), k[:, :, :hi].contiguous(), v[:, :, :hi].contiguous(), window=window,
+                       n_sink=sinks, q_pos0=lo)
+        assert ((got.double() - ref[:, :, lo:hi]).abs() <= tol[:, :, lo:hi]).all()
+    for at in (650, 651, 699):
+        got = apex.decode(q[:, :, at:at + 1].contiguous(), k, v, at, window=window, n_sink=sinks)
+        assert ((got.double() - ref[:, :, at:at + 1]).abs() <= tol[:, :, at:at + 1]).all()
+
+
+@pytest.mark.gpu
+def test_captured_and_replayed():
+    dev = _gpu()
+    q, k, v = _inputs(dev, 9, 1, 8, 2, 600, 600, 128)
+    q1 = q[:, :, -1:].contiguous()
+    ws = torch.empty(apex.decode_workspace_bytes(1, 8, 2, 600, 128), dtype=torch.uint8, device=dev)
+
+    def calls():
+        return (apex.fwd(q, k, v, window=100, n_sink=4, workspace=False),
+                apex.decode(q1, k, v, 599, window=100, n_sink=4, workspace=ws))
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = calls()
+    for _ in range(2):
+        for x in (q, k, v, q1):
+            x.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in outs]
+        assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+
+
+# ------------------------------------------------------------------------------------------------- refusals
+@pytest.fixture(scope="module")
+def lib():
+    try:
+        return apex.load_library()
+    except RuntimeError:
+        pytest.skip("library not built")
+
+
+P = 1 << 20  # an aligned address that a refused call never touches
+BAD, UNSUPPORTED = 1, 2
+
+REFUSED = [
+    (dict(q=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD), (dict(out=None), BAD), (dict(q=P + 2), BAD),
+    (dict(out=P + 8), BAD), (dict(n_sink=-1), BAD), (dict(d_r=-64), BAD), (dict(d_r=63), BAD),
+    (dict(d_r=32), UNSUPPORTED), (dict(d=64, d_r=64), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(H_kv=3), BAD),
+    (dict(B=0), BAD), (dict(opt=dict(rope_base=-1.0)), BAD),
+]
+
+
+@pytest.mark.parametrize("o,code", REFUSED + [(dict(ws=P + 8), BAD), (dict(S=0), BAD), (dict(S=65), BAD),
+                                              (dict(opt=dict(prefix_len=65)), BAD), (dict(opt=dict(q_pos=-1)), BAD)])
+def test_prefill_refuses(lib, o, code):
+    a = dict(q=P, k=P, v=P, out=2 * P, B=1, H_q=8, H_kv=2, S=64, Sk=64, d=128, d_r=0, n_sink=4, ws=None, n=0, opt={})
+    a.update(o)
+    opt = apex.Options(**dict(dict(window=16), **a["opt"]))
+    assert apex.apex_attn_sink_fwd(a["q"], a["k"], a["v"], a["out"], a["B"], a["H_q"], a["H_kv"], a["S"], a["Sk"], a["d"],
+                                   a["d_r"], a["n_sink"], opt, a["ws"], a["n"], None) == code
+    assert apex.apex_attn_sink_fwd(P, P, P, 2 * P, 1, 8, 2, 64, 64, 128, 0, 4, None, None, 0, None) == BAD
+
+
+@pytest.mark.parametrize("o,code", REFUSED + [(dict(ws=None), BAD), (dict(ws=P + 8), BAD), (dict(n=15), BAD),
+                                              (dict(opt=dict(q_pos=64)), BAD), (dict(opt=dict(q_pos=-1)), BAD)])
+def test_decode_refuses(lib, o, code):
+    a = dict(q=P, k=P, v=P, out=2 * P, B=1, H_q=8, H_kv=2, Sk=64, d=128, d_r=0, n_sink=4, ws=P, n=1 << 40, opt={})
+    a.update(o)
+    opt = apex.Options(**dict(dict(window=16), **a["opt"]))
+    assert apex.apex_attn_sink_decode(a["q"], a["k"], a["v"], a["out"], a["B"], a["H_q"], a["H_kv"], a["Sk"], a["d"],
+                                      a["d_r"], a["n_sink"], opt, a["ws"], a["n"], None) == code
+
+
+def test_workspace_bytes(lib):
+    opt, plain = apex.Options(window=4096), apex.apex_attn_fwd_workspace_bytes
+    sized = apex.apex_attn_sink_fwd_workspace_bytes
+    assert sized(1, 32, 8, 65536, 65536, 128, 0, 64, opt) == plain(1, 32, 8, 65536, 65536, 128, opt) > 0
+    assert sized(1, 32, 8, 65536, 65536, 128, 0, -1, opt) == 0 and sized(1, 32, 8, 64, 64, 128, 0, 4, None) == 0
+    assert sized(1, 32, 8, 64, 65, 128, -64, 4, opt) == 0 and sized(1, 32, 8, 64, 64, 64, 64, 4, opt) == 0
+
+
+@pytest.mark.gpu
+def test_conveniences_refuse():
+    dev = _gpu()
+    q, k, v = _inputs(dev, 10, 1, 4, 2, 64, 64, 128)
+    for bad in (lambda: apex.fwd(q, k, v, window=8, n_sink=-1), lambda: apex.decode(q[:, :, :1].contiguous(), k, v, 63, window=8, n_sink=-2)):
+        with pytest.raises(ValueError):
+            bad()

@@ -11,15 +11,22 @@ Raw C-ABI names (pointers and sizes):
     apex_attn_fwd_ex, apex_attn_fwd_ws, apex_attn_fwd_workspace_bytes, apex_attn_decode_ex, apex_attn_rope_keys,
     apex_attn_mla_fwd, apex_attn_mla_fwd_ws, apex_attn_mla_fwd_workspace_bytes, apex_attn_mla_decode,
     apex_attn_mla_rope_keys (with an Options struct),
+    apex_attn_sink_fwd, apex_attn_sink_fwd_workspace_bytes, apex_attn_sink_decode (windows with sinks),
     apex_attn_rope (with RopeOptions and RopeTensor structs), apex_attn_tree_decode, apex_attn_tree_workspace_bytes,
     apex_attn_decode_weights, apex_attn_decode_weights_workspace_bytes, apex_attn_evict,
-    apex_attn_evict_workspace_bytes
+    apex_attn_evict_workspace_bytes, apex_attn_norm_rope and apex_attn_norm_rope_grad (with NormTensor structs),
+    apex_attn_norm_rope_grad_workspace_bytes, apex_attn_append4 and apex_attn_unpack4 (with Bits4Tensor structs),
+    apex_attn_decode4, apex_attn_decode4_workspace_bytes
 Tensor conveniences (torch, bf16, contiguous, on the current CUDA device):
     fwd(q, k, v, ...), decode(q, k_cache, v_cache, q_pos, ...), rope_keys(k, ...), mla_fwd(q, k, v, d_r, ...),
     mla_decode(q, k_cache, v_cache, q_pos, d_r, ...), mla_rope_keys(k, d_r, ...)
 Over caches of rotated keys (int32 lengths and positions on the device; the tensors' own device):
-    rope(q, k, v, positions=...), tree_decode(q, k_cache, v_cache, lens, ...),
+    rope(q, k, v, positions=...), norm_rope(q, k, v, positions=..., q_weight=..., k_weight=...) and its gradient
+    norm_rope_grad(q_grad, q, k_grad, k, positions=...), tree_decode(q, k_cache, v_cache, lens, ...),
     decode_weights(q, k_cache, v_cache, lens, acc, ...), evict(k_cache, v_cache, acc, lens, budget, ...)
+Over caches held in 4 bits:
+    append4(k, v, k4, k_scale, v4, v_scale, row0=...), unpack4(k4, k_scale, v4, v_scale, row0=..., n_rows=...),
+    decode4(q, k4, k_scale, v4, v_scale, lens, ...)
 """
 from __future__ import annotations
 
@@ -42,6 +49,11 @@ __all__ = [
     "apex_attn_decode_weights_workspace_bytes", "apex_attn_evict", "apex_attn_evict_workspace_bytes",
     "RopeOptions", "RopeTensor", "rope", "tree_decode", "tree_workspace_bytes", "decode_weights",
     "decode_weights_workspace_bytes", "evict", "evict_workspace_bytes",
+    "apex_attn_norm_rope", "apex_attn_norm_rope_grad", "apex_attn_norm_rope_grad_workspace_bytes", "NormTensor",
+    "norm_rope", "norm_rope_grad", "norm_rope_grad_workspace_bytes",
+    "apex_attn_append4", "apex_attn_unpack4", "apex_attn_decode4", "apex_attn_decode4_workspace_bytes", "Bits4Tensor",
+    "append4", "unpack4", "decode4", "decode4_workspace_bytes",
+    "apex_attn_sink_fwd", "apex_attn_sink_fwd_workspace_bytes", "apex_attn_sink_decode",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -75,6 +87,22 @@ class RopeTensor(ctypes.Structure):
     _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n_heads", ctypes.c_int),
                 ("d_row", ctypes.c_int)] + [(n, ctypes.c_longlong) for n in ("in_b", "in_h", "in_s", "out_b",
                                                                              "out_h", "out_s")]
+
+
+class NormTensor(ctypes.Structure):
+    """apex_norm_tensor of include/apex_attn.h (strides in elements)."""
+    _fields_ = [("x", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("dweight", ctypes.c_void_p), ("n_heads", ctypes.c_int),
+                ("d_row", ctypes.c_int), ("weight_f32", ctypes.c_int), ("weight_per_head", ctypes.c_int)] + \
+               [(n, ctypes.c_longlong) for n in ("x_b", "x_h", "x_s", "dy_b", "dy_h", "dy_s", "out_b", "out_h",
+                                                 "out_s")]
+
+
+class Bits4Tensor(ctypes.Structure):
+    """apex_bits4_tensor of include/apex_attn.h (strides in elements)."""
+    _fields_ = [("rows", ctypes.c_void_p), ("bytes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("factor", ctypes.c_void_p), ("b", ctypes.c_longlong), ("h", ctypes.c_longlong),
+                ("s", ctypes.c_longlong), ("d", ctypes.c_int)]
 
 
 class ApexError(RuntimeError):
@@ -121,6 +149,12 @@ def load_library():
             lib.apex_attn_mla_fwd_workspace_bytes.restype = sz
             lib.apex_attn_mla_decode.argtypes = [vp, vp, vp, vp] + [i32] * 6 + [op, vp, sz, vp]
             lib.apex_attn_mla_decode.restype = i32
+            lib.apex_attn_sink_fwd.argtypes = [vp, vp, vp, vp] + [i32] * 8 + [op, vp, sz, vp]
+            lib.apex_attn_sink_fwd.restype = i32
+            lib.apex_attn_sink_fwd_workspace_bytes.argtypes = [i32] * 8 + [op]
+            lib.apex_attn_sink_fwd_workspace_bytes.restype = sz
+            lib.apex_attn_sink_decode.argtypes = [vp, vp, vp, vp] + [i32] * 7 + [op, vp, sz, vp]
+            lib.apex_attn_sink_decode.restype = i32
             lib.apex_attn_decode_ex.argtypes = [vp, vp, vp, vp] + [i32] * 5 + [op, vp, sz, vp]
             lib.apex_attn_decode_ex.restype = i32
             lib.apex_attn_rope_keys.argtypes = [vp, vp] + [i32] * 4 + [ctypes.c_longlong] * 2 + [op, vp]
@@ -131,6 +165,19 @@ def load_library():
             # the structs by address: byref(...) or their bytes
             lib.apex_attn_rope.argtypes = [vp, vp, vp, i32, i32, vp, i64, vp, i32, vp, vp]
             lib.apex_attn_rope.restype = i32
+            lib.apex_attn_norm_rope.argtypes = [vp, vp, vp, i32, i32, vp, i64, vp, i32, vp, f32, vp]
+            lib.apex_attn_norm_rope.restype = i32
+            lib.apex_attn_norm_rope_grad.argtypes = [vp, vp, i32, i32, vp, i64, vp, f32, vp, sz, vp]
+            lib.apex_attn_norm_rope_grad.restype = i32
+            lib.apex_attn_norm_rope_grad_workspace_bytes.argtypes = [i32] * 4
+            lib.apex_attn_norm_rope_grad_workspace_bytes.restype = sz
+            for move in (lib.apex_attn_append4, lib.apex_attn_unpack4):
+                move.argtypes = [vp, vp] + [i32] * 4 + [vp, vp]
+                move.restype = i32
+            lib.apex_attn_decode4.argtypes = [vp] * 6 + [i32] * 7 + [vp, i32, i32, vp, vp, f32, vp, sz, vp]
+            lib.apex_attn_decode4.restype = i32
+            lib.apex_attn_decode4_workspace_bytes.argtypes = [i32] * 7
+            lib.apex_attn_decode4_workspace_bytes.restype = sz
             lib.apex_attn_tree_decode.argtypes = [vp] * 4 + [i32] * 7 + [vp, vp, i64, vp, i32, f32, vp, sz, vp]
             lib.apex_attn_tree_decode.restype = i32
             lib.apex_attn_tree_workspace_bytes.argtypes = [i32] * 7
@@ -215,6 +262,25 @@ def apex_attn_mla_decode(q, k_cache, v_cache, out, B, H_q, H_kv, S_k, d_h, d_r, 
                                                workspace_bytes, stream)
 
 
+def apex_attn_sink_fwd(q, k, v, out, B, H_q, H_kv, S_q, S_k, d_h, d_r, n_sink, opt, workspace, workspace_bytes,
+                       stream) -> int:
+    return load_library().apex_attn_sink_fwd(q, k, v, out, B, H_q, H_kv, S_q, S_k, d_h, d_r, n_sink,
+                                             ctypes.byref(opt) if opt is not None else None, workspace,
+                                             workspace_bytes, stream)
+
+
+def apex_attn_sink_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, d_r, n_sink, opt) -> int:
+    return load_library().apex_attn_sink_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, d_r, n_sink,
+                                                             ctypes.byref(opt) if opt is not None else None)
+
+
+def apex_attn_sink_decode(q, k_cache, v_cache, out, B, H_q, H_kv, S_k, d_h, d_r, n_sink, opt, workspace,
+                          workspace_bytes, stream) -> int:
+    return load_library().apex_attn_sink_decode(q, k_cache, v_cache, out, B, H_q, H_kv, S_k, d_h, d_r, n_sink,
+                                                ctypes.byref(opt) if opt is not None else None, workspace,
+                                                workspace_bytes, stream)
+
+
 def apex_attn_decode_ex(q, k_cache, v_cache, out, B, H_q, H_kv, S_k, d_h, opt, workspace, workspace_bytes,
                         stream) -> int:
     return load_library().apex_attn_decode_ex(q, k_cache, v_cache, out, B, H_q, H_kv, S_k, d_h,
@@ -240,6 +306,43 @@ def apex_attn_rope(q, k, v, B, S, positions, pos_stride, row0, out_rows, opt, st
     ref = [ctypes.byref(t) if isinstance(t, ctypes.Structure) else t for t in (q, k, v, opt)]
     return load_library().apex_attn_rope(ref[0], ref[1], ref[2], B, S, positions, pos_stride, row0, out_rows, ref[3],
                                          stream)
+
+
+def apex_attn_norm_rope(q, k, v, B, S, positions, pos_stride, row0, out_rows, opt, eps, stream) -> int:
+    ref = [ctypes.byref(t) if isinstance(t, ctypes.Structure) else t for t in (q, k, v, opt)]
+    return load_library().apex_attn_norm_rope(ref[0], ref[1], ref[2], B, S, positions, pos_stride, row0, out_rows,
+                                              ref[3], eps, stream)
+
+
+def apex_attn_norm_rope_grad(q, k, B, S, positions, pos_stride, opt, eps, workspace, workspace_bytes, stream) -> int:
+    ref = [ctypes.byref(t) if isinstance(t, ctypes.Structure) else t for t in (q, k, opt)]
+    return load_library().apex_attn_norm_rope_grad(ref[0], ref[1], B, S, positions, pos_stride, ref[2], eps, workspace,
+                                                   workspace_bytes, stream)
+
+
+def apex_attn_norm_rope_grad_workspace_bytes(H_q, H_kv, d_q, d_k) -> int:
+    return load_library().apex_attn_norm_rope_grad_workspace_bytes(H_q, H_kv, d_q, d_k)
+
+
+def apex_attn_append4(k, v, B, H_kv, S, S_cap, row0, stream) -> int:
+    ref = [ctypes.byref(t) if isinstance(t, ctypes.Structure) else t for t in (k, v)]
+    return load_library().apex_attn_append4(ref[0], ref[1], B, H_kv, S, S_cap, row0, stream)
+
+
+def apex_attn_unpack4(k, v, B, H_kv, S, S_cap, row0, stream) -> int:
+    ref = [ctypes.byref(t) if isinstance(t, ctypes.Structure) else t for t in (k, v)]
+    return load_library().apex_attn_unpack4(ref[0], ref[1], B, H_kv, S, S_cap, row0, stream)
+
+
+def apex_attn_decode4(q, k4, k_scale, v4, v_scale, out, B, H_q, H_kv, T, S_cap, d_qk, d_v, lens, window, n_sink,
+                      k_factor, v_factor, scale, workspace, workspace_bytes, stream) -> int:
+    return load_library().apex_attn_decode4(q, k4, k_scale, v4, v_scale, out, B, H_q, H_kv, T, S_cap, d_qk, d_v, lens,
+                                            window, n_sink, k_factor, v_factor, scale, workspace, workspace_bytes,
+                                            stream)
+
+
+def apex_attn_decode4_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_v) -> int:
+    return load_library().apex_attn_decode4_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_v)
 
 
 def apex_attn_tree_decode(q, k_cache, v_cache, out, B, H_q, H_kv, T, S_cap, d_qk, d_v, lens, tree_mask, mask_stride,
@@ -315,6 +418,27 @@ def _options(window=0, q_pos=0, rope_base=10000.0, yarn_scale=1.0, yarn_beta_fas
                    float(yarn_beta_slow), int(prefix_len), 1 if keys_prerotated else 0)
 
 
+def _sinks(n_sink, window) -> int:
+    """Sinks of a call: none without a window."""
+    if n_sink < 0:
+        raise ValueError("n_sink must not be negative")
+    return min(int(n_sink), 2 ** 24) if window > 0 else 0
+
+
+def _sink_fwd(q, k, v, out, sizes, d_r, n_sink, opt, workspace, stream):
+    """Prefill with sinks: apex_attn_sink_fwd, its workspace as for the calls without."""
+    import torch
+    if workspace is None:
+        need = int(apex_attn_sink_fwd_workspace_bytes(*sizes, d_r, n_sink, opt))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else False
+    ws, n = (None, 0) if workspace is False else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = apex_attn_sink_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *sizes, d_r, n_sink, opt, ws, n,
+                            _stream_handle(stream))
+    if st != APEX_OK:
+        raise ApexError(st, "apex_attn_sink_fwd")
+    return out
+
+
 def fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, *, window: int = 0, q_pos0: int = 0,
                         rope_base: float = 10000.0, yarn_scale: float = 1.0, yarn_beta_fast: float = 32.0,
                         yarn_beta_slow: float = 1.0, prefix_len: int = 0, keys_prerotated: bool = False) -> int:
@@ -326,8 +450,10 @@ def fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, *, window: int = 0, q_pos0:
 
 def fwd(q, k, v, *, window: int = 0, q_pos0: int = 0, rope_base: float = 10000.0, out=None, stream=None,
         yarn_scale: float = 1.0, yarn_beta_fast: float = 32.0, yarn_beta_slow: float = 1.0, prefix_len: int = 0,
-        keys_prerotated: bool = False, workspace=None):
+        keys_prerotated: bool = False, workspace=None, n_sink: int = 0):
     """Prefill. q [B,H_q,S_q,d], k/v [B,H_kv,S_k,d] (bf16, CUDA) -> out [B,H_q,S_q,d].
+
+    n_sink: the first keys, which stay visible behind a window (sinks).
 
     workspace: None -- when the library would rotate the keys once before the
     prefill (fwd_workspace_bytes > 0), a buffer for them is taken from torch's
@@ -341,6 +467,11 @@ def fwd(q, k, v, *, window: int = 0, q_pos0: int = 0, rope_base: float = 10000.0
     if out is None:
         out = torch.empty_like(q)
     _check(out, "out", 4)
+    n_sink = _sinks(n_sink, window)
+    if n_sink:
+        opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
+                       keys_prerotated)
+        return _sink_fwd(q, k, v, out, (B, H_q, H_kv, S_q, S_k, d), 0, n_sink, opt, workspace, stream)
     if workspace is None:
         need = fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d, window=window, q_pos0=q_pos0, rope_base=rope_base,
                                    yarn_scale=yarn_scale, yarn_beta_fast=yarn_beta_fast,
@@ -380,9 +511,11 @@ def mla_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, d_r, *, window: int = 0
 
 def mla_fwd(q, k, v, d_r: int, *, window: int = 0, q_pos0: int = 0, rope_base: float = 10000.0, out=None,
             stream=None, yarn_scale: float = 1.0, yarn_beta_fast: float = 32.0, yarn_beta_slow: float = 1.0,
-            prefix_len: int = 0, keys_prerotated: bool = False, workspace=None):
+            prefix_len: int = 0, keys_prerotated: bool = False, workspace=None, n_sink: int = 0):
     """Decoupled-RoPE prefill. q [B,H_q,S_q,d_h+d_r], k [B,H_kv,S_k,d_h+d_r], v [B,H_kv,S_k,d_h]
     (bf16, CUDA; rows [content | rope part]) -> out [B,H_q,S_q,d_h].
+
+    n_sink: the first keys, which stay visible behind a window (sinks).
 
     workspace: None -- a buffer from torch's allocator when the library would rotate
     the keys' rope parts once before the prefill (mla_fwd_workspace_bytes > 0); a
@@ -399,6 +532,9 @@ def mla_fwd(q, k, v, d_r: int, *, window: int = 0, q_pos0: int = 0, rope_base: f
     _check(out, "out", 4)
     opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                    keys_prerotated)
+    n_sink = _sinks(n_sink, window)
+    if n_sink:
+        return _sink_fwd(q, k, v, out, (B, H_q, H_kv, S_q, S_k, d_h), int(d_r), n_sink, opt, workspace, stream)
     if workspace is None:
         need = int(apex_attn_mla_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, int(d_r), opt))
         if need > 0:
@@ -423,8 +559,10 @@ def decode_workspace_bytes(B, H_q, H_kv, S_k, d_h) -> int:
 
 def decode(q, k_cache, v_cache, q_pos: int, *, window: int = 0, rope_base: float = 10000.0, out=None,
            workspace=None, stream=None, yarn_scale: float = 1.0, yarn_beta_fast: float = 32.0,
-           yarn_beta_slow: float = 1.0, prefix_len: int = 0, keys_prerotated: bool = False):
-    """Decode. q [B,H_q,1,d], caches [B,H_kv,S_k,d] (bf16, CUDA) -> out [B,H_q,1,d]."""
+           yarn_beta_slow: float = 1.0, prefix_len: int = 0, keys_prerotated: bool = False, n_sink: int = 0):
+    """Decode. q [B,H_q,1,d], caches [B,H_kv,S_k,d] (bf16, CUDA) -> out [B,H_q,1,d].
+
+    n_sink: the first keys, which stay visible behind a window (sinks)."""
     import torch
     for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
         _check(t, n, 4)
@@ -439,7 +577,8 @@ def decode(q, k_cache, v_cache, q_pos: int, *, window: int = 0, rope_base: float
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     ws_bytes = workspace.numel() * workspace.element_size()
-    plain = yarn_scale <= 1.0 and prefix_len == 0 and not keys_prerotated
+    n_sink = _sinks(n_sink, window)
+    plain = yarn_scale <= 1.0 and prefix_len == 0 and not keys_prerotated and not n_sink
     if plain:
         st = apex_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
                               S_k, d, int(window), int(q_pos), float(rope_base), workspace.data_ptr(), ws_bytes,
@@ -447,8 +586,13 @@ def decode(q, k_cache, v_cache, q_pos: int, *, window: int = 0, rope_base: float
     else:
         opt = _options(window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                        keys_prerotated)
-        st = apex_attn_decode_ex(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q,
-                                 H_kv, S_k, d, opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
+        if n_sink:
+            st = apex_attn_sink_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q,
+                                       H_kv, S_k, d, 0, n_sink, opt, workspace.data_ptr(), ws_bytes,
+                                       _stream_handle(stream))
+        else:
+            st = apex_attn_decode_ex(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q,
+                                     H_kv, S_k, d, opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
     if st != APEX_OK:
         raise ApexError(st, "apex_attn_decode")
     return out
@@ -456,9 +600,12 @@ def decode(q, k_cache, v_cache, q_pos: int, *, window: int = 0, rope_base: float
 
 def mla_decode(q, k_cache, v_cache, q_pos: int, d_r: int, *, window: int = 0, rope_base: float = 10000.0,
                out=None, workspace=None, stream=None, yarn_scale: float = 1.0, yarn_beta_fast: float = 32.0,
-               yarn_beta_slow: float = 1.0, prefix_len: int = 0, keys_prerotated: bool = False):
+               yarn_beta_slow: float = 1.0, prefix_len: int = 0, keys_prerotated: bool = False,
+               n_sink: int = 0):
     """Decoupled-RoPE decode. q [B,H_q,1,d_h+d_r], k_cache [B,H_kv,S_k,d_h+d_r], v_cache [B,H_kv,S_k,d_h]
-    (bf16, CUDA; rows [content | rope part]) -> out [B,H_q,1,d_h]."""
+    (bf16, CUDA; rows [content | rope part]) -> out [B,H_q,1,d_h].
+
+    n_sink: the first keys, which stay visible behind a window (sinks)."""
     import torch
     for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
         _check(t, n, 4)
@@ -477,8 +624,14 @@ def mla_decode(q, k_cache, v_cache, q_pos: int, d_r: int, *, window: int = 0, ro
     ws_bytes = workspace.numel() * workspace.element_size()
     opt = _options(window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                    keys_prerotated)
-    st = apex_attn_mla_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
-                              S_k, d_h, int(d_r), opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
+    n_sink = _sinks(n_sink, window)
+    if n_sink:
+        st = apex_attn_sink_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
+                                   S_k, d_h, int(d_r), n_sink, opt, workspace.data_ptr(), ws_bytes,
+                                   _stream_handle(stream))
+    else:
+        st = apex_attn_mla_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
+                                  S_k, d_h, int(d_r), opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
     if st != APEX_OK:
         raise ApexError(st, "apex_attn_mla_decode")
     return out
@@ -613,8 +766,24 @@ assert _ROPE_TENSOR.size == ctypes.sizeof(RopeTensor) and _ROPE_OPTIONS.size == 
 _rope_options = functools.lru_cache(maxsize=64)(_ROPE_OPTIONS.pack)
 
 
-def _rope_rows(x, out, name, B, S, into, device):
-    """apex_rope_tensor of a tensor and its output, as bytes."""
+def _turn_options(name, layout, rot_start, d_rot, inverse, rope_base, linear_scale, yarn_scale, yarn_beta_fast,
+                  yarn_beta_slow):
+    """apex_rope_options as bytes."""
+    if layout != "interleaved" and layout != "half":
+        raise ValueError("layout must be 'interleaved' or 'half'")
+    if d_rot is None:
+        d_rot = 0
+    elif d_rot <= 0:
+        raise ValueError("d_rot must be positive")
+    try:
+        return _rope_options(1 if layout == "half" else 0, rot_start, d_rot, 1 if inverse else 0, rope_base,
+                             linear_scale, yarn_scale, yarn_beta_fast, yarn_beta_slow)
+    except struct.error as e:
+        raise ValueError("%s's options: %s" % (name, e)) from None
+
+
+def _row_pair(x, out, name, B, S, into, device):
+    """Shape and strides of a tensor and of its output."""
     bf16 = _torch.bfloat16
     try:
         known = x.dtype is bf16 and out.dtype is bf16 and x.get_device() == device == out.get_device()
@@ -632,13 +801,19 @@ def _rope_rows(x, out, name, B, S, into, device):
     if (to != xs and not into) or to[0] != B or to[1] != xs[1] or to[3] != xs[3]:
         raise ValueError("%s_out does not fit %s" % (name, name))
     if xs[1] > _INT_MAX or xs[3] > _INT_MAX or to[2] > _INT_MAX:
-        raise ValueError("%s has more heads or entries, or %s_out more rows, than rope takes" % (name, name))
+        raise ValueError("%s has more heads or entries, or %s_out more rows, than are taken" % (name, name))
     xb, xh, xr, xe = x.stride()
     ob, oh, orow, oe = out.stride()
     if (xe != 1 or oe != 1) and xs[3] > 1:
         raise ValueError("the last dimension of %s and %s_out must be contiguous" % (name, name))
     if (ob == 0 and B > 1) or (oh == 0 and to[1] > 1) or (orow == 0 and to[2] > 1):
         raise ValueError("%s_out repeats its elements" % name)
+    return xs, xb, xh, xr, ob, oh, orow
+
+
+def _rope_rows(x, out, name, B, S, into, device):
+    """apex_rope_tensor of a tensor and its output, as bytes."""
+    xs, xb, xh, xr, ob, oh, orow = _row_pair(x, out, name, B, S, into, device)
     return _ROPE_TENSOR.pack(x.data_ptr(), out.data_ptr(), xs[1], xs[3], xb, xh, xr, ob, oh, orow)
 
 
@@ -656,23 +831,14 @@ def rope(q, k=None, v=None, *, positions, layout: str = "interleaved", rot_start
     other output.  row0 [B] int32: token s of k and v goes to row row0[b] + s of k_out and v_out
     (caches [B,H_kv,S_cap,d]); rows outside them are dropped, the others untouched."""
     torch = _torch or _load_torch()
-    if layout != "interleaved" and layout != "half":
-        raise ValueError("layout must be 'interleaved' or 'half'")
-    if d_rot is None:
-        d_rot = 0
-    elif d_rot <= 0:
-        raise ValueError("d_rot must be positive")
+    opt = _turn_options("rope", layout, rot_start, d_rot, inverse, rope_base, linear_scale, yarn_scale,
+                        yarn_beta_fast, yarn_beta_slow)
     if k is None and (v is not None or k_out is not None) or v is None and v_out is not None:
         raise ValueError("k_out goes with k, and v and v_out with k")
     B, _, S, _ = _rows4(q, "q")
     if B > _INT_MAX or S > _INT_MAX:
         raise ValueError("more sequences or tokens than rope takes")
     device = q.get_device()
-    try:
-        opt = _rope_options(1 if layout == "half" else 0, rot_start, d_rot, 1 if inverse else 0, rope_base,
-                            linear_scale, yarn_scale, yarn_beta_fast, yarn_beta_slow)
-    except struct.error as e:
-        raise ValueError("rope's options: %s" % e) from None
     at = _Launch(device, stream)
     try:
         pos = _fit(positions, "positions", torch.int32, (S,) if positions.dim() == 1 else (B, S), device)
@@ -703,6 +869,142 @@ def rope(q, k=None, v=None, *, positions, layout: str = "interleaved", rot_start
     finally:
         at.leave()
     return q_out if k is None else (q_out, k_out) if v is None else (q_out, k_out, v_out)
+
+
+_NORM_TENSOR = struct.Struct("@PPPPPiiiiqqqqqqqqq")
+assert _NORM_TENSOR.size == ctypes.sizeof(NormTensor)
+
+
+def _norm_weight(w, name, heads, d, device):
+    """Address of a norm's weights, whether they are fp32 and whether each head has its own."""
+    torch = _torch
+    if w is None:
+        return 0, 0, 0
+    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("%s must be a CUDA bfloat16 or float32 tensor" % name)
+    if w.get_device() != device:
+        raise ValueError("%s is on another device than the other tensors" % name)
+    if (w.shape != (d,) and w.shape != (heads, d)) or not w.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of shape %s or %s" % (name, (d,), (heads, d)))
+    return w.data_ptr(), 1 if w.dtype is torch.float32 else 0, 1 if w.dim() == 2 else 0
+
+
+def _norm_rows(x, out, weight, name, B, S, into, device):
+    """apex_norm_tensor of a tensor, its output and weights, as bytes."""
+    xs, xb, xh, xr, ob, oh, orow = _row_pair(x, out, name, B, S, into, device)
+    pw, f32, per_head = _norm_weight(weight, name + "_weight", xs[1], xs[3], device)
+    return _NORM_TENSOR.pack(x.data_ptr(), 0, out.data_ptr(), pw, 0, xs[1], xs[3], f32, per_head, xb, xh, xr, 0, 0, 0,
+                             ob, oh, orow)
+
+
+def norm_rope(q, k=None, v=None, *, positions, q_weight=None, k_weight=None, eps: float = 1e-6,
+              layout: str = "interleaved", rot_start: int = 0, d_rot=None, rope_base: float = 10000.0,
+              linear_scale: float = 1.0, yarn_scale: float = 1.0, yarn_beta_fast: float = 32.0,
+              yarn_beta_slow: float = 1.0, q_out=None, k_out=None, v_out=None, row0=None, stream=None):
+    """RMS norm of every head, then its rotary position, in one pass. q [B,H_q,S,d], optional k [B,H_kv,S,d] and
+    v [B,H_kv,S,d_v] (bf16, CUDA; any strides, rows contiguous), positions [B,S] or [S] int32 -> the new q, or
+    (q, k) or (q, k, v) as given.
+
+    A row x becomes R(x / sqrt(mean(x^2) + eps) * weight): the whole row is normed, the d_rot entries from
+    rot_start on are turned.  q_weight, k_weight: bf16 or fp32, [d] or, for each head its own, [H,d] (None: ones).
+    Layouts, frequencies, outputs and row0 (appending k and v to caches) as for rope."""
+    torch = _torch or _load_torch()
+    if k is None and (v is not None or k_out is not None or k_weight is not None) or v is None and v_out is not None:
+        raise ValueError("k_out and k_weight go with k, and v and v_out with k")
+    B, _, S, _ = _rows4(q, "q")
+    if B > _INT_MAX or S > _INT_MAX:
+        raise ValueError("more sequences or tokens than norm_rope takes")
+    device = q.get_device()
+    opt = _turn_options("norm_rope", layout, rot_start, d_rot, False, rope_base, linear_scale, yarn_scale,
+                        yarn_beta_fast, yarn_beta_slow)
+    at = _Launch(device, stream)
+    try:
+        pos = _fit(positions, "positions", torch.int32, (S,) if positions.dim() == 1 else (B, S), device)
+        if q_out is None:
+            q_out = at.new(q, q.shape, torch.bfloat16)
+        tq, tk, tv = _norm_rows(q, q_out, q_weight, "q", B, S, False, device), None, None
+        into, rows, start = row0 is not None, 0, None
+        if into:
+            if k is None or k_out is None or (v is not None and v_out is None):
+                raise ValueError("row0 needs k_out, and v_out where there is a v")
+            start = _fit(row0, "row0", torch.int32, (B,), device)
+        if k is not None:
+            if k_out is None:
+                k_out = at.new(k, k.shape, torch.bfloat16)
+            tk = _norm_rows(k, k_out, k_weight, "k", B, S, into, device)
+        if v is not None:
+            if v_out is None:
+                v_out = at.new(v, v.shape, torch.bfloat16)
+            tv = _rope_rows(v, v_out, "v", B, S, into, device)
+        if into:
+            rows = k_out.shape[2]
+            if v is not None and v_out.shape[2] != rows:
+                raise ValueError("k_out and v_out must have the same number of rows")
+        status = (_lib or load_library()).apex_attn_norm_rope(
+            tq, tk, tv, B, S, pos, S if positions.dim() == 2 else 0, start, rows, opt, eps, at.handle)
+        if status:
+            raise ApexError(status, "apex_attn_norm_rope")
+    finally:
+        at.leave()
+    return q_out if k is None else (q_out, k_out) if v is None else (q_out, k_out, v_out)
+
+
+@functools.lru_cache(maxsize=256)
+def norm_rope_grad_workspace_bytes(H_q, H_kv, d_q, d_k=None) -> int:
+    """Workspace bytes of norm_rope_grad for these sizes (0: invalid; H_kv 0: without k)."""
+    return int(apex_attn_norm_rope_grad_workspace_bytes(H_q, H_kv, d_q, d_q if d_k is None else d_k))
+
+
+def norm_rope_grad(q_grad, q, k_grad=None, k=None, *, positions, q_weight=None, k_weight=None, eps: float = 1e-6,
+                   layout: str = "interleaved", rot_start: int = 0, d_rot=None, rope_base: float = 10000.0,
+                   linear_scale: float = 1.0, yarn_scale: float = 1.0, yarn_beta_fast: float = 32.0,
+                   yarn_beta_slow: float = 1.0, q_out=None, k_out=None, workspace=None, stream=None):
+    """Gradients of norm_rope. q_grad and k_grad (of its results), q and k (its inputs) and the options as given to
+    it -> (gradient of q, of q_weight) or, with k, (of q, of k, of q_weight, of k_weight).
+
+    The gradients of q and k are bf16 (q_out, k_out: where to, any strides; such an output may be its own gradient
+    or input), those of the weights fp32, shaped as they (None without weights)."""
+    torch = _torch or _load_torch()
+    if (k is None) != (k_grad is None) or k is None and (k_out is not None or k_weight is not None):
+        raise ValueError("k, k_grad, k_out and k_weight go together")
+    B, H_q, S, d_q = _rows4(q, "q")
+    if B > _INT_MAX or S > _INT_MAX:
+        raise ValueError("more sequences or tokens than norm_rope_grad takes")
+    device = q.get_device()
+    opt = _turn_options("norm_rope_grad", layout, rot_start, d_rot, False, rope_base, linear_scale, yarn_scale,
+                        yarn_beta_fast, yarn_beta_slow)
+    at = _Launch(device, stream)
+
+    def rows(x, grad, out, weight, name):
+        if out is None:
+            out = at.new(x, x.shape, torch.bfloat16)
+        xs, xb, xh, xr, ob, oh, orow = _row_pair(x, out, name, B, S, False, device)
+        if _rows4(grad, name + "_grad") != xs or grad.get_device() != device:
+            raise ValueError("%s_grad does not fit %s" % (name, name))
+        gb, gh, gr, ge = grad.stride()
+        if ge != 1 and xs[3] > 1:
+            raise ValueError("the last dimension of %s_grad must be contiguous" % name)
+        pw, f32, per_head = _norm_weight(weight, name + "_weight", xs[1], xs[3], device)
+        dw = None if weight is None else at.new(weight, weight.shape, torch.float32)
+        return out, dw, _NORM_TENSOR.pack(x.data_ptr(), grad.data_ptr(), out.data_ptr(), pw,
+                                          0 if dw is None else dw.data_ptr(), xs[1], xs[3], f32, per_head, xb, xh, xr,
+                                          gb, gh, gr, ob, oh, orow)
+
+    try:
+        pos = _fit(positions, "positions", torch.int32, (S,) if positions.dim() == 1 else (B, S), device)
+        q_out, q_dw, tq = rows(q, q_grad, q_out, q_weight, "q")
+        tk, k_dw, H_kv, d_k = None, None, 0, 0
+        if k is not None:
+            _, H_kv, _, d_k = _rows4(k, "k")
+            k_out, k_dw, tk = rows(k, k_grad, k_out, k_weight, "k")
+        ws = at.workspace(workspace, q, norm_rope_grad_workspace_bytes(H_q, H_kv, d_q, d_k))
+        status = (_lib or load_library()).apex_attn_norm_rope_grad(
+            tq, tk, B, S, pos, S if positions.dim() == 2 else 0, opt, eps, ws.data_ptr(), ws.nbytes, at.handle)
+        if status:
+            raise ApexError(status, "apex_attn_norm_rope_grad")
+    finally:
+        at.leave()
+    return (q_out, q_dw) if k is None else (q_out, k_out, q_dw, k_dw)
 
 
 def _cache_shapes(q, k_cache, v_cache):
@@ -855,3 +1157,150 @@ def evict(k_cache, v_cache, acc, lens, budget: int, *, n_sink: int = 0, n_recent
     finally:
         at.leave()
     return acc_out, positions_out, lens_out
+
+
+# ------------------------------------------------------------------ over caches held in 4 bits
+_BITS4_TENSOR = struct.Struct("@PPPPqqqi4x")
+assert _BITS4_TENSOR.size == ctypes.sizeof(Bits4Tensor)
+
+
+def _packed4(x4, scales, name, like):
+    """Sizes (B, H_kv, S_cap, d) and device of a packed tensor, and its addresses."""
+    torch = _torch
+    try:
+        B, H, S_cap, half = x4.shape
+        device = x4.get_device()
+    except (AttributeError, ValueError):
+        device = -1
+    if device < 0:
+        raise (ValueError if isinstance(x4, torch.Tensor) and x4.is_cuda else TypeError)(
+            "%s4 must be a 4-D CUDA uint8 tensor" % name)
+    if like is not None and like != (B, H, S_cap, device):
+        raise ValueError("%s4 must have the batch, heads, rows and device of k4" % name)
+    if max(B, H, S_cap, half) > _INT_MAX // 2:
+        raise ValueError("%s4 has more sequences, heads or rows than a 4-bit cache takes" % name)
+    return (B, H, S_cap, device), 2 * half, _fit(x4, name + "4", torch.uint8, (B, H, S_cap, half), device), \
+        _fit(scales, name + "_scale", torch.float8_e4m3fn, (B, H, S_cap, half // 8), device)
+
+
+def _factor4(f, name, H, device):
+    return None if f is None else _fit(f, name + "_factor", _torch.float32, (H,), device)
+
+
+def _rows4_of(x, name, B, H, S, d, device):
+    """Address and strides of bf16 rows [B,H,S,d] of any strides."""
+    if _rows4(x, name) != (B, H, S, d) or x.get_device() != device:
+        raise ValueError("%s must be of shape %s, on the device of k4" % (name, (B, H, S, d)))
+    b, h, s, e = x.stride()
+    if e != 1 and d > 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+    return x.data_ptr(), b, h, s
+
+
+def append4(k, v, k4, k_scale, v4, v_scale, *, row0=None, k_factor=None, v_factor=None, stream=None):
+    """Append keys and values to a 4-bit cache, in place. k [B,H_kv,S,d_k], v [B,H_kv,S,d_v] (bf16, CUDA; any strides,
+    rows contiguous) go to rows row0[b] + s (row0 [B] int32; None: s) of k4 [B,H_kv,S_cap,d_k/2], v4 (uint8: two e2m1
+    values to a byte) and k_scale [B,H_kv,S_cap,d_k/16], v_scale (float8_e4m3fn: of 16 entries).
+
+    k_factor, v_factor [H_kv] fp32 (None: 1): entries stand for value * scale * factor; best a power of two near the
+    head's largest entry / 1000.  Rows outside the cache are dropped, the others untouched."""
+    torch = _torch or _load_torch()
+    size, d_k, pk4, pks = _packed4(k4, k_scale, "k", None)
+    _, d_v, pv4, pvs = _packed4(v4, v_scale, "v", size)
+    B, H, S_cap, device = size
+    S = _rows4(k, "k")[2]
+    if S > _INT_MAX:
+        raise ValueError("more tokens than append4 takes")
+    pk, kb, kh, ks = _rows4_of(k, "k", B, H, S, d_k, device)
+    pv, vb, vh, vs = _rows4_of(v, "v", B, H, S, d_v, device)
+    tk = _BITS4_TENSOR.pack(pk, pk4, pks, _factor4(k_factor, "k", H, device) or 0, kb, kh, ks, d_k)
+    tv = _BITS4_TENSOR.pack(pv, pv4, pvs, _factor4(v_factor, "v", H, device) or 0, vb, vh, vs, d_v)
+    start = None if row0 is None else _fit(row0, "row0", torch.int32, (B,), device)
+    at = _Launch(device, stream)
+    try:
+        status = (_lib or load_library()).apex_attn_append4(tk, tv, B, H, S, S_cap, start, at.handle)
+        if status:
+            raise ApexError(status, "apex_attn_append4")
+    finally:
+        at.leave()
+
+
+def unpack4(k4, k_scale, v4, v_scale, *, row0=None, n_rows=None, k_factor=None, v_factor=None, k_out=None, v_out=None,
+            stream=None):
+    """Rows of a 4-bit cache as bf16: row0[b] + s for s < n_rows (row0 [B] int32; None: from 0; n_rows None: S_cap)
+    -> (k [B,H_kv,n_rows,d_k], v [B,H_kv,n_rows,d_v]); rows outside the cache give zeros.
+
+    Packed tensors and factors as for append4; k_out, v_out: outputs of any strides, rows contiguous."""
+    torch = _torch or _load_torch()
+    size, d_k, pk4, pks = _packed4(k4, k_scale, "k", None)
+    _, d_v, pv4, pvs = _packed4(v4, v_scale, "v", size)
+    B, H, S_cap, device = size
+    S = S_cap if n_rows is None else n_rows
+    if not 0 < S <= _INT_MAX:
+        raise ValueError("n_rows must be positive and fit 32 bits")
+    fk, fv = _factor4(k_factor, "k", H, device), _factor4(v_factor, "v", H, device)
+    start = None if row0 is None else _fit(row0, "row0", torch.int32, (B,), device)
+    at = _Launch(device, stream)
+    try:
+        if k_out is None:
+            k_out = at.new(k4, (B, H, S, d_k), torch.bfloat16)
+        if v_out is None:
+            v_out = at.new(v4, (B, H, S, d_v), torch.bfloat16)
+        pk, kb, kh, ks = _rows4_of(k_out, "k_out", B, H, S, d_k, device)
+        pv, vb, vh, vs = _rows4_of(v_out, "v_out", B, H, S, d_v, device)
+        status = (_lib or load_library()).apex_attn_unpack4(
+            _BITS4_TENSOR.pack(pk, pk4, pks, fk or 0, kb, kh, ks, d_k),
+            _BITS4_TENSOR.pack(pv, pv4, pvs, fv or 0, vb, vh, vs, d_v), B, H, S, S_cap, start, at.handle)
+        if status:
+            raise ApexError(status, "apex_attn_unpack4")
+    finally:
+        at.leave()
+    return k_out, v_out
+
+
+@functools.lru_cache(maxsize=256)
+def decode4_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_v=None) -> int:
+    """Workspace bytes of decode4 for these sizes (0: invalid; see apex_attn_decode4_workspace_bytes)."""
+    return int(apex_attn_decode4_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_qk if d_v is None else d_v))
+
+
+def decode4(q, k4, k_scale, v4, v_scale, lens, *, window: int = 0, n_sink: int = 0, k_factor=None, v_factor=None,
+            scale=None, out=None, workspace=None, stream=None):
+    """Attention of T new tokens per sequence over a 4-bit cache of rotated keys. q [B,H_q,T,d_qk] (rotated), packed
+    tensors and factors as for append4 with the tokens' own rows at lens[b] + t, lens [B] int32 -> out [B,H_q,T,d_v].
+
+    Token t sees the rows j <= lens[b] + t and, with a window > 0, of those only the last `window` and the first n_sink
+    (sinks); row j is then at position j.  scale: factor of the scores (None or 0: 1 / sqrt(d_qk))."""
+    torch = _torch or _load_torch()
+    size, d_k, pk4, pks = _packed4(k4, k_scale, "k", None)
+    _, d_v, pv4, pvs = _packed4(v4, v_scale, "v", size)
+    B, H_kv, S_cap, device = size
+    shape = _rows4(q, "q")
+    if shape[0] != B or shape[3] != d_k:
+        raise ValueError("q must have the batch and row length of k4's keys")
+    _, H_q, T, d_qk = shape
+    if max(H_q, T) > _INT_MAX:
+        raise ValueError("more heads or tokens than decode4 takes")
+    pq = _fit(q, "q", torch.bfloat16, shape, device)
+    plens = _fit(lens, "lens", torch.int32, (B,), device)
+    if not 0 < window <= _INT_MAX:  # rows are int32: a wider window is none
+        window = 0
+    if n_sink < 0:
+        raise ValueError("n_sink must not be negative")
+    fk, fv = _factor4(k_factor, "k", H_kv, device), _factor4(v_factor, "v", H_kv, device)
+    at = _Launch(device, stream)
+    try:
+        if out is None:
+            out = at.new(q, (B, H_q, T, d_v), torch.bfloat16)
+            pout = out.data_ptr()
+        else:
+            pout = _fit(out, "out", torch.bfloat16, (B, H_q, T, d_v), device)
+        ws = at.workspace(workspace, q, decode4_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_v))
+        status = (_lib or load_library()).apex_attn_decode4(
+            pq, pk4, pks, pv4, pvs, pout, B, H_q, H_kv, T, S_cap, d_qk, d_v, plens, window, min(n_sink, S_cap), fk, fv,
+            0.0 if scale is None else scale, ws.data_ptr(), ws.nbytes, at.handle)
+        if status:
+            raise ApexError(status, "apex_attn_decode4")
+    finally:
+        at.leave()
+    return out

@@ -312,7 +312,7 @@ struct PrerotateCost {
 constexpr PrerotateCost kCostPlain{17, 100};
 constexpr PrerotateCost kCostDecoupled{11, 150};
 
-PrerotatePlan plan_prerotate(int units, int S_q, int S_k, int q_pos0, int window, int P, int block_rows,
+PrerotatePlan plan_prerotate(int units, int S_q, int S_k, int q_pos0, int window, int n_sink, int P, int block_rows,
                              PrerotateCost cost)
 {
     long long visits = 0;
@@ -322,7 +322,7 @@ PrerotatePlan plan_prerotate(int units, int S_q, int S_k, int q_pos0, int window
         const int m_first = q_pos0 + r0, m_last = q_pos0 + r0 + rows - 1;
         const int key_lo = (m_first < P || window <= 0) ? 0 : std::max(0, m_first - window + 1);
         const int key_hi = (m_first < P) ? std::max(m_last, P - 1) : m_last;
-        visits += key_hi / 128 - key_lo / 128 + 1;
+        visits += key_hi / 128 - key_lo / 128 + 1 + std::min(key_lo / 128, (n_sink + 127) / 128);
         kmax = std::max(kmax, key_hi);
     }
     const int n_pos = std::min(S_k, (kmax / 128 + 1) * 128);
@@ -410,7 +410,8 @@ size_t apex_attn_decode_workspace_bytes(int B, int H_q, int H_kv, int S_k, int d
 // attention (d_qk = d_v + d_rope); argument checks of the callers done.
 apex_status decode_launch(const void *q, const void *k_cache, const void *v_cache, void *out, int B, int H_q,
                           int H_kv, int S_k, int d_qk, int d_v, int d_rope, const apex_attn_options *opt,
-                          const RopeFreq &f, void *workspace, size_t workspace_bytes, apex_stream_t stream)
+                          const RopeFreq &f, void *workspace, size_t workspace_bytes, apex_stream_t stream,
+                          int n_sink = 0)
 {
     const int q_pos = opt->q_pos, window = opt->window, P = opt->prefix_len;
     if (q_pos < 0 || q_pos >= S_k) return APEX_ERR_INVALID_ARG;
@@ -463,6 +464,11 @@ apex_status decode_launch(const void *q, const void *k_cache, const void *v_cach
     }
     p.stage0 = p.k_lo / kDecodeKeysPerStage;
     p.n_stages = p.k_hi / kDecodeKeysPerStage - p.stage0 + 1;
+    // sinks behind the window: their stages come first
+    p.n_sink = std::min(n_sink, p.k_lo);
+    p.sink_stages = std::min(p.stage0, (p.n_sink + kDecodeKeysPerStage - 1) / kDecodeKeysPerStage);
+    p.stage0 -= p.sink_stages;
+    p.n_stages += p.sink_stages;
     const int capacity = decode_ctas_per_sm(d_qk, d_v, p.G) * st->sm_count;
     if (st->plan_key[0] != units || st->plan_key[1] != p.n_stages || st->plan_key[2] != capacity) {
         st->plan = plan_decode(units, p.n_stages, capacity);
@@ -531,7 +537,7 @@ apex_status apex_attn_decode(const void *q, const void *k_cache, const void *v_c
 // attention (d_qk = d_v + d_rope): validation done by the callers.
 apex_status prefill_launch(const void *q, const void *k, const void *v, void *out, int B, int H_q, int H_kv, int S_q,
                            int S_k, int d_qk, int d_v, int d_rope, const apex_attn_options *opt, const RopeFreq &f,
-                           apex_stream_t stream, void *workspace = nullptr)
+                           apex_stream_t stream, void *workspace = nullptr, int n_sink = 0)
 {
     const int q_pos0 = opt->q_pos, window = opt->window, P = opt->prefix_len;
     if (S_q <= 0 || q_pos0 < 0 || (long long)q_pos0 + S_q > (long long)S_k) return APEX_ERR_INVALID_ARG;
@@ -556,8 +562,8 @@ apex_status prefill_launch(const void *q, const void *k, const void *v, void *ou
     // them in every work item that visits them
     PrerotatePlan pre{false, 0};
     if (workspace && !opt->keys_prerotated)
-        pre = plan_prerotate(B * H_kv, S_q, S_k, q_pos0, window > 0 ? window : 0, P, (pair ? 4 : 2) * rows_per_head,
-                             mla ? kCostDecoupled : kCostPlain);
+        pre = plan_prerotate(B * H_kv, S_q, S_k, q_pos0, window > 0 ? window : 0, n_sink, P,
+                             (pair ? 4 : 2) * rows_per_head, mla ? kCostDecoupled : kCostPlain);
     PrefillLaunch L;
     memset(&L, 0, sizeof L);
     if (!make_map(&L.tm_q, q, d_qk, S_q, B * H_q, rows_per_head, G) ||
@@ -594,6 +600,7 @@ apex_status prefill_launch(const void *q, const void *k, const void *v, void *ou
     p.window = window > 0 ? window : 0;
     p.q_pos0 = q_pos0;
     p.prefix_len = P;
+    p.n_sink = std::min(n_sink, S_k);
     p.keys_prerotated = pre.use || opt->keys_prerotated != 0;
     p.rows_per_head = rows_per_head;
     const int block_rows = (pair ? 4 : 2) * rows_per_head;
@@ -625,7 +632,7 @@ apex_status apex_attn_fwd_ex(const void *q, const void *k, const void *v, void *
 // Workspace of the key-rotation pass (0: the pass would not run); d_r = 0 for
 // the plain block, else the rope part of decoupled-RoPE rows [d_h | d_r].
 static size_t prefill_workspace_bytes(int B, int H_q, int H_kv, int S_q, int S_k, int d_h, int d_r,
-                               const apex_attn_options *opt)
+                               const apex_attn_options *opt, int n_sink = 0)
 {
     if (!opt || opt->keys_prerotated) return 0;
     RopeFreq f;
@@ -636,8 +643,8 @@ static size_t prefill_workspace_bytes(int B, int H_q, int H_kv, int S_q, int S_k
     // a work item covers 4 M tiles of 128 / G query rows on CTA pairs, 2 on one CTA
     const bool pair = d_r != 0 || use_pair_prefill(d_h, 2);
     const int block_rows = (pair ? 4 : 2) * (128 / (H_q / H_kv));
-    const PrerotatePlan pr = plan_prerotate(B * H_kv, S_q, S_k, q_pos0, opt->window > 0 ? opt->window : 0, P,
-                                            block_rows, d_r ? kCostDecoupled : kCostPlain);
+    const PrerotatePlan pr = plan_prerotate(B * H_kv, S_q, S_k, q_pos0, opt->window > 0 ? opt->window : 0, n_sink,
+                                            P, block_rows, d_r ? kCostDecoupled : kCostPlain);
     return pr.use ? (size_t)B * H_kv * (size_t)S_k * (d_h + d_r) * 2 : 0;
 }
 
@@ -763,6 +770,57 @@ apex_status apex_attn_mla_rope_keys(const void *k_in, void *k_out, int n_heads, 
     if (d_h != 128 || d_r != 64) return APEX_ERR_UNSUPPORTED;
     return rope_keys_launch(k_in, k_out, n_heads, n_pos, d_h + d_r, d_r, pos0, in_head_stride, out_head_stride,
                             opt, stream);
+}
+
+// ----------------------------------------------------------------- windows with sinks
+
+// Sinks that a call has: none without a window, behind which they would stay visible.
+static int sinks_of(const apex_attn_options *opt, int n_sink, int S_k)
+{
+    return opt->window > 0 ? std::min(n_sink, S_k) : 0;
+}
+
+size_t apex_attn_sink_fwd_workspace_bytes(int B, int H_q, int H_kv, int S_q, int S_k, int d_h, int d_r, int n_sink,
+                                          const apex_attn_options *opt)
+{
+    if (!opt || n_sink < 0 || d_r < 0) return 0;
+    return prefill_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, d_r, opt, sinks_of(opt, n_sink, S_k));
+}
+
+apex_status apex_attn_sink_fwd(const void *q, const void *k, const void *v, void *out, int B, int H_q, int H_kv,
+                               int S_q, int S_k, int d_h, int d_r, int n_sink, const apex_attn_options *opt,
+                               void *workspace, size_t workspace_bytes, apex_stream_t stream)
+{
+    if (!q || !k || !v || !out || !opt || n_sink < 0) return APEX_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return APEX_ERR_INVALID_ARG;
+    if (d_r < 0 || (d_r & 1)) return APEX_ERR_INVALID_ARG;
+    RopeFreq f;
+    if (!freq_of(*opt, &f)) return APEX_ERR_INVALID_ARG;
+    apex_status s = check_common(B, H_q, H_kv, S_k, d_h, f.base);
+    if (s != APEX_OK) return s;
+    if (d_r != 0 && (d_h != 128 || d_r != 64)) return APEX_ERR_UNSUPPORTED;
+    if (workspace && (!aligned16(workspace) ||
+                      workspace_bytes < apex_attn_sink_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, d_r, n_sink, opt)))
+        return APEX_ERR_INVALID_ARG;
+    return prefill_launch(q, k, v, out, B, H_q, H_kv, S_q, S_k, d_h + d_r, d_h, d_r ? d_r : d_h, opt, f, stream,
+                          workspace, sinks_of(opt, n_sink, S_k));
+}
+
+apex_status apex_attn_sink_decode(const void *q, const void *k_cache, const void *v_cache, void *out, int B, int H_q,
+                                  int H_kv, int S_k, int d_h, int d_r, int n_sink, const apex_attn_options *opt,
+                                  void *workspace, size_t workspace_bytes, apex_stream_t stream)
+{
+    if (!q || !k_cache || !v_cache || !out || !workspace || !opt || n_sink < 0) return APEX_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace))
+        return APEX_ERR_INVALID_ARG;
+    if (d_r < 0 || (d_r & 1)) return APEX_ERR_INVALID_ARG;
+    RopeFreq f;
+    if (!freq_of(*opt, &f)) return APEX_ERR_INVALID_ARG;
+    apex_status s = check_common(B, H_q, H_kv, S_k, d_h, f.base);
+    if (s != APEX_OK) return s;
+    if (d_r != 0 && (d_h != 128 || d_r != 64)) return APEX_ERR_UNSUPPORTED;
+    return decode_launch(q, k_cache, v_cache, out, B, H_q, H_kv, S_k, d_h + d_r, d_h, d_r ? d_r : d_h, opt, f, workspace,
+                         workspace_bytes, stream, sinks_of(opt, n_sink, S_k));
 }
 
 }  // extern "C"

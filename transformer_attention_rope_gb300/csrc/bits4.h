@@ -1,0 +1,85 @@
+// bits4.h -- caches held in 4 bits: their layout, and parameters of the kernels that write
+// them, read them back (bits4.cu) and attend to them (decode4.cu).
+//
+// A row of d entries is d / 2 bytes of e2m1 values, entry 2i in the low half of byte i, and
+// d / 16 e4m3 scales, one for 16 neighbouring entries; an entry stands for
+//   value * scale * factor,
+// factor an fp32 number of the KV head (1 without).  value * scale has six significant bits at
+// most, so it is exact in fp16 and in bf16.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cache_attn.h"
+
+namespace apex {
+
+constexpr int kBits4Threads = 256;
+constexpr int kBits4Block = 16;    // entries of a scale
+constexpr int kBits4MaxRow = 512;  // widest row that is written and read back
+
+// Rows of one tensor: bf16 at x + b * x_b + h * x_h + s * x_s and packed rows of a cache
+// [B, H, S_cap, d / 2], [B, H, S_cap, d / 16].
+struct Bits4Tensor {
+    uint16_t *x;
+    long long x_b, x_h, x_s;
+    uint8_t *bytes, *scales;
+    const float *factor;
+    int d;
+    int wide;  // 16 bytes of x at a time
+};
+
+struct Bits4Params {
+    Bits4Tensor t[2];  // k, v
+    const int *row0;   // first row of each sequence; NULL: 0
+    int B, H, S, S_cap;
+};
+
+cudaError_t launch_append4(const Bits4Params &p, cudaStream_t stream);
+cudaError_t launch_unpack4(const Bits4Params &p, cudaStream_t stream);
+
+// ---------------------------------------------------------------- attention
+struct Decode4Params {
+    CacheAttnParams c;  // sizes, lengths, masks, schedule and workspace, as for bf16 caches
+    const uint16_t *q;
+    const uint8_t *k, *v, *k_scale, *v_scale;
+    const float *k_factor, *v_factor;
+};
+
+// Rows of a KV head's queries that are worked on together: they share each key's conversion.
+inline int decode4_group(int R) { return R <= 8 ? 8 : 16; }
+
+constexpr int kDecode4CtasPerSm = 2;
+constexpr int kDecode4MaxCtas = 2 * kCacheMaxCtas;
+
+inline int decode4_shares(long long units, int S_cap, int ctas)
+{
+    const long long tiles = units * ((S_cap + kCacheTileKeys - 1) / kCacheTileKeys);
+    return (int)std::min<long long>(std::min(ctas, kDecode4MaxCtas), tiles);
+}
+
+struct Decode4Workspace {
+    size_t ml, units, bytes;
+    int rows_cap, n_groups;
+};
+
+inline Decode4Workspace decode4_workspace(int B, int H_q, int H_kv, int T, int S_cap, int d_v)
+{
+    Decode4Workspace w;
+    const int R = H_q / H_kv * T, group = decode4_group(R);
+    w.rows_cap = std::min(R, group);
+    w.n_groups = (R + group - 1) / group;
+    auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+    const long long units = (long long)B * H_kv * w.n_groups;
+    const size_t slots = (size_t)2 * decode4_shares(units, S_cap, kDecode4MaxCtas) * w.rows_cap;
+    w.ml = up(slots * d_v * sizeof(float));
+    w.units = w.ml + up(slots * sizeof(float2));
+    w.bytes = w.units + up((size_t)units * sizeof(int2));
+    return w;
+}
+
+// chooses how the work is cut (p.c.whole), launches the attention and what joins it
+cudaError_t launch_decode4(Decode4Params &p, int sm_count, cudaStream_t stream);
+
+}  // namespace apex

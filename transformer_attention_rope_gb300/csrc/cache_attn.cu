@@ -537,7 +537,11 @@ cudaError_t launch_cache_attn(CacheAttnLaunch &L, int sm_count, cudaStream_t str
     else
         err = p.acc ? launch_t<192, 128, 1, true>(L, shares, stream) : launch_t<192, 128, 1, false>(L, shares, stream);
     if (err != cudaSuccess) return err;
-    if (p.whole) return cudaSuccess;
+    return p.whole ? cudaSuccess : launch_cache_join(p, shares, stream);
+}
+
+cudaError_t launch_cache_join(const CacheAttnParams &p, int shares, cudaStream_t stream)
+{
     return p.d_v == 64 ? launch_join<64>(p, shares, stream) : launch_join<128>(p, shares, stream);
 }
 

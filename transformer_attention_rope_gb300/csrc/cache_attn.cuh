@@ -68,10 +68,11 @@ __device__ __forceinline__ bool elect_one()
 }
 
 // ---------------------------------------------------------------- schedule
-// Lengths of sequence b: cached keys, keys with its drafts, its first key tile and
-// number of tiles (one at least, so that every unit writes its output).
+// Lengths of sequence b: cached keys, keys with its drafts, and its tiles (one at least, so
+// that every unit writes its output): the first `sink` tiles of the cache, which stay visible
+// behind a window, and those from tile0 on.
 struct Seq {
-    int len, total, tile0, tiles;
+    int len, total, tile0, tiles, sink;
     int cost;  // of a unit in the schedule: its tiles and kCacheUnitCost for its start; 1 when units stay whole
     __device__ __forceinline__ void load(const CacheAttnParams &p, int b)
     {
@@ -79,7 +80,8 @@ struct Seq {
         total = min(len + p.drafts, p.S_cap);
         const int lo = p.window > 0 ? max(0, len - p.window + 1) : 0;
         tile0 = lo / kCacheTileKeys;
-        tiles = max(1, (total + kCacheTileKeys - 1) / kCacheTileKeys - tile0);
+        sink = p.n_sink > 0 ? min(tile0, (min(p.n_sink, total) + kCacheTileKeys - 1) / kCacheTileKeys) : 0;
+        tiles = max(1, (total + kCacheTileKeys - 1) / kCacheTileKeys - tile0) + sink;
         cost = p.whole ? 1 : tiles + kCacheUnitCost;
     }
 };
@@ -146,11 +148,17 @@ __device__ __forceinline__ void make_sched(const CacheAttnParams &p, int c, int 
     if (lane == 0) *out = r;
 }
 
-// The part of one unit in a share: n tiles from tile `first` of the sequence.
+// The part of one unit in a share: n tiles of the sequence, `first` + j the j-th but for the
+// sinks' tiles before it (tile()).
 struct Frag {
     Seq s;
     int b, hk, group, unit;  // unit: index over all units
     int first, n;
+    __device__ __forceinline__ int tile(int j) const
+    {
+        const int t = first + j;
+        return t >= s.tile0 ? t : t - s.tile0 + s.sink;
+    }
     bool head, tail;         // holds the unit's first / last tile
     int last;                // share of the unit's last tile
 };
@@ -176,7 +184,7 @@ struct Walk {
             f.hk = s.unit / p.n_groups;
             f.group = s.unit % p.n_groups;
             f.unit = s.b * per_b + s.unit;
-            f.first = seq.tile0 + t0;
+            f.first = seq.tile0 + t0 - seq.sink;
             f.n = t1 - t0;
             f.head = t0 == 0;
             f.tail = t1 == seq.tiles;

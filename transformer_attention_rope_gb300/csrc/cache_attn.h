@@ -24,6 +24,7 @@ struct CacheAttnParams {
     long long mask_stride;
     const int *positions;
     int window;  // 0: none
+    int n_sink;  // first keys that stay visible behind a window
     int drafts;  // draft rows behind lens[b]: T, or 0 for the decode
     float *acc;  // [B, H_kv, S_cap], or NULL
     float scale_log2;
@@ -134,5 +135,7 @@ struct CacheAttnLaunch {
 cudaError_t launch_cache_attn(CacheAttnLaunch &L, int sm_count, cudaStream_t stream);
 // the attention kernel on CTA pairs alone (the caller joins)
 cudaError_t launch_cache_pair(const CacheAttnLaunch &L, int pairs, cudaStream_t stream);
+// joins the partial results that `shares` shares left
+cudaError_t launch_cache_join(const CacheAttnParams &p, int shares, cudaStream_t stream);
 
 }  // namespace apex

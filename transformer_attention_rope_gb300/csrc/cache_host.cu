@@ -9,19 +9,10 @@
 #include "cache_attn.h"
 #include "evict.h"
 #include "host_common.h"
-#include "rope.h"
+#include "rope_host.h"
 
 namespace apex {
 namespace {
-
-bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-// Whether na bytes at a and nb at b share one (b may be NULL: no).
-bool overlap(const void *a, size_t na, const void *b, size_t nb)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return b && (x < y ? y - x < na : x - y < nb);
-}
 
 // ----------------------------------------------------------------- rope
 
@@ -34,6 +25,8 @@ struct TurnSet {
     int d_rot;  // 0: empty
     uint64_t turns[kRopeMaxPairs];
 };
+
+}  // namespace
 
 bool turns_of(const RopeFreq &f, float linear, int d_rot, uint64_t *out)
 {
@@ -65,17 +58,7 @@ bool turns_of(const RopeFreq &f, float linear, int d_rot, uint64_t *out)
     return true;
 }
 
-bool rope_tensor_ok(const apex_rope_tensor *t)
-{
-    return t->in && t->out && t->n_heads > 0 && t->d_row > 0 && aligned(t->in, 2) && aligned(t->out, 2);
-}
-
-// Rows of a tensor: elements at + b * stride[0] + h * stride[1] + s * stride[2] + [0, d).
-struct RowSet {
-    __int128 at;
-    long long stride[3];
-    int count[3], d;
-};
+namespace {
 
 // The span of stride * x over the counts, from its least (negative strides) to its largest.
 void span_of(const RowSet &r, __int128 *lo, __int128 *hi)
@@ -133,6 +116,8 @@ bool nested(const RowSet &r)
     return true;
 }
 
+}  // namespace
+
 bool share_elements(const RowSet &a, const RowSet &b)
 {
     RowSearch r;
@@ -157,6 +142,13 @@ bool share_elements(const RowSet &a, const RowSet &b)
     }
     const __int128 apart = b.at - a.at;
     return r.search(0, apart - (a.d - 1), apart + b.d - 1, false);
+}
+
+namespace {
+
+bool rope_tensor_ok(const apex_rope_tensor *t)
+{
+    return t->in && t->out && t->n_heads > 0 && t->d_row > 0 && aligned(t->in, 2) && aligned(t->out, 2);
 }
 
 // Whether the tensors' outputs may be written while other threads still read or write: an

@@ -70,6 +70,12 @@ __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// First key of stage index st.
+__device__ __forceinline__ int stage_key0(const DecodeParams &p, int st)
+{
+    return (st - p.stage0 < p.sink_stages ? st - p.stage0 : st) * kKeys;
+}
+
 // PREROT: the cached keys already hold RoPE(k_j, j); the query is rotated to
 // its absolute position and the keys are used as they are.
 template <int DQK, int DV, int DR, int NT, bool PREROT>
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int slot = it % kStages;
                 const uint32_t ph = (it / kStages) & 1;
                 mbar_wait(bar_empty + 8 * slot, ph ^ 1, p.wait);
-                const int j0 = st * kKeys;
+                const int j0 = stage_key0(p, st);
                 const uint32_t kdst = sbase + slot * C::kStageBytes;
                 const uint32_t vdst = kdst + C::kKBytes;
                 if (lane == 0) {
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int st = s_begin; st < s_end; ++st, ++it) {
             const int slot = it % kStages;
             mbar_wait(bar_full + 8 * slot, (it / kStages) & 1, p.wait);
-            const int j0 = st * kKeys;
+            const int j0 = stage_key0(p, st);
             const uint32_t kb = sbase + slot * C::kStageBytes;
             const uint32_t vb = kb + C::kKBytes;
             const uint32_t qp = vb + C::kVBytes;
@@ -268,8 +274,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             // online softmax over this warp's 16 keys (log2 units)
             const bool edge = (j0 < p.k_lo) || (j0 + kKeys - 1 > p.k_hi);
             const int key0 = j0 + 16 * warp + g, key1 = key0 + 8;
-            const bool ok0 = !edge || (key0 >= p.k_lo && key0 <= p.k_hi);
-            const bool ok1 = !edge || (key1 >= p.k_lo && key1 <= p.k_hi);
+            const bool ok0 = !edge || ((key0 >= p.k_lo || key0 < p.n_sink) && key0 <= p.k_hi);
+            const bool ok1 = !edge || ((key1 >= p.k_lo || key1 < p.n_sink) && key1 <= p.k_hi);
             uint32_t bp[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {

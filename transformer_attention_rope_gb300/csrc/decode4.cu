@@ -1,0 +1,481 @@
+// decode4.cu -- attention of one or a few new tokens over a cache held in 4 bits (layout:
+// bits4.h), with a window and sinks.
+//
+// Work: as for bf16 caches (cache_attn.cuh): tiles of 128 keys of all (sequence, KV head,
+// row group) units are dealt out in equal shares, cut units leave partial results.  A tile is
+// 16 keys for each of a CTA's 8 warps; a warp has its own running maximum, sum and output, and
+// its own ring of slices in shared memory, filled by its own asynchronous copies: warps wait
+// for one another only where a unit ends.
+//
+// Mathematics: S^T = K Q^T and O^T += V^T P^T on mma.sync (keys and value entries as rows of
+// A, the queries of a KV head as the 8 columns of B), fp16 with fp32 sums.  A product of an
+// e2m1 value with its e4m3 scale is exact in fp16.  Queries go to fp16 scaled by a power of two
+// for each row, exact but for entries 2^-24 below the row's largest; the factor goes into the
+// scores' scale.  Weights are taken relative to a reference 2^11 below the running
+// maximum, as fp16 up to 2^15 is: those of 2^-25 of the largest keep 11 bits, and what is lost
+// lies below 2^-36 of it.  The reference moves only when a score outgrows it, so a slice costs one
+// vote and no exchange of maxima.
+//
+// Keys: lane 4g + t holds bytes 8t.. (16 of 64) of key g's row, 32 neighbouring entries, as the
+// order of the sum over entries is free; queries are laid out alike.  Values: lane 4g + t holds
+// entries 16g.. of keys 2t, 2t + 1, 2t + 8, 2t + 9; the halves of two keys' bytes are
+// interleaved so that one conversion gives both keys' values of an entry, which is how the
+// second product takes them.
+//
+// Bound: HBM, 0.5625 bytes an entry.
+#include <math.h>
+
+#include "bits4.cuh"
+#include "bits4.h"
+#include "cache_attn.cuh"
+
+namespace apex {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSlice = 16;  // keys of a warp's slice
+constexpr int kStages = 4;  // slices of a warp's ring
+static_assert(kWarps * kSlice == kCacheTileKeys, "a tile is a slice for each warp");
+constexpr float kHeadroom = 11.f;  // the reference of weights below the maximum, log2
+constexpr float kSlack = 15.f;     // scores may lie this far above the reference
+
+template <int DQK, int DV, int NT>
+struct Cfg {
+    static constexpr bool kWide = DQK >= 128;     // keys have a part of 128 entries
+    static constexpr bool kNarrow = DQK % 128 != 0;  // and one of 64
+    static constexpr int kStepsWide = kWide ? 8 : 0, kSteps = DQK / 16;
+    static constexpr int kBlocks = DV / 16;  // 16-entry row blocks of O^T
+    static constexpr int kRows = 8 * NT;
+    // a slice: wide parts of the keys | narrow parts | values | key scales | value scales
+    static constexpr int kKNarrow = kWide ? kSlice * 64 : 0;
+    static constexpr int kV = kKNarrow + (kNarrow ? kSlice * 32 : 0);
+    static constexpr int kKScale = kV + kSlice * DV / 2;
+    static constexpr int kVScale = kKScale + kSlice * DQK / 16;
+    static constexpr int kStage = kVScale + kSlice * DV / 16;
+    static_assert(kStage % 16 == 0, "slices of 16-byte chunks");
+    static constexpr int kRing = kWarps * kStages * kStage;
+    // where a unit ends the ring holds the warps' outputs instead
+    static constexpr int kMerge = kWarps * kRows * DV * 4;
+    static constexpr int kMl = kRing > kMerge ? kRing : kMerge;  // [warps][rows] (reference, sum)
+    static constexpr int kSched = kMl + kWarps * kRows * 8;
+    static constexpr int kBytes = kSched + 64;
+    static_assert(kBytes <= 113 * 1024, "two CTAs an SM");
+};
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where key i of a slice lies among its value rows, and which of its 16-byte chunks comes first: the
+// four keys of a load are neighbours, and at 128 entries the chunks of every other pair trade
+// places, so that the load's words lie in all 32 banks.
+__device__ __forceinline__ int value_slot(int i) { return ((i >> 1) & 3) + 4 * (i & 1) + 8 * (i >> 3); }
+template <int DV>
+__device__ __forceinline__ int value_chunk(int slot, int c)
+{
+    return DV == 128 ? c ^ (slot & 2) : c;
+}
+
+// The slice of 16 keys at key0 of cache row block kv: the copies of one warp.
+template <typename C, int DQK, int DV>
+__device__ __forceinline__ void load_slice(const Decode4Params &p, uint32_t dst, size_t kv, int key0)
+{
+    const int lane = threadIdx.x & 31, last = p.c.S_cap - 1;
+    const size_t base = kv * p.c.S_cap;
+    // rows past the capacity are read from its last one, and masked
+    constexpr int kKChunks = DQK / 32, kVChunks = DV / 32;
+#pragma unroll
+    for (int i = 0; i < kSlice * kKChunks / 32; ++i) {
+        const int id = lane + 32 * i, key = id / kKChunks, c = id % kKChunks;
+        const uint32_t at = (C::kWide && c < 4) ? key * 64 + 16 * c : C::kKNarrow + key * 32 + 16 * (c - (C::kWide ? 4 : 0));
+        copy16(dst + at, p.k + (base + min(key0 + key, last)) * (DQK / 2) + 16 * c);
+    }
+#pragma unroll
+    for (int i = 0; i < kSlice * kVChunks / 32; ++i) {
+        const int id = lane + 32 * i, key = id / kVChunks, c = id % kVChunks;
+        const int slot = value_slot(key);
+        copy16(dst + C::kV + slot * (DV / 2) + 16 * value_chunk<DV>(slot, c),
+               p.v + (base + min(key0 + key, last)) * (DV / 2) + 16 * c);
+    }
+    constexpr int kKWords = DQK / 64, kVWords = DV / 64;  // of a row's scales
+#pragma unroll
+    for (int i = 0; i < (kSlice * kKWords + 31) / 32; ++i) {
+        const int id = lane + 32 * i, key = id / kKWords, c = id % kKWords;
+        if (key < kSlice)
+            copy4(dst + C::kKScale + 4 * id, p.k_scale + (base + min(key0 + key, last)) * (DQK / 16) + 4 * c);
+    }
+#pragma unroll
+    for (int i = 0; i < (kSlice * kVWords + 31) / 32; ++i) {
+        const int id = lane + 32 * i, key = id / kVWords, c = id % kVWords;
+        if (key < kSlice)
+            copy4(dst + C::kVScale + 4 * id, p.v_scale + (base + min(key0 + key, last)) * (DV / 16) + 4 * c);
+    }
+}
+
+__device__ __forceinline__ uint32_t splat_lo(uint32_t w) { return __byte_perm(w, 0, 0x1010); }
+__device__ __forceinline__ uint32_t splat_hi(uint32_t w) { return __byte_perm(w, 0, 0x3232); }
+
+// Four steps' rows of keys times queries: 16 entries (two words) of keys g and g + 8 of one scale
+// each.
+template <int NT>
+__device__ __forceinline__ void key_steps(float (&s)[NT][4], const uint32_t (&lo)[2], const uint32_t (&hi)[2],
+                                          uint32_t scale_lo, uint32_t scale_hi, const uint32_t (*qb)[NT][2])
+{
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        uint32_t x[4], y[4];
+        e2m1_bytes_to_f16x2(lo[w], x);
+        e2m1_bytes_to_f16x2(hi[w], y);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {mul_f16x2(x[2 * h], scale_lo), mul_f16x2(y[2 * h], scale_hi),
+                                   mul_f16x2(x[2 * h + 1], scale_lo), mul_f16x2(y[2 * h + 1], scale_hi)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16_16816(s[n], a, qb[2 * w + h][n][0], qb[2 * w + h][n][1]);
+        }
+    }
+}
+
+template <int DQK, int DV, int NT>
+__global__ void __launch_bounds__(kThreads, 2) decode4_kernel(const __grid_constant__ Decode4Params p)
+{
+    using C = Cfg<DQK, DV, NT>;
+    const CacheAttnParams &pc = p.c;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_u32(smem) + warp * kStages * C::kStage;
+    const uint8_t *ring_at = smem + warp * kStages * C::kStage;
+    float *merge = reinterpret_cast<float *>(smem);                // [warps][rows][DV]
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::kMl);        // [warps][rows]
+    Sched *sched = reinterpret_cast<Sched *>(smem + C::kSched);
+    // launched as a programmatic dependent: inputs may be the previous kernel's output
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 0) make_sched(pc, blockIdx.x, gridDim.x, sched);
+    __syncthreads();
+
+    Walk walk(pc, *sched);
+    Frag f;
+    while (walk.next(pc, f)) {
+        const size_t kv = (size_t)f.b * pc.H_kv + f.hk;
+        if (threadIdx.x == 0 && f.head) pc.units[f.unit] = make_int2(blockIdx.x, f.last);
+#pragma unroll
+        for (int j = 0; j < kStages - 1; ++j) {
+            if (j < f.n)
+                load_slice<C, DQK, DV>(p, ring + j * C::kStage, kv, kCacheTileKeys * f.tile(j) + kSlice * warp);
+            copies_commit();
+        }
+
+        // ---- queries: column n of tile nt is row 8 nt + n of the group
+        uint32_t qb[C::kSteps][NT][2];
+        float factor[NT][2];  // of the scores of columns 2t, 2t + 1, in log2 units
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int rc = 8 * nt + g, r = f.group * pc.group + rc;
+            const bool ok = rc < pc.rows_cap && r < pc.R;
+            const uint16_t *row = p.q + (kv * pc.R + r) * DQK;
+            uint32_t w[DQK / 8];  // the lane's entries: 32 of the wide part, 16 of the narrow one
+#pragma unroll
+            for (int i = 0; i < DQK / 32; ++i) {
+                const int e = (C::kWide && i < 4) ? 32 * t + 8 * i : (C::kWide ? 128 : 0) + 16 * t + 8 * (i - (C::kWide ? 4 : 0));
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (ok) x = *reinterpret_cast<const uint4 *>(row + e);
+                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < DQK / 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+            top = max(top & 0xffffu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // largest magnitude 2^(ex - 127) to under twice that: entries times 2^(131 - ex) are below 32
+            const uint32_t ex = min(max(top >> 7, 5u), 254u);
+            const float down = __uint_as_float((258u - ex) << 23), up = __uint_as_float((ex - 4u) << 23);
+#pragma unroll
+            for (int i = 0; i < DQK / 8; ++i)
+                qb[i >> 1][nt][i & 1] = pack_f16x2(bf16lo_to_f32(w[i]) * down, bf16hi_to_f32(w[i]) * down);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) factor[nt][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + e));
+        }
+        const float kf = (p.k_factor ? p.k_factor[f.hk] : 1.f) * pc.scale_log2;
+        const float vf = p.v_factor ? p.v_factor[f.hk] : 1.f;
+        int lo[NT][2], hi[NT][2];  // keys that a column's row sees, beside the sinks
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                factor[nt][e] *= kf;
+                const int rc = 8 * nt + 2 * t + e, r = f.group * pc.group + rc;
+                const int m = f.s.len + r % pc.T;
+                const bool ok = rc < pc.rows_cap && r < pc.R;
+                hi[nt][e] = ok ? min(m, pc.S_cap - 1) : -1;
+                lo[nt][e] = pc.window > 0 ? max(0, m - pc.window + 1) : 0;
+            }
+        // keys that every row sees: [all_lo, len]; that some row sees: [any_lo, any_hi] and the sinks
+        const int m1 = f.s.len + pc.T - 1;
+        const int all_lo = pc.window > 0 ? m1 - pc.window + 1 : 0;
+        const int any_lo = pc.window > 0 ? f.s.len - pc.window + 1 : 0, any_hi = min(m1, pc.S_cap - 1);
+        const int all_hi = min(f.s.len, pc.S_cap - 1);
+
+        float o[NT][C::kBlocks][4], ref[NT][2], sum[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < C::kBlocks; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+            ref[nt][0] = ref[nt][1] = -INFINITY;
+            sum[nt][0] = sum[nt][1] = 0.f;
+        }
+
+        for (int j = 0; j < f.n; ++j) {
+            __syncwarp();  // all lanes are done with the slot that is filled next
+            if (j + kStages - 1 < f.n)
+                load_slice<C, DQK, DV>(p, ring + (j + kStages - 1) % kStages * C::kStage, kv,
+                                       kCacheTileKeys * f.tile(j + kStages - 1) + kSlice * warp);
+            copies_commit();
+            copies_wait<kStages - 1>();
+            __syncwarp();
+            const uint8_t *at = ring_at + j % kStages * C::kStage;
+            const int key0 = kCacheTileKeys * f.tile(j) + kSlice * warp;
+
+            // ---- scores of keys g, g + 8 (rows) and queries 2t, 2t + 1 (columns)
+            float s[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+            if (C::kWide) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(at + g * 64 + 16 * t);
+                const uint4 b = *reinterpret_cast<const uint4 *>(at + (g + 8) * 64 + 16 * t);
+                const uint32_t sa = e4m3x2_to_f16x2(
+                    *reinterpret_cast<const uint16_t *>(at + C::kKScale + g * (DQK / 16) + 2 * t));
+                const uint32_t sc = e4m3x2_to_f16x2(
+                    *reinterpret_cast<const uint16_t *>(at + C::kKScale + (g + 8) * (DQK / 16) + 2 * t));
+                const uint32_t a0[2] = {a.x, a.y}, a1[2] = {a.z, a.w}, b0[2] = {b.x, b.y}, b1[2] = {b.z, b.w};
+                key_steps<NT>(s, a0, b0, splat_lo(sa), splat_lo(sc), &qb[0]);
+                key_steps<NT>(s, a1, b1, splat_hi(sa), splat_hi(sc), &qb[4]);
+            }
+            if (C::kNarrow) {
+                const uint2 a = *reinterpret_cast<const uint2 *>(at + C::kKNarrow + g * 32 + 8 * t);
+                const uint2 b = *reinterpret_cast<const uint2 *>(at + C::kKNarrow + (g + 8) * 32 + 8 * t);
+                const int block = (C::kWide ? 8 : 0) + t;
+                const uint32_t sa = e4m3x2_to_f16x2(at[C::kKScale + g * (DQK / 16) + block]);
+                const uint32_t sc = e4m3x2_to_f16x2(at[C::kKScale + (g + 8) * (DQK / 16) + block]);
+                const uint32_t a0[2] = {a.x, a.y}, b0[2] = {b.x, b.y};
+                key_steps<NT>(s, a0, b0, splat_lo(sa), splat_lo(sc), &qb[C::kStepsWide]);
+            }
+            const bool all = key0 >= all_lo && key0 + kSlice - 1 <= all_hi;
+            bool above = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[nt][e] *= factor[nt][e & 1];
+                    if (!all) {
+                        const int key = key0 + g + 8 * (e >> 1);
+                        if (key > hi[nt][e & 1] || (key < lo[nt][e & 1] && key >= pc.n_sink)) s[nt][e] = -INFINITY;
+                    }
+                    above = above || s[nt][e] > ref[nt][e & 1] + kSlack;
+                }
+            if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(s[nt][e], s[nt][e + 2]);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                        if (top > ref[nt][e] + kSlack) {
+                            const float now = top - kHeadroom;
+                            const float keep = fast_exp2(ref[nt][e] - now);
+                            ref[nt][e] = now;
+                            sum[nt][e] *= keep;
+#pragma unroll
+                            for (int i = 0; i < C::kBlocks; ++i) {
+                                o[nt][i][e] *= keep;
+                                o[nt][i][e + 2] *= keep;
+                            }
+                        }
+                    }
+            }
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float r0 = ref[nt][0] == -INFINITY ? 0.f : ref[nt][0], r1 = ref[nt][1] == -INFINITY ? 0.f : ref[nt][1];
+                const float p0 = fast_exp2(s[nt][0] - r0), p1 = fast_exp2(s[nt][1] - r1);
+                const float p2 = fast_exp2(s[nt][2] - r0), p3 = fast_exp2(s[nt][3] - r1);
+                sum[nt][0] += p0 + p2;
+                sum[nt][1] += p1 + p3;
+                pb[nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
+                pb[nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
+            }
+
+            // ---- outputs: keys 2t, 2t + 1 and 2t + 8, 2t + 9 of the lane's entries
+            uint32_t vs[2];
+            {
+                const int block = DV == 128 ? g : g >> 1;
+                const uint8_t *sv = at + C::kVScale + 2 * t * (DV / 16) + block;
+                vs[0] = e4m3x2_to_f16x2(sv[0] | (uint32_t)sv[DV / 16] << 8);
+                vs[1] = e4m3x2_to_f16x2(sv[8 * (DV / 16)] | (uint32_t)sv[9 * (DV / 16)] << 8);
+                if (!all) {  // values of keys that no row sees may be anything: codes are finite, scales not
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = key0 + 2 * t + 8 * h + e;
+                            if (key > any_hi || (key < any_lo && key >= pc.n_sink)) vs[h] &= e ? 0x0000ffffu : 0xffff0000u;
+                        }
+                }
+            }
+            constexpr int kWords = DV / 64;  // of a lane's entries of one key
+            uint32_t x[4][kWords];           // keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int slot = t + 4 * h;  // value_slot of the key
+                const uint8_t *row = at + C::kV + slot * (DV / 2);
+                if (DV == 128) {
+                    const uint2 two =
+                        *reinterpret_cast<const uint2 *>(row + 16 * value_chunk<DV>(slot, g >> 1) + 8 * (g & 1));
+                    x[h][0] = two.x;
+                    x[h][kWords - 1] = two.y;
+                } else {
+                    x[h][0] = *reinterpret_cast<const uint32_t *>(row + 4 * g);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                uint32_t even[2][4], odd[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t a = x[2 * h][w], b = x[2 * h + 1][w];
+                    e2m1_bytes_to_f16x2((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even[h]);
+                    e2m1_bytes_to_f16x2(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd[h]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a[4] = {mul_f16x2(even[0][i], vs[0]), mul_f16x2(odd[0][i], vs[0]),
+                                           mul_f16x2(even[1][i], vs[1]), mul_f16x2(odd[1][i], vs[1])};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * w + i], a, pb[nt][0], pb[nt][1]);
+                }
+            }
+        }
+
+        // ---- the warps' results become one
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = sum[nt][e];
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+                if (g == 0) ml[warp * C::kRows + 8 * nt + 2 * t + e] = make_float2(row_max(ref[nt][e], x), x);
+            }
+        copies_wait<0>();
+        __syncthreads();  // and every ring is done with
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int rc = 8 * nt + 2 * t + e;
+                if (rc >= pc.rows_cap) continue;
+                float *to = merge + (warp * C::kRows + rc) * DV + (DV / 8) * g;
+#pragma unroll
+                for (int i = 0; i < C::kBlocks; i += 2)  // entries 2i .. 2i + 3 of the lane's
+                    *reinterpret_cast<float4 *>(to + 2 * i) =
+                        make_float4(o[nt][i][e], o[nt][i][e + 2], o[nt][i + 1][e], o[nt][i + 1][e + 2]);
+            }
+        __syncthreads();
+        const int slot = 2 * blockIdx.x + (f.head ? 1 : 0);
+        for (int i = threadIdx.x; i < pc.rows_cap * (DV / 4); i += kThreads) {
+            const int rc = i / (DV / 4), c = i % (DV / 4), r = f.group * pc.group + rc;
+            if (r >= pc.R) break;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * C::kRows + rc].x);
+            float L = 0.f;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 part = ml[w * C::kRows + rc];
+                if (part.x == -INFINITY) continue;
+                const float k = exp2f(part.x - top);
+                const float4 y = *reinterpret_cast<const float4 *>(merge + (w * C::kRows + rc) * DV + 4 * c);
+                L = fmaf(part.y, k, L);
+                x.x = fmaf(y.x, k, x.x);
+                x.y = fmaf(y.y, k, x.y);
+                x.z = fmaf(y.z, k, x.z);
+                x.w = fmaf(y.w, k, x.w);
+            }
+            if (f.head && f.tail) {
+                const float inv = (L == 0.f ? 0.f : 1.f / L) * vf;
+                *reinterpret_cast<uint2 *>(pc.out + (kv * pc.R + r) * DV + 4 * c) =
+                    make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+            } else {
+                if (c == 0) pc.ws_ml[(size_t)slot * pc.rows_cap + rc] = make_float2(top, L);
+                reinterpret_cast<float4 *>(pc.ws_o + (size_t)slot * pc.rows_cap * DV)[(size_t)c * pc.rows_cap + rc] =
+                    make_float4(x.x * vf, x.y * vf, x.z * vf, x.w * vf);
+            }
+        }
+        __syncthreads();  // the rings are filled again
+    }
+}
+
+template <int DQK, int DV, int NT>
+cudaError_t launch_t(const Decode4Params &p, int grid, cudaStream_t stream)
+{
+    using C = Cfg<DQK, DV, NT>;
+    static KernelSetup setup;
+    const cudaError_t err = setup(decode4_kernel<DQK, DV, NT>, C::kBytes);
+    if (err != cudaSuccess) return err;
+    return launch_dependent(decode4_kernel<DQK, DV, NT>, grid, kThreads, C::kBytes, stream, p);
+}
+
+template <int NT>
+cudaError_t launch_rows(const Decode4Params &p, int grid, cudaStream_t stream)
+{
+    if (p.c.d_qk == 64) return launch_t<64, 64, NT>(p, grid, stream);
+    if (p.c.d_qk == 128) return launch_t<128, 128, NT>(p, grid, stream);
+    return launch_t<192, 128, NT>(p, grid, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_decode4(Decode4Params &p, int sm_count, cudaStream_t stream)
+{
+    CacheAttnParams &c = p.c;
+    const long long n_units = (long long)c.B * c.H_kv * c.n_groups;
+    const int room = std::min(kDecode4CtasPerSm * sm_count, kDecode4MaxCtas);
+    int shares = decode4_shares(n_units, c.S_cap, room);
+    // keys that a unit can reach: a window and the sinks bound them, the new rows and a tile's slack beside
+    const int reach = c.window > 0 ? (int)std::min<long long>(c.S_cap, (long long)c.window + c.n_sink + c.drafts + 2 * kCacheTileKeys)
+                                   : c.S_cap;
+    c.whole = cache_attn_whole(n_units, reach, room);
+    if (c.whole) shares = (int)std::min<long long>(shares, n_units);
+    const cudaError_t err = c.group == 8 ? launch_rows<1>(p, shares, stream) : launch_rows<2>(p, shares, stream);
+    if (err != cudaSuccess || c.whole) return err;
+    return launch_cache_join(c, shares, stream);
+}
+
+}  // namespace apex

@@ -278,6 +278,15 @@ __device__ __forceinline__ void mask_row128(uint32_t (&v)[128], int lo, int hi)
     }
 }
 
+// The same for a tile whose first `sink` keys stay visible (sinks).
+__device__ __forceinline__ void mask_row128_sink(uint32_t (&v)[128], int lo, int hi, int sink)
+{
+    const uint32_t ninf = 0xff800000u;
+#pragma unroll
+    for (int e = 0; e < 128; ++e)
+        if ((e < lo && e >= sink) || e > hi) v[e] = ninf;
+}
+
 // Byte offset of 16-byte chunk `chunk` (0..7) of row `row` inside a tile that a
 // TMA load wrote with CU_TENSOR_MAP_SWIZZLE_128B (rows of 128 bytes, tile base
 // 1024-byte aligned): the chunk index is XORed with the row index mod 8.

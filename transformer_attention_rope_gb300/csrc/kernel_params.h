@@ -42,8 +42,10 @@ struct DecodeParams {
     int q_pos;              // query position
     int k_lo;               // first visible key
     int k_hi;               // last visible key (q_pos, or P - 1 for a query inside a prefix of P)
-    int stage0;             // first stage index (stage s covers keys [64 s, 64 s + 64))
-    int n_stages;           // stages per (b, kv-head)
+    int n_sink;             // keys before this are visible too (with k_lo > 0); 0: none
+    // stages per (b, kv-head): stage index s of stage0 .. stage0 + n_stages - 1 covers keys [64 s, 64 s + 64),
+    // but for the first `sink_stages` of them, which cover the cache's first ones
+    int stage0, n_stages, sink_stages;
     int n_split;            // splits per (b, kv-head)
     int stages_per_split;   // last split may have fewer
     int n_items;            // B * H_kv * n_split
@@ -71,6 +73,7 @@ struct PrefillParams {
     int window;     // <= 0: none
     int q_pos0;
     int prefix_len;       // bidirectional prefix [0, P); 0: none
+    int n_sink;           // first keys that stay visible behind the window; 0: none
     int keys_prerotated;  // keys already rotated: no K RoPE
     int rows_per_head;   // query positions per head in one 128-row M tile (128 / G)
     int n_qblocks;       // position blocks per (b, kv-head); a block = 2 M tiles (4 on CTA pairs)

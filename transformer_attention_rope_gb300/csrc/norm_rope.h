@@ -1,0 +1,55 @@
+// norm_rope.h -- parameters of the kernels that norm and turn heads in one pass, and of
+// their gradients (norm_rope.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "rope.h"
+
+namespace apex {
+
+constexpr int kNormThreads = 256;
+constexpr int kNormFastRow = 256;      // widest row of the kernels that go 16 bytes at a time
+constexpr int kNormGradBlocks = 1024;  // blocks of a gradient at most: one partial sum of weights each
+
+// Rows at x + b * x_b + h * x_h + s * x_s, likewise dy (gradients) and out (the result, or x's gradient).
+struct NormTensor {
+    const uint16_t *x, *dy;
+    uint16_t *out;
+    long long x_b, x_h, x_s, dy_b, dy_h, dy_s, out_b, out_h, out_s;
+    const void *weight;   // bf16 or fp32; NULL: ones
+    int weight_f32;
+    int weight_h;         // entries between the weights of two heads (0: the same for all)
+    int n_heads, d_row;
+    int n_groups;         // groups of `per` heads: the tensor's share of the grid's y
+    int norm;             // 0: rows copied (values)
+    int append;           // rows go to row0[b] + s when row0 is given
+    float inv_d;
+    float *partial;       // gradients: [n_groups * blocks][d_row] sums of weights
+    float *dweight;       // [d_row] or [n_heads][d_row]
+};
+
+struct NormRopeParams {
+    NormTensor t[3];  // q, k, v (those present, in this order)
+    const int *positions;
+    long long pos_stride;
+    const int *row0;
+    int out_rows;
+    int B, S;
+    int rot_start, d_rot;  // d_rot 0: nothing turns
+    int n_tensors, per;
+    float eps, sign;
+    uint64_t turns[kRopeMaxPairs];
+};
+static_assert(sizeof(NormRopeParams) <= 4096, "kernel parameters");
+
+// half: pair layout; lanes: lanes of a row (8, 16 or 32; 0: rows that go 2 bytes at a time)
+cudaError_t launch_norm_rope(const NormRopeParams &p, bool half, int lanes, int grid_x, int grid_y,
+                             cudaStream_t stream);
+cudaError_t launch_norm_rope_grad(const NormRopeParams &p, bool half, int lanes, int grid_x, int grid_y,
+                                  cudaStream_t stream);
+
+}  // namespace apex

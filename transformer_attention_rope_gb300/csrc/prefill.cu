@@ -205,8 +205,16 @@ __device__ __forceinline__ void rope_q_tile(uint8_t *tile, int rt, const float2 
 // One work item: (batch, kv head) unit and a block of 2P query rows.
 struct Item {
     int unit, b, hk, r0, j_lo, n_kt, zq;
+    int sink;  // of the n_kt key tiles, how many are the first ones of the sequence
+    // the j-th key tile
+    template <bool SINK>
+    __device__ __forceinline__ int tile(int j) const
+    {
+        return SINK && j < sink ? j : j_lo + j;
+    }
 };
 
+template <bool SINK>
 __device__ __forceinline__ Item make_item(const PrefillParams &p, int w)
 {
     Item it;
@@ -225,6 +233,12 @@ __device__ __forceinline__ Item make_item(const PrefillParams &p, int w)
     const int key_hi = (m_first < p.prefix_len) ? max(m_last, p.prefix_len - 1) : m_last;
     it.j_lo = key_lo / 128;
     it.n_kt = key_hi / 128 - it.j_lo + 1;
+    it.sink = 0;
+    if (SINK) {  // the tiles of the sinks that lie before the window's
+        it.sink = min(it.j_lo, (p.n_sink + 127) / 128);
+        it.j_lo -= it.sink;
+        it.n_kt += it.sink;
+    }
     it.zq = it.b * p.H_q + it.hk * p.G;
     return it;
 }
@@ -237,7 +251,9 @@ __device__ __forceinline__ int item_index(int k)
     return k * g + ((k & 1) ? (g - 1 - c) : c);
 }
 
-template <int D>
+// SINK: the first n_sink keys stay visible behind the window; a work item then visits
+// their tiles before the window's.
+template <int D, bool SINK>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const PrefillParams p)
@@ -288,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_prefetch_desc(&tm_v);
             int kc = 0;  // K/V tiles issued so far (ring position)
             for (int k = 0, w = item_index(0); w < p.n_work; ++k, w = item_index(k)) {
-                const Item it = make_item(p, w);
+                const Item it = make_item<SINK>(p, w);
                 for (int t = 0; t < 2; ++t) {
                     mbar_wait(bar(C::kBarQEmpty + t), (k & 1) ^ 1, p.wait);
                     mbar_arrive_expect_tx(bar(C::kBarQFull + t), C::kTile);
@@ -298,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     64 * bx, it.r0 + t * P, it.zq);
                 }
                 for (int j = 0; j < it.n_kt; ++j, ++kc) {
-                    const int key0 = 128 * (it.j_lo + j);
+                    const int key0 = 128 * it.tile<SINK>(j);
                     const int ks = kc % kKStages, vs = kc % kVStages;
                     mbar_wait(bar(C::kBarKEmpty + ks), ((kc / kKStages) & 1) ^ 1, p.wait);
                     mbar_arrive_expect_tx(bar(C::kBarKFull + ks), C::kTile);
@@ -347,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             int kc = 0;
             for (int k = 0, w = item_index(0); w < p.n_work; ++k, w = item_index(k)) {
-                const Item it = make_item(p, w);
+                const Item it = make_item<SINK>(p, w);
                 const int n = it.n_kt;
                 mbar_wait(bar(C::kBarKReady + kc % kKStages), (kc / kKStages) & 1, p.wait);
                 for (int t = 0; t < 2; ++t) {
@@ -402,13 +418,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         kr.init(p.rope.cs, c);
         int kc = 0;
         for (int k = 0, w = item_index(0); w < p.n_work; ++k, w = item_index(k)) {
-            const Item it = make_item(p, w);
-            kr.load_seed(p.rope.cs, min(128 * it.j_lo + r0, max_row), c);
+            const Item it = make_item<SINK>(p, w);
+            kr.load_seed(p.rope.cs, min(128 * it.tile<SINK>(0) + r0, max_row), c);
             for (int j = 0; j < it.n_kt; ++j, ++kc) {
                 const int ks = kc % kKStages;
                 mbar_wait(bar(C::kBarKFull + ks), (kc / kKStages) & 1, p.wait);
                 if (!p.keys_prerotated) kr.rotate(smem + C::kKOff + ks * C::kTile, rt);
-                if (j + 1 < it.n_kt) kr.load_seed(p.rope.cs, min(128 * (it.j_lo + j + 1) + r0, max_row), c);
+                if (j + 1 < it.n_kt) kr.load_seed(p.rope.cs, min(128 * it.tile<SINK>(j + 1) + r0, max_row), c);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::kBarKReady + ks));
@@ -433,9 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(C::kBarQReady + t));
         };
         int kc = 0;
-        if (item_index(0) < p.n_work) rotate_q(make_item(p, item_index(0)), 0);
+        if (item_index(0) < p.n_work) rotate_q(make_item<SINK>(p, item_index(0)), 0);
         for (int k = 0, w = item_index(0); w < p.n_work; ++k, w = item_index(k)) {
-            const Item it = make_item(p, w);
+            const Item it = make_item<SINK>(p, w);
             const int r = it.r0 + t * P + i % P;  // query row index
             const int m = p.q_pos0 + r;           // its position
             // keys this row sees: [key_lo, key_hi]
@@ -447,11 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < it.n_kt; ++j) {
                 mbar_wait(bar(C::kBarSFull + t), (kc + j) & 1, p.wait);
                 tc_fence_after();
-                const int kstart = 128 * (it.j_lo + j);
+                const int kstart = 128 * it.tile<SINK>(j);
                 // columns [lo_c, hi_c] of this tile are visible to the row
                 const int hi_c = key_hi - kstart;
                 const int lo_c = key_lo - kstart;
-                const bool full_vis = lo_c <= 0 && hi_c >= 127;
+                const bool full_vis = (lo_c <= 0 || (SINK && kstart + 128 <= p.n_sink)) && hi_c >= 127;
                 const bool all_full = __all_sync(0xffffffffu, full_vis);
                 // the whole 128-column row of S in registers
                 uint32_t v[128];
@@ -459,7 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int ch = 0; ch < 4; ++ch)
                     tmem_ld32(s_addr + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * ch]));
                 tmem_wait_ld();
-                if (!all_full) mask_row128(v, lo_c, hi_c);
+                if (SINK && !all_full && kstart < p.n_sink)
+                    mask_row128_sink(v, lo_c, hi_c, p.n_sink - kstart);
+                else if (!all_full)
+                    mask_row128(v, lo_c, hi_c);
                 // row max of the visible scores (8 independent chains)
                 float acc[8];
 #pragma unroll
@@ -527,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the next item's Q tile was loaded once this item's last QK was done:
             // rotate it now, so its first QK overlaps this item's epilogue
             const int w_next = item_index(k + 1);
-            if (w_next < p.n_work) rotate_q(make_item(p, w_next), k + 1);
+            if (w_next < p.n_work) rotate_q(make_item<SINK>(p, w_next), k + 1);
 
             // ---- epilogue: O / l -> bf16 -> global, one row per thread
             mbar_wait(bar(C::kBarODone + t), k & 1, p.wait);
@@ -563,28 +582,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
+template <int D, bool SINK>
 cudaError_t launch_t(const PrefillLaunch &L, cudaStream_t stream)
 {
     using C = Cfg<D>;
     cudaError_t err =
-        cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        cudaFuncSetAttribute(prefill_kernel<D, SINK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (err != cudaSuccess) return err;
     // setmaxnreg.inc blocks until the block's own pool can serve it: never
     // launch unless the split fits the registers the block is launched with
     cudaFuncAttributes fa;
-    err = cudaFuncGetAttributes(&fa, prefill_kernel<D>);
+    err = cudaFuncGetAttributes(&fa, prefill_kernel<D, SINK>);
     if (err != cudaSuccess) return err;
     if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-    return launch_dependent(prefill_kernel<D>, L.grid, kThreads, C::kSmemBytes, stream, L.tm_q, L.tm_k, L.tm_v, L.p);
+    return launch_dependent(prefill_kernel<D, SINK>, L.grid, kThreads, C::kSmemBytes, stream, L.tm_q, L.tm_k, L.tm_v,
+                            L.p);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill(const PrefillLaunch &L, cudaStream_t stream)
 {
-    if (L.p.d_h == 128) return launch_t<128>(L, stream);
-    if (L.p.d_h == 64) return launch_t<64>(L, stream);
+    const bool sink = L.p.n_sink > 0;
+    if (L.p.d_h == 128) return sink ? launch_t<128, true>(L, stream) : launch_t<128, false>(L, stream);
+    if (L.p.d_h == 64) return sink ? launch_t<64, true>(L, stream) : launch_t<64, false>(L, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -6,7 +6,7 @@
 //
 // Same computation as prefill.cu (RoPE on Q and K tiles in shared memory, GQA
 // packing of the G heads that share a KV head into each 128-row M tile, online
-// exp2 softmax, key tiles outside the causal/window/prefix bounds skipped), but
+// exp2 softmax, key tiles outside the causal/window/prefix/sink bounds skipped), but
 // a work item is four M tiles of one (batch, kv head) unit spread over the two
 // CTAs of a cluster, and each 128-key tile is shared by both CTAs:
 //
@@ -267,8 +267,16 @@ __device__ __forceinline__ int q_heads_softmax(int G) { return G - G / 4; }
 // tile T = 2 rank + t of the pair covers rows r0 + T P .. r0 + T P + P - 1.
 struct Item {
     int unit, r0, j_lo, n_kt, zq;
+    int sink;  // of the n_kt key tiles, how many are the first ones of the sequence
+    // the j-th key tile
+    template <bool SINK>
+    __device__ __forceinline__ int tile(int j) const
+    {
+        return SINK && j < sink ? j : j_lo + j;
+    }
 };
 
+template <bool SINK>
 __device__ __forceinline__ Item make_item(const PrefillParams &p, int w)
 {
     Item it;
@@ -284,6 +292,12 @@ __device__ __forceinline__ Item make_item(const PrefillParams &p, int w)
     const int key_hi = (m_first < p.prefix_len) ? max(m_last, p.prefix_len - 1) : m_last;
     it.j_lo = key_lo / 128;
     it.n_kt = key_hi / 128 - it.j_lo + 1;
+    it.sink = 0;
+    if (SINK) {  // the tiles of the sinks that lie before the window's
+        it.sink = min(it.j_lo, (p.n_sink + 127) / 128);
+        it.j_lo -= it.sink;
+        it.n_kt += it.sink;
+    }
     it.zq = b * p.H_q + hk * p.G;
     return it;
 }
@@ -297,8 +311,9 @@ __device__ __forceinline__ int item_index(int k)
 
 // KROT: the K tiles are rotated in shared memory; false: the instance for keys
 // rotated beforehand (by the library's key pass or by the caller), at both row
-// widths.
-template <int DQK, int DR, bool KROT>
+// widths.  SINK: the first n_sink keys stay visible behind the window; a work item
+// then visits their tiles before the window's.
+template <int DQK, int DR, bool KROT, bool SINK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -366,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (C::kTmaStoreO) tma_prefetch_desc(&tm_o);
             int kc = 0;
             for (int k = 0, w = item_index(0); w < p.n_work; ++k, w = item_index(k)) {
-                const Item it = make_item(p, w);
+                const Item it = make_item<SINK>(p, w);
                 auto load_q = [&]() {
                     for (int t = 0; t < 2; ++t) {
                         pair_wait(bar(kBarQEmpty + t), (k & 1) ^ 1, p.wait, abort);
@@ -378,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 };
                 for (int j = 0; j < it.n_kt; ++j, ++kc) {
-                    const int key0 = 128 * (it.j_lo + j);
+                    const int key0 = 128 * it.tile<SINK>(j);
                     const int ks = kc % kKStages, vs = kc % kVStages;
                     // one "stage empty" barrier frees K(kc) and V(kc) together: it is
                     // committed after PV(kc - stages), which follows QK(kc - stages)
@@ -427,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             };
             int kc = 0;
             for (int k = 0, w = item_index(0); w < p.n_work; ++k, w = item_index(k)) {
-                const Item it = make_item(p, w);
+                const Item it = make_item<SINK>(p, w);
                 const int n = it.n_kt;
                 pair_wait(bar(kBarKReady + kc % kKStages), (kc / kKStages) & 1, p.wait, abort);
                 for (int t = 0; t < 2; ++t) {
@@ -480,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (KROT) kr.init(p.rope.cs, c);
         int kc = 0;
         for (int k = 0, w = item_index(0); w < p.n_work; ++k, w = item_index(k)) {
-            const Item it = make_item(p, w);
+            const Item it = make_item<SINK>(p, w);
             if (q_shared(KROT, p.G)) {
                 // this CTA's share of the item's Q tiles: heads [hs, G) of both
                 const int hs = q_heads_softmax(p.G);
@@ -497,13 +512,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (lane == 0) arrive_leader(bar(kBarQReady + t));
                 }
             }
-            if (KROT) kr.load_seed(p.rope.cs, min(128 * it.j_lo + half0 + r0, max_row), c);
+            if (KROT) kr.load_seed(p.rope.cs, min(128 * it.tile<SINK>(0) + half0 + r0, max_row), c);
             for (int j = 0; j < it.n_kt; ++j, ++kc) {
                 const int ks = kc % kKStages;
                 pair_wait(bar(kBarKFull + ks), (kc / kKStages) & 1, p.wait, abort);
                 if (KROT && !p.keys_prerotated) kr.rotate(smem + kKOff + ks * kKTile, rt);
                 if (KROT && j + 1 < it.n_kt)
-                    kr.load_seed(p.rope.cs, min(128 * (it.j_lo + j + 1) + half0 + r0, max_row), c);
+                    kr.load_seed(p.rope.cs, min(128 * it.tile<SINK>(j + 1) + half0 + r0, max_row), c);
                 // K(j) ready also means V(j) has landed: the MMA thread waits for
                 // KReady(j) before QK(j), which precedes PV(j)
                 pair_wait(bar(kBarVFull + kc % kVStages), (kc / kVStages) & 1, p.wait, abort);
@@ -545,9 +560,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) arrive_leader(bar(kBarQReady + t));
         };
         int kc = 0;
-        if (item_index(0) < p.n_work) rotate_q(make_item(p, item_index(0)), 0);
+        if (item_index(0) < p.n_work) rotate_q(make_item<SINK>(p, item_index(0)), 0);
         for (int k = 0, w = item_index(0); w < p.n_work; ++k, w = item_index(k)) {
-            const Item it = make_item(p, w);
+            const Item it = make_item<SINK>(p, w);
             const int r = it.r0 + T * P + i % P;  // query row index
             const int m = p.q_pos0 + r;           // its position
             const bool in_prefix = m < p.prefix_len;
@@ -558,17 +573,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int j = 0; j < it.n_kt; ++j) {
                 pair_wait(bar(kBarSFull + t), (kc + j) & 1, p.wait, abort);
                 tc_fence_after();
-                const int kstart = 128 * (it.j_lo + j);
+                const int kstart = 128 * it.tile<SINK>(j);
                 const int hi_c = key_hi - kstart;
                 const int lo_c = key_lo - kstart;
-                const bool full_vis = lo_c <= 0 && hi_c >= 127;
+                const bool full_vis = (lo_c <= 0 || (SINK && kstart + 128 <= p.n_sink)) && hi_c >= 127;
                 const bool all_full = __all_sync(0xffffffffu, full_vis);
                 uint32_t v[128];
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch)
                     tmem_ld32(s_addr + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * ch]));
                 tmem_wait_ld();
-                if (!all_full) mask_row128(v, lo_c, hi_c);
+                if (SINK && !all_full && kstart < p.n_sink)
+                    mask_row128_sink(v, lo_c, hi_c, p.n_sink - kstart);
+                else if (!all_full)
+                    mask_row128(v, lo_c, hi_c);
                 float acc[8];
 #pragma unroll
                 for (int a = 0; a < 8; ++a) acc[a] = __uint_as_float(v[a]);
@@ -632,7 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             kc += it.n_kt;
 
             const int w_next = item_index(k + 1);
-            if (w_next < p.n_work) rotate_q(make_item(p, w_next), k + 1);
+            if (w_next < p.n_work) rotate_q(make_item<SINK>(p, w_next), k + 1);
 
             // ---- epilogue: O / l -> bf16 -> global, one row per thread
             pair_wait(bar(kBarODone + t), k & 1, p.wait, abort);
@@ -708,32 +726,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int DQK, int DR, bool KROT>
+template <int DQK, int DR, bool KROT, bool SINK>
 cudaError_t launch_pair_t(const PrefillLaunch &L, cudaStream_t stream)
 {
     using C = PairCfg<DQK, DR>;
-    cudaError_t err = cudaFuncSetAttribute(prefill_pair_kernel<DQK, DR, KROT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t err = cudaFuncSetAttribute(prefill_pair_kernel<DQK, DR, KROT, SINK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            C::kSmemBytes);
     if (err != cudaSuccess) return err;
     // setmaxnreg.inc blocks until the block's own pool can serve it: never
     // launch unless the split fits the registers the block is launched with
     cudaFuncAttributes fa;
-    err = cudaFuncGetAttributes(&fa, prefill_pair_kernel<DQK, DR, KROT>);
+    err = cudaFuncGetAttributes(&fa, prefill_pair_kernel<DQK, DR, KROT, SINK>);
     if (err != cudaSuccess) return err;
     if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-    return launch_dependent(prefill_pair_kernel<DQK, DR, KROT>, L.grid, kThreads, C::kSmemBytes, stream, L.tm_q, L.tm_k,
+    return launch_dependent(prefill_pair_kernel<DQK, DR, KROT, SINK>, L.grid, kThreads, C::kSmemBytes, stream, L.tm_q, L.tm_k,
                             L.tm_v, L.tm_o, L.p);
 }
 
 }  // namespace
 
+template <int DQK, int DR>
+static cudaError_t launch_pair_rows(const PrefillLaunch &L, cudaStream_t stream)
+{
+    if (L.p.n_sink > 0)
+        return L.p.keys_prerotated ? launch_pair_t<DQK, DR, false, true>(L, stream)
+                                   : launch_pair_t<DQK, DR, true, true>(L, stream);
+    return L.p.keys_prerotated ? launch_pair_t<DQK, DR, false, false>(L, stream)
+                               : launch_pair_t<DQK, DR, true, false>(L, stream);
+}
+
 cudaError_t launch_prefill_pair(const PrefillLaunch &L, cudaStream_t stream)
 {
     if (L.grid & 1) return cudaErrorInvalidValue;
-    if (L.p.d_h == 128 && L.p.d_rope == 128)
-        return L.p.keys_prerotated ? launch_pair_t<128, 128, false>(L, stream) : launch_pair_t<128, 128, true>(L, stream);
-    if (L.p.d_h == 192 && L.p.d_rope == 64)
-        return L.p.keys_prerotated ? launch_pair_t<192, 64, false>(L, stream) : launch_pair_t<192, 64, true>(L, stream);
+    if (L.p.d_h == 128 && L.p.d_rope == 128) return launch_pair_rows<128, 128>(L, stream);
+    if (L.p.d_h == 192 && L.p.d_rope == 64) return launch_pair_rows<192, 64>(L, stream);
     return cudaErrorInvalidValue;
 }
 

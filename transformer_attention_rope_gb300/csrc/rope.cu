@@ -1,13 +1,6 @@
 // rope.cu -- rotary positions of query and key rows at given token positions
 // (Part 1, §4.2-§4.4), interleaved or half layout, any part of the row, with an
-// optional append of rotated keys and of values to cache rows.
-//
-// Angles: theta_i is held as a 64-bit fraction of a turn, f_i = 2^64 theta_i / 2 pi.
-// m * f_i mod 2^64 is then the angle of position m reduced to one turn -- exactly,
-// for every int32 m of either sign -- and its top 32 bits, as a signed fraction of
-// half a turn, go to sincospi.  theta_i carries the 2^-53 of double precision, so
-// the reduced angle of m = 2^24 is off by under 2^-30 turns; made a float, of 24 bits, it is
-// rounded by up to 2^-26 turns at any m, about 10^-7 of what turns.
+// optional append of rotated keys and of values to cache rows.  How angles are made: rope.cuh.
 //
 // A thread owns one unit of a token's row and walks over heads, so the sines and
 // cosines of the unit (4 or 8 pairs) are computed once per head group; a unit is
@@ -16,6 +9,7 @@
 // 128 + 8 heads of 192 entries (856 MB): 130 us, 6.6 TB/s; one token of 32 + 8 heads with its
 // key and value appended: 2.4 us.
 #include "device_common.cuh"
+#include "rope.cuh"
 #include "rope.h"
 
 namespace apex {
@@ -24,19 +18,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;  // heads whose loads are in flight together
 
-// (cos, sin) of pair i at position m; sign: +1, or -1 for the inverse rotation
+// (cos, sin) of pair i at position m
 __device__ __forceinline__ void pair_angle(const RopeParams &p, int i, int m, float &c, float &s)
 {
-    const uint64_t turn = (uint64_t)(int64_t)m * p.turns[i];
-    const int32_t top = (int32_t)(turn >> 32);
-    sincospif((float)top * 0x1p-31f, &s, &c);
-    s *= p.sign;
-}
-
-__device__ __forceinline__ void rotate2(float x, float y, float c, float s, float &u, float &w)
-{
-    u = fmaf(x, c, -y * s);
-    w = fmaf(x, s, y * c);
+    turn_angle(p.turns[i], m, p.sign, c, s);
 }
 
 // Output row of token s of sequence b, or -1 when it is not written.
