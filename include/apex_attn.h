@@ -480,7 +480,7 @@ typedef struct apex_norm_tensor {
  * An out may be its own x with the same strides (of k and v only without row0); otherwise no
  * out may share an element with any x, weight or other out, nor hold one twice.
  * d_row <= 1024, n_heads <= 16384, d_rot <= 512; eps >= 0 and finite.  16-byte aligned rows of
- * up to 256 entries with d_rot (half layout: d_rot / 2), rot_start and d_row multiples of 8 run
+ * up to 512 entries with d_rot (half layout: d_rot / 2), rot_start and d_row multiples of 8 run
  * 16 bytes at a time.
  */
 apex_status apex_attn_norm_rope(const apex_norm_tensor *q, const apex_norm_tensor *k, const apex_rope_tensor *v, int B,

@@ -127,6 +127,10 @@ CASES = [  # B, S, Hq, Hkv, d, options, weights
     (1, 3, 2, 1, 1024, dict(d_rot=512, half=True, rot_start=256), "bf16"),  # the widest row
     (2, 700, 6, 3, 64, dict(half=True), "bf16"),
     (1, 1500, 32, 8, 128, dict(half=True), "bf16"),
+    (2, 45, 9, 3, 512, dict(half=True, d_rot=256), "heads"),   # 32 lanes a row
+    (1, 90, 20, 5, 384, dict(rot_start=128, d_rot=256), "heads"),
+    (2, 300, 12, 5, 72, dict(half=True, d_rot=64, rot_start=8), "heads"),  # an odd number of chunks
+    (2, 300, 12, 5, 72, dict(d_rot=8, rot_start=64), "fp32"),
 ]
 
 

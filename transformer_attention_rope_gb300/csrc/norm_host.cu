@@ -75,7 +75,7 @@ bool outputs_apart(const apex_norm_tensor *const (&t)[3], bool grad, int B, int 
     return true;
 }
 
-// Whether 16-byte chunks fit the rows; a lane then holds one.
+// Whether 16-byte chunks fit the rows; a lane then holds two.
 bool rows_of_16_bytes(const apex_norm_tensor &t, bool grad)
 {
     long long strides = t.x_b | t.x_h | t.x_s | t.out_b | t.out_h | t.out_s;
@@ -90,7 +90,7 @@ struct Plan {
     int lanes;   // of a row; 0: 2 bytes at a time
     int heads;   // of all tensors
     int sm_count;
-    long long rows_x;  // blocks for all tokens
+    int slots;   // rows that a block works on at once
 };
 
 // Checks and parameters shared by the pass and its gradient; t: q, k, v.
@@ -159,9 +159,8 @@ apex_status make_plan(const apex_norm_tensor *const (&t)[3], bool grad, int B, i
         plan->heads += a.n_heads;
         width = std::max(width, a.d_row);
     }
-    plan->lanes = !wide ? 0 : width <= 64 ? 8 : width <= 128 ? 16 : 32;
-    const int rows = kNormThreads / (wide ? plan->lanes : 32);
-    plan->rows_x = ((long long)B * S + rows - 1) / rows;
+    plan->lanes = !wide ? 0 : width <= 64 ? 4 : width <= 128 ? 8 : width <= 256 ? 16 : 32;
+    plan->slots = kNormThreads / (wide ? plan->lanes : 32);
     p.positions = positions;
     p.pos_stride = pos_stride;
     p.row0 = row0;
@@ -180,13 +179,43 @@ apex_status make_plan(const apex_norm_tensor *const (&t)[3], bool grad, int B, i
     return APEX_OK;
 }
 
-// Groups of `per` heads; their number over all tensors.
-int make_groups(NormRopeParams &p, int per)
+// Cuts the work for rows that go 16 bytes at a time, into `blocks` (group, tile)s if there is so
+// much.  A block makes the sines of its tile for all heads of its group, and so has `rows` rows for each
+// of its slots, of as many heads and then tokens as there are; a slot takes two heads of a token, whose
+// loads are in flight together.  Where that leaves SMs without blocks, a block has fewer rows, and
+// at last one for each slot.  Weights of each head's own are held for `most` heads of a block; a
+// gradient's slot has one head then, whose sums it makes.
+void cut_rows(Plan &plan, int rows, bool grad, int most, long long blocks)
 {
-    int n = 0;
-    p.per = per;
-    for (int i = 0; i < p.n_tensors; ++i) n += p.t[i].n_groups = (p.t[i].n_heads + per - 1) / per;
-    return n;
+    NormRopeParams &p = plan.p;
+    for (;; rows /= 2) {
+        long long n = 0;
+        for (int i = 0; i < p.n_tensors; ++i) {
+            NormTensor &t = p.t[i];
+            const int room = std::max(1, rows) * plan.slots;
+            t.per = std::min(t.n_heads, room);
+            t.batch = rows > 0 ? 2 : 1;
+            if (t.weight_h != 0) {
+                t.per = std::min(t.per, most);
+                if (grad) t.batch = 1;
+            }
+            t.n_groups = (t.n_heads + t.per - 1) / t.per;
+            t.tile = std::max(1, std::min({plan.slots, room / t.per, p.S}));
+            t.tiles = (p.S + t.tile - 1) / t.tile;
+            n += (long long)t.n_groups * p.B * t.tiles;
+        }
+        if (n >= blocks || rows == 0) return;
+    }
+}
+
+// The same for rows that go 2 bytes at a time: a token for each warp, head after head.
+void cut_tokens(Plan &plan, int per)
+{
+    for (int i = 0; i < plan.p.n_tensors; ++i) {
+        NormTensor &t = plan.p.t[i];
+        t.per = per;
+        t.n_groups = (t.n_heads + per - 1) / per;
+    }
 }
 
 }  // namespace
@@ -214,14 +243,19 @@ apex_status apex_attn_norm_rope(const apex_norm_tensor *q, const apex_norm_tenso
     Plan plan;
     const apex_status s = make_plan(t, false, B, S, positions, pos_stride, row0, out_rows, opt, eps, &plan);
     if (s != APEX_OK) return s;
-    // Heads per group: as for apex_attn_rope, up to 4 (whose loads are in flight together) as
-    // far as a block for every SM goes, and 8 beyond.
-    const long long share = (plan.rows_x * plan.heads + plan.sm_count - 1) / plan.sm_count;
-    const int per = share >= 8 ? 8 : (int)std::min<long long>(4, share);
-    const int groups = make_groups(plan.p, per);  // 3 * 16384 at most
-    const int grid_x = (int)std::min<long long>(plan.rows_x, 1 << 20);
-    if (launch_norm_rope(plan.p, plan.half, plan.lanes, grid_x, groups, reinterpret_cast<cudaStream_t>(stream)) !=
-        cudaSuccess)
+    NormRopeParams &p = plan.p;
+    if (plan.lanes) {
+        cut_rows(plan, 8, false, kNormHeads / plan.lanes, 2 * plan.sm_count);
+        for (int i = 0; i < p.n_tensors; ++i)
+            p.t[i].blocks = (int)std::min<long long>((long long)B * p.t[i].tiles, 1 << 16);
+    } else {
+        // up to 8 heads with four blocks an SM
+        const long long bx = ((long long)B * S + plan.slots - 1) / plan.slots;
+        const long long share = (bx * plan.heads + 4 * plan.sm_count - 1) / (4 * plan.sm_count);
+        cut_tokens(plan, (int)std::min<long long>(8, share));
+        for (int i = 0; i < p.n_tensors; ++i) p.t[i].blocks = (int)std::min<long long>(bx, 1 << 16);
+    }
+    if (launch_norm_rope(p, plan.half, plan.lanes, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return APEX_ERR_CUDA;
     return APEX_OK;
 }
@@ -229,7 +263,7 @@ apex_status apex_attn_norm_rope(const apex_norm_tensor *q, const apex_norm_tenso
 size_t apex_attn_norm_rope_grad_workspace_bytes(int H_q, int H_kv, int d_q, int d_k)
 {
     if (H_q <= 0 || H_kv < 0 || d_q <= 0 || d_k < 0 || H_q > 16384 || H_kv > 16384 || d_q > 1024 || d_k > 1024) return 0;
-    return (size_t)std::max(kNormGradBlocks, H_q + H_kv) * std::max(d_q, d_k) * sizeof(float);
+    return ((size_t)kNormGradBlocks * kNormGradHeads + H_q + H_kv) * std::max(d_q, d_k) * sizeof(float);
 }
 
 apex_status apex_attn_norm_rope_grad(const apex_norm_tensor *q, const apex_norm_tensor *k, int B, int S,
@@ -244,21 +278,28 @@ apex_status apex_attn_norm_rope_grad(const apex_norm_tensor *q, const apex_norm_
     Plan plan;
     const apex_status s = make_plan(t, true, B, S, positions, pos_stride, nullptr, 0, opt, eps, &plan);
     if (s != APEX_OK) return s;
-    // With weights for each head a block has one head, as it adds up one head's sums.
-    bool per_head = false;
-    for (int i = 0; i < plan.p.n_tensors; ++i) per_head = per_head || plan.p.t[i].weight_h != 0;
-    const long long share = (plan.rows_x * plan.heads + 2 * plan.sm_count - 1) / (2 * plan.sm_count);
-    const int per = per_head ? 1 : share >= 8 ? 8 : (int)std::max<long long>(1, std::min<long long>(4, share));
-    int groups = make_groups(plan.p, per);
-    // as many blocks as run at once, so that a block's sums are of many rows
-    const int grid_x = (int)std::min<long long>(plan.rows_x, std::max(1, std::min(kNormGradBlocks, 3 * plan.sm_count) / groups));
-    float *partial = static_cast<float *>(workspace);
-    for (int i = 0; i < plan.p.n_tensors; ++i) {
-        plan.p.t[i].partial = partial;
-        partial += (size_t)plan.p.t[i].n_groups * grid_x * plan.p.t[i].d_row;
+    NormRopeParams &p = plan.p;
+    const int room = std::min(kNormGradBlocks, 2 * plan.sm_count);  // as many blocks as run at once
+    if (plan.lanes) {
+        cut_rows(plan, 8, true, std::min({kNormGradHeads, plan.slots, kNormHeads / plan.lanes}), room);
+    } else {
+        // with weights for each head a block has one head, whose sums it makes
+        cut_tokens(plan, 8);
+        for (int i = 0; i < p.n_tensors; ++i)
+            if (p.t[i].weight_h != 0) p.t[i].n_groups = p.t[i].n_heads, p.t[i].per = 1;
     }
-    if (launch_norm_rope_grad(plan.p, plan.half, plan.lanes, grid_x, groups, reinterpret_cast<cudaStream_t>(stream)) !=
-        cudaSuccess)
+    // blocks in proportion to the heads, so that a block's sums are of many rows and all end together:
+    // room at most in all, or one for each group
+    float *partial = static_cast<float *>(workspace);
+    for (int i = 0; i < p.n_tensors; ++i) {
+        NormTensor &a = p.t[i];
+        const long long most = plan.lanes ? (long long)B * a.tiles : ((long long)B * S + plan.slots - 1) / plan.slots;
+        const long long share = (long long)room * a.n_heads / plan.heads / a.n_groups;
+        a.blocks = (int)std::max(1ll, std::min(most, share));
+        a.partial = partial;
+        partial += (size_t)(a.weight_h != 0 ? a.n_heads : a.n_groups) * a.blocks * a.d_row;
+    }
+    if (launch_norm_rope_grad(p, plan.half, plan.lanes, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return APEX_ERR_CUDA;
     return APEX_OK;
 }

@@ -8,10 +8,12 @@
 // rs is made again from x: keeping it would save none of x's bytes.
 //
 // The bound is HBM: a row is read once (twice as many bytes for the gradient) and written once.
-// A row belongs to 8, 16 or 32 neighbouring lanes with 16 bytes each, so its sums are a few
-// shuffles, the other half of a pair (half layout) is one lane away, and nothing goes through
-// shared memory.  A lane walks over the heads of its token: their loads are in flight
-// together and share the sines.
+// A row belongs to 4, 8, 16 or 32 neighbouring lanes.  A lane holds two 16-byte chunks, chosen so
+// that it has both entries of its 8 pairs: pairs need no exchange, sums a few shuffles.  A block
+// has a tile of neighbouring tokens and a slice of one tensor's heads; it makes the tile's sines
+// once, in shared memory (c = 1, s = 0 where nothing turns, so that every pair goes the same way),
+// and a lane takes them, times the weights, once for its heads of a token.  Pairs are worked on
+// two at a time, as packed fp32.
 //
 // dw: a thread adds up its 8 columns over all rows that it meets, a block its threads' sums,
 // and a second kernel the blocks' sums, in 64 bits: a fixed order, so equal inputs give equal
@@ -23,8 +25,7 @@
 namespace apex {
 namespace {
 
-constexpr int kBatch = 4;      // heads whose loads are in flight together
-constexpr int kGradBatch = 2;  // of the gradient, with two rows each
+constexpr int kBatch = 2;  // rows of a lane whose loads are in flight together
 
 __device__ __forceinline__ long long out_row(const NormRopeParams &p, const NormTensor &t, int b, int s)
 {
@@ -41,20 +42,11 @@ __device__ __forceinline__ float weight_at(const NormTensor &t, int h, int e)
                         : bf16lo_to_f32(static_cast<const uint16_t *>(t.weight)[i]);
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8])
+__device__ __forceinline__ float sum2(uint64_t x)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        f[2 * e] = bf16lo_to_f32(w[e]);
-        f[2 * e + 1] = bf16hi_to_f32(w[e]);
-    }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8])
-{
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+    float lo, hi;
+    f2_unpack(x, lo, hi);
+    return lo + hi;
 }
 
 template <int L>
@@ -65,210 +57,415 @@ __device__ __forceinline__ float sum_lanes(float x)
     return x;
 }
 
-__device__ __forceinline__ uint4 shfl4(const uint4 &v, int lane)
+// Number of a block's tensor, and its group of heads and its number within the group.
+__device__ __forceinline__ int tensor_of(const NormRopeParams &p, int &group, int &block)
 {
-    return make_uint4(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane),
-                      __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane));
+    int i = 0;
+    block = blockIdx.x;
+    while (block >= p.t[i].n_groups * p.t[i].blocks) {
+        block -= p.t[i].n_groups * p.t[i].blocks;
+        ++i;
+    }
+    group = block / p.t[i].blocks;
+    block -= group * p.t[i].blocks;
+    return i;
 }
 
-// What a lane does with its chunk of 8 entries: which pairs they belong to and where the
-// other halves of the pairs are.
-template <int L, bool HALF>
-struct Chunk {
-    int at;       // its index in the row
-    bool mine;    // inside the row
-    bool turned;  // inside the part that turns
-    bool second;  // half layout: holds the second entries of its pairs
-    int pair;     // first pair
-    int other;    // lane (and chunk, below) of the pairs' other entries
-    int other_at;
-    __device__ __forceinline__ Chunk(const NormRopeParams &p, const NormTensor &t)
-    {
-        const int lane = threadIdx.x & 31;
-        at = lane % L;
-        mine = at < (t.d_row >> 3);
-        const int c0 = p.rot_start >> 3, n = p.d_rot >> 3, in = at - c0;
-        turned = t.norm && in >= 0 && in < n;
-        second = HALF && turned && in >= n / 2;
-        pair = HALF ? 8 * (second ? in - n / 2 : in) : 4 * in;
-        other_at = (HALF && turned) ? (second ? at - n / 2 : at + n / 2) : at;
-        other = lane - at + other_at;
+// The two chunks of 8 entries that lane u of a row holds (-1: none).  Half layout: those whose
+// entries pair up, then the others two by two; interleaved: neighbours.
+template <bool HALF>
+__device__ __forceinline__ void chunks_of(const NormRopeParams &p, int d_row, bool turns, int u, int &a, int &b)
+{
+    const int n = d_row >> 3, c0 = p.rot_start >> 3, nrot = HALF && turns ? p.d_rot >> 3 : 0, np = nrot >> 1;
+    if (u < np) {
+        a = c0 + u;
+        b = a + np;
+        return;
     }
-    // entries a (own) and o (the other halves', half layout) turned by (c, s)
-    __device__ __forceinline__ void turn(float (&a)[8], const float (&o)[8], const float *c, const float *s) const
-    {
+    a = 2 * (u - np);
+    b = a + 1;
+    if (nrot > 0) {  // past the turned part
+        if (a >= c0) a += nrot;
+        if (b >= c0) b += nrot;
+    }
+    if (a >= n) a = -1;
+    if (b >= n) b = -1;
+}
+
+// Two chunks as pairs of fp32: A the first entries of the lane's pairs, B the second ones.
+template <bool HALF>
+__device__ __forceinline__ void unpack(const uint4 &x, const uint4 &y, uint64_t (&A)[4], uint64_t (&B)[4])
+{
+    const uint32_t v[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
         if (HALF) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) a[e] = second ? fmaf(o[e], s[e], a[e] * c[e]) : fmaf(a[e], c[e], -o[e] * s[e]);
+            A[e] = f2_pack(bf16lo_to_f32(v[e]), bf16hi_to_f32(v[e]));
+            B[e] = f2_pack(bf16lo_to_f32(w[e]), bf16hi_to_f32(w[e]));
         } else {
+            const uint32_t lo = e < 2 ? v[2 * e] : w[2 * e - 4], hi = e < 2 ? v[2 * e + 1] : w[2 * e - 3];
+            A[e] = f2_pack(bf16lo_to_f32(lo), bf16lo_to_f32(hi));
+            B[e] = f2_pack(bf16hi_to_f32(lo), bf16hi_to_f32(hi));
+        }
+    }
+}
+
+template <bool HALF>
+__device__ __forceinline__ void pack(const uint64_t (&A)[4], const uint64_t (&B)[4], uint4 &x, uint4 &y)
+{
+    uint32_t v[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) rotate2(a[2 * e], a[2 * e + 1], c[e], s[e], a[2 * e], a[2 * e + 1]);
+    for (int e = 0; e < 4; ++e) {
+        float a0, a1, b0, b1;
+        f2_unpack(A[e], a0, a1);
+        f2_unpack(B[e], b0, b1);
+        if (HALF) {
+            v[e] = pack_bf16x2(a0, a1);
+            v[4 + e] = pack_bf16x2(b0, b1);
+        } else {
+            v[2 * e] = pack_bf16x2(a0, b0);
+            v[2 * e + 1] = pack_bf16x2(a1, b1);
+        }
+    }
+    x = make_uint4(v[0], v[1], v[2], v[3]);
+    y = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
+// Where a lane stands: its chunks of a row, and its slot's place among the rows of a tile.  `wide`
+// slots beside one another share the heads of a token, per_token each; the others have further
+// tokens.
+template <int L, bool HALF>
+struct Lane {
+    int u, a, b;  // number in the row, entries where its chunks start (-1: none)
+    int wide, deep, h0, t0, per_token;
+    __device__ __forceinline__ Lane(const NormRopeParams &p, const NormTensor &t, int heads)
+    {
+        const int slot = threadIdx.x / L;
+        u = threadIdx.x % L;
+        chunks_of<HALF>(p, t.d_row, t.norm, u, a, b);
+        a *= 8, b *= 8;
+        wide = min((heads + t.batch - 1) / t.batch, kNormThreads / L);
+        deep = kNormThreads / L / wide;
+        h0 = slot % wide;
+        t0 = slot / wide;
+        if (t0 >= deep) t0 = kNormThreads / L;  // a slot that is left over: past every tile
+        per_token = (heads + wide - 1) / wide;
+    }
+    // address of the lane's first chunk: of its second where there is none, which is not used then
+    template <typename T>
+    __device__ __forceinline__ T *at(T *row) const
+    {
+        return row + max(a, 0);
+    }
+    __device__ __forceinline__ int apart() const { return b - a; }
+};
+
+// Weight of the first or second entry of pair e of the chunks at entries a and b, for head h.
+template <bool HALF>
+__device__ __forceinline__ float pair_weight(const NormTensor &t, int h, int a, int b, int e, bool second)
+{
+    const int at = HALF ? (second ? b : a) + e : (e < 4 ? a : b) + 2 * (e & 3) + second;
+    const bool there = HALF ? (second ? b : a) >= 0 : (e < 4 ? a : b) >= 0;
+    return there ? weight_at(t, h, at) : 0.f;
+}
+
+// Sines of a tile's tokens and the weights that all heads share, as the lanes' pairs lie:
+// [four pairs][lane][4].
+template <int L>
+struct Shared {
+    float c[kNormThreads / L][2][L][4], s[kNormThreads / L][2][L][4], ns[kNormThreads / L][2][L][4];  // a tile has a token for each slot at most
+    float wa[kNormHeads / L][2][L][4], wb[kNormHeads / L][2][L][4];  // of the group's heads, or of all
+
+    static __device__ __forceinline__ void get(const float (&from)[2][L][4], int u, uint64_t (&x)[4])
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(from[h][u]);
+            x[2 * h] = v.x;
+            x[2 * h + 1] = v.y;
+        }
+    }
+    // weights of the group's heads, or those that all share, by the block
+    template <bool HALF>
+    __device__ __forceinline__ void weights(const NormRopeParams &p, const NormTensor &t, int first, int heads)
+    {
+        const int n = t.weight_h == 0 ? 1 : heads;
+        for (int i = threadIdx.x; i < n * 8 * L; i += kNormThreads) {
+            const int h = i / (8 * L), u = i / 8 % L, e = i % 8;
+            int a, b;
+            chunks_of<HALF>(p, t.d_row, true, u, a, b);
+            wa[h][e >> 2][u][e & 3] = pair_weight<HALF>(t, first + h, 8 * a, 8 * b, e, false);
+            wb[h][e >> 2][u][e & 3] = pair_weight<HALF>(t, first + h, 8 * a, 8 * b, e, true);
+        }
+    }
+    // sines of tokens s0 .. s0 + n - 1 of sequence b, by the block
+    template <bool HALF>
+    __device__ __forceinline__ void turn(const NormRopeParams &p, const NormTensor &t, int b, int s0, int n)
+    {
+#pragma unroll 2
+        for (int i = threadIdx.x; i < n * 8 * L; i += kNormThreads) {
+            const int k = i / (8 * L), u = i / 8 % L, e = i % 8;
+            int ca, cb;
+            chunks_of<HALF>(p, t.d_row, true, u, ca, cb);
+            // entry that the pair starts with
+            const int x = HALF ? 8 * ca + e : 8 * (e < 4 ? ca : cb) + 2 * (e & 3), in = x - p.rot_start;
+            float cos = 1.f, sin = 0.f;
+            if (ca >= 0 && (HALF ? u < p.d_rot >> 4 : (e < 4 || cb >= 0) && in >= 0 && in < p.d_rot))
+                turn_angle(p.turns[HALF ? in : in >> 1], p.positions[b * p.pos_stride + s0 + k], p.sign, cos, sin);
+            c[k][e >> 2][u][e & 3] = cos;
+            s[k][e >> 2][u][e & 3] = sin;
+            ns[k][e >> 2][u][e & 3] = -sin;
         }
     }
 };
 
-__device__ __forceinline__ const NormTensor &tensor_of(const NormRopeParams &p, int &group)
-{
-    int i = 0;
-    group = blockIdx.y;
-    while (group >= p.t[i].n_groups) group -= p.t[i++].n_groups;
-    return p.t[i];
-}
-
 template <int L, bool HALF>
-__global__ void __launch_bounds__(kNormThreads) norm_rows_kernel(const __grid_constant__ NormRopeParams p)
+__global__ void __launch_bounds__(kNormThreads, 3) norm_rows_kernel(const __grid_constant__ NormRopeParams p)
 {
     // launched as a programmatic dependent: inputs may be the previous kernel's output
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int kRows = kNormThreads / L, kWarpRows = 32 / L, NA = HALF ? 8 : 4;
-    int group;
-    const NormTensor &t = tensor_of(p, group);
-    const int h0 = group * p.per, h1 = min(h0 + p.per, t.n_heads);
-    const Chunk<L, HALF> ch(p, t);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float w[8], wo[8];
+    __shared__ Shared<L> sh;
+    int group, block;
+    const NormTensor t = p.t[tensor_of(p, group, block)];
+    const int first = group * t.per, heads = min(t.per, t.n_heads - first);
+    const Lane<L, HALF> my(p, t, heads);
+    const bool shared = t.weight_h == 0;
+    if (t.norm) sh.template weights<HALF>(p, t, first, heads);
+    const long long x_step = my.wide * t.x_h, out_step = my.wide * t.out_h;
+    for (int tile = block; tile < p.B * t.tiles; tile += t.blocks) {  // below 2^31
+        const int b = tile / t.tiles, s0 = tile % t.tiles * t.tile, n = min(t.tile, p.S - s0);
+        const bool moved = t.append && p.row0;
+        const long long row0 = (moved ? p.row0[b] : 0) + (long long)s0, rows = moved ? p.out_rows : p.S;
+        const uint16_t *src = my.at(t.x + b * t.x_b + (s0 + my.t0) * t.x_s + (first + my.h0) * t.x_h);
+        uint16_t *dst = my.at(t.out + b * t.out_b + (row0 + my.t0) * t.out_s + (first + my.h0) * t.out_h);
+        bool made = !t.norm;
+        for (int tok = my.t0, i = 0; i < n; i += my.deep, tok += my.deep, src += my.deep * t.x_s, dst += my.deep * t.out_s) {
+            const bool in = my.a >= 0 && tok < n, two = my.b >= 0, out = in && row0 + tok >= 0 && row0 + tok < rows;
+            const uint16_t *from = src;
+            uint16_t *to = dst;
+            // u = a ca + b nsb, w = a sa + b cb: sines, times weights
+            uint64_t ca[4], sa[4], cb[4], nsb[4];
+            auto factors = [&](int h) {
+                uint64_t wa[4], wb[4], c[4], s[4], ns[4];
+                Shared<L>::get(sh.c[min(tok, n - 1)], my.u, c);
+                Shared<L>::get(sh.s[min(tok, n - 1)], my.u, s);
+                Shared<L>::get(sh.ns[min(tok, n - 1)], my.u, ns);
+                Shared<L>::get(sh.wa[h], my.u, wa);
+                Shared<L>::get(sh.wb[h], my.u, wb);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = wo[e] = 1.f;
-    auto load_weights = [&](int h) {
-        if (!t.norm || !t.weight || !ch.mine) return;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[e] = weight_at(t, h, 8 * ch.at + e);
-            if (HALF) wo[e] = weight_at(t, h, 8 * ch.other_at + e);
-        }
-    };
-    if (t.weight_h == 0) load_weights(0);
-    const int tokens = p.B * p.S;  // below 2^31
-    // the warp's rows together: every lane takes part in the shuffles
-    for (long long base = (long long)blockIdx.x * kRows + warp * kWarpRows; base < tokens;
-         base += (long long)gridDim.x * kRows) {
-        const long long token = base + lane / L;
-        const bool real = token < tokens;
-        const int b = real ? (int)(token / p.S) : 0, s = real ? (int)(token % p.S) : 0;
-        const long long row = out_row(p, t, b, s);
-        const bool ok = real && ch.mine && row >= 0;
-        const uint16_t *src = t.x + b * t.x_b + s * t.x_s + 8 * ch.at;
-        uint16_t *dst = t.out + b * t.out_b + row * t.out_s + 8 * ch.at;
-        float c[NA], sn[NA];
-        if (ch.turned) {
-            const int m = p.positions[b * p.pos_stride + s];
-#pragma unroll
-            for (int e = 0; e < NA; ++e) turn_angle(p.turns[ch.pair + e], m, p.sign, c[e], sn[e]);
-        }
-        for (int h = h0; h < h1; h += kBatch) {
-            uint4 x[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                x[k] = make_uint4(0, 0, 0, 0);
-                if (ok && h + k < h1) x[k] = *reinterpret_cast<const uint4 *>(src + (h + k) * t.x_h);
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (h + k >= h1) break;
-                if (t.norm) {
-                    float a[8], o[8];
-                    unpack8(x[k], a);
-                    if (HALF) unpack8(shfl4(x[k], ch.other), o);
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
-                    const float rs = rsqrtf(fmaf(sum_lanes<L>(ss), t.inv_d, p.eps));
-                    if (t.weight_h != 0) load_weights(h + k);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        a[e] *= rs * w[e];
-                        if (HALF) o[e] *= rs * wo[e];
-                    }
-                    if (ch.turned) ch.turn(a, o, c, sn);
-                    x[k] = pack8(a);
+                for (int e = 0; e < 4; ++e) {
+                    ca[e] = f2_mul(wa[e], c[e]);
+                    sa[e] = f2_mul(wa[e], s[e]);
+                    cb[e] = f2_mul(wb[e], c[e]);
+                    nsb[e] = f2_mul(wb[e], ns[e]);
                 }
-                if (ok) *reinterpret_cast<uint4 *>(dst + (h + k) * t.out_h) = x[k];
+            };
+            for (int h = my.h0, j = 0; j < my.per_token; j += kBatch) {
+                uint4 x[kBatch], y[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k, from += x_step) {
+                    x[k] = y[k] = make_uint4(0, 0, 0, 0);
+                    if (in && h + k * my.wide < heads) {
+                        x[k] = *reinterpret_cast<const uint4 *>(from);
+                        if (two) y[k] = *reinterpret_cast<const uint4 *>(from + my.apart());
+                    }
+                }
+                if (!made) {          // while the first rows are on the way
+                    __syncthreads();  // the last tile's sines are done with
+                    sh.template turn<HALF>(p, t, b, s0, n);
+                    __syncthreads();
+                    made = true;
+                }
+                if (t.norm && j == 0 && shared) factors(0);
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k, h += my.wide, to += out_step) {
+                    if (j + k >= my.per_token) break;
+                    if (t.norm) {
+                        if (!shared) factors(min(h, heads - 1));
+                        uint64_t A[4], B[4];
+                        unpack<HALF>(x[k], y[k], A, B);
+                        uint64_t s2 = 0, s3 = 0;  // +0
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s2 = f2_fma(A[e], A[e], s2);
+                            s3 = f2_fma(B[e], B[e], s3);
+                        }
+                        const float rs = rsqrtf(fmaf(sum_lanes<L>(sum2(f2_add(s2, s3))), t.inv_d, p.eps));
+                        const uint64_t rs2 = f2_pack(rs, rs);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint64_t u = f2_fma(B[e], nsb[e], f2_mul(A[e], ca[e]));
+                            B[e] = f2_mul(f2_fma(A[e], sa[e], f2_mul(B[e], cb[e])), rs2);
+                            A[e] = f2_mul(u, rs2);
+                        }
+                        pack<HALF>(A, B, x[k], y[k]);
+                    }
+                    if (out && h < heads) {
+                        *reinterpret_cast<uint4 *>(to) = x[k];
+                        if (two) *reinterpret_cast<uint4 *>(to + my.apart()) = y[k];
+                    }
+                }
             }
         }
     }
 }
 
+// Where the next row to load of a lane's slot is: over the heads of a token, the tokens of a tile
+// and the tiles of a block.
 template <int L, bool HALF>
-__global__ void __launch_bounds__(kNormThreads, 3) norm_grad_rows_kernel(const __grid_constant__ NormRopeParams p)
+struct Ahead {
+    const uint16_t *x, *dy;
+    long long x_step, dy_step, x_wrap, dy_wrap;  // to the next head, and from the last to the next token's first
+    int tile, n, tok, j, h;
+    __device__ __forceinline__ Ahead(const NormTensor &t, const Lane<L, HALF> &my, int block)
+        : x_step(my.wide * t.x_h), dy_step(my.wide * t.dy_h), x_wrap(my.deep * t.x_s - my.per_token * x_step),
+          dy_wrap(my.deep * t.dy_s - my.per_token * dy_step), tile(block)
+    {
+    }
+    __device__ __forceinline__ void start(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int first)
+    {
+        n = 0;
+        j = 0;
+        h = my.h0;
+        tok = my.t0;
+        if (tile >= p.B * t.tiles) return;
+        const int b = tile / t.tiles, s0 = tile % t.tiles * t.tile;
+        n = min(t.tile, p.S - s0);
+        x = my.at(t.x + b * t.x_b + (s0 + tok) * t.x_s + (first + h) * t.x_h);
+        dy = my.at(t.dy + b * t.dy_b + (s0 + tok) * t.dy_s + (first + h) * t.dy_h);
+    }
+    __device__ __forceinline__ void load(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int first,
+                                         int heads, uint4 (&v)[4])
+    {
+        v[0] = v[1] = v[2] = v[3] = make_uint4(0, 0, 0, 0);
+        if (my.a >= 0 && tok < n && h < heads) {
+            v[0] = *reinterpret_cast<const uint4 *>(x);
+            v[2] = *reinterpret_cast<const uint4 *>(dy);
+            if (my.b >= 0) {
+                v[1] = *reinterpret_cast<const uint4 *>(x + my.apart());
+                v[3] = *reinterpret_cast<const uint4 *>(dy + my.apart());
+            }
+        }
+        x += x_step;
+        dy += dy_step;
+        h += my.wide;
+        if (++j < my.per_token) return;
+        j = 0;
+        h = my.h0;
+        tok += my.deep;
+        x += x_wrap;
+        dy += dy_wrap;
+        if (tok - my.t0 >= n && n > 0) {  // the same for all slots
+            tile += t.blocks;
+            start(p, t, my, first);
+        }
+    }
+};
+
+template <int L, bool HALF>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_grad_rows_kernel(const __grid_constant__ NormRopeParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int kRows = kNormThreads / L, kWarpRows = 32 / L, NA = HALF ? 8 : 4;
-    __shared__ float sums[kRows][8 * L];
-    int group;
-    const NormTensor &t = tensor_of(p, group);
-    const int h0 = group * p.per, h1 = min(h0 + p.per, t.n_heads);
-    const Chunk<L, HALF> ch(p, t);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float w[8], dw[8];
+    __shared__ union {
+        Shared<L> t;
+        float sums[kNormThreads / L][16 * L];  // of each slot
+    } sh;
+    int group, block;
+    const NormTensor t = p.t[tensor_of(p, group, block)];
+    const int first = group * t.per, heads = min(t.per, t.n_heads - first);
+    const Lane<L, HALF> my(p, t, heads);
+    // with weights for each head a slot has one head
+    sh.t.template weights<HALF>(p, t, first, heads);
+    const int w = t.weight_h == 0 ? 0 : my.h0;
+    uint64_t da[4] = {0, 0, 0, 0}, db[4] = {0, 0, 0, 0};
+    const long long out_step = my.wide * t.out_h;
+    Ahead<L, HALF> ahead(t, my, block);
+    ahead.start(p, t, my, first);
+    uint4 v[4];  // the next row and its gradient are under way while one is worked on
+    ahead.load(p, t, my, first, heads, v);
+    for (int tile = block; tile < p.B * t.tiles; tile += t.blocks) {
+        const int b = tile / t.tiles, s0 = tile % t.tiles * t.tile, n = min(t.tile, p.S - s0);
+        uint16_t *dst = my.at(t.out + b * t.out_b + (s0 + my.t0) * t.out_s + (first + my.h0) * t.out_h);
+        __syncthreads();  // the last tile's sines are done with
+        sh.t.template turn<HALF>(p, t, b, s0, n);
+        __syncthreads();
+        for (int tok = my.t0, i = 0; i < n; i += my.deep, tok += my.deep, dst += my.deep * t.out_s) {
+            uint16_t *to = dst;
+            for (int h = my.h0, j = 0; j < my.per_token; ++j, h += my.wide, to += out_step) {
+                const bool real = tok < n && h < heads;
+                uint64_t A[4], B[4], G[4], H[4];
+                unpack<HALF>(v[0], v[1], A, B);
+                unpack<HALF>(v[2], v[3], G, H);
+                ahead.load(p, t, my, first, heads, v);
+                uint64_t c[4], s[4], ns[4], s2 = 0, s3 = 0, d2 = 0, d3 = 0;  // +0
+                Shared<L>::get(sh.t.c[min(tok, n - 1)], my.u, c);
+                Shared<L>::get(sh.t.s[min(tok, n - 1)], my.u, s);
+                Shared<L>::get(sh.t.ns[min(tok, n - 1)], my.u, ns);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        dw[e] = 0.f;
-        // with weights for each head a block has one head
-        w[e] = ch.mine ? weight_at(t, h0, 8 * ch.at + e) : 0.f;
-    }
-    const int tokens = p.B * p.S;
-    for (long long base = (long long)blockIdx.x * kRows + warp * kWarpRows; base < tokens;
-         base += (long long)gridDim.x * kRows) {
-        const long long token = base + lane / L;
-        const bool real = token < tokens, ok = real && ch.mine;
-        const int b = real ? (int)(token / p.S) : 0, s = real ? (int)(token % p.S) : 0;
-        const uint16_t *src = t.x + b * t.x_b + s * t.x_s + 8 * ch.at;
-        const uint16_t *grad = t.dy + b * t.dy_b + s * t.dy_s + 8 * ch.at;
-        uint16_t *dst = t.out + b * t.out_b + s * t.out_s + 8 * ch.at;
-        float c[NA], sn[NA];
-        if (ch.turned) {
-            const int m = p.positions[b * p.pos_stride + s];
-#pragma unroll
-            for (int e = 0; e < NA; ++e) turn_angle(p.turns[ch.pair + e], m, p.sign, c[e], sn[e]);
-        }
-        for (int h = h0; h < h1; h += kGradBatch) {
-            uint4 x[kGradBatch], y[kGradBatch];
-#pragma unroll
-            for (int k = 0; k < kGradBatch; ++k) {
-                x[k] = y[k] = make_uint4(0, 0, 0, 0);
-                if (ok && h + k < h1) {
-                    x[k] = *reinterpret_cast<const uint4 *>(src + (h + k) * t.x_h);
-                    y[k] = *reinterpret_cast<const uint4 *>(grad + (h + k) * t.dy_h);
+                for (int e = 0; e < 4; ++e) {  // the gradient turned back
+                    const uint64_t g = f2_fma(H[e], ns[e], f2_mul(G[e], c[e]));
+                    H[e] = f2_fma(G[e], s[e], f2_mul(H[e], c[e]));
+                    G[e] = g;
+                    s2 = f2_fma(A[e], A[e], s2);
+                    s3 = f2_fma(B[e], B[e], s3);
                 }
-            }
+                Shared<L>::get(sh.t.wa[w], my.u, c);
+                Shared<L>::get(sh.t.wb[w], my.u, s);
 #pragma unroll
-            for (int k = 0; k < kGradBatch; ++k) {
-                if (h + k >= h1) break;
-                float a[8], g[8], o[8];
-                unpack8(x[k], a);
-                unpack8(y[k], g);
-                if (HALF) unpack8(shfl4(y[k], ch.other), o);
-                if (ch.turned) ch.turn(g, o, c, sn);
-                float ss = 0.f, gx = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ss = fmaf(a[e], a[e], ss);
-                    gx = fmaf(g[e] * w[e], a[e], gx);
+                for (int e = 0; e < 4; ++e) {
+                    d2 = f2_fma(f2_mul(G[e], c[e]), A[e], d2);
+                    d3 = f2_fma(f2_mul(H[e], s[e]), B[e], d3);
                 }
-                ss = sum_lanes<L>(ss);
-                gx = sum_lanes<L>(gx);
-                const float rs = rsqrtf(fmaf(ss, t.inv_d, p.eps));
-                const float mean = gx * rs * t.inv_d;
+                const float all = sum_lanes<L>(sum2(f2_add(s2, s3))), dot = sum_lanes<L>(sum2(f2_add(d2, d3)));
+                const float rs = real ? rsqrtf(fmaf(all, t.inv_d, p.eps)) : 0.f;  // no row adds to the weights' sums
+                const float back = -(dot * rs * t.inv_d) * rs * rs;  // dx = rs g w - x rs^2 mean(g w u)
+                const uint64_t rs2 = f2_pack(rs, rs), back2 = f2_pack(back, back);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float u = a[e] * rs;
-                    dw[e] = fmaf(g[e], u, dw[e]);
-                    a[e] = rs * fmaf(-u, mean, g[e] * w[e]);
+                for (int e = 0; e < 4; ++e) {
+                    G[e] = f2_mul(G[e], rs2);
+                    H[e] = f2_mul(H[e], rs2);
+                    da[e] = f2_fma(G[e], A[e], da[e]);
+                    db[e] = f2_fma(H[e], B[e], db[e]);
+                    A[e] = f2_fma(A[e], back2, f2_mul(G[e], c[e]));
+                    B[e] = f2_fma(B[e], back2, f2_mul(H[e], s[e]));
                 }
-                if (ok) *reinterpret_cast<uint4 *>(dst + (h + k) * t.out_h) = pack8(a);
+                uint4 o0, o1;
+                pack<HALF>(A, B, o0, o1);
+                if (real && my.a >= 0) {
+                    *reinterpret_cast<uint4 *>(to) = o0;
+                    if (my.b >= 0) *reinterpret_cast<uint4 *>(to + my.apart()) = o1;
+                }
             }
         }
     }
     if (!t.dweight) return;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sums[threadIdx.x / L][8 * (threadIdx.x % L) + e] = dw[e];
     __syncthreads();
-    float *to = t.partial + ((size_t)group * gridDim.x + blockIdx.x) * t.d_row;
-    for (int e = threadIdx.x; e < t.d_row; e += kNormThreads) {
-        float x = 0.f;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) x += sums[r][e];
-        to[e] = x;
+    for (int e = 0; e < 4; ++e) {
+        float4 *to = reinterpret_cast<float4 *>(&sh.sums[threadIdx.x / L][16 * my.u + 4 * e]);
+        float4 v;
+        f2_unpack(da[e], v.x, v.y);
+        f2_unpack(db[e], v.z, v.w);
+        *to = v;
+    }
+    __syncthreads();
+    // the slots of a head, or all of them, in order
+    const bool each = t.weight_h != 0;
+    for (int i = threadIdx.x; i < (each ? heads : 1) * 16 * L; i += kNormThreads) {
+        // pairs 2q, 2q + 1: first entries, then second ones
+        const int h = i / (16 * L), at = i % (16 * L), u = at / 16, q = at % 16 / 4, second = at % 4 / 2, e = 2 * q + at % 2;
+        int a, b;
+        chunks_of<HALF>(p, t.d_row, true, u, a, b);
+        const int chunk = HALF ? (second ? b : a) : e < 4 ? a : b;
+        if (chunk < 0) continue;
+        float x = 0.f;
+        if (each)
+            for (int r = 0; r < my.deep; ++r) x += sh.sums[r * my.wide + h][at];
+        else
+#pragma unroll
+            for (int r = 0; r < kNormThreads / L; ++r) x += sh.sums[r][at];
+        float *to = t.partial + ((size_t)(each ? first + h : group) * t.blocks + block) * t.d_row;
+        to[8 * chunk + (HALF ? e : 2 * (e & 3) + second)] = x;
     }
 }
 
@@ -294,12 +491,12 @@ struct Unit {
 __global__ void __launch_bounds__(kNormThreads) norm_pairs_kernel(const __grid_constant__ NormRopeParams p, bool half)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int group;
-    const NormTensor &t = tensor_of(p, group);
-    const int h0 = group * p.per, h1 = min(h0 + p.per, t.n_heads);
+    int group, block;
+    const NormTensor &t = p.t[tensor_of(p, group, block)];
+    const int h0 = group * t.per, h1 = min(h0 + t.per, t.n_heads);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kNormThreads / 32;
     const int tokens = p.B * p.S;
-    for (long long token = (long long)blockIdx.x * warps + warp; token < tokens; token += (long long)gridDim.x * warps) {
+    for (long long token = (long long)block * warps + warp; token < tokens; token += (long long)t.blocks * warps) {
         const int b = (int)(token / p.S), s = (int)(token % p.S);
         const long long row = out_row(p, t, b, s);
         if (row < 0) continue;
@@ -336,9 +533,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_pairs_kernel(const __g
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     extern __shared__ float acc[];  // [warps][d_row]
-    int group;
-    const NormTensor &t = tensor_of(p, group);
-    const int h0 = group * p.per, h1 = min(h0 + p.per, t.n_heads);
+    int group, block;
+    const NormTensor &t = p.t[tensor_of(p, group, block)];
+    const int h0 = group * t.per, h1 = min(h0 + t.per, t.n_heads);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kNormThreads / 32;
     const int tokens = p.B * p.S;
     float *dw = acc + warp * t.d_row;  // an entry always belongs to the same lane
@@ -348,7 +545,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_pairs_kernel(const __g
         dw[at.a] = 0.f;
         if (at.b >= 0) dw[at.b] = 0.f;
     }
-    for (long long token = (long long)blockIdx.x * warps + warp; token < tokens; token += (long long)gridDim.x * warps) {
+    for (long long token = (long long)block * warps + warp; token < tokens; token += (long long)t.blocks * warps) {
         const int b = (int)(token / p.S), s = (int)(token % p.S);
         const int m = p.d_rot ? p.positions[b * p.pos_stride + s] : 0;
         for (int h = h0; h < h1; ++h) {
@@ -395,7 +592,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_pairs_kernel(const __g
     }
     if (!t.dweight) return;
     __syncthreads();
-    float *to = t.partial + ((size_t)group * gridDim.x + blockIdx.x) * t.d_row;
+    float *to = t.partial + ((size_t)group * t.blocks + block) * t.d_row;
     for (int e = threadIdx.x; e < t.d_row; e += kNormThreads) {
         float x = 0.f;
         for (int r = 0; r < warps; ++r) x += acc[r * t.d_row + e];
@@ -405,7 +602,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_pairs_kernel(const __g
 
 // Weights' gradients: a block adds up 8 columns of the partial sums of a tensor (of a head of
 // it, with weights for each head); blocks in the grid's z, heads in its y.
-__global__ void __launch_bounds__(kNormThreads) norm_weights_kernel(const __grid_constant__ NormRopeParams p, int blocks)
+__global__ void __launch_bounds__(kNormThreads) norm_weights_kernel(const __grid_constant__ NormRopeParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ double sums[32][8];
@@ -413,8 +610,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_weights_kernel(const __grid
     const int e = 8 * blockIdx.x + threadIdx.x % 8, r0 = threadIdx.x / 8;
     const bool heads = t.weight_h != 0;
     if (!t.dweight || (int)blockIdx.y >= (heads ? t.n_heads : 1)) return;  // whole blocks
-    const int rows = heads ? blocks : t.n_groups * blocks;
-    const float *from = t.partial + (heads ? (size_t)blockIdx.y * blocks * t.d_row : 0) + e;
+    const int rows = heads ? t.blocks : t.n_groups * t.blocks;
+    const float *from = t.partial + (heads ? (size_t)blockIdx.y * t.blocks * t.d_row : 0) + e;
     double x = 0.;
     if (e < t.d_row) {
 #pragma unroll 4
@@ -444,28 +641,46 @@ cudaError_t launch_grid(K kernel, dim3 grid, int smem, cudaStream_t stream, cons
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-}  // namespace
-
-cudaError_t launch_norm_rope(const NormRopeParams &p, bool half, int lanes, int grid_x, int grid_y,
-                             cudaStream_t stream)
+unsigned grid_of(const NormRopeParams &p)
 {
-    const dim3 grid(grid_x, grid_y);
-    if (lanes == 8)
-        return half ? launch_grid(norm_rows_kernel<8, true>, grid, 0, stream, p)
-                    : launch_grid(norm_rows_kernel<8, false>, grid, 0, stream, p);
-    if (lanes == 16)
-        return half ? launch_grid(norm_rows_kernel<16, true>, grid, 0, stream, p)
-                    : launch_grid(norm_rows_kernel<16, false>, grid, 0, stream, p);
-    if (lanes == 32)
-        return half ? launch_grid(norm_rows_kernel<32, true>, grid, 0, stream, p)
-                    : launch_grid(norm_rows_kernel<32, false>, grid, 0, stream, p);
-    return launch_grid(norm_pairs_kernel, grid, 0, stream, p, half);
+    unsigned n = 0;
+    for (int i = 0; i < p.n_tensors; ++i) n += (unsigned)p.t[i].n_groups * p.t[i].blocks;
+    return n;
 }
 
-cudaError_t launch_norm_rope_grad(const NormRopeParams &p, bool half, int lanes, int grid_x, int grid_y,
-                                  cudaStream_t stream)
+}  // namespace
+
+namespace {
+
+template <int L>
+cudaError_t launch_rows(const NormRopeParams &p, bool half, bool grad, cudaStream_t stream)
 {
-    const dim3 grid(grid_x, grid_y);
+    const dim3 grid(grid_of(p));
+    if (grad)
+        return half ? launch_grid(norm_grad_rows_kernel<L, true>, grid, 0, stream, p)
+                    : launch_grid(norm_grad_rows_kernel<L, false>, grid, 0, stream, p);
+    return half ? launch_grid(norm_rows_kernel<L, true>, grid, 0, stream, p)
+                : launch_grid(norm_rows_kernel<L, false>, grid, 0, stream, p);
+}
+
+cudaError_t launch_lanes(const NormRopeParams &p, bool half, bool grad, int lanes, cudaStream_t stream)
+{
+    return lanes == 4    ? launch_rows<4>(p, half, grad, stream)
+           : lanes == 8  ? launch_rows<8>(p, half, grad, stream)
+           : lanes == 16 ? launch_rows<16>(p, half, grad, stream)
+                         : launch_rows<32>(p, half, grad, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const NormRopeParams &p, bool half, int lanes, cudaStream_t stream)
+{
+    return lanes ? launch_lanes(p, half, false, lanes, stream)
+                 : launch_grid(norm_pairs_kernel, dim3(grid_of(p)), 0, stream, p, half);
+}
+
+cudaError_t launch_norm_rope_grad(const NormRopeParams &p, bool half, int lanes, cudaStream_t stream)
+{
     int width = 0, heads = 1;
     bool weights = false;
     for (int i = 0; i < p.n_tensors; ++i) {
@@ -473,20 +688,11 @@ cudaError_t launch_norm_rope_grad(const NormRopeParams &p, bool half, int lanes,
         weights = weights || p.t[i].dweight;
         if (p.t[i].weight_h != 0) heads = std::max(heads, p.t[i].n_heads);
     }
-    cudaError_t err;
-    if (lanes == 8)
-        err = half ? launch_grid(norm_grad_rows_kernel<8, true>, grid, 0, stream, p)
-                   : launch_grid(norm_grad_rows_kernel<8, false>, grid, 0, stream, p);
-    else if (lanes == 16)
-        err = half ? launch_grid(norm_grad_rows_kernel<16, true>, grid, 0, stream, p)
-                   : launch_grid(norm_grad_rows_kernel<16, false>, grid, 0, stream, p);
-    else if (lanes == 32)
-        err = half ? launch_grid(norm_grad_rows_kernel<32, true>, grid, 0, stream, p)
-                   : launch_grid(norm_grad_rows_kernel<32, false>, grid, 0, stream, p);
-    else
-        err = launch_grid(norm_grad_pairs_kernel, grid, kNormThreads / 32 * width * (int)sizeof(float), stream, p, half);
+    const cudaError_t err =
+        lanes ? launch_lanes(p, half, true, lanes, stream)
+              : launch_grid(norm_grad_pairs_kernel, dim3(grid_of(p)), kNormThreads / 32 * width * (int)sizeof(float), stream, p, half);
     if (err != cudaSuccess || !weights) return err;
-    return launch_grid(norm_weights_kernel, dim3((width + 7) / 8, heads, p.n_tensors), 0, stream, p, grid_x);
+    return launch_grid(norm_weights_kernel, dim3((width + 7) / 8, heads, p.n_tensors), 0, stream, p);
 }
 
 }  // namespace apex

@@ -12,8 +12,10 @@
 namespace apex {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormFastRow = 256;      // widest row of the kernels that go 16 bytes at a time
-constexpr int kNormGradBlocks = 1024;  // blocks of a gradient at most: one partial sum of weights each
+constexpr int kNormFastRow = 512;      // widest row of the kernels that go 16 bytes at a time
+constexpr int kNormHeads = 128;        // heads with weights of their own that a block takes, times lanes of a row
+constexpr int kNormGradBlocks = 512;   // blocks of a gradient at most (but for one of each group),
+constexpr int kNormGradHeads = 8;      // and partial sums of weights of each at most
 
 // Rows at x + b * x_b + h * x_h + s * x_s, likewise dy (gradients) and out (the result, or x's gradient).
 struct NormTensor {
@@ -24,11 +26,14 @@ struct NormTensor {
     int weight_f32;
     int weight_h;         // entries between the weights of two heads (0: the same for all)
     int n_heads, d_row;
-    int n_groups;         // groups of `per` heads: the tensor's share of the grid's y
+    int per, n_groups;    // heads of a group, groups
+    int blocks;           // blocks of each group
+    int tile, tiles;      // tokens of a tile, tiles of a sequence (rows that go 16 bytes at a time)
+    int batch;            // heads of a token that a slot takes, where there are as many
     int norm;             // 0: rows copied (values)
     int append;           // rows go to row0[b] + s when row0 is given
     float inv_d;
-    float *partial;       // gradients: [n_groups * blocks][d_row] sums of weights
+    float *partial;       // gradients: sums of weights, [n_groups * blocks][d_row], or [n_heads][blocks][d_row]
     float *dweight;       // [d_row] or [n_heads][d_row]
 };
 
@@ -40,16 +45,14 @@ struct NormRopeParams {
     int out_rows;
     int B, S;
     int rot_start, d_rot;  // d_rot 0: nothing turns
-    int n_tensors, per;
+    int n_tensors;
     float eps, sign;
     uint64_t turns[kRopeMaxPairs];
 };
 static_assert(sizeof(NormRopeParams) <= 4096, "kernel parameters");
 
-// half: pair layout; lanes: lanes of a row (8, 16 or 32; 0: rows that go 2 bytes at a time)
-cudaError_t launch_norm_rope(const NormRopeParams &p, bool half, int lanes, int grid_x, int grid_y,
-                             cudaStream_t stream);
-cudaError_t launch_norm_rope_grad(const NormRopeParams &p, bool half, int lanes, int grid_x, int grid_y,
-                                  cudaStream_t stream);
+// half: pair layout; lanes: lanes of a row (4, 8, 16 or 32; 0: rows that go 2 bytes at a time)
+cudaError_t launch_norm_rope(const NormRopeParams &p, bool half, int lanes, cudaStream_t stream);
+cudaError_t launch_norm_rope_grad(const NormRopeParams &p, bool half, int lanes, cudaStream_t stream);
 
 }  // namespace apex
