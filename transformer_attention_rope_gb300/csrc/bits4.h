@@ -50,8 +50,10 @@ struct Decode4Params {
 // Rows of a KV head's queries that are worked on together: they share each key's conversion.
 inline int decode4_group(int R) { return R <= 8 ? 8 : 16; }
 
-constexpr int kDecode4CtasPerSm = 2;
-constexpr int kDecode4MaxCtas = 2 * kCacheMaxCtas;
+// CTAs of an SM: with 16 rows the sums of outputs take twice the registers.  8 caches of 9001 to
+// 32768 keys, 16 rows: 56 us with 2, 58 with 3 and the queries in shared memory, 70 with 4.
+constexpr int decode4_ctas(int group) { return group == 8 ? 4 : 2; }
+constexpr int kDecode4MaxCtas = 4 * kCacheMaxCtas;
 
 inline int decode4_shares(long long units, int S_cap, int ctas)
 {

@@ -3,7 +3,7 @@
 //
 // Work: as for bf16 caches (cache_attn.cuh): tiles of 128 keys of all (sequence, KV head,
 // row group) units are dealt out in equal shares, cut units leave partial results.  A tile is
-// 16 keys for each of a CTA's 8 warps; a warp has its own running maximum, sum and output, and
+// 32 keys for each of a CTA's 4 warps; a warp has its own running maximum, sum and output, and
 // its own ring of slices in shared memory, filled by its own asynchronous copies: warps wait
 // for one another only where a unit ends.
 //
@@ -32,10 +32,11 @@
 namespace apex {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSlice = 16;  // keys of a warp's slice
-constexpr int kStages = 4;  // slices of a warp's ring
+constexpr int kSlice = 32;  // keys of a warp's slice
+constexpr int kStep = 16;   // keys of a step: the rows of one product
+constexpr int kStages = 2;  // slices of a warp's ring
 static_assert(kWarps * kSlice == kCacheTileKeys, "a tile is a slice for each warp");
 constexpr float kHeadroom = 11.f;  // the reference of weights below the maximum, log2
 constexpr float kSlack = 15.f;     // scores may lie this far above the reference
@@ -60,12 +61,12 @@ struct Cfg {
     static constexpr int kMl = kRing > kMerge ? kRing : kMerge;  // [warps][rows] (reference, sum)
     static constexpr int kSched = kMl + kWarps * kRows * 8;
     static constexpr int kBytes = kSched + 64;
-    static_assert(kBytes <= 113 * 1024, "two CTAs an SM");
+    static_assert(decode4_ctas(8 * NT) * (kBytes + 1024) <= 227 * 1024, "CTAs of an SM");
 };
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(  // not volatile: may move among the conversions
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -75,6 +76,10 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src)
 {
@@ -87,51 +92,100 @@ __device__ __forceinline__ void copies_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Where key i of a slice lies among its value rows, and which of its 16-byte chunks comes first: the
+// Where key i of a step lies among its value rows, and which of its 16-byte chunks comes first: the
 // four keys of a load are neighbours, and at 128 entries the chunks of every other pair trade
 // places, so that the load's words lie in all 32 banks.
-__device__ __forceinline__ int value_slot(int i) { return ((i >> 1) & 3) + 4 * (i & 1) + 8 * (i >> 3); }
+__device__ __forceinline__ int value_slot(int i) { return ((i >> 1) & 3) + 4 * (i & 1) + (i & ~7); }
 template <int DV>
 __device__ __forceinline__ int value_chunk(int slot, int c)
 {
     return DV == 128 ? c ^ (slot & 2) : c;
 }
 
-// The slice of 16 keys at key0 of cache row block kv: the copies of one warp.
+// A warp's copies of its slices, one tile after another.
 template <typename C, int DQK, int DV>
-__device__ __forceinline__ void load_slice(const Decode4Params &p, uint32_t dst, size_t kv, int key0)
-{
-    const int lane = threadIdx.x & 31, last = p.c.S_cap - 1;
-    const size_t base = kv * p.c.S_cap;
-    // rows past the capacity are read from its last one, and masked
-    constexpr int kKChunks = DQK / 32, kVChunks = DV / 32;
-#pragma unroll
-    for (int i = 0; i < kSlice * kKChunks / 32; ++i) {
-        const int id = lane + 32 * i, key = id / kKChunks, c = id % kKChunks;
-        const uint32_t at = (C::kWide && c < 4) ? key * 64 + 16 * c : C::kKNarrow + key * 32 + 16 * (c - (C::kWide ? 4 : 0));
-        copy16(dst + at, p.k + (base + min(key0 + key, last)) * (DQK / 2) + 16 * c);
+struct Feed {
+    const uint8_t *k, *v, *k_scale, *v_scale;  // of the next slice, where this lane's copies start
+    int key, left, pre, gap;                   // its first key; tiles to go, those before the sinks' end, keys behind it
+    uint32_t slot, first, last;                // ring
+
+    __device__ __forceinline__ void start(const Decode4Params &p, const Frag &f, size_t kv, uint32_t ring)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        first = slot = ring;
+        last = ring + kStages * C::kStage;
+        left = f.n;
+        gap = kCacheTileKeys * (f.s.tile0 - f.s.sink);
+        pre = f.s.tile0 - f.first;  // below 1: the fragment has none of the sinks' tiles
+        key = kCacheTileKeys * f.tile(0) + kSlice * warp;
+        const size_t row = kv * p.c.S_cap + key;
+        // rows follow one another, so a slice is one run of bytes
+        k = p.k + row * (DQK / 2) + 16 * lane;
+        v = p.v + row * (DV / 2) + 16 * lane;
+        k_scale = p.k_scale + row * (DQK / 16);
+        v_scale = p.v_scale + row * (DV / 16);
     }
+    // keys past the capacity are not copied: what their slots hold is masked
+    template <bool WHOLE>
+    __device__ __forceinline__ void copies(int room)
+    {
+        const int lane = threadIdx.x & 31;
+        constexpr int kKChunks = DQK / 32, kVChunks = DV / 32;
 #pragma unroll
-    for (int i = 0; i < kSlice * kVChunks / 32; ++i) {
-        const int id = lane + 32 * i, key = id / kVChunks, c = id % kVChunks;
-        const int slot = value_slot(key);
-        copy16(dst + C::kV + slot * (DV / 2) + 16 * value_chunk<DV>(slot, c),
-               p.v + (base + min(key0 + key, last)) * (DV / 2) + 16 * c);
-    }
-    constexpr int kKWords = DQK / 64, kVWords = DV / 64;  // of a row's scales
+        for (int i = 0; i < kSlice * kKChunks / 32; ++i) {
+            const int id = lane + 32 * i, key = id / kKChunks, c = id % kKChunks;
+            const uint32_t at = !C::kWide || !C::kNarrow ? 16 * id
+                                : c < 4                  ? key * 64 + 16 * c
+                                                         : C::kKNarrow + key * 32 + 16 * (c - 4);
+            if (WHOLE || key < room) copy16(slot + at, k + 512 * i);
+        }
 #pragma unroll
-    for (int i = 0; i < (kSlice * kKWords + 31) / 32; ++i) {
-        const int id = lane + 32 * i, key = id / kKWords, c = id % kKWords;
-        if (key < kSlice)
-            copy4(dst + C::kKScale + 4 * id, p.k_scale + (base + min(key0 + key, last)) * (DQK / 16) + 4 * c);
+        for (int i = 0; i < kSlice * kVChunks / 32; ++i) {
+            const int id = lane + 32 * i, key = id / kVChunks, c = id % kVChunks, to = value_slot(key);
+            if (WHOLE || key < room) copy16(slot + C::kV + to * (DV / 2) + 16 * value_chunk<DV>(to, c), v + 512 * i);
+        }
+        // scales: a word or two of a row at a time, as rows need not start on 16 bytes
+        scales<DQK, WHOLE>(slot + C::kKScale, k_scale, room);
+        scales<DV, WHOLE>(slot + C::kVScale, v_scale, room);
     }
+    template <int D, bool WHOLE>
+    static __device__ __forceinline__ void scales(uint32_t dst, const uint8_t *src, int room)
+    {
+        const int lane = threadIdx.x & 31;
+        if (D == 128) {
+            if (WHOLE || lane < room) copy8(dst + 8 * lane, src + 8 * lane);
+        } else {
 #pragma unroll
-    for (int i = 0; i < (kSlice * kVWords + 31) / 32; ++i) {
-        const int id = lane + 32 * i, key = id / kVWords, c = id % kVWords;
-        if (key < kSlice)
-            copy4(dst + C::kVScale + 4 * id, p.v_scale + (base + min(key0 + key, last)) * (DV / 16) + 4 * c);
+            for (int i = 0; i < D / 64; ++i) {
+                const int id = lane + 32 * i;
+                if (WHOLE || id / (D / 64) < room) copy4(dst + 4 * id, src + 4 * id);
+            }
+        }
     }
-}
+    __device__ __forceinline__ void skip(int keys)
+    {
+        key += keys;
+        k += (long long)keys * (DQK / 2);
+        v += (long long)keys * (DV / 2);
+        k_scale += (long long)keys * (DQK / 16);
+        v_scale += (long long)keys * (DV / 16);
+    }
+    __device__ __forceinline__ void next(int S_cap)
+    {
+        if (left > 0) {
+            if (S_cap - key >= kSlice)
+                copies<true>(kSlice);
+            else
+                copies<false>(S_cap - key);
+            skip(kCacheTileKeys);
+            if (--pre == 0) skip(gap);
+            --left;
+        }
+        copies_commit();
+        slot += C::kStage;
+        if (slot == last) slot = first;
+    }
+};
 
 __device__ __forceinline__ uint32_t splat_lo(uint32_t w) { return __byte_perm(w, 0, 0x1010); }
 __device__ __forceinline__ uint32_t splat_hi(uint32_t w) { return __byte_perm(w, 0, 0x3232); }
@@ -139,33 +193,31 @@ __device__ __forceinline__ uint32_t splat_hi(uint32_t w) { return __byte_perm(w,
 // Four steps' rows of keys times queries: 16 entries (two words) of keys g and g + 8 of one scale
 // each.
 template <int NT>
-__device__ __forceinline__ void key_steps(float (&s)[NT][4], const uint32_t (&lo)[2], const uint32_t (&hi)[2],
-                                          uint32_t scale_lo, uint32_t scale_hi, const uint32_t (*qb)[NT][2])
+__device__ __forceinline__ void key_steps(float (&s)[NT][4], uint32_t lo0, uint32_t lo1, uint32_t hi0, uint32_t hi1,
+                                          uint32_t scale_lo, uint32_t scale_hi, const uint32_t (*q)[NT][2])
 {
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         uint32_t x[4], y[4];
-        e2m1_bytes_to_f16x2(lo[w], x);
-        e2m1_bytes_to_f16x2(hi[w], y);
+        e2m1_bytes_to_f16x2(w ? lo1 : lo0, x);
+        e2m1_bytes_to_f16x2(w ? hi1 : hi0, y);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t a[4] = {mul_f16x2(x[2 * h], scale_lo), mul_f16x2(y[2 * h], scale_hi),
                                    mul_f16x2(x[2 * h + 1], scale_lo), mul_f16x2(y[2 * h + 1], scale_hi)};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16_16816(s[n], a, qb[2 * w + h][n][0], qb[2 * w + h][n][1]);
+            for (int n = 0; n < NT; ++n) mma_f16_16816(s[n], a, q[2 * w + h][n][0], q[2 * w + h][n][1]);
         }
     }
 }
 
 template <int DQK, int DV, int NT>
-__global__ void __launch_bounds__(kThreads, 2) decode4_kernel(const __grid_constant__ Decode4Params p)
+__global__ void __launch_bounds__(kThreads, decode4_ctas(8 * NT)) decode4_kernel(const __grid_constant__ Decode4Params p)
 {
     using C = Cfg<DQK, DV, NT>;
     const CacheAttnParams &pc = p.c;
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t ring = smem_u32(smem) + warp * kStages * C::kStage;
-    const uint8_t *ring_at = smem + warp * kStages * C::kStage;
     float *merge = reinterpret_cast<float *>(smem);                // [warps][rows][DV]
     float2 *ml = reinterpret_cast<float2 *>(smem + C::kMl);        // [warps][rows]
     Sched *sched = reinterpret_cast<Sched *>(smem + C::kSched);
@@ -179,15 +231,13 @@ __global__ void __launch_bounds__(kThreads, 2) decode4_kernel(const __grid_const
     while (walk.next(pc, f)) {
         const size_t kv = (size_t)f.b * pc.H_kv + f.hk;
         if (threadIdx.x == 0 && f.head) pc.units[f.unit] = make_int2(blockIdx.x, f.last);
+        Feed<C, DQK, DV> feed;
+        feed.start(p, f, kv, smem_u32(smem) + warp * kStages * C::kStage);
 #pragma unroll
-        for (int j = 0; j < kStages - 1; ++j) {
-            if (j < f.n)
-                load_slice<C, DQK, DV>(p, ring + j * C::kStage, kv, kCacheTileKeys * f.tile(j) + kSlice * warp);
-            copies_commit();
-        }
+        for (int j = 0; j < kStages - 1; ++j) feed.next(pc.S_cap);
 
         // ---- queries: column n of tile nt is row 8 nt + n of the group
-        uint32_t qb[C::kSteps][NT][2];
+        uint32_t q[C::kSteps][NT][2];
         float factor[NT][2];  // of the scores of columns 2t, 2t + 1, in log2 units
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -213,30 +263,23 @@ __global__ void __launch_bounds__(kThreads, 2) decode4_kernel(const __grid_const
             const float down = __uint_as_float((258u - ex) << 23), up = __uint_as_float((ex - 4u) << 23);
 #pragma unroll
             for (int i = 0; i < DQK / 8; ++i)
-                qb[i >> 1][nt][i & 1] = pack_f16x2(bf16lo_to_f32(w[i]) * down, bf16hi_to_f32(w[i]) * down);
+                q[i >> 1][nt][i & 1] = pack_f16x2(bf16lo_to_f32(w[i]) * down, bf16hi_to_f32(w[i]) * down);
 #pragma unroll
             for (int e = 0; e < 2; ++e) factor[nt][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + e));
         }
         const float kf = (p.k_factor ? p.k_factor[f.hk] : 1.f) * pc.scale_log2;
         const float vf = p.v_factor ? p.v_factor[f.hk] : 1.f;
-        int lo[NT][2], hi[NT][2];  // keys that a column's row sees, beside the sinks
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                factor[nt][e] *= kf;
-                const int rc = 8 * nt + 2 * t + e, r = f.group * pc.group + rc;
-                const int m = f.s.len + r % pc.T;
-                const bool ok = rc < pc.rows_cap && r < pc.R;
-                hi[nt][e] = ok ? min(m, pc.S_cap - 1) : -1;
-                lo[nt][e] = pc.window > 0 ? max(0, m - pc.window + 1) : 0;
-            }
-        // keys that every row sees: [all_lo, len]; that some row sees: [any_lo, any_hi] and the sinks
+            for (int e = 0; e < 2; ++e) factor[nt][e] *= kf;
+        // keys that every row sees: [all_lo, all_hi]; that some row sees: [any_lo, any_hi] and the sinks
         const int m1 = f.s.len + pc.T - 1;
-        const int all_lo = pc.window > 0 ? m1 - pc.window + 1 : 0;
+        const int all_lo = pc.window > 0 ? m1 - pc.window + 1 : 0, all_hi = min(f.s.len, pc.S_cap - 1);
         const int any_lo = pc.window > 0 ? f.s.len - pc.window + 1 : 0, any_hi = min(m1, pc.S_cap - 1);
-        const int all_hi = min(f.s.len, pc.S_cap - 1);
 
+        // weights are 2^(score - ref); a row that has seen nothing starts far below every score
+        constexpr float kUnseen = -3e38f;
         float o[NT][C::kBlocks][4], ref[NT][2], sum[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -244,71 +287,90 @@ __global__ void __launch_bounds__(kThreads, 2) decode4_kernel(const __grid_const
             for (int i = 0; i < C::kBlocks; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-            ref[nt][0] = ref[nt][1] = -INFINITY;
+            ref[nt][0] = ref[nt][1] = kUnseen;
             sum[nt][0] = sum[nt][1] = 0.f;
         }
 
+        constexpr int U = kSlice / kStep;  // steps whose scores are there together
+        const uint8_t *at = smem + warp * kStages * C::kStage;
+        int slice0 = kCacheTileKeys * f.tile(0) + kSlice * warp, pre = f.s.tile0 - f.first;
         for (int j = 0; j < f.n; ++j) {
             __syncwarp();  // all lanes are done with the slot that is filled next
-            if (j + kStages - 1 < f.n)
-                load_slice<C, DQK, DV>(p, ring + (j + kStages - 1) % kStages * C::kStage, kv,
-                                       kCacheTileKeys * f.tile(j + kStages - 1) + kSlice * warp);
-            copies_commit();
+            feed.next(pc.S_cap);
             copies_wait<kStages - 1>();
             __syncwarp();
-            const uint8_t *at = ring_at + j % kStages * C::kStage;
-            const int key0 = kCacheTileKeys * f.tile(j) + kSlice * warp;
 
-            // ---- scores of keys g, g + 8 (rows) and queries 2t, 2t + 1 (columns)
-            float s[NT][4];
+            // ---- scores of keys g, g + 8 (rows) and queries 2t, 2t + 1 (columns) of each step
+            float s[U][NT][4];
+            int key0[U];
+            bool all[U];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < U; ++u) {
+                const int r0 = kStep * u;  // first row of the slot
+                key0[u] = slice0 + r0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-            if (C::kWide) {
-                const uint4 a = *reinterpret_cast<const uint4 *>(at + g * 64 + 16 * t);
-                const uint4 b = *reinterpret_cast<const uint4 *>(at + (g + 8) * 64 + 16 * t);
-                const uint32_t sa = e4m3x2_to_f16x2(
-                    *reinterpret_cast<const uint16_t *>(at + C::kKScale + g * (DQK / 16) + 2 * t));
-                const uint32_t sc = e4m3x2_to_f16x2(
-                    *reinterpret_cast<const uint16_t *>(at + C::kKScale + (g + 8) * (DQK / 16) + 2 * t));
-                const uint32_t a0[2] = {a.x, a.y}, a1[2] = {a.z, a.w}, b0[2] = {b.x, b.y}, b1[2] = {b.z, b.w};
-                key_steps<NT>(s, a0, b0, splat_lo(sa), splat_lo(sc), &qb[0]);
-                key_steps<NT>(s, a1, b1, splat_hi(sa), splat_hi(sc), &qb[4]);
-            }
-            if (C::kNarrow) {
-                const uint2 a = *reinterpret_cast<const uint2 *>(at + C::kKNarrow + g * 32 + 8 * t);
-                const uint2 b = *reinterpret_cast<const uint2 *>(at + C::kKNarrow + (g + 8) * 32 + 8 * t);
-                const int block = (C::kWide ? 8 : 0) + t;
-                const uint32_t sa = e4m3x2_to_f16x2(at[C::kKScale + g * (DQK / 16) + block]);
-                const uint32_t sc = e4m3x2_to_f16x2(at[C::kKScale + (g + 8) * (DQK / 16) + block]);
-                const uint32_t a0[2] = {a.x, a.y}, b0[2] = {b.x, b.y};
-                key_steps<NT>(s, a0, b0, splat_lo(sa), splat_lo(sc), &qb[C::kStepsWide]);
-            }
-            const bool all = key0 >= all_lo && key0 + kSlice - 1 <= all_hi;
-            bool above = false;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[nt][e] *= factor[nt][e & 1];
-                    if (!all) {
-                        const int key = key0 + g + 8 * (e >> 1);
-                        if (key > hi[nt][e & 1] || (key < lo[nt][e & 1] && key >= pc.n_sink)) s[nt][e] = -INFINITY;
-                    }
-                    above = above || s[nt][e] > ref[nt][e & 1] + kSlack;
+                    for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
+                if (C::kWide) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(at + (r0 + g) * 64 + 16 * t);
+                    const uint4 b = *reinterpret_cast<const uint4 *>(at + (r0 + g + 8) * 64 + 16 * t);
+                    const uint32_t sa = e4m3x2_to_f16x2(
+                        *reinterpret_cast<const uint16_t *>(at + C::kKScale + (r0 + g) * (DQK / 16) + 2 * t));
+                    const uint32_t sc = e4m3x2_to_f16x2(
+                        *reinterpret_cast<const uint16_t *>(at + C::kKScale + (r0 + g + 8) * (DQK / 16) + 2 * t));
+                    key_steps<NT>(s[u], a.x, a.y, b.x, b.y, splat_lo(sa), splat_lo(sc), &q[0]);
+                    key_steps<NT>(s[u], a.z, a.w, b.z, b.w, splat_hi(sa), splat_hi(sc), &q[C::kWide ? 4 : 0]);
                 }
-            if (__any_sync(0xffffffffu, above)) {
+                if (C::kNarrow) {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(at + C::kKNarrow + (r0 + g) * 32 + 8 * t);
+                    const uint2 b = *reinterpret_cast<const uint2 *>(at + C::kKNarrow + (r0 + g + 8) * 32 + 8 * t);
+                    const int block = (C::kWide ? 8 : 0) + t;
+                    const uint32_t sa = e4m3x2_to_f16x2(at[C::kKScale + (r0 + g) * (DQK / 16) + block]);
+                    const uint32_t sc = e4m3x2_to_f16x2(at[C::kKScale + (r0 + g + 8) * (DQK / 16) + block]);
+                    key_steps<NT>(s[u], a.x, a.y, b.x, b.y, splat_lo(sa), splat_lo(sc), &q[C::kStepsWide]);
+                }
+                all[u] = key0[u] >= all_lo && key0[u] + kStep - 1 <= all_hi;
+                if (!all[u]) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int rc = 8 * nt + 2 * t + e, r = f.group * pc.group + rc;
+                            const int m = f.s.len + r % pc.T, hi = min(m, pc.S_cap - 1);
+                            const int lo = pc.window > 0 ? m - pc.window + 1 : 0;
+                            const bool none = rc >= pc.rows_cap || r >= pc.R;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int key = key0[u] + g + 8 * h;
+                                if (none || key > hi || (key < lo && key >= pc.n_sink)) s[u][nt][e + 2 * h] = -INFINITY;
+                            }
+                        }
+                }
+            }
+            float x[U][NT][4];  // scores above the reference
+            float most = kUnseen;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[u][nt][e] = fmaf(s[u][nt][e], factor[nt][e & 1], -ref[nt][e & 1]);
+                    most = fmax3(most, fmaxf(x[u][nt][0], x[u][nt][1]), fmaxf(x[u][nt][2], x[u][nt][3]));
+                }
+            if (__any_sync(0xffffffffu, most > kSlack)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(s[nt][e], s[nt][e + 2]);
+                        float top = kUnseen;
 #pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                        if (top > ref[nt][e] + kSlack) {
-                            const float now = top - kHeadroom;
-                            const float keep = fast_exp2(ref[nt][e] - now);
+                        for (int u = 0; u < U; ++u)
+                            top = fmax3(top, s[u][nt][e] * factor[nt][e], s[u][nt][e + 2] * factor[nt][e]);
+#pragma unroll
+                        for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+                        if (top - ref[nt][e] > kSlack) {
+                            const float now = top - kHeadroom, keep = fast_exp2(ref[nt][e] - now);
                             ref[nt][e] = now;
                             sum[nt][e] *= keep;
 #pragma unroll
@@ -316,70 +378,81 @@ __global__ void __launch_bounds__(kThreads, 2) decode4_kernel(const __grid_const
                                 o[nt][i][e] *= keep;
                                 o[nt][i][e + 2] *= keep;
                             }
+#pragma unroll
+                            for (int u = 0; u < U; ++u) {
+                                x[u][nt][e] = fmaf(s[u][nt][e], factor[nt][e], -now);
+                                x[u][nt][e + 2] = fmaf(s[u][nt][e + 2], factor[nt][e], -now);
+                            }
                         }
                     }
             }
-            uint32_t pb[NT][2];
+            uint32_t pb[U][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float r0 = ref[nt][0] == -INFINITY ? 0.f : ref[nt][0], r1 = ref[nt][1] == -INFINITY ? 0.f : ref[nt][1];
-                const float p0 = fast_exp2(s[nt][0] - r0), p1 = fast_exp2(s[nt][1] - r1);
-                const float p2 = fast_exp2(s[nt][2] - r0), p3 = fast_exp2(s[nt][3] - r1);
-                sum[nt][0] += p0 + p2;
-                sum[nt][1] += p1 + p3;
-                pb[nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
-                pb[nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
-            }
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float p0 = fast_exp2(x[u][nt][0]), p1 = fast_exp2(x[u][nt][1]);
+                    const float p2 = fast_exp2(x[u][nt][2]), p3 = fast_exp2(x[u][nt][3]);
+                    sum[nt][0] += p0 + p2;
+                    sum[nt][1] += p1 + p3;
+                    pb[u][nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
+                    pb[u][nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
+                }
 
             // ---- outputs: keys 2t, 2t + 1 and 2t + 8, 2t + 9 of the lane's entries
-            uint32_t vs[2];
-            {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r0 = kStep * u;
+                uint32_t vs[2];
                 const int block = DV == 128 ? g : g >> 1;
-                const uint8_t *sv = at + C::kVScale + 2 * t * (DV / 16) + block;
+                const uint8_t *sv = at + C::kVScale + (r0 + 2 * t) * (DV / 16) + block;
                 vs[0] = e4m3x2_to_f16x2(sv[0] | (uint32_t)sv[DV / 16] << 8);
                 vs[1] = e4m3x2_to_f16x2(sv[8 * (DV / 16)] | (uint32_t)sv[9 * (DV / 16)] << 8);
-                if (!all) {  // values of keys that no row sees may be anything: codes are finite, scales not
+                if (!all[u]) {  // values of keys that no row sees may be anything: codes are finite, scales not
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int key = key0 + 2 * t + 8 * h + e;
+                            const int key = key0[u] + 2 * t + 8 * h + e;
                             if (key > any_hi || (key < any_lo && key >= pc.n_sink)) vs[h] &= e ? 0x0000ffffu : 0xffff0000u;
                         }
                 }
-            }
-            constexpr int kWords = DV / 64;  // of a lane's entries of one key
-            uint32_t x[4][kWords];           // keys 2t, 2t + 1, 2t + 8, 2t + 9
+                constexpr int kWords = DV / 64;  // of a lane's entries of one key
+                uint32_t v[4][kWords];           // keys 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const int slot = t + 4 * h;  // value_slot of the key
-                const uint8_t *row = at + C::kV + slot * (DV / 2);
-                if (DV == 128) {
-                    const uint2 two =
-                        *reinterpret_cast<const uint2 *>(row + 16 * value_chunk<DV>(slot, g >> 1) + 8 * (g & 1));
-                    x[h][0] = two.x;
-                    x[h][kWords - 1] = two.y;
-                } else {
-                    x[h][0] = *reinterpret_cast<const uint32_t *>(row + 4 * g);
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                uint32_t even[2][4], odd[2][4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t a = x[2 * h][w], b = x[2 * h + 1][w];
-                    e2m1_bytes_to_f16x2((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even[h]);
-                    e2m1_bytes_to_f16x2(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd[h]);
+                for (int h = 0; h < 4; ++h) {
+                    const int slot = r0 + t + 4 * h;  // value_slot of the key
+                    const uint8_t *row = at + C::kV + slot * (DV / 2);
+                    if (DV == 128) {
+                        const uint2 two =
+                            *reinterpret_cast<const uint2 *>(row + 16 * value_chunk<DV>(t, g >> 1) + 8 * (g & 1));
+                        v[h][0] = two.x;
+                        v[h][kWords - 1] = two.y;
+                    } else {
+                        v[h][0] = *reinterpret_cast<const uint32_t *>(row + 4 * g);
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t a[4] = {mul_f16x2(even[0][i], vs[0]), mul_f16x2(odd[0][i], vs[0]),
-                                           mul_f16x2(even[1][i], vs[1]), mul_f16x2(odd[1][i], vs[1])};
+                for (int w = 0; w < kWords; ++w) {
+                    uint32_t even[2][4], odd[2][4];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * w + i], a, pb[nt][0], pb[nt][1]);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t a = v[2 * h][w], b = v[2 * h + 1][w];
+                        e2m1_bytes_to_f16x2((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even[h]);
+                        e2m1_bytes_to_f16x2(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd[h]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a[4] = {mul_f16x2(even[0][i], vs[0]), mul_f16x2(odd[0][i], vs[0]),
+                                               mul_f16x2(even[1][i], vs[1]), mul_f16x2(odd[1][i], vs[1])};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * w + i], a, pb[u][nt][0], pb[u][nt][1]);
+                    }
                 }
             }
+            at = smem + (warp * kStages + (j + 1) % kStages) * C::kStage;
+            slice0 += kCacheTileKeys;
+            if (--pre == 0) slice0 += kCacheTileKeys * (f.s.tile0 - f.s.sink);
         }
 
         // ---- the warps' results become one
@@ -390,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode4_kernel(const __grid_const
                 float x = sum[nt][e];
 #pragma unroll
                 for (int k = 4; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-                if (g == 0) ml[warp * C::kRows + 8 * nt + 2 * t + e] = make_float2(row_max(ref[nt][e], x), x);
+                if (g == 0)
+                    ml[warp * C::kRows + 8 * nt + 2 * t + e] = make_float2(ref[nt][e] == kUnseen ? row_max(-INFINITY, x) : ref[nt][e], x);
             }
         copies_wait<0>();
         __syncthreads();  // and every ring is done with
@@ -466,7 +540,7 @@ cudaError_t launch_decode4(Decode4Params &p, int sm_count, cudaStream_t stream)
 {
     CacheAttnParams &c = p.c;
     const long long n_units = (long long)c.B * c.H_kv * c.n_groups;
-    const int room = std::min(kDecode4CtasPerSm * sm_count, kDecode4MaxCtas);
+    const int room = std::min(decode4_ctas(c.group) * sm_count, kDecode4MaxCtas);
     int shares = decode4_shares(n_units, c.S_cap, room);
     // keys that a unit can reach: a window and the sinks bound them, the new rows and a tile's slack beside
     const int reach = c.window > 0 ? (int)std::min<long long>(c.S_cap, (long long)c.window + c.n_sink + c.drafts + 2 * kCacheTileKeys)
