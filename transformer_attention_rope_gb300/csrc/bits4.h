@@ -27,7 +27,8 @@ struct Bits4Tensor {
     uint8_t *bytes, *scales;
     const float *factor;
     int d;
-    int wide;  // 16 bytes of x at a time
+    int wide;             // bytes that the addresses of 16 entries of x are multiples of: 32, 16 or less
+    int per, inv_blocks;  // rows of a block at a time; 2^16 / (d / 16), rounded up (set by the launch)
 };
 
 struct Bits4Params {
@@ -36,8 +37,8 @@ struct Bits4Params {
     int B, H, S, S_cap;
 };
 
-cudaError_t launch_append4(const Bits4Params &p, cudaStream_t stream);
-cudaError_t launch_unpack4(const Bits4Params &p, cudaStream_t stream);
+cudaError_t launch_append4(Bits4Params &p, cudaStream_t stream);
+cudaError_t launch_unpack4(Bits4Params &p, cudaStream_t stream);
 
 // ---------------------------------------------------------------- attention
 struct Decode4Params {

@@ -57,9 +57,13 @@ apex_status move_rows(const apex_bits4_tensor *const (&t)[2], bool append, int B
     memset(&p, 0, sizeof p);
     for (int i = 0; i < 2; ++i) {
         const apex_bits4_tensor &a = *t[i];
+        const long long strides = a.b | a.h | a.s;
         p.t[i] = Bits4Tensor{static_cast<uint16_t *>(a.rows), a.b, a.h, a.s, static_cast<uint8_t *>(a.bytes),
                              static_cast<uint8_t *>(a.scales), a.factor, a.d,
-                             aligned16(a.rows) && (a.b | a.h | a.s) % 8 == 0};
+                             aligned(a.rows, 32) && strides % 16 == 0  ? 32
+                             : aligned16(a.rows) && strides % 8 == 0 ? 16
+                                                                     : 2,
+                             0, 0};
     }
     p.row0 = row0;
     p.B = B;

@@ -287,6 +287,14 @@ __device__ __forceinline__ void mask_row128_sink(uint32_t (&v)[128], int lo, int
         if ((e < lo && e >= sink) || e > hi) v[e] = ninf;
 }
 
+// Sets to -inf the scores of a 128-key row from key n on.
+__device__ __forceinline__ void mask_row128_from(uint32_t (&v)[128], int n)
+{
+#pragma unroll
+    for (int e = 0; e < 128; ++e)
+        if (e >= n) v[e] = 0xff800000u;
+}
+
 // Byte offset of 16-byte chunk `chunk` (0..7) of row `row` inside a tile that a
 // TMA load wrote with CU_TENSOR_MAP_SWIZZLE_128B (rows of 128 bytes, tile base
 // 1024-byte aligned): the chunk index is XORed with the row index mod 8.

@@ -475,7 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int ch = 0; ch < 4; ++ch)
                     tmem_ld32(s_addr + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * ch]));
                 tmem_wait_ld();
-                if (SINK && !all_full && kstart < p.n_sink)
+                if (SINK && j < it.sink)  // before every row's window: the sinks alone, the same for all rows
+                    mask_row128_from(v, p.n_sink - kstart);
+                else if (SINK && !all_full && kstart < p.n_sink)
                     mask_row128_sink(v, lo_c, hi_c, p.n_sink - kstart);
                 else if (!all_full)
                     mask_row128(v, lo_c, hi_c);
