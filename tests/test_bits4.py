@@ -383,6 +383,19 @@ def test_queries_of_any_size(s):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scale", [None, 1e-30])
+def test_queries_of_zeros(scale):
+    """Scores of 0: the mean of the values that are seen, with masked keys beside them."""
+    dev = _gpu()
+    lens = [200, 3, 0]
+    q, cache, ln, f, vals = _attn_inputs(dev, 19, 8, 2, 3, 128, 128, 300, lens)
+    q[:, 1:5] = 0
+    q[:, 5] *= 2.0 ** -120
+    got = apex.decode4(q, *cache, ln, window=50, n_sink=2, scale=scale)
+    _close(got, *_attn_ref(q, *vals, lens, 50, 2, scale=scale))
+
+
+@pytest.mark.gpu
 def test_values_that_are_not_finite_stay_alone():
     dev = _gpu()
     q, cache, ln, f, vals = _attn_inputs(dev, 11, 8, 2, 3, 128, 128, 300, [290, 100])

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, decode4_ctas(8 * NT)) decode4_kernel
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) factor[nt][e] *= kf;
+            for (int e = 0; e < 2; ++e) factor[nt][e] = fmaxf(factor[nt][e] * kf, 1e-37f);  // not 0: masked scores stay -inf
         // keys that every row sees: [all_lo, all_hi]; that some row sees: [any_lo, any_hi] and the sinks
         const int m1 = f.s.len + pc.T - 1;
         const int all_lo = pc.window > 0 ? m1 - pc.window + 1 : 0, all_hi = min(f.s.len, pc.S_cap - 1);
