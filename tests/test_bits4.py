@@ -303,6 +303,11 @@ ATTN = [  # Hq, Hkv, T, dk, dv, cap, lens, window, sinks
     (8, 1, 64, 128, 128, 400, [336, 0], 50, 2),   # 512 rows
     (4, 4, 16, 128, 128, 2000, [1900, 1984], 0, 0),
     (4, 2, 1, 128, 128, 40000, [39999], 0, 0),
+    (16, 1, 2, 192, 128, 900, [898, 5], 200, 140),   # 32 rows: the kernel for many
+    (32, 2, 6, 192, 128, 1300, [1294, 600, 0], 0, 0),
+    (16, 1, 16, 64, 64, 1000, [984, 130], 100, 4),   # 256 rows: two groups
+    (8, 1, 9, 128, 128, 3000, [2991, 2000, 64], 0, 0),
+    (16, 2, 40, 128, 128, 700, [660, 1], 1, 1),
 ]
 
 
@@ -350,7 +355,7 @@ def test_lengths_out_of_range_and_past_the_capacity():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("T", [1, 5, 20])
 def test_rising_and_peaked_scores(T):
     """Every slice outgrows the ones before it; one key takes nearly all; scales of the scores."""
     dev = _gpu()

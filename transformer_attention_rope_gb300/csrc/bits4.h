@@ -48,14 +48,16 @@ struct Decode4Params {
     const float *k_factor, *v_factor;
 };
 
-// Rows of a KV head's queries that are worked on together: they share each key's conversion.
-inline int decode4_group(int R) { return R <= 8 ? 8 : 16; }
+// Rows of a KV head's queries that are worked on together: they share each key's conversion.  Up
+// to 16 on mma.sync (decode4.cu), more on tcgen05 (decode4_wide.cu).
+inline int decode4_group(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 128; }
 
 // CTAs of an SM: with 16 rows the sums of outputs take twice the registers.  8 caches of 9001 to
 // 32768 keys, 16 rows: 56 us with 2, 58 with 3 and the queries in shared memory, 70 with 4.
-constexpr int decode4_ctas(int group) { return group == 8 ? 4 : 2; }
+constexpr int decode4_ctas(int group) { return group == 8 ? 4 : group == 16 ? 2 : 1; }
 constexpr int kDecode4MaxCtas = 4 * kCacheMaxCtas;
 
+// shares of a call at most: a tile each
 inline int decode4_shares(long long units, int S_cap, int ctas)
 {
     const long long tiles = units * ((S_cap + kCacheTileKeys - 1) / kCacheTileKeys);
@@ -75,14 +77,16 @@ inline Decode4Workspace decode4_workspace(int B, int H_q, int H_kv, int T, int S
     w.n_groups = (R + group - 1) / group;
     auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
     const long long units = (long long)B * H_kv * w.n_groups;
-    const size_t slots = (size_t)2 * decode4_shares(units, S_cap, kDecode4MaxCtas) * w.rows_cap;
+    const size_t slots = (size_t)2 * decode4_shares(units, S_cap, decode4_ctas(group) * kCacheMaxCtas) * w.rows_cap;
     w.ml = up(slots * d_v * sizeof(float));
     w.units = w.ml + up(slots * sizeof(float2));
     w.bytes = w.units + up((size_t)units * sizeof(int2));
     return w;
 }
 
-// chooses how the work is cut (p.c.whole), launches the attention and what joins it
+// the attention of groups of 128 rows alone (the caller joins)
+cudaError_t launch_decode4_wide(const Decode4Params &p, int grid, cudaStream_t stream);
+// chooses the kernel and how the work is cut (p.c.whole), launches it and what joins it
 cudaError_t launch_decode4(Decode4Params &p, int sm_count, cudaStream_t stream);
 
 }  // namespace apex

@@ -139,10 +139,8 @@ apex_status apex_attn_decode4(const void *q, const void *k4, const void *k_scale
         return APEX_ERR_INVALID_ARG;
     const Decode4Workspace w = decode4_workspace(B, H_q, H_kv, T, S_cap, d_v);
     if (workspace_bytes < w.bytes) return APEX_ERR_INVALID_ARG;
-    int sm_count = 0, dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return APEX_ERR_CUDA;
+    DeviceScope dev;
+    if (dev.status != APEX_OK) return dev.status;
     Decode4Params p;
     memset(&p, 0, sizeof p);
     CacheAttnParams &c = p.c;
@@ -175,7 +173,8 @@ apex_status apex_attn_decode4(const void *q, const void *k4, const void *k_scale
     p.v_scale = static_cast<const uint8_t *>(v_scale);
     p.k_factor = k_factor;
     p.v_factor = v_factor;
-    if (launch_decode4(p, sm_count, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return APEX_ERR_CUDA;
+    c.wait = dev.wait;
+    if (launch_decode4(p, dev.sm_count, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return APEX_ERR_CUDA;
     return APEX_OK;
 }
 

@@ -540,14 +540,16 @@ cudaError_t launch_decode4(Decode4Params &p, int sm_count, cudaStream_t stream)
 {
     CacheAttnParams &c = p.c;
     const long long n_units = (long long)c.B * c.H_kv * c.n_groups;
-    const int room = std::min(decode4_ctas(c.group) * sm_count, kDecode4MaxCtas);
+    const int room = decode4_ctas(c.group) * std::min(sm_count, kCacheMaxCtas);
     int shares = decode4_shares(n_units, c.S_cap, room);
     // keys that a unit can reach: a window and the sinks bound them, the new rows and a tile's slack beside
     const int reach = c.window > 0 ? (int)std::min<long long>(c.S_cap, (long long)c.window + c.n_sink + c.drafts + 2 * kCacheTileKeys)
                                    : c.S_cap;
     c.whole = cache_attn_whole(n_units, reach, room);
     if (c.whole) shares = (int)std::min<long long>(shares, n_units);
-    const cudaError_t err = c.group == 8 ? launch_rows<1>(p, shares, stream) : launch_rows<2>(p, shares, stream);
+    const cudaError_t err = c.group == 8    ? launch_rows<1>(p, shares, stream)
+                            : c.group == 16 ? launch_rows<2>(p, shares, stream)
+                                            : launch_decode4_wide(p, shares, stream);
     if (err != cudaSuccess || c.whole) return err;
     return launch_cache_join(c, shares, stream);
 }
