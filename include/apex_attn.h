@@ -542,6 +542,17 @@ apex_status apex_attn_tree_decode(const void *q, const void *k_cache, const void
                                   const uint64_t *tree_mask, long long mask_stride, const int *positions, int window,
                                   float scale, void *workspace, size_t workspace_bytes, apex_stream_t stream);
 
+/*
+ * The same under a window whose first n_sink positions stay visible (sinks): with a window > 0 a
+ * key is also seen if its position is below n_sink (>= 0).  Workspace as for
+ * apex_attn_tree_decode.
+ */
+apex_status apex_attn_sink_tree_decode(const void *q, const void *k_cache, const void *v_cache, void *out, int B,
+                                       int H_q, int H_kv, int T, int S_cap, int d_qk, int d_v, const int *lens,
+                                       const uint64_t *tree_mask, long long mask_stride, const int *positions,
+                                       int window, int n_sink, float scale, void *workspace, size_t workspace_bytes,
+                                       apex_stream_t stream);
+
 /* Bytes of workspace apex_attn_tree_decode needs; 0 when the sizes are invalid.  Host-only. */
 size_t apex_attn_tree_workspace_bytes(int B, int H_q, int H_kv, int T, int S_cap, int d_qk, int d_v);
 

@@ -1,4 +1,5 @@
-"""Prefill and decode under a window whose first tokens stay visible, against plain 64-bit attention.
+"""Prefill, decode and drafted trees under a window whose first tokens stay visible, against plain 64-bit
+attention.
 
 Tolerances (u = 2^-8: half a step of bf16, relative to the value): the rotated queries and keys are
 rounded to bf16, each by u relative, so a score moves by at most e = (2 u + u^2) scale sum |q k| over
@@ -6,7 +7,8 @@ the worst signs; the sum of d such roundings of either sign stays below 6 standa
 each (a row's largest over n keys: 6 covers n = 2^20), which is what is counted:
   e = 6 (2 u / sqrt 3) scale sqrt(sum (q k)^2) + d 2^-24 scale sum |q k|;
 numerators and denominators of the weights move by e: 2 e A, A = sum p |v|, in the sum.  Weights are rounded
-to bf16: u A; the result: u |out|; exp2 and sums in fp32: 2^-13 A.
+to bf16: u A; the result: u |out|; exp2 and sums in fp32: 2^-13 A.  Trees take rotated rows: there
+e = d 2^-24 scale sum |q k|.
 """
 import math
 
@@ -190,6 +192,81 @@ def test_decode_matches_the_formula(B, Hq, Hkv, Sk, at, d, d_r, window, sinks, t
     assert (err <= ref[1]).all(), float((err - ref[1]).max())
 
 
+TREES = [  # Hq, Hkv, T, dk, dv, cap, lens, window, sinks
+    (4, 2, 1, 64, 64, 300, [299, 5, 0], 16, 4),
+    (32, 8, 1, 128, 128, 1500, [1400, 300, 60], 128, 4),
+    (32, 8, 4, 128, 128, 1500, [1400, 130, 3], 1, 1),
+    (8, 2, 6, 192, 128, 900, [890, 255], 70, 300),
+    (16, 1, 12, 128, 128, 1300, [1288, 700, 2], 100, 130),   # CTA pairs, one M tile
+    (16, 1, 40, 128, 128, 2000, [1960, 20], 300, 5),         # two
+    (16, 1, 20, 192, 128, 900, [880, 500], 129, 64),
+    (16, 1, 12, 64, 64, 1000, [988, 400], 33, 140),          # two M tiles on one CTA
+    (8, 1, 64, 64, 64, 700, [636, 10], 20, 3),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,T,dk,dv,cap,lens,window,sinks", TREES)
+def test_drafts_match_the_formula(Hq, Hkv, T, dk, dv, cap, lens, window, sinks, tree):
+    dev = _gpu()
+    g = torch.Generator(device=dev)
+    g.manual_seed(cap + T)
+    B, G = len(lens), Hq // Hkv
+    q, k, v = (torch.randn(B, h, n, d, generator=g, device=dev).to(torch.bfloat16)
+               for h, n, d in ((Hq, T, dk), (Hkv, cap, dk), (Hkv, cap, dv)))
+    ln = torch.tensor(lens, dtype=torch.int32, device=dev)
+    mask = pos = None
+    words = [(1 << (t + 1)) - 1 for t in range(T)]
+    depth = list(range(T))
+    if tree:  # every draft but the first hangs on one a little before it
+        for t in range(1, T):
+            p = max(0, t - 1 - t % 3)
+            words[t], depth[t] = words[p] | (1 << t), depth[p] + 1
+        mask = torch.tensor([w - (1 << 64) if w >> 63 else w for w in words], dtype=torch.int64, device=dev)
+        pos = ln[:, None] + torch.tensor(depth, dtype=torch.int32, device=dev)
+    # rows that nobody sees may hold anything
+    j = torch.arange(cap, device=dev)
+    seen = torch.zeros(B, T, cap, dtype=torch.bool, device=dev)
+    for b, n in enumerate(lens):
+        at = j.clone()
+        at[n:n + T] = n + torch.tensor(depth, device=dev)[:cap - n]
+        for t in range(T):
+            m = n + depth[t]
+            draft = torch.zeros(cap, dtype=torch.bool, device=dev)
+            for u in range(min(T, cap - n)):
+                draft[n + u] = bool((words[t] >> u) & 1)
+            seen[b, t] = ((j < n) | draft) & ((m - at < window) | (at < sinks))
+        hidden = ~seen[b].any(0)
+        k[b, :, hidden] = float("nan")
+        v[b, :, hidden] = float("inf")
+    got = apex.tree_decode(q, k, v, ln, tree_mask=mask, positions=pos, window=window, n_sink=sinks)
+    scale = 1 / math.sqrt(dk)
+    for b in range(B):
+        for h in range(Hq):
+            x, kk, vv = q[b, h].double(), k[b, h // G].double().nan_to_num(0.0), v[b, h // G].double().nan_to_num(0.0, 0.0, 0.0)
+            s = (x @ kk.T * scale).masked_fill(~seen[b], -math.inf)
+            p = torch.softmax(s, -1).nan_to_num(0.0)
+            o, A = p @ vv, p @ vv.abs()
+            e = (dk * 2.0 ** -24 * scale * (x.abs() @ kk.abs().T)).masked_fill(~seen[b], 0).amax(-1, keepdim=True)
+            err = (got[b, h].double() - o).abs()
+            assert torch.isfinite(err).all()
+            assert (err <= U * o.abs() + A * (U + 2 * e + 2.0 ** -13)).all()
+    assert apex.apex_attn_device_status() == 0
+
+
+@pytest.mark.gpu
+def test_drafts_without_a_window_are_the_plain_call():
+    dev = _gpu()
+    q, k, v = _inputs(dev, 11, 2, 8, 2, 5, 600, 128)
+    ln = torch.tensor([590, 77], dtype=torch.int32, device=dev)
+    assert torch.equal(apex.tree_decode(q, k, v, ln, n_sink=9), apex.tree_decode(q, k, v, ln))
+    # a window that sinks fill up
+    assert torch.equal(apex.tree_decode(q, k, v, ln, window=1, n_sink=600), apex.tree_decode(q, k, v, ln))
+    with pytest.raises(ValueError):
+        apex.tree_decode(q, k, v, ln, window=8, n_sink=-1)
+
+
 @pytest.mark.gpu
 def test_prompt_then_tokens():
     """Chunks of a prompt and then single tokens give the rows of one call over all."""
@@ -271,6 +348,12 @@ def test_decode_refuses(lib, o, code):
     opt = apex.Options(**dict(dict(window=16), **a["opt"]))
     assert apex.apex_attn_sink_decode(a["q"], a["k"], a["v"], a["out"], a["B"], a["H_q"], a["H_kv"], a["Sk"], a["d"],
                                       a["d_r"], a["n_sink"], opt, a["ws"], a["n"], None) == code
+
+
+def test_drafts_refuse(lib):
+    call = lambda n_sink, window, q=P: apex.apex_attn_sink_tree_decode(  # noqa: E731
+        q, P, P, 8 * P, 1, 8, 2, 4, 64, 128, 128, P, None, 0, None, window, n_sink, 0.0, P, 1 << 40, None)
+    assert call(-1, 16) == BAD and call(-1, 0) == BAD and call(4, 16, None) == BAD
 
 
 def test_workspace_bytes(lib):

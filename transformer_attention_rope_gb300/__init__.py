@@ -11,7 +11,8 @@ Raw C-ABI names (pointers and sizes):
     apex_attn_fwd_ex, apex_attn_fwd_ws, apex_attn_fwd_workspace_bytes, apex_attn_decode_ex, apex_attn_rope_keys,
     apex_attn_mla_fwd, apex_attn_mla_fwd_ws, apex_attn_mla_fwd_workspace_bytes, apex_attn_mla_decode,
     apex_attn_mla_rope_keys (with an Options struct),
-    apex_attn_sink_fwd, apex_attn_sink_fwd_workspace_bytes, apex_attn_sink_decode (windows with sinks),
+    apex_attn_sink_fwd, apex_attn_sink_fwd_workspace_bytes, apex_attn_sink_decode, apex_attn_sink_tree_decode (windows
+    with sinks),
     apex_attn_rope (with RopeOptions and RopeTensor structs), apex_attn_tree_decode, apex_attn_tree_workspace_bytes,
     apex_attn_decode_weights, apex_attn_decode_weights_workspace_bytes, apex_attn_evict,
     apex_attn_evict_workspace_bytes, apex_attn_norm_rope and apex_attn_norm_rope_grad (with NormTensor structs),
@@ -53,7 +54,7 @@ __all__ = [
     "norm_rope", "norm_rope_grad", "norm_rope_grad_workspace_bytes",
     "apex_attn_append4", "apex_attn_unpack4", "apex_attn_decode4", "apex_attn_decode4_workspace_bytes", "Bits4Tensor",
     "append4", "unpack4", "decode4", "decode4_workspace_bytes",
-    "apex_attn_sink_fwd", "apex_attn_sink_fwd_workspace_bytes", "apex_attn_sink_decode",
+    "apex_attn_sink_fwd", "apex_attn_sink_fwd_workspace_bytes", "apex_attn_sink_decode", "apex_attn_sink_tree_decode",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -180,6 +181,8 @@ def load_library():
             lib.apex_attn_decode4_workspace_bytes.restype = sz
             lib.apex_attn_tree_decode.argtypes = [vp] * 4 + [i32] * 7 + [vp, vp, i64, vp, i32, f32, vp, sz, vp]
             lib.apex_attn_tree_decode.restype = i32
+            lib.apex_attn_sink_tree_decode.argtypes = [vp] * 4 + [i32] * 7 + [vp, vp, i64, vp, i32, i32, f32, vp, sz, vp]
+            lib.apex_attn_sink_tree_decode.restype = i32
             lib.apex_attn_tree_workspace_bytes.argtypes = [i32] * 7
             lib.apex_attn_tree_workspace_bytes.restype = sz
             lib.apex_attn_decode_weights.argtypes = [vp] * 4 + [i32] * 6 + [vp, vp, f32, vp, sz, vp]
@@ -350,6 +353,13 @@ def apex_attn_tree_decode(q, k_cache, v_cache, out, B, H_q, H_kv, T, S_cap, d_qk
     return load_library().apex_attn_tree_decode(q, k_cache, v_cache, out, B, H_q, H_kv, T, S_cap, d_qk, d_v, lens,
                                                 tree_mask, mask_stride, positions, window, scale, workspace,
                                                 workspace_bytes, stream)
+
+
+def apex_attn_sink_tree_decode(q, k_cache, v_cache, out, B, H_q, H_kv, T, S_cap, d_qk, d_v, lens, tree_mask,
+                               mask_stride, positions, window, n_sink, scale, workspace, workspace_bytes, stream) -> int:
+    return load_library().apex_attn_sink_tree_decode(q, k_cache, v_cache, out, B, H_q, H_kv, T, S_cap, d_qk, d_v, lens,
+                                                     tree_mask, mask_stride, positions, window, n_sink, scale,
+                                                     workspace, workspace_bytes, stream)
 
 
 def apex_attn_tree_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_v) -> int:
@@ -1032,7 +1042,7 @@ def tree_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_v=None) -> int:
 
 
 def tree_decode(q, k_cache, v_cache, lens, *, tree_mask=None, positions=None, window: int = 0, scale=None, out=None,
-                workspace=None, stream=None):
+                workspace=None, stream=None, n_sink: int = 0):
     """Attention of T drafted tokens per sequence over a cache of rotated keys. q [B,H_q,T,d_qk] (rotated),
     caches [B,H_kv,S_cap,d_qk] / [B,H_kv,S_cap,d_v] with the drafts' rows at lens[b] + u, lens [B] int32
     -> out [B,H_q,T,d_v].
@@ -1040,12 +1050,14 @@ def tree_decode(q, k_cache, v_cache, lens, *, tree_mask=None, positions=None, wi
     tree_mask [B,T] or [T] int64: bit u of word t set when draft t sees draft u (None: u <= t);
     positions [B,T] int32: the drafts' positions, for a window (None: lens[b] + t); cached row j is
     then at position j, which is not so after evict or an append at other rows.
+    n_sink: the first positions, which stay visible behind a window (sinks).
     scale: factor of the scores (None or 0: 1 / sqrt(d_qk))."""
     torch = _torch or _load_torch()
     B, H_q, T, d_qk, H_kv, S_cap, d_v, device, pq, pk, pv = _cache_shapes(q, k_cache, v_cache)
     plens = _fit(lens, "lens", torch.int32, (B,), device)
     if not 0 < window <= _INT_MAX:  # positions are int32: a wider window is none
         window = 0
+    n_sink = _sinks(n_sink, window)
     pmask = ppos = None
     stride = 0
     if tree_mask is not None:
@@ -1062,8 +1074,10 @@ def tree_decode(q, k_cache, v_cache, lens, *, tree_mask=None, positions=None, wi
         else:
             pout = _fit(out, "out", torch.bfloat16, (B, H_q, T, d_v), device)
         ws = at.workspace(workspace, q, tree_workspace_bytes(B, H_q, H_kv, T, S_cap, d_qk, d_v))
-        status = (_lib or load_library()).apex_attn_tree_decode(
-            pq, pk, pv, pout, B, H_q, H_kv, T, S_cap, d_qk, d_v, plens, pmask, stride, ppos, window,
+        # the calls without sinks and with them differ by one argument
+        lib, sinks = _lib or load_library(), (n_sink,) if n_sink else ()
+        status = (lib.apex_attn_sink_tree_decode if n_sink else lib.apex_attn_tree_decode)(
+            pq, pk, pv, pout, B, H_q, H_kv, T, S_cap, d_qk, d_v, plens, pmask, stride, ppos, window, *sinks,
             0.0 if scale is None else scale, ws.data_ptr(), ws.nbytes, at.handle)
         if status:
             raise ApexError(status, "apex_attn_tree_decode")

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
                 const int kv = f.b * p.H_kv + f.hk;
                 if (f.head) p.units[f.unit] = make_int2(blockIdx.x, f.last);
                 for (int j = 0; j < f.n; ++j, ++g) {
-                    const int key0 = kKeys * (f.first + j);
+                    const int key0 = kKeys * f.tile(j);
                     const int ks = g % C::kKStages, vs = g % C::kVStages;
                     mbar_wait(bar(C::kBarKEmpty + ks), ((g / C::kKStages) & 1) ^ 1, p.wait);
                     mbar_arrive_expect_tx(bar(C::kBarKFull + ks), C::kKTile);
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
                     if (j + 2 == f.n) commit(C::kBarQEmpty);
                 }
                 mbar_wait(bar(C::kBarVFull + vs), (g / C::kVStages) & 1, p.wait);
-                mend_v<C::kVBoxes>(f, some, kKeys * (f.first + j), smem + C::kVOff + vs * C::kVTile);
+                mend_v<C::kVBoxes>(p, f, some, kKeys * f.tile(j), smem + C::kVOff + vs * C::kVTile);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     const int s = MT == 2 ? t : (g & 1);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
             for (int j = 0; j < f.n; ++j, ++g) {
                 const int s = MT == 2 ? t : (g & 1);
                 const uint32_t s_addr = lane_base + C::col_s(s);
-                const int key0 = kKeys * (f.first + j);
+                const int key0 = kKeys * f.tile(j);
                 mbar_wait(bar(C::kBarSFull + s), (MT == 2 ? g : g >> 1) & 1, p.wait);
                 tc_fence_after();
                 // O's product of tile g - 1 must be done before O is touched.  With one S buffer a
@@ -522,7 +522,7 @@ cudaError_t launch_cache_attn(CacheAttnLaunch &L, int sm_count, cudaStream_t str
     const int n_units = p.B * p.H_kv * p.n_groups, room = pairs ? sm_count / 2 : sm_count;
     int shares = std::min(room, cache_attn_shares(p.B, p.H_kv, p.n_groups, p.S_cap, pairs));
     // keys that a unit can reach: a window bounds them, the drafts and a tile's slack beside it
-    const int reach = p.window > 0 ? (int)std::min<long long>(p.S_cap, (long long)p.window + p.drafts + kKeys) : p.S_cap;
+    const int reach = p.window > 0 ? (int)std::min<long long>(p.S_cap, (long long)p.window + p.drafts + kKeys + (p.n_sink ? p.n_sink + kKeys : 0)) : p.S_cap;
     p.whole = !p.acc && cache_attn_whole(n_units, reach, room);
     if (p.whole) shares = std::min(shares, n_units);
     cudaError_t err;

@@ -222,7 +222,7 @@ __device__ __forceinline__ uint64_t draft_sight(const CacheAttnParams &p, int b,
         lo = (int)min((long long)len, max(0ll, m - p.window + 1));
         for (int u = 0; u < n; ++u) {
             const long long at = pos ? max(pos[u], len) : (long long)len + u;
-            if (m - at >= p.window) w &= ~(1ull << u);
+            if (m - at >= p.window && at >= p.n_sink) w &= ~(1ull << u);
         }
     }
     return w;
@@ -230,11 +230,12 @@ __device__ __forceinline__ uint64_t draft_sight(const CacheAttnParams &p, int b,
 
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
-// Visibility of the 128 keys of the tile at k0: cached keys [lo, len) and drafts.
-__device__ __forceinline__ void sight_words(uint32_t (&w)[4], int k0, int lo, int len, uint64_t drafts)
+// Visibility of the 128 keys of the tile at k0: cached keys [lo, len), those before `sink`, and drafts.
+__device__ __forceinline__ void sight_words(uint32_t (&w)[4], int k0, int lo, int len, int sink, uint64_t drafts)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = bits_below(len - k0 - 32 * i) & ~bits_below(lo - k0 - 32 * i);
+    for (int i = 0; i < 4; ++i)
+        w[i] = bits_below(len - k0 - 32 * i) & (~bits_below(lo - k0 - 32 * i) | bits_below(sink - k0 - 32 * i));
     const int s = len - k0;  // column of draft 0
     uint64_t d0 = 0, d1 = 0;
     if (s <= -64 || s >= 128) {
@@ -264,7 +265,7 @@ __device__ __forceinline__ void tma_load_3d_policy(uint32_t dst, const CUtensorM
         : "memory");
 }
 
-// What some row of a unit sees: the drafts in `any` and the cached keys from `lo` on -- the
+// What some row of a unit sees: the sinks, the drafts in `any` and the cached keys from `lo` on -- the
 // first that any draft's window reaches, which is past len - window + 1 when every draft's
 // position is past len.  Made once a fragment by one warp, while its first tile is on the way.
 struct Sight {
@@ -289,12 +290,12 @@ struct Sight {
 // Zero the rows of a V tile in shared memory (NB boxes of [128 keys][64 entries]) whose
 // key no row of the unit sees; by one warp.
 template <int NB>
-__device__ __forceinline__ void mend_v(const Frag &f, const Sight &some, int key0, uint8_t *tile)
+__device__ __forceinline__ void mend_v(const CacheAttnParams &p, const Frag &f, const Sight &some, int key0, uint8_t *tile)
 {
     const int lane = threadIdx.x & 31;
     if (key0 >= some.lo && key0 + kCacheTileKeys <= f.s.len) return;
     uint32_t w[4];
-    sight_words(w, key0, some.lo, f.s.len, some.any);
+    sight_words(w, key0, some.lo, f.s.len, p.n_sink, some.any);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (!((w[i] >> lane) & 1))
@@ -326,7 +327,7 @@ __device__ __forceinline__ void softmax_tile(const CacheAttnParams &p, uint32_t 
     tmem_wait_ld();
     if (!__all_sync(0xffffffffu, key0 >= lo && key0 + kCacheTileKeys <= len)) {
         uint32_t w[4];
-        sight_words(w, key0, lo, len, drafts);
+        sight_words(w, key0, lo, len, p.n_sink, drafts);
 #pragma unroll
         for (int e = 0; e < 128; ++e)
             if (!((w[e >> 5] >> (e & 31)) & 1)) v[e] = 0xff800000u;

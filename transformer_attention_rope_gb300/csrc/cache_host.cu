@@ -379,14 +379,14 @@ static apex_status check_cache_attn(int B, int H_q, int H_kv, int T, int S_cap, 
 static apex_status cache_attn(const void *q, const void *k_cache, const void *v_cache, void *out, int B, int H_q,
                               int H_kv, int T, int S_cap, int d_qk, int d_v, const int *lens,
                               const uint64_t *tree_mask, long long mask_stride, const int *positions, int window,
-                              float *acc, bool weights, float scale, void *workspace, size_t workspace_bytes,
+                              int n_sink, float *acc, bool weights, float scale, void *workspace, size_t workspace_bytes,
                               apex_stream_t stream)
 {
     if (!q || !k_cache || !v_cache || !out || !lens || !workspace || (weights && !acc)) return APEX_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace) ||
         !aligned(lens, 4) || !aligned(tree_mask, 8) || !aligned(positions, 4) || !aligned(acc, 4))
         return APEX_ERR_INVALID_ARG;
-    if (!isfinite(scale) || scale < 0.f || mask_stride < 0) return APEX_ERR_INVALID_ARG;
+    if (!isfinite(scale) || scale < 0.f || mask_stride < 0 || n_sink < 0) return APEX_ERR_INVALID_ARG;
     apex_status s = check_cache_attn(B, H_q, H_kv, T, S_cap, d_qk, d_v);
     if (s != APEX_OK) return s;
     // a CTA writes its rows while others still read theirs
@@ -416,6 +416,7 @@ static apex_status cache_attn(const void *q, const void *k_cache, const void *v_
     p.mask_stride = mask_stride;
     p.positions = positions;
     p.window = window > 0 ? window : 0;
+    p.n_sink = window > 0 ? std::min(n_sink, S_cap) : 0;  // without a window every key stays visible
     p.drafts = weights ? 0 : T;
     p.acc = acc;
     p.scale_log2 = (float)(1.4426950408889634 * (scale == 0.f ? 1.0 / sqrt((double)d_qk) : (double)scale));
@@ -447,14 +448,24 @@ apex_status apex_attn_tree_decode(const void *q, const void *k_cache, const void
                                   float scale, void *workspace, size_t workspace_bytes, apex_stream_t stream)
 {
     return cache_attn(q, k_cache, v_cache, out, B, H_q, H_kv, T, S_cap, d_qk, d_v, lens, tree_mask, mask_stride,
-                      positions, window, nullptr, false, scale, workspace, workspace_bytes, stream);
+                      positions, window, 0, nullptr, false, scale, workspace, workspace_bytes, stream);
+}
+
+apex_status apex_attn_sink_tree_decode(const void *q, const void *k_cache, const void *v_cache, void *out, int B,
+                                       int H_q, int H_kv, int T, int S_cap, int d_qk, int d_v, const int *lens,
+                                       const uint64_t *tree_mask, long long mask_stride, const int *positions,
+                                       int window, int n_sink, float scale, void *workspace, size_t workspace_bytes,
+                                       apex_stream_t stream)
+{
+    return cache_attn(q, k_cache, v_cache, out, B, H_q, H_kv, T, S_cap, d_qk, d_v, lens, tree_mask, mask_stride,
+                      positions, window, n_sink, nullptr, false, scale, workspace, workspace_bytes, stream);
 }
 
 apex_status apex_attn_decode_weights(const void *q, const void *k_cache, const void *v_cache, void *out, int B,
                                      int H_q, int H_kv, int S_cap, int d_qk, int d_v, const int *lens, float *acc,
                                      float scale, void *workspace, size_t workspace_bytes, apex_stream_t stream)
 {
-    return cache_attn(q, k_cache, v_cache, out, B, H_q, H_kv, 1, S_cap, d_qk, d_v, lens, nullptr, 0, nullptr, 0, acc,
+    return cache_attn(q, k_cache, v_cache, out, B, H_q, H_kv, 1, S_cap, d_qk, d_v, lens, nullptr, 0, nullptr, 0, 0, acc,
                       true, scale, workspace, workspace_bytes, stream);
 }
 

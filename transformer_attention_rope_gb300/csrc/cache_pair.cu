@@ -190,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                 const int kv = f.b * p.H_kv + f.hk;
                 if (f.head && rank == 0) p.units[f.unit] = make_int2(share, f.last);
                 for (int j = 0; j < f.n; ++j, ++g) {
-                    const int key0 = kKeys * (f.first + j);
+                    const int key0 = kKeys * f.tile(j);
                     const int st = g % C::kStages;
                     const uint32_t at = sb + C::kStageOff + st * C::kStage;
                     pair_wait(bar(C::kBarEmpty + st), ((g / C::kStages) & 1) ^ 1, p.wait, abort);
@@ -224,7 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
             for (int j = 0; j < f.n; ++j, ++g) {
                 const int st = g % C::kStages;
                 pair_wait(bar(C::kBarFull + st), (g / C::kStages) & 1, p.wait, abort);
-                mend_v<1>(f, some, kKeys * (f.first + j), smem + C::kStageOff + st * C::kStage + C::kKTile);
+                mend_v<1>(p, f, some, kKeys * f.tile(j), smem + C::kStageOff + st * C::kStage + C::kKTile);
                 __syncwarp();
                 if (lane == 0) arrive_leader(bar(C::kBarReady + st));
             }
@@ -324,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                     pair_wait(bar(C::kBarSFull + t), (MT == 2 ? g : g >> 1) & 1, p.wait, abort);
                     tc_fence_after();
                     // O's last product came before the product that made these scores: O may be touched
-                    softmax_tile<DV, false>(p, s_addr, o_addr, kKeys * (f.first + j), lo, f.s.len, drafts, m_run, l_run,
+                    softmax_tile<DV, false>(p, s_addr, o_addr, kKeys * f.tile(j), lo, f.s.len, drafts, m_run, l_run,
                                             nullptr, [] {}, [&] {
                                                 tmem_wait_st();
                                                 tc_fence_before();
