@@ -59,7 +59,7 @@ struct Cfg {
 };
 
 // ---------------------------------------------------------------- attention
-template <int DQK, int DV, int MT, bool WEIGHTS>
+template <int DQK, int DV, int MT, bool WEIGHTS, bool SINK>
 __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CacheAttnParams p)
@@ -105,13 +105,13 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
     // before the stream's previous kernel is done
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Sched *sched = reinterpret_cast<Sched *>(smem + C::kSched);
-    if (warp == C::kWarpTma) make_sched(p, blockIdx.x, gridDim.x, sched);
+    if (warp == C::kWarpTma) make_sched<SINK>(p, blockIdx.x, gridDim.x, sched);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::kTmemSlot);
 
-    Walk walk(p, *sched);
+    Walk<SINK> walk(p, *sched);
     Frag f;
     if (warp == C::kWarpTma) {
         // ------------------------------------------------------------ TMA producer
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
                 const int kv = f.b * p.H_kv + f.hk;
                 if (f.head) p.units[f.unit] = make_int2(blockIdx.x, f.last);
                 for (int j = 0; j < f.n; ++j, ++g) {
-                    const int key0 = kKeys * f.tile(j);
+                    const int key0 = kKeys * f.tile<SINK>(j);
                     const int ks = g % C::kKStages, vs = g % C::kVStages;
                     mbar_wait(bar(C::kBarKEmpty + ks), ((g / C::kKStages) & 1) ^ 1, p.wait);
                     mbar_arrive_expect_tx(bar(C::kBarKFull + ks), C::kKTile);
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
             for (int t = 0; t < MT; ++t) issue_qk(t, MT == 2 ? t : (g & 1), g % C::kKStages);
             commit(C::kBarKEmpty + g % C::kKStages);
             if (f.n == 1) commit(C::kBarQEmpty);
-            const Sight some(p, f);
+            const Sight<SINK> some(p, f);
             for (int j = 0; j < f.n; ++j, ++g) {
                 const int ks = (g + 1) % C::kKStages, vs = g % C::kVStages;
                 const bool nxt = j + 1 < f.n;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
                     if (j + 2 == f.n) commit(C::kBarQEmpty);
                 }
                 mbar_wait(bar(C::kBarVFull + vs), (g / C::kVStages) & 1, p.wait);
-                mend_v<C::kVBoxes>(p, f, some, kKeys * f.tile(j), smem + C::kVOff + vs * C::kVTile);
+                mend_v<C::kVBoxes, SINK>(p, f, some, kKeys * f.tile<SINK>(j), smem + C::kVOff + vs * C::kVTile);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     const int s = MT == 2 ? t : (g & 1);
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
             const bool row_ok = r < p.R;  // padding rows of the last M tile
             const int kv = f.b * p.H_kv + f.hk;
             int lo;
-            const uint64_t drafts = draft_sight(p, f.b, row_ok ? r % p.T : 0, f.s.len, f.s.total, lo);
+            const uint64_t drafts = draft_sight<SINK>(p, f.b, row_ok ? r % p.T : 0, f.s.len, f.s.total, lo);
             float m_run = -INFINITY, l_run = 0.f;
             float *scores = nullptr;
             if (WEIGHTS) scores = p.scores + ((size_t)kv * p.R + r) * p.S_pad;
@@ -251,13 +251,13 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, MT>::kThreads, 1)
             for (int j = 0; j < f.n; ++j, ++g) {
                 const int s = MT == 2 ? t : (g & 1);
                 const uint32_t s_addr = lane_base + C::col_s(s);
-                const int key0 = kKeys * f.tile(j);
+                const int key0 = kKeys * f.tile<SINK>(j);
                 mbar_wait(bar(C::kBarSFull + s), (MT == 2 ? g : g >> 1) & 1, p.wait);
                 tc_fence_after();
                 // O's product of tile g - 1 must be done before O is touched.  With one S buffer a
                 // tile these scores follow it; with two it is waited for, in every tile, so
                 // that no phase of its barrier is skipped.
-                softmax_tile<DV, WEIGHTS>(
+                softmax_tile<DV, WEIGHTS, SINK>(
                     p, s_addr, o_addr, key0, lo, f.s.len, drafts, m_run, l_run, row_ok ? scores : nullptr,
                     [&] { if (MT == 1 && g > 0) mbar_wait(bar(C::kBarPV + t), (g - 1) & 1, p.wait); }, [] {});
                 __syncwarp();
@@ -478,15 +478,22 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
         add_weights(p, blockIdx.x - join_blocks, chunks, lse);
 }
 
-template <int DQK, int DV, int MT, bool WEIGHTS>
+template <int DQK, int DV, int MT, bool WEIGHTS, bool SINK>
 cudaError_t launch_t(const CacheAttnLaunch &L, int grid, cudaStream_t stream)
 {
     using C = Cfg<DQK, DV, MT>;
-    auto kernel = cache_attn_kernel<DQK, DV, MT, WEIGHTS>;
+    auto kernel = cache_attn_kernel<DQK, DV, MT, WEIGHTS, SINK>;
     static KernelSetup setup;
     const cudaError_t err = setup(kernel, C::kSmemBytes);
     if (err != cudaSuccess) return err;
     return launch_dependent(kernel, grid, C::kThreads, C::kSmemBytes, stream, L.tm_q, L.tm_k, L.tm_v, L.p);
+}
+
+template <int DQK, int DV, int MT>
+cudaError_t launch_sink(const CacheAttnLaunch &L, int grid, cudaStream_t stream)
+{
+    return L.p.n_sink > 0 ? launch_t<DQK, DV, MT, false, true>(L, grid, stream)
+                          : launch_t<DQK, DV, MT, false, false>(L, grid, stream);
 }
 
 template <int DV, int SPLIT>
@@ -529,13 +536,13 @@ cudaError_t launch_cache_attn(CacheAttnLaunch &L, int sm_count, cudaStream_t str
     if (pairs)
         err = launch_cache_pair(L, shares, stream);
     else if (p.d_qk == 64)
-        err = p.acc              ? launch_t<64, 64, 1, true>(L, shares, stream)
-              : p.group == 128 ? launch_t<64, 64, 1, false>(L, shares, stream)
-                               : launch_t<64, 64, 2, false>(L, shares, stream);
+        err = p.acc              ? launch_t<64, 64, 1, true, false>(L, shares, stream)
+              : p.group == 128 ? launch_sink<64, 64, 1>(L, shares, stream)
+                               : launch_sink<64, 64, 2>(L, shares, stream);
     else if (p.d_qk == 128)
-        err = p.acc ? launch_t<128, 128, 1, true>(L, shares, stream) : launch_t<128, 128, 1, false>(L, shares, stream);
+        err = p.acc ? launch_t<128, 128, 1, true, false>(L, shares, stream) : launch_sink<128, 128, 1>(L, shares, stream);
     else
-        err = p.acc ? launch_t<192, 128, 1, true>(L, shares, stream) : launch_t<192, 128, 1, false>(L, shares, stream);
+        err = p.acc ? launch_t<192, 128, 1, true, false>(L, shares, stream) : launch_sink<192, 128, 1>(L, shares, stream);
     if (err != cudaSuccess) return err;
     return p.whole ? cudaSuccess : launch_cache_join(p, shares, stream);
 }

@@ -68,19 +68,23 @@ __device__ __forceinline__ bool elect_one()
 }
 
 // ---------------------------------------------------------------- schedule
+// SINK, here and below: with first keys that stay visible behind a window; kernels without them are
+// built without what they cost (0.3 us of a 9.5 us call under a window).
+
 // Lengths of sequence b: cached keys, keys with its drafts, and its tiles (one at least, so
 // that every unit writes its output): the first `sink` tiles of the cache, which stay visible
 // behind a window, and those from tile0 on.
 struct Seq {
     int len, total, tile0, tiles, sink;
     int cost;  // of a unit in the schedule: its tiles and kCacheUnitCost for its start; 1 when units stay whole
+    template <bool SINK>
     __device__ __forceinline__ void load(const CacheAttnParams &p, int b)
     {
         len = min(max(p.lens[b], 0), p.S_cap);
         total = min(len + p.drafts, p.S_cap);
         const int lo = p.window > 0 ? max(0, len - p.window + 1) : 0;
         tile0 = lo / kCacheTileKeys;
-        sink = p.n_sink > 0 ? min(tile0, (min(p.n_sink, total) + kCacheTileKeys - 1) / kCacheTileKeys) : 0;
+        sink = SINK && p.n_sink > 0 ? min(tile0, (min(p.n_sink, total) + kCacheTileKeys - 1) / kCacheTileKeys) : 0;
         tiles = max(1, (total + kCacheTileKeys - 1) / kCacheTileKeys - tile0) + sink;
         cost = p.whole ? 1 : tiles + kCacheUnitCost;
     }
@@ -100,6 +104,7 @@ struct Sched {
 // a time, and beyond 32 sequences twice, before the first tile: 512 caches of 256 to 512 keys
 // take 1.29 times their bytes and 4096 of them 1.24, but 65536 caches of 8 keys, one KV head,
 // 2.4 ms, nearly all of it here.
+template <bool SINK>
 __device__ __forceinline__ void make_sched(const CacheAttnParams &p, int c, int n, Sched *out)
 {
     const int lane = threadIdx.x & 31;
@@ -108,7 +113,7 @@ __device__ __forceinline__ void make_sched(const CacheAttnParams &p, int c, int 
     Seq s;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         s.cost = 0;
-        if (b0 + lane < p.B) s.load(p, b0 + lane);
+        if (b0 + lane < p.B) s.load<SINK>(p, b0 + lane);
         total += __reduce_add_sync(0xffffffffu, s.cost);
     }
     total *= per_b;
@@ -123,7 +128,7 @@ __device__ __forceinline__ void make_sched(const CacheAttnParams &p, int c, int 
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             if (p.B > 32) {  // else the lanes still hold the lengths
                 s.cost = 0;
-                if (b0 + lane < p.B) s.load(p, b0 + lane);
+                if (b0 + lane < p.B) s.load<SINK>(p, b0 + lane);
             }
             int incl = s.cost;
 #pragma unroll
@@ -154,10 +159,11 @@ struct Frag {
     Seq s;
     int b, hk, group, unit;  // unit: index over all units
     int first, n;
+    template <bool SINK>
     __device__ __forceinline__ int tile(int j) const
     {
         const int t = first + j;
-        return t >= s.tile0 ? t : t - s.tile0 + s.sink;
+        return !SINK || t >= s.tile0 ? t : t - s.tile0 + s.sink;
     }
     bool head, tail;         // holds the unit's first / last tile
     int last;                // share of the unit's last tile
@@ -165,6 +171,7 @@ struct Frag {
 
 static_assert(sizeof(Sched) <= 48, "schedule slot");
 
+template <bool SINK>
 struct Walk {
     Sched s;
     Seq seq;
@@ -174,7 +181,7 @@ struct Walk {
     {
         const int per_b = p.H_kv * p.n_groups;
         while (s.left > 0) {
-            if (fresh) seq.load(p, s.b);
+            if (fresh) seq.template load<SINK>(p, s.b);
             fresh = false;
             const int n = min(seq.cost - s.off, s.left);  // cost of this unit in the share
             const int t0 = p.whole ? 0 : max(0, s.off - kCacheUnitCost);
@@ -184,7 +191,7 @@ struct Walk {
             f.hk = s.unit / p.n_groups;
             f.group = s.unit % p.n_groups;
             f.unit = s.b * per_b + s.unit;
-            f.first = seq.tile0 + t0 - seq.sink;
+            f.first = seq.tile0 + t0 - (SINK ? seq.sink : 0);
             f.n = t1 - t0;
             f.head = t0 == 0;
             f.tail = t1 == seq.tiles;
@@ -209,6 +216,7 @@ struct Walk {
 
 // ---------------------------------------------------------------- masks
 // Drafts that draft t of sequence b sees, and its first visible cached key.
+template <bool SINK>
 __device__ __forceinline__ uint64_t draft_sight(const CacheAttnParams &p, int b, int t, int len, int total, int &lo)
 {
     lo = 0;
@@ -222,7 +230,7 @@ __device__ __forceinline__ uint64_t draft_sight(const CacheAttnParams &p, int b,
         lo = (int)min((long long)len, max(0ll, m - p.window + 1));
         for (int u = 0; u < n; ++u) {
             const long long at = pos ? max(pos[u], len) : (long long)len + u;
-            if (m - at >= p.window && at >= p.n_sink) w &= ~(1ull << u);
+            if (m - at >= p.window && (!SINK || at >= p.n_sink)) w &= ~(1ull << u);
         }
     }
     return w;
@@ -231,11 +239,12 @@ __device__ __forceinline__ uint64_t draft_sight(const CacheAttnParams &p, int b,
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
 // Visibility of the 128 keys of the tile at k0: cached keys [lo, len), those before `sink`, and drafts.
+template <bool SINK>
 __device__ __forceinline__ void sight_words(uint32_t (&w)[4], int k0, int lo, int len, int sink, uint64_t drafts)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = bits_below(len - k0 - 32 * i) & (~bits_below(lo - k0 - 32 * i) | bits_below(sink - k0 - 32 * i));
+        w[i] = bits_below(len - k0 - 32 * i) & (~bits_below(lo - k0 - 32 * i) | (SINK ? bits_below(sink - k0 - 32 * i) : 0u));
     const int s = len - k0;  // column of draft 0
     uint64_t d0 = 0, d1 = 0;
     if (s <= -64 || s >= 128) {
@@ -268,6 +277,7 @@ __device__ __forceinline__ void tma_load_3d_policy(uint32_t dst, const CUtensorM
 // What some row of a unit sees: the sinks, the drafts in `any` and the cached keys from `lo` on -- the
 // first that any draft's window reaches, which is past len - window + 1 when every draft's
 // position is past len.  Made once a fragment by one warp, while its first tile is on the way.
+template <bool SINK>
 struct Sight {
     uint64_t any;
     int lo;
@@ -278,7 +288,7 @@ struct Sight {
         int first = f.s.len;
         for (int t = threadIdx.x & 31; t < p.T; t += 32) {
             int from;
-            any |= draft_sight(p, f.b, t, f.s.len, f.s.total, from);
+            any |= draft_sight<SINK>(p, f.b, t, f.s.len, f.s.total, from);
             first = min(first, from);
         }
         any = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)any) |
@@ -289,13 +299,13 @@ struct Sight {
 
 // Zero the rows of a V tile in shared memory (NB boxes of [128 keys][64 entries]) whose
 // key no row of the unit sees; by one warp.
-template <int NB>
-__device__ __forceinline__ void mend_v(const CacheAttnParams &p, const Frag &f, const Sight &some, int key0, uint8_t *tile)
+template <int NB, bool SINK>
+__device__ __forceinline__ void mend_v(const CacheAttnParams &p, const Frag &f, const Sight<SINK> &some, int key0, uint8_t *tile)
 {
     const int lane = threadIdx.x & 31;
     if (key0 >= some.lo && key0 + kCacheTileKeys <= f.s.len) return;
     uint32_t w[4];
-    sight_words(w, key0, some.lo, f.s.len, p.n_sink, some.any);
+    sight_words<SINK>(w, key0, some.lo, f.s.len, p.n_sink, some.any);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (!((w[i] >> lane) & 1))
@@ -315,7 +325,7 @@ __device__ __forceinline__ void mend_v(const CacheAttnParams &p, const Frag &f, 
 // than 2^8: the final O / l does not depend on the reference point.  scores: where the
 // row's scores are kept, or NULL; wait_pv: waits until O may be touched;
 // half_done: called once the first 64 keys' weights are stored.
-template <int DV, bool WEIGHTS, typename WaitPV, typename Half>
+template <int DV, bool WEIGHTS, bool SINK, typename WaitPV, typename Half>
 __device__ __forceinline__ void softmax_tile(const CacheAttnParams &p, uint32_t s_addr, uint32_t o_addr, int key0,
                                              int lo, int len, uint64_t drafts, float &m_run, float &l_run,
                                              float *scores, WaitPV wait_pv, Half half_done)
@@ -327,7 +337,7 @@ __device__ __forceinline__ void softmax_tile(const CacheAttnParams &p, uint32_t 
     tmem_wait_ld();
     if (!__all_sync(0xffffffffu, key0 >= lo && key0 + kCacheTileKeys <= len)) {
         uint32_t w[4];
-        sight_words(w, key0, lo, len, p.n_sink, drafts);
+        sight_words<SINK>(w, key0, lo, len, p.n_sink, drafts);
 #pragma unroll
         for (int e = 0; e < 128; ++e)
             if (!((w[e >> 5] >> (e & 31)) & 1)) v[e] = 0xff800000u;

@@ -113,7 +113,7 @@ __device__ __forceinline__ void join_half(const CacheAttnParams &p, uint32_t lan
     }
 }
 
-template <int DQK, int MT>
+template <int DQK, int MT, bool SINK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kThreads, 1)
     cache_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CacheAttnParams p)
@@ -166,14 +166,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
     // before the stream's previous kernel is done
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Sched *sched = reinterpret_cast<Sched *>(smem + C::kSched);
-    if (warp == C::kWarpTma) make_sched(p, share, shares, sched);
+    if (warp == C::kWarpTma) make_sched<SINK>(p, share, shares, sched);
     __syncwarp();
     tc_fence_before();
     cluster_sync();  // both CTAs' barriers initialised, TMEM allocated, schedules made
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::kTmemSlot);
 
-    Walk walk(p, *sched);
+    Walk<SINK> walk(p, *sched);
     Frag f;
     if (warp >= C::kWarpTma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsCtl));
     if (warp == C::kWarpTma) {
@@ -190,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                 const int kv = f.b * p.H_kv + f.hk;
                 if (f.head && rank == 0) p.units[f.unit] = make_int2(share, f.last);
                 for (int j = 0; j < f.n; ++j, ++g) {
-                    const int key0 = kKeys * f.tile(j);
+                    const int key0 = kKeys * f.tile<SINK>(j);
                     const int st = g % C::kStages;
                     const uint32_t at = sb + C::kStageOff + st * C::kStage;
                     pair_wait(bar(C::kBarEmpty + st), ((g / C::kStages) & 1) ^ 1, p.wait, abort);
@@ -218,13 +218,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                                     f.group * p.group + 128 * (2 * t + rank), f.b * p.H_kv + f.hk);
             }
             __syncwarp();
-            const Sight some(p, f);
+            const Sight<SINK> some(p, f);
             pair_wait(bar(C::kBarQFull), fi & 1, p.wait, abort);
             if (lane == 0) arrive_leader(bar(C::kBarQReady));
             for (int j = 0; j < f.n; ++j, ++g) {
                 const int st = g % C::kStages;
                 pair_wait(bar(C::kBarFull + st), (g / C::kStages) & 1, p.wait, abort);
-                mend_v<1>(p, f, some, kKeys * f.tile(j), smem + C::kStageOff + st * C::kStage + C::kKTile);
+                mend_v<1, SINK>(p, f, some, kKeys * f.tile<SINK>(j), smem + C::kStageOff + st * C::kStage + C::kKTile);
                 __syncwarp();
                 if (lane == 0) arrive_leader(bar(C::kBarReady + st));
             }
@@ -317,14 +317,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
                 const int r = f.group * p.group + 128 * T + i;  // row of the KV head
                 const bool row_ok = r < p.R;                    // padding rows of the last M tile
                 int lo;
-                const uint64_t drafts = draft_sight(p, f.b, row_ok ? r % p.T : 0, f.s.len, f.s.total, lo);
+                const uint64_t drafts = draft_sight<SINK>(p, f.b, row_ok ? r % p.T : 0, f.s.len, f.s.total, lo);
                 float m_run = -INFINITY, l_run = 0.f;
                 for (int j = 0; j < f.n; ++j, ++g) {
                     if (MT == 1 && (g & 1) != t) continue;
                     pair_wait(bar(C::kBarSFull + t), (MT == 2 ? g : g >> 1) & 1, p.wait, abort);
                     tc_fence_after();
                     // O's last product came before the product that made these scores: O may be touched
-                    softmax_tile<DV, false>(p, s_addr, o_addr, kKeys * f.tile(j), lo, f.s.len, drafts, m_run, l_run,
+                    softmax_tile<DV, false, SINK>(p, s_addr, o_addr, kKeys * f.tile<SINK>(j), lo, f.s.len, drafts, m_run, l_run,
                                             nullptr, [] {}, [&] {
                                                 tmem_wait_st();
                                                 tc_fence_before();
@@ -376,23 +376,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<DQK, MT>::kT
     }
 }
 
-template <int DQK, int MT>
+template <int DQK, int MT, bool SINK>
 cudaError_t launch_t(const CacheAttnLaunch &L, int pairs, cudaStream_t stream)
 {
     using C = PairCfg<DQK, MT>;
-    auto kernel = cache_pair_kernel<DQK, MT>;
+    auto kernel = cache_pair_kernel<DQK, MT, SINK>;
     static KernelSetup setup;
     const cudaError_t err = setup(kernel, C::kSmemBytes, C::kLaunchRegs);
     if (err != cudaSuccess) return err;
     return launch_dependent(kernel, 2 * pairs, C::kThreads, C::kSmemBytes, stream, L.tm_q, L.tm_k, L.tm_v, L.p);
 }
 
+template <bool SINK>
+cudaError_t launch_rows(const CacheAttnLaunch &L, int pairs, cudaStream_t stream)
+{
+    const bool one = L.p.group == 256;  // M tiles of a CTA
+    if (L.p.d_qk == 128) return one ? launch_t<128, 1, SINK>(L, pairs, stream) : launch_t<128, 2, SINK>(L, pairs, stream);
+    return one ? launch_t<192, 1, SINK>(L, pairs, stream) : launch_t<192, 2, SINK>(L, pairs, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_pair(const CacheAttnLaunch &L, int pairs, cudaStream_t stream)
 {
-    if (L.p.d_qk == 128) return L.p.group == 256 ? launch_t<128, 1>(L, pairs, stream) : launch_t<128, 2>(L, pairs, stream);
-    return L.p.group == 256 ? launch_t<192, 1>(L, pairs, stream) : launch_t<192, 2>(L, pairs, stream);
+    return L.p.n_sink > 0 ? launch_rows<true>(L, pairs, stream) : launch_rows<false>(L, pairs, stream);
 }
 
 }  // namespace apex

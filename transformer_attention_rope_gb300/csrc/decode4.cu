@@ -117,7 +117,7 @@ struct Feed {
         left = f.n;
         gap = kCacheTileKeys * (f.s.tile0 - f.s.sink);
         pre = f.s.tile0 - f.first;  // below 1: the fragment has none of the sinks' tiles
-        key = kCacheTileKeys * f.tile(0) + kSlice * warp;
+        key = kCacheTileKeys * f.tile<true>(0) + kSlice * warp;
         const size_t row = kv * p.c.S_cap + key;
         // rows follow one another, so a slice is one run of bytes
         k = p.k + row * (DQK / 2) + 16 * lane;
@@ -223,10 +223,10 @@ __global__ void __launch_bounds__(kThreads, decode4_ctas(8 * NT)) decode4_kernel
     Sched *sched = reinterpret_cast<Sched *>(smem + C::kSched);
     // launched as a programmatic dependent: inputs may be the previous kernel's output
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == 0) make_sched(pc, blockIdx.x, gridDim.x, sched);
+    if (warp == 0) make_sched<true>(pc, blockIdx.x, gridDim.x, sched);
     __syncthreads();
 
-    Walk walk(pc, *sched);
+    Walk<true> walk(pc, *sched);
     Frag f;
     while (walk.next(pc, f)) {
         const size_t kv = (size_t)f.b * pc.H_kv + f.hk;
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, decode4_ctas(8 * NT)) decode4_kernel
 
         constexpr int U = kSlice / kStep;  // steps whose scores are there together
         const uint8_t *at = smem + warp * kStages * C::kStage;
-        int slice0 = kCacheTileKeys * f.tile(0) + kSlice * warp, pre = f.s.tile0 - f.first;
+        int slice0 = kCacheTileKeys * f.tile<true>(0) + kSlice * warp, pre = f.s.tile0 - f.first;
         for (int j = 0; j < f.n; ++j) {
             __syncwarp();  // all lanes are done with the slot that is filled next
             feed.next(pc.S_cap);

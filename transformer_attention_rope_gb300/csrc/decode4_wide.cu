@@ -120,13 +120,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_wide_kernel(const __grid_
     // before the stream's previous kernel is done
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Sched *sched = reinterpret_cast<Sched *>(smem + C::kSched);
-    if (warp == kWarpK) make_sched(pc, blockIdx.x, gridDim.x, sched);
+    if (warp == kWarpK) make_sched<true>(pc, blockIdx.x, gridDim.x, sched);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::kTmemSlot);
 
-    Walk walk(pc, *sched);
+    Walk<true> walk(pc, *sched);
     Frag f;
     if (warp >= kWarpMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (warp >= kWarpK && warp < kWarpMma) {
@@ -143,11 +143,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_wide_kernel(const __grid_
                 const int hi = values ? min(f.s.len + pc.T, pc.S_cap) : pc.S_cap;
                 const int lo = values && pc.window > 0 ? f.s.len - pc.window + 1 : 0;
                 auto there = [&](int key) { return key < hi && (key >= lo || key < pc.n_sink); };
-                int key = kKeys * f.tile(0) + r;
+                int key = kKeys * f.tile<true>(0) + r;
                 packed.load(bytes, scales, base + key, there(key));
                 for (int j = 0; j < f.n; ++j, ++g) {
                     const int st = g % C::kStages;
-                    key = kKeys * f.tile(min(j + 1, f.n - 1)) + r;
+                    key = kKeys * f.tile<true>(min(j + 1, f.n - 1)) + r;
                     mbar_wait(bar(empty + st), ((g / C::kStages) & 1) ^ 1, p.c.wait);
                     packed.store(smem + off + st * size, r);
                     packed.load(bytes, scales, base + key, there(key));
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_wide_kernel(const __grid_
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < f.n; ++j, ++g) {
                 const uint32_t s_addr = lane_base + C::col_s(g & 1);
-                const int key0 = kKeys * f.tile(j), lo = key_lo - key0, hi = key_hi - key0, sink = pc.n_sink - key0;
+                const int key0 = kKeys * f.tile<true>(j), lo = key_lo - key0, hi = key_hi - key0, sink = pc.n_sink - key0;
                 mbar_wait(bar(C::kBarSFull + (g & 1)), (g >> 1) & 1, p.c.wait);
                 tc_fence_after();
                 uint32_t v[128];
