@@ -16,13 +16,17 @@
 // lies below 2^-36 of it.  The reference moves only when a score outgrows it, so a slice costs one
 // vote and no exchange of maxima.
 //
-// Keys: lane 4g + t holds bytes 8t.. (16 of 64) of key g's row, 32 neighbouring entries, as the
+// Keys: lane 4g + t holds bytes 16t .. 16t + 15 of key g's row, 32 neighbouring entries, as the
 // order of the sum over entries is free; queries are laid out alike.  Values: lane 4g + t holds
 // entries 16g.. of keys 2t, 2t + 1, 2t + 8, 2t + 9; the halves of two keys' bytes are
 // interleaved so that one conversion gives both keys' values of an entry, which is how the
 // second product takes them.
 //
-// Bound: HBM, 0.5625 bytes an entry.
+// Bound: HBM, 0.5625 bytes an entry, and close behind it the issue of conversions: a step of 16
+// keys takes some 290 instructions a warp, 64 of them conversions and 64 scales.  64 caches of 9001 to
+// 32767 keys, 32/8 heads of 128 (1.54 GB): 251 us, 6.1 TB/s; with slices of 16 keys for 8 warps 279, and 303
+// with addresses and masks made anew for each.  16 rows over 8 such caches (193 MB): 56 us, where the
+// conversions are the same and the products twice as many.  One cache under a window of 1024: 6.5 us.
 #include <math.h>
 
 #include "bits4.cuh"
@@ -545,7 +549,7 @@ cudaError_t launch_decode4(Decode4Params &p, int sm_count, cudaStream_t stream)
     // keys that a unit can reach: a window and the sinks bound them, the new rows and a tile's slack beside
     const int reach = c.window > 0 ? (int)std::min<long long>(c.S_cap, (long long)c.window + c.n_sink + c.drafts + 2 * kCacheTileKeys)
                                    : c.S_cap;
-    c.whole = cache_attn_whole(n_units, reach, room);
+    c.whole = decode4_whole(n_units, reach, c.group);
     if (c.whole) shares = (int)std::min<long long>(shares, n_units);
     const cudaError_t err = c.group == 8    ? launch_rows<1>(p, shares, stream)
                             : c.group == 16 ? launch_rows<2>(p, shares, stream)
