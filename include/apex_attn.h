@@ -677,12 +677,11 @@ apex_status apex_attn_unpack4(const apex_bits4_tensor *k, const apex_bits4_tenso
  *             the caller, not read before written; calls that may run at the same time need
  *             one each
  *
- * Row lengths, groups and limits as for apex_attn_tree_decode (1 <= T <= 64); made for few rows
- * G * T of a KV head, which are worked on 16 at a time.  A row that sees no key gives zeros.
- * Cache rows that no token of the sequence sees may hold anything; the values of the others must
- * be finite.  Queries are held in fp16 relative to their row's largest entry, where entries below
- * 2^-24 of it lose precision; scores, statistics and sums are fp32, weights are rounded to fp16 for
- * the tensor cores.  Equal inputs give equal bits.
+ * Row lengths, groups and limits as for apex_attn_tree_decode (1 <= T <= 64).  A row that sees no
+ * key gives zeros.  Cache rows that no token of the sequence sees may hold anything; the values of
+ * the others must be finite, and factors from 2^-90 to 2^90.  Queries are held in fp16 relative to
+ * their row's largest entry, where entries below 2^-21 of it lose precision; scores, statistics
+ * and sums are fp32, weights are rounded to fp16 for the tensor cores.  Equal inputs give equal bits.
  */
 apex_status apex_attn_decode4(const void *q, const void *k4, const void *k_scale, const void *v4, const void *v_scale,
                               void *out, int B, int H_q, int H_kv, int T, int S_cap, int d_qk, int d_v, const int *lens,

@@ -10,7 +10,7 @@
 // Mathematics: S^T = K Q^T and O^T += V^T P^T on mma.sync (keys and value entries as rows of
 // A, the queries of a KV head as the 8 columns of B), fp16 with fp32 sums.  A product of an
 // e2m1 value with its e4m3 scale is exact in fp16.  Queries go to fp16 scaled by a power of two
-// for each row, exact but for entries 2^-24 below the row's largest; the factor goes into the
+// for each row, exact but for entries below 2^-21 of the row's largest; the factor goes into the
 // scores' scale.  Weights are taken relative to a reference 2^11 below the running
 // maximum, as fp16 up to 2^15 is: those of 2^-25 of the largest keep 11 bits, and what is lost
 // lies below 2^-36 of it.  The reference moves only when a score outgrows it, so a slice costs one

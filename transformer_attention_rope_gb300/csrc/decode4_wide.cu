@@ -4,10 +4,11 @@
 // in cache_attn.cuh.
 //
 // Warp roles: 0-3 softmax and epilogue (thread i owns row i = TMEM lane i; before a fragment's first
-// tile it writes its query row to shared memory as fp16), 4-7 conversion (thread i turns key
+// tile it writes its query row to shared memory as fp16), 4-7 conversion of keys (thread i turns key
 // i of a tile, from 64 bytes of codes and 8 of scales to a row of fp16 in the tiles' 128-byte
-// swizzle; the next tile's bytes are under way meanwhile), 8 issues S = Q K^T and O += P V.  S has
-// two buffers, so the product of the next tile runs under this tile's softmax.
+// swizzle; the next tile's bytes are under way meanwhile), 8-11 the same for values, 12 issues
+// S = Q K^T and O += P V.  S has two buffers, so the product of the next tile runs under this tile's
+// softmax.
 //
 // Bound: the softmax of a tile (0.9 us beside the conversions' instructions) and the products (0.6) in
 // turn, 1.3 us a tile of 128 keys and SM whatever the rows; its bytes take 0.4.  8 caches of 9001 to
@@ -220,13 +221,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_wide_kernel(const __grid_
         }
     } else if (warp < kWarpK) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-      if (warp < live) {
         // ------------------------------------------------------------ queries, softmax, epilogue
         const int i = threadIdx.x;  // row of the M tile == TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
         const uint32_t o_addr = lane_base + C::kColO;
         int g = 0;
-        for (int fi = 0; walk.next(pc, f); ++fi) {
+        for (int fi = 0; warp < live && walk.next(pc, f); ++fi) {
             const int r = f.group * pc.group + i;  // row of the KV head
             const bool row_ok = i < pc.rows_cap && r < pc.R;
             const size_t kv = (size_t)f.b * pc.H_kv + f.hk, row = kv * pc.R + r;
@@ -351,7 +351,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_wide_kernel(const __grid_
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::kBarOEmpty));
         }
-      }
     }
 
     tc_fence_before();
