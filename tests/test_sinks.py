@@ -371,3 +371,54 @@ def test_conveniences_refuse():
     for bad in (lambda: apex.fwd(q, k, v, window=8, n_sink=-1), lambda: apex.decode(q[:, :, :1].contiguous(), k, v, 63, window=8, n_sink=-2)):
         with pytest.raises(ValueError):
             bad()
+    # tensors that do not belong together: nothing is launched
+    k1, k2, long = k[:, :1].contiguous(), torch.cat([k, k]), torch.cat([k, k], dim=2)
+    one = q[:, :, :1].contiguous()
+    for bad in ((q, k1, v), (q, k, k1), (q, k2, v), (q, k, k2), (q, long, v), (q, k, v[..., :64].contiguous())):
+        with pytest.raises(ValueError):
+            apex.fwd(*bad, window=8, n_sink=2)
+        with pytest.raises(ValueError):
+            apex.decode(one, *bad[1:], 63, window=8, n_sink=2)
+    with pytest.raises(ValueError):
+        apex.fwd(q, k, v, window=8, n_sink=2, out=torch.empty_like(k))
+    with pytest.raises(ValueError):
+        apex.decode(one, k, v, 63, window=8, n_sink=2, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(apex.ApexError):
+        apex.decode(one, k, v, 63, window=8, n_sink=2, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
+
+
+@pytest.mark.gpu
+def test_a_window_past_32_bits_is_none():
+    dev = _gpu()
+    q, k, v = _inputs(dev, 11, 1, 4, 2, 300, 300, 128)
+    wide = 2 ** 32 + 5
+    assert torch.equal(apex.fwd(q, k, v, window=wide, n_sink=3), apex.fwd(q, k, v, window=300, n_sink=3))
+    one = q[:, :, -1:].contiguous()
+    assert torch.equal(apex.decode(one, k, v, 299, window=wide, n_sink=3), apex.decode(one, k, v, 299))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,d_r", [(128, 0), (128, 64)])
+def test_on_another_stream(d, d_r):
+    """Inputs made on a stream that the call is given, with the allocator busy on both."""
+    dev = _gpu()
+    S, window, sinks = 1200, 300, 4
+    made = _inputs(dev, 12, 1, 16, 2, S, S, d, d_r)
+    ref, tol = _ref(*made, 0, window, sinks, d_r)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            q, k, v = (x.clone() for x in made)
+            q1 = q[:, :, -1:].contiguous()
+        if d_r:
+            out = apex.mla_fwd(q, k, v, d_r, window=window, n_sink=sinks, stream=side)
+            one = apex.mla_decode(q1, k, v, S - 1, d_r, window=window, n_sink=sinks, stream=side)
+        else:
+            out = apex.fwd(q, k, v, window=window, n_sink=sinks, stream=side)
+            one = apex.decode(q1, k, v, S - 1, window=window, n_sink=sinks, stream=side)
+        junk = [torch.full((1 << 22,), float("nan"), device=dev) for _ in range(4)]  # over memory that is free
+        side.synchronize()
+        _close(out, ref, tol)
+        assert ((one.double() - ref[:, :, -1:]).abs() <= tol[:, :, -1:]).all()
+        del junk

@@ -424,7 +424,7 @@ def _stream_handle(stream):
 
 def _options(window=0, q_pos=0, rope_base=10000.0, yarn_scale=1.0, yarn_beta_fast=32.0, yarn_beta_slow=1.0,
              prefix_len=0, keys_prerotated=False) -> Options:
-    return Options(int(window), int(q_pos), float(rope_base), float(yarn_scale), float(yarn_beta_fast),
+    return Options(min(int(window), _INT_MAX), int(q_pos), float(rope_base), float(yarn_scale), float(yarn_beta_fast),
                    float(yarn_beta_slow), int(prefix_len), 1 if keys_prerotated else 0)
 
 
@@ -435,18 +435,62 @@ def _sinks(n_sink, window) -> int:
     return min(int(n_sink), 2 ** 24) if window > 0 else 0
 
 
-def _sink_fwd(q, k, v, out, sizes, d_r, n_sink, opt, workspace, stream):
-    """Prefill with sinks: apex_attn_sink_fwd, its workspace as for the calls without."""
-    import torch
-    if workspace is None:
-        need = int(apex_attn_sink_fwd_workspace_bytes(*sizes, d_r, n_sink, opt))
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else False
-    ws, n = (None, 0) if workspace is False else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = apex_attn_sink_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *sizes, d_r, n_sink, opt, ws, n,
-                            _stream_handle(stream))
-    if st != APEX_OK:
-        raise ApexError(st, "apex_attn_sink_fwd")
+def _sink_fwd(q, k, v, d_r, n_sink, opt, out, workspace, stream):
+    """Prefill with sinks on q's device (apex_attn_sink_fwd), its workspace as for the calls without."""
+    torch = _torch or _load_torch()
+    B, H_q, S_q, S_k, H_kv, d, device, pq, pk, pv = _sink_shapes(q, k, v, d_r)
+    sizes = (B, H_q, H_kv, S_q, S_k, d, d_r, n_sink)
+    at = _Launch(device, stream)
+    try:
+        if out is None:
+            out = at.new(q, (B, H_q, S_q, d), torch.bfloat16)
+        pout = _fit(out, "out", torch.bfloat16, (B, H_q, S_q, d), device)
+        lib, pws, size = _lib or load_library(), None, 0
+        if workspace is None:
+            size = lib.apex_attn_sink_fwd_workspace_bytes(*sizes, opt)
+        if workspace is not None and workspace is not False or size:
+            ws = at.workspace(workspace, q, size)
+            pws, size = ws.data_ptr(), ws.nbytes
+        status = lib.apex_attn_sink_fwd(pq, pk, pv, pout, *sizes, opt, pws, size, at.handle)
+        if status:
+            raise ApexError(status, "apex_attn_sink_fwd")
+    finally:
+        at.leave()
     return out
+
+
+def _sink_decode(q, k_cache, v_cache, d_r, n_sink, opt, out, workspace, stream):
+    """Decode with sinks on q's device (apex_attn_sink_decode)."""
+    torch = _torch or _load_torch()
+    B, H_q, _, S_k, H_kv, d, device, pq, pk, pv = _sink_shapes(q, k_cache, v_cache, d_r)
+    at = _Launch(device, stream)
+    try:
+        if out is None:
+            out = at.new(q, (B, H_q, 1, d), torch.bfloat16)
+        pout = _fit(out, "out", torch.bfloat16, (B, H_q, 1, d), device)
+        lib = _lib or load_library()
+        ws = at.workspace(workspace, q, lib.apex_attn_decode_workspace_bytes(B, H_q, H_kv, S_k, d))
+        status = lib.apex_attn_sink_decode(pq, pk, pv, pout, B, H_q, H_kv, S_k, d, d_r, n_sink, opt, ws.data_ptr(),
+                                           ws.nbytes, at.handle)
+        if status:
+            raise ApexError(status, "apex_attn_sink_decode")
+    finally:
+        at.leave()
+    return out
+
+
+def _sink_shapes(q, k, v, d_r):
+    """Sizes of queries, keys and values, their device and addresses."""
+    bf16 = _torch.bfloat16
+    B, H_q, S_q, d_qk = _rows4(q, "q")
+    _, H_kv, S_k, d = _rows4(v, "v")
+    if max(B, H_q, S_q, H_kv, S_k, d_qk) > _INT_MAX:
+        raise ValueError("more sequences, heads or tokens than are taken")
+    if d_qk != d + d_r:
+        raise ValueError("q must have the row length of v" + (" and d_r" if d_r else ""))
+    device = q.get_device()
+    return (B, H_q, S_q, S_k, H_kv, d, device, _fit(q, "q", bf16, (B, H_q, S_q, d_qk), device),
+            _fit(k, "k", bf16, (B, H_kv, S_k, d_qk), device), _fit(v, "v", bf16, (B, H_kv, S_k, d), device))
 
 
 def fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, *, window: int = 0, q_pos0: int = 0,
@@ -472,16 +516,16 @@ def fwd(q, k, v, *, window: int = 0, q_pos0: int = 0, rope_base: float = 10000.0
     import torch
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _check(t, n, 4)
+    n_sink = _sinks(n_sink, window)
+    if n_sink:
+        opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
+                       keys_prerotated)
+        return _sink_fwd(q, k, v, 0, n_sink, opt, out, workspace, stream)
     B, H_q, S_q, d = q.shape
     _, H_kv, S_k, _ = k.shape
     if out is None:
         out = torch.empty_like(q)
     _check(out, "out", 4)
-    n_sink = _sinks(n_sink, window)
-    if n_sink:
-        opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
-                       keys_prerotated)
-        return _sink_fwd(q, k, v, out, (B, H_q, H_kv, S_q, S_k, d), 0, n_sink, opt, workspace, stream)
     if workspace is None:
         need = fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d, window=window, q_pos0=q_pos0, rope_base=rope_base,
                                    yarn_scale=yarn_scale, yarn_beta_fast=yarn_beta_fast,
@@ -537,14 +581,14 @@ def mla_fwd(q, k, v, d_r: int, *, window: int = 0, q_pos0: int = 0, rope_base: f
     _, H_kv, S_k, d_h = v.shape
     if d_qk != d_h + d_r or k.shape[-1] != d_qk:
         raise ValueError("q / k rows must hold d_h + d_r entries")
-    if out is None:
-        out = torch.empty((B, H_q, S_q, d_h), dtype=torch.bfloat16, device=q.device)
-    _check(out, "out", 4)
     opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                    keys_prerotated)
     n_sink = _sinks(n_sink, window)
     if n_sink:
-        return _sink_fwd(q, k, v, out, (B, H_q, H_kv, S_q, S_k, d_h), int(d_r), n_sink, opt, workspace, stream)
+        return _sink_fwd(q, k, v, int(d_r), n_sink, opt, out, workspace, stream)
+    if out is None:
+        out = torch.empty((B, H_q, S_q, d_h), dtype=torch.bfloat16, device=q.device)
+    _check(out, "out", 4)
     if workspace is None:
         need = int(apex_attn_mla_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, int(d_r), opt))
         if need > 0:
@@ -580,6 +624,11 @@ def decode(q, k_cache, v_cache, q_pos: int, *, window: int = 0, rope_base: float
     _, H_kv, S_k, _ = k_cache.shape
     if one != 1:
         raise ValueError("decode takes one query per sequence")
+    n_sink = _sinks(n_sink, window)
+    if n_sink:
+        opt = _options(window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
+                       keys_prerotated)
+        return _sink_decode(q, k_cache, v_cache, 0, n_sink, opt, out, workspace, stream)
     if out is None:
         out = torch.empty_like(q)
     _check(out, "out", 4)
@@ -587,8 +636,7 @@ def decode(q, k_cache, v_cache, q_pos: int, *, window: int = 0, rope_base: float
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     ws_bytes = workspace.numel() * workspace.element_size()
-    n_sink = _sinks(n_sink, window)
-    plain = yarn_scale <= 1.0 and prefix_len == 0 and not keys_prerotated and not n_sink
+    plain = yarn_scale <= 1.0 and prefix_len == 0 and not keys_prerotated
     if plain:
         st = apex_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
                               S_k, d, int(window), int(q_pos), float(rope_base), workspace.data_ptr(), ws_bytes,
@@ -596,13 +644,8 @@ def decode(q, k_cache, v_cache, q_pos: int, *, window: int = 0, rope_base: float
     else:
         opt = _options(window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                        keys_prerotated)
-        if n_sink:
-            st = apex_attn_sink_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q,
-                                       H_kv, S_k, d, 0, n_sink, opt, workspace.data_ptr(), ws_bytes,
-                                       _stream_handle(stream))
-        else:
-            st = apex_attn_decode_ex(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q,
-                                     H_kv, S_k, d, opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
+        st = apex_attn_decode_ex(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q,
+                                 H_kv, S_k, d, opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
     if st != APEX_OK:
         raise ApexError(st, "apex_attn_decode")
     return out
@@ -625,6 +668,11 @@ def mla_decode(q, k_cache, v_cache, q_pos: int, d_r: int, *, window: int = 0, ro
         raise ValueError("decode takes one query per sequence")
     if d_qk != d_h + d_r or k_cache.shape[-1] != d_qk:
         raise ValueError("q / k_cache rows must hold d_h + d_r entries")
+    opt = _options(window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
+                   keys_prerotated)
+    n_sink = _sinks(n_sink, window)
+    if n_sink:
+        return _sink_decode(q, k_cache, v_cache, int(d_r), n_sink, opt, out, workspace, stream)
     if out is None:
         out = torch.empty((B, H_q, 1, d_h), dtype=torch.bfloat16, device=q.device)
     _check(out, "out", 4)
@@ -632,16 +680,8 @@ def mla_decode(q, k_cache, v_cache, q_pos: int, d_r: int, *, window: int = 0, ro
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     ws_bytes = workspace.numel() * workspace.element_size()
-    opt = _options(window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
-                   keys_prerotated)
-    n_sink = _sinks(n_sink, window)
-    if n_sink:
-        st = apex_attn_sink_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
-                                   S_k, d_h, int(d_r), n_sink, opt, workspace.data_ptr(), ws_bytes,
-                                   _stream_handle(stream))
-    else:
-        st = apex_attn_mla_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
-                                  S_k, d_h, int(d_r), opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
+    st = apex_attn_mla_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
+                              S_k, d_h, int(d_r), opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
     if st != APEX_OK:
         raise ApexError(st, "apex_attn_mla_decode")
     return out
@@ -793,7 +833,7 @@ def _turn_options(name, layout, rot_start, d_rot, inverse, rope_base, linear_sca
 
 
 def _row_pair(x, out, name, B, S, into, device):
-    """Shape and strides of a tensor and of its output."""
+    """Heads, entries and strides of a tensor and of its output."""
     bf16 = _torch.bfloat16
     try:
         known = x.dtype is bf16 and out.dtype is bf16 and x.get_device() == device == out.get_device()
@@ -806,25 +846,26 @@ def _row_pair(x, out, name, B, S, into, device):
     xs, to = x.shape, out.shape
     if len(xs) != 4 or len(to) != 4:
         raise ValueError("%s and %s_out must be 4-D tensors" % (name, name))
-    if xs[0] != B or xs[2] != S:
+    n_seq, heads, n, d = xs
+    if n_seq != B or n != S:
         raise ValueError("%s must have the batch and length of q" % name)
-    if (to != xs and not into) or to[0] != B or to[1] != xs[1] or to[3] != xs[3]:
+    rows = to[2]
+    if to != xs and (not into or to != (B, heads, rows, d)):
         raise ValueError("%s_out does not fit %s" % (name, name))
-    if xs[1] > _INT_MAX or xs[3] > _INT_MAX or to[2] > _INT_MAX:
+    if heads > _INT_MAX or d > _INT_MAX or rows > _INT_MAX:
         raise ValueError("%s has more heads or entries, or %s_out more rows, than are taken" % (name, name))
     xb, xh, xr, xe = x.stride()
     ob, oh, orow, oe = out.stride()
-    if (xe != 1 or oe != 1) and xs[3] > 1:
+    if (xe != 1 or oe != 1) and d > 1:
         raise ValueError("the last dimension of %s and %s_out must be contiguous" % (name, name))
-    if (ob == 0 and B > 1) or (oh == 0 and to[1] > 1) or (orow == 0 and to[2] > 1):
+    if (ob == 0 and B > 1) or (oh == 0 and heads > 1) or (orow == 0 and rows > 1):
         raise ValueError("%s_out repeats its elements" % name)
-    return xs, xb, xh, xr, ob, oh, orow
+    return heads, d, xb, xh, xr, ob, oh, orow
 
 
 def _rope_rows(x, out, name, B, S, into, device):
     """apex_rope_tensor of a tensor and its output, as bytes."""
-    xs, xb, xh, xr, ob, oh, orow = _row_pair(x, out, name, B, S, into, device)
-    return _ROPE_TENSOR.pack(x.data_ptr(), out.data_ptr(), xs[1], xs[3], xb, xh, xr, ob, oh, orow)
+    return _ROPE_TENSOR.pack(x.data_ptr(), out.data_ptr(), *_row_pair(x, out, name, B, S, into, device))
 
 
 def rope(q, k=None, v=None, *, positions, layout: str = "interleaved", rot_start: int = 0, d_rot=None,
@@ -890,21 +931,23 @@ def _norm_weight(w, name, heads, d, device):
     torch = _torch
     if w is None:
         return 0, 0, 0
-    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("%s must be a CUDA bfloat16 or float32 tensor" % name)
+    f32 = isinstance(w, torch.Tensor) and w.dtype is torch.float32
+    if not f32 and (not isinstance(w, torch.Tensor) or w.dtype is not torch.bfloat16) or not w.is_cuda:
+        raise TypeError("%s_weight must be a CUDA bfloat16 or float32 tensor" % name)
     if w.get_device() != device:
-        raise ValueError("%s is on another device than the other tensors" % name)
-    if (w.shape != (d,) and w.shape != (heads, d)) or not w.is_contiguous():
-        raise ValueError("%s must be a contiguous tensor of shape %s or %s" % (name, (d,), (heads, d)))
-    return w.data_ptr(), 1 if w.dtype is torch.float32 else 0, 1 if w.dim() == 2 else 0
+        raise ValueError("%s_weight is on another device than the other tensors" % name)
+    shape = w.shape
+    if shape != (d,) and shape != (heads, d) or not w.is_contiguous():
+        raise ValueError("%s_weight must be a contiguous tensor of shape %s or %s" % (name, (d,), (heads, d)))
+    return w.data_ptr(), 1 if f32 else 0, 1 if len(shape) == 2 else 0
 
 
 def _norm_rows(x, out, weight, name, B, S, into, device):
     """apex_norm_tensor of a tensor, its output and weights, as bytes."""
-    xs, xb, xh, xr, ob, oh, orow = _row_pair(x, out, name, B, S, into, device)
-    pw, f32, per_head = _norm_weight(weight, name + "_weight", xs[1], xs[3], device)
-    return _NORM_TENSOR.pack(x.data_ptr(), 0, out.data_ptr(), pw, 0, xs[1], xs[3], f32, per_head, xb, xh, xr, 0, 0, 0,
-                             ob, oh, orow)
+    heads, d, xb, xh, xr, ob, oh, orow = _row_pair(x, out, name, B, S, into, device)
+    pw, f32, per_head = _norm_weight(weight, name, heads, d, device)
+    return _NORM_TENSOR.pack(x.data_ptr(), 0, out.data_ptr(), pw, 0, heads, d, f32, per_head, xb, xh, xr, 0, 0, 0, ob,
+                             oh, orow)
 
 
 def norm_rope(q, k=None, v=None, *, positions, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -988,17 +1031,17 @@ def norm_rope_grad(q_grad, q, k_grad=None, k=None, *, positions, q_weight=None, 
     def rows(x, grad, out, weight, name):
         if out is None:
             out = at.new(x, x.shape, torch.bfloat16)
-        xs, xb, xh, xr, ob, oh, orow = _row_pair(x, out, name, B, S, False, device)
-        if _rows4(grad, name + "_grad") != xs or grad.get_device() != device:
+        heads, d, xb, xh, xr, ob, oh, orow = _row_pair(x, out, name, B, S, False, device)
+        if _rows4(grad, name + "_grad") != x.shape or grad.get_device() != device:
             raise ValueError("%s_grad does not fit %s" % (name, name))
         gb, gh, gr, ge = grad.stride()
-        if ge != 1 and xs[3] > 1:
+        if ge != 1 and d > 1:
             raise ValueError("the last dimension of %s_grad must be contiguous" % name)
-        pw, f32, per_head = _norm_weight(weight, name + "_weight", xs[1], xs[3], device)
+        pw, f32, per_head = _norm_weight(weight, name, heads, d, device)
         dw = None if weight is None else at.new(weight, weight.shape, torch.float32)
         return out, dw, _NORM_TENSOR.pack(x.data_ptr(), grad.data_ptr(), out.data_ptr(), pw,
-                                          0 if dw is None else dw.data_ptr(), xs[1], xs[3], f32, per_head, xb, xh, xr,
-                                          gb, gh, gr, ob, oh, orow)
+                                          0 if dw is None else dw.data_ptr(), heads, d, f32, per_head, xb, xh, xr, gb,
+                                          gh, gr, ob, oh, orow)
 
     try:
         pos = _fit(positions, "positions", torch.int32, (S,) if positions.dim() == 1 else (B, S), device)
