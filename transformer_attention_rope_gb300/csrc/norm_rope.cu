@@ -24,6 +24,7 @@
 // value appended: 3.0 us; the gradient of 16384 tokens of 32 + 8 heads (503 MB): 113 us, 4.5 TB/s, where
 // 128 registers leave 16 warps an SM (with 24 and spills 146, with half as many entries a lane and
 // 24 warps 123); of 1026 tokens with weights for each head: 19 us in two kernels.
+#include "cache_attn.cuh"
 #include "device_common.cuh"
 #include "norm_rope.h"
 #include "rope.cuh"
@@ -32,6 +33,8 @@ namespace apex {
 namespace {
 
 constexpr int kBatch = 2;  // rows of a lane whose loads are in flight together
+constexpr int kGradStages = 4;  // a lane's rows in shared memory: one worked on, the others on their way
+constexpr int kGradStage = 4 * kNormThreads * 16;
 
 __device__ __forceinline__ long long out_row(const NormRopeParams &p, const NormTensor &t, int b, int s)
 {
@@ -316,42 +319,70 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_rows_kernel(const __grid
     }
 }
 
+// A block of a gradient has an equal part of all tokens of its tensor's sequences, in tiles of neighbours.
+struct Span {
+    int at, end;  // next token, over all sequences
+    __device__ __forceinline__ Span(const NormRopeParams &p, const NormTensor &t, int block)
+        : at((int)((long long)p.B * p.S * block / t.blocks)), end((int)((long long)p.B * p.S * (block + 1) / t.blocks))
+    {
+    }
+    // the next tile: its sequence, first token, and number of tokens (0: none left)
+    __device__ __forceinline__ int next(const NormRopeParams &p, const NormTensor &t, int &b, int &s0)
+    {
+        b = at / p.S;
+        s0 = at - b * p.S;
+        const int n = min(t.tile, min(p.S - s0, end - at));
+        at += n;
+        return n;
+    }
+};
+
 // Where the next row to load of a lane's slot is: over the heads of a token, the tokens of a tile
 // and the tiles of a block.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ uint4 shared16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
 template <int L, bool HALF>
 struct Ahead {
     const uint16_t *x, *dy;
     long long x_step, dy_step, x_wrap, dy_wrap;  // to the next head, and from the last to the next token's first
-    int tile, n, tok, j, h;
-    __device__ __forceinline__ Ahead(const NormTensor &t, const Lane<L, HALF> &my, int block)
+    Span span;
+    int n, tok, j, h;
+    __device__ __forceinline__ Ahead(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int block)
         : x_step(my.wide * t.x_h), dy_step(my.wide * t.dy_h), x_wrap(my.deep * t.x_s - my.per_token * x_step),
-          dy_wrap(my.deep * t.dy_s - my.per_token * dy_step), tile(block)
+          dy_wrap(my.deep * t.dy_s - my.per_token * dy_step), span(p, t, block)
     {
     }
     __device__ __forceinline__ void start(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int first)
     {
-        n = 0;
+        int b, s0;
+        n = span.next(p, t, b, s0);
         j = 0;
         h = my.h0;
         tok = my.t0;
-        if (tile >= p.B * t.tiles) return;
-        const int b = tile / t.tiles, s0 = tile % t.tiles * t.tile;
-        n = min(t.tile, p.S - s0);
+        if (n == 0) return;
         x = my.at(t.x + b * t.x_b + (s0 + tok) * t.x_s + (first + h) * t.x_h);
         dy = my.at(t.dy + b * t.dy_b + (s0 + tok) * t.dy_s + (first + h) * t.dy_h);
     }
+    // the row and its gradient to a stage of the ring, zeros where there is none
     __device__ __forceinline__ void load(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int first,
-                                         int heads, uint4 (&v)[4])
+                                         int heads, uint32_t slot)
     {
-        v[0] = v[1] = v[2] = v[3] = make_uint4(0, 0, 0, 0);
-        if (my.a >= 0 && tok < n && h < heads) {
-            v[0] = *reinterpret_cast<const uint4 *>(x);
-            v[2] = *reinterpret_cast<const uint4 *>(dy);
-            if (my.b >= 0) {
-                v[1] = *reinterpret_cast<const uint4 *>(x + my.apart());
-                v[3] = *reinterpret_cast<const uint4 *>(dy + my.apart());
-            }
-        }
+        const bool in = my.a >= 0 && tok < n && h < heads, two = in && my.b >= 0;
+        copy16(slot, in ? x : t.x, in);
+        copy16(slot + kNormThreads * 16, two ? x + my.apart() : t.x, two);
+        copy16(slot + 2 * kNormThreads * 16, in ? dy : t.x, in);
+        copy16(slot + 3 * kNormThreads * 16, two ? dy + my.apart() : t.x, two);
+        asm volatile("cp.async.commit_group;" ::: "memory");
         x += x_step;
         dy += dy_step;
         h += my.wide;
@@ -361,10 +392,7 @@ struct Ahead {
         tok += my.deep;
         x += x_wrap;
         dy += dy_wrap;
-        if (tok - my.t0 >= n && n > 0) {  // the same for all slots
-            tile += t.blocks;
-            start(p, t, my, first);
-        }
+        if (tok - my.t0 >= n && n > 0) start(p, t, my, first);  // the same for all slots
     }
 };
 
@@ -385,12 +413,21 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_rows_kernel(const _
     const int w = t.weight_h == 0 ? 0 : my.h0;
     uint64_t da[4] = {0, 0, 0, 0}, db[4] = {0, 0, 0, 0};
     const long long out_step = my.wide * t.out_h;
-    Ahead<L, HALF> ahead(t, my, block);
+    Ahead<L, HALF> ahead(p, t, my, block);
     ahead.start(p, t, my, first);
-    uint4 v[4];  // the next row and its gradient are under way while one is worked on
-    ahead.load(p, t, my, first, heads, v);
-    for (int tile = block; tile < p.B * t.tiles; tile += t.blocks) {
-        const int b = tile / t.tiles, s0 = tile % t.tiles * t.tile, n = min(t.tile, p.S - s0);
+    // rows that follow are under way while one is worked on; a lane reads its own copies alone
+    extern __shared__ __align__(16) uint8_t ring[];
+    const uint32_t ring0 = smem_u32(ring) + 16 * threadIdx.x, ring1 = ring0 + kGradStages * kGradStage;
+    uint32_t slot = ring0, next = ring0;
+    auto turn_slot = [&](uint32_t &at) {
+        at += kGradStage;
+        if (at == ring1) at = ring0;
+    };
+#pragma unroll
+    for (int k = 0; k < kGradStages - 1; ++k, turn_slot(next)) ahead.load(p, t, my, first, heads, next);
+    Span span(p, t, block);
+    int b, s0;
+    while (const int n = span.next(p, t, b, s0)) {
         uint16_t *dst = my.at(t.out + b * t.out_b + (s0 + my.t0) * t.out_s + (first + my.h0) * t.out_h);
         __syncthreads();  // the last tile's sines are done with
         sh.t.template turn<HALF>(p, t, b, s0, n);
@@ -400,9 +437,12 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_rows_kernel(const _
             for (int h = my.h0, j = 0; j < my.per_token; ++j, h += my.wide, to += out_step) {
                 const bool real = tok < n && h < heads;
                 uint64_t A[4], B[4], G[4], H[4];
-                unpack<HALF>(v[0], v[1], A, B);
-                unpack<HALF>(v[2], v[3], G, H);
-                ahead.load(p, t, my, first, heads, v);
+                asm volatile("cp.async.wait_group %0;" ::"n"(kGradStages - 2) : "memory");
+                unpack<HALF>(shared16(slot), shared16(slot + kNormThreads * 16), A, B);
+                unpack<HALF>(shared16(slot + 2 * kNormThreads * 16), shared16(slot + 3 * kNormThreads * 16), G, H);
+                ahead.load(p, t, my, first, heads, next);  // over the row before
+                turn_slot(slot);
+                turn_slot(next);
                 uint64_t c[4], s[4], ns[4], s2 = 0, s3 = 0, d2 = 0, d3 = 0;  // +0
                 Shared<L>::get(sh.t.c[min(tok, n - 1)], my.u, c);
                 Shared<L>::get(sh.t.s[min(tok, n - 1)], my.u, s);
@@ -444,6 +484,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_rows_kernel(const _
             }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!t.dweight) return;
     __syncthreads();
 #pragma unroll
@@ -662,9 +703,13 @@ template <int L>
 cudaError_t launch_rows(const NormRopeParams &p, bool half, bool grad, cudaStream_t stream)
 {
     const dim3 grid(grid_of(p));
-    if (grad)
-        return half ? launch_grid(norm_grad_rows_kernel<L, true>, grid, 0, stream, p)
-                    : launch_grid(norm_grad_rows_kernel<L, false>, grid, 0, stream, p);
+    if (grad) {
+        constexpr int ring = kGradStages * kGradStage;
+        static KernelSetup setup[2];
+        const auto kernel = half ? norm_grad_rows_kernel<L, true> : norm_grad_rows_kernel<L, false>;
+        const cudaError_t err = setup[half](kernel, ring);
+        return err != cudaSuccess ? err : launch_grid(kernel, grid, ring, stream, p);
+    }
     return half ? launch_grid(norm_rows_kernel<L, true>, grid, 0, stream, p)
                 : launch_grid(norm_rows_kernel<L, false>, grid, 0, stream, p);
 }
