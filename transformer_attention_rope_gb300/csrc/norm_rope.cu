@@ -16,14 +16,17 @@
 // two at a time, as packed fp32.
 //
 // dw: a thread adds up its 16 columns over all rows that it meets, a block its threads' sums,
-// and a second kernel the blocks' sums, in 64 bits: a fixed order, so equal inputs give equal
+// and a second kernel the blocks' sums, to 64 bits: a fixed order, so equal inputs give equal
 // bits.  With weights for each head a thread has one head.
 //
-// Measured: 8191 tokens of 128 + 8 heads of 128, half layout (570 MB): 101 us, 5.6 TB/s (195 with a
-// chunk a lane and the pairs' other halves exchanged); one token of 32 + 8 heads with its key and
-// value appended: 3.0 us; the gradient of 16384 tokens of 32 + 8 heads (503 MB): 113 us, 4.5 TB/s, where
-// 128 registers leave 16 warps an SM (with 24 and spills 146, with half as many entries a lane and
-// 24 warps 123); of 1026 tokens with weights for each head: 19 us in two kernels.
+// Measured: 8191 tokens of 128 + 8 heads of 128, half layout (570 MB): 91.5 us, 6.2 TB/s (97 with two
+// rows of a lane in flight and 24 warps an SM in place of four and 20, 109 to 124 with rows by
+// asynchronous copies as the gradient has them, 195 with a chunk a lane and the pairs' other halves
+// exchanged); one token of 32 + 8 heads with its key and value appended: 3.0 us; the gradient of 16384
+// tokens of 32 + 8 heads (503 MB): 96 us, 5.2 TB/s, with two rows in shared memory on their way (111 with
+// one in registers, 125 with three copied beside three blocks an SM), where the issue of some 320
+// instructions for a row of four warps a scheduler is behind it; of 1026 tokens with weights for each
+// head: 19 us, 5 of them the second kernel.
 #include "cache_attn.cuh"
 #include "device_common.cuh"
 #include "norm_rope.h"
@@ -32,9 +35,8 @@
 namespace apex {
 namespace {
 
-constexpr int kBatch = 2;  // rows of a lane whose loads are in flight together
-constexpr int kGradStages = 4;  // a lane's rows in shared memory: one worked on, the others on their way
-constexpr int kGradStage = 4 * kNormThreads * 16;
+constexpr int kStages = 3;  // a lane's rows of a gradient in shared memory: one worked on, the others on their way
+constexpr int kPart = 16 * kNormThreads;  // a chunk of each lane
 
 __device__ __forceinline__ long long out_row(const NormRopeParams &p, const NormTensor &t, int b, int s)
 {
@@ -229,7 +231,7 @@ struct Shared {
 };
 
 template <int L, bool HALF>
-__global__ void __launch_bounds__(kNormThreads, 3) norm_rows_kernel(const __grid_constant__ NormRopeParams p)
+__global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_rows_kernel(const __grid_constant__ NormRopeParams p)
 {
     // launched as a programmatic dependent: inputs may be the previous kernel's output
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -269,10 +271,10 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_rows_kernel(const __grid
                     nsb[e] = f2_mul(wb[e], ns[e]);
                 }
             };
-            for (int h = my.h0, j = 0; j < my.per_token; j += kBatch) {
-                uint4 x[kBatch], y[kBatch];
+            for (int h = my.h0, j = 0; j < my.per_token; j += kNormBatch) {
+                uint4 x[kNormBatch], y[kNormBatch];
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k, from += x_step) {
+                for (int k = 0; k < kNormBatch; ++k, from += x_step) {
                     x[k] = y[k] = make_uint4(0, 0, 0, 0);
                     if (in && h + k * my.wide < heads) {
                         x[k] = *reinterpret_cast<const uint4 *>(from);
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_rows_kernel(const __grid
                 }
                 if (t.norm && j == 0 && shared) factors(0);
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k, h += my.wide, to += out_step) {
+                for (int k = 0; k < kNormBatch; ++k, h += my.wide, to += out_step) {
                     if (j + k >= my.per_token) break;
                     if (t.norm) {
                         if (!shared) factors(min(h, heads - 1));
@@ -337,8 +339,6 @@ struct Span {
     }
 };
 
-// Where the next row to load of a lane's slot is: over the heads of a token, the tokens of a tile
-// and the tiles of a block.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -351,18 +351,30 @@ __device__ __forceinline__ uint4 shared16(uint32_t at)
     return v;
 }
 
+// A lane's rows, one after another over the heads of a token, the tokens of a tile and the tiles of
+// a block, and their gradients, copied to its own ring: those that follow are under way while one is
+// worked on.
 template <int L, bool HALF>
-struct Ahead {
+struct Feed {
+    static constexpr int kStage = 4 * kPart, kBytes = kStages * kStage;
     const uint16_t *x, *dy;
     long long x_step, dy_step, x_wrap, dy_wrap;  // to the next head, and from the last to the next token's first
     Span span;
-    int n, tok, j, h;
-    __device__ __forceinline__ Ahead(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int block)
+    int n, tok, j, h;  // the row to copy next
+    uint32_t first, slot, next;
+    __device__ __forceinline__ Feed(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int block,
+                                    uint32_t ring)
         : x_step(my.wide * t.x_h), dy_step(my.wide * t.dy_h), x_wrap(my.deep * t.x_s - my.per_token * x_step),
-          dy_wrap(my.deep * t.dy_s - my.per_token * dy_step), span(p, t, block)
+          dy_wrap(my.deep * t.dy_s - my.per_token * dy_step), span(p, t, block), first(ring + 16 * threadIdx.x),
+          slot(first), next(first)
     {
     }
-    __device__ __forceinline__ void start(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int first)
+    static __device__ __forceinline__ void turn(uint32_t &at, uint32_t first)
+    {
+        at += kStage;
+        if (at == first + kBytes) at = first;
+    }
+    __device__ __forceinline__ void tile(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int head0)
     {
         int b, s0;
         n = span.next(p, t, b, s0);
@@ -370,19 +382,20 @@ struct Ahead {
         h = my.h0;
         tok = my.t0;
         if (n == 0) return;
-        x = my.at(t.x + b * t.x_b + (s0 + tok) * t.x_s + (first + h) * t.x_h);
-        dy = my.at(t.dy + b * t.dy_b + (s0 + tok) * t.dy_s + (first + h) * t.dy_h);
+        x = my.at(t.x + b * t.x_b + (s0 + tok) * t.x_s + (head0 + h) * t.x_h);
+        dy = my.at(t.dy + b * t.dy_b + (s0 + tok) * t.dy_s + (head0 + h) * t.dy_h);
     }
-    // the row and its gradient to a stage of the ring, zeros where there is none
-    __device__ __forceinline__ void load(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int first,
-                                         int heads, uint32_t slot)
+    // zeros where there is no row
+    __device__ __forceinline__ void load(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int head0,
+                                         int heads)
     {
         const bool in = my.a >= 0 && tok < n && h < heads, two = in && my.b >= 0;
-        copy16(slot, in ? x : t.x, in);
-        copy16(slot + kNormThreads * 16, two ? x + my.apart() : t.x, two);
-        copy16(slot + 2 * kNormThreads * 16, in ? dy : t.x, in);
-        copy16(slot + 3 * kNormThreads * 16, two ? dy + my.apart() : t.x, two);
+        copy16(next, in ? x : t.x, in);
+        copy16(next + kPart, two ? x + my.apart() : t.x, two);
+        copy16(next + 2 * kPart, in ? dy : t.x, in);
+        copy16(next + 3 * kPart, two ? dy + my.apart() : t.x, two);
         asm volatile("cp.async.commit_group;" ::: "memory");
+        turn(next, first);
         x += x_step;
         dy += dy_step;
         h += my.wide;
@@ -392,12 +405,29 @@ struct Ahead {
         tok += my.deep;
         x += x_wrap;
         dy += dy_wrap;
-        if (tok - my.t0 >= n && n > 0) start(p, t, my, first);  // the same for all slots
+        if (tok - my.t0 >= n && n > 0) tile(p, t, my, head0);  // the same for all slots
+    }
+    __device__ __forceinline__ void start(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int head0,
+                                          int heads)
+    {
+        tile(p, t, my, head0);
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) load(p, t, my, head0, heads);
+    }
+    // the next row, in the order of the copies; the one before it is overwritten
+    __device__ __forceinline__ void take(const NormRopeParams &p, const NormTensor &t, const Lane<L, HALF> &my, int head0,
+                                         int heads, uint4 (&v)[4])
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = shared16(slot + i * kPart);
+        turn(slot, first);
+        load(p, t, my, head0, heads);
     }
 };
 
 template <int L, bool HALF>
-__global__ void __launch_bounds__(kNormThreads, 2) norm_grad_rows_kernel(const __grid_constant__ NormRopeParams p)
+__global__ void __launch_bounds__(kNormThreads, kNormGradCtas) norm_grad_rows_kernel(const __grid_constant__ NormRopeParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ union {
@@ -408,23 +438,14 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_rows_kernel(const _
     const NormTensor t = p.t[tensor_of(p, group, block)];
     const int first = group * t.per, heads = min(t.per, t.n_heads - first);
     const Lane<L, HALF> my(p, t, heads);
+    uint64_t da[4] = {0, 0, 0, 0}, db[4] = {0, 0, 0, 0};
+    const long long out_step = my.wide * t.out_h;
+    extern __shared__ __align__(16) uint8_t ring[];
+    Feed<L, HALF> feed(p, t, my, block, smem_u32(ring));
+    feed.start(p, t, my, first, heads);
     // with weights for each head a slot has one head
     sh.t.template weights<HALF>(p, t, first, heads);
     const int w = t.weight_h == 0 ? 0 : my.h0;
-    uint64_t da[4] = {0, 0, 0, 0}, db[4] = {0, 0, 0, 0};
-    const long long out_step = my.wide * t.out_h;
-    Ahead<L, HALF> ahead(p, t, my, block);
-    ahead.start(p, t, my, first);
-    // rows that follow are under way while one is worked on; a lane reads its own copies alone
-    extern __shared__ __align__(16) uint8_t ring[];
-    const uint32_t ring0 = smem_u32(ring) + 16 * threadIdx.x, ring1 = ring0 + kGradStages * kGradStage;
-    uint32_t slot = ring0, next = ring0;
-    auto turn_slot = [&](uint32_t &at) {
-        at += kGradStage;
-        if (at == ring1) at = ring0;
-    };
-#pragma unroll
-    for (int k = 0; k < kGradStages - 1; ++k, turn_slot(next)) ahead.load(p, t, my, first, heads, next);
     Span span(p, t, block);
     int b, s0;
     while (const int n = span.next(p, t, b, s0)) {
@@ -437,12 +458,10 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_rows_kernel(const _
             for (int h = my.h0, j = 0; j < my.per_token; ++j, h += my.wide, to += out_step) {
                 const bool real = tok < n && h < heads;
                 uint64_t A[4], B[4], G[4], H[4];
-                asm volatile("cp.async.wait_group %0;" ::"n"(kGradStages - 2) : "memory");
-                unpack<HALF>(shared16(slot), shared16(slot + kNormThreads * 16), A, B);
-                unpack<HALF>(shared16(slot + 2 * kNormThreads * 16), shared16(slot + 3 * kNormThreads * 16), G, H);
-                ahead.load(p, t, my, first, heads, next);  // over the row before
-                turn_slot(slot);
-                turn_slot(next);
+                uint4 v[4];
+                feed.take(p, t, my, first, heads, v);
+                unpack<HALF>(v[0], v[1], A, B);
+                unpack<HALF>(v[2], v[3], G, H);
                 uint64_t c[4], s[4], ns[4], s2 = 0, s3 = 0, d2 = 0, d3 = 0;  // +0
                 Shared<L>::get(sh.t.c[min(tok, n - 1)], my.u, c);
                 Shared<L>::get(sh.t.s[min(tok, n - 1)], my.u, s);
@@ -517,7 +536,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_rows_kernel(const _
 }
 
 // Rows whose parts, strides or alignment do not fit 16-byte chunks, or that are wider than
-// 256 entries: a warp has a row, and its lanes go over the pairs and the other entries, 2 bytes
+// 512 entries: a warp has a row, and its lanes go over the pairs and the other entries, 2 bytes
 // at a time.  Unit u of a row is its pair u, or past the pairs a copied entry.
 struct Unit {
     int a, b;  // entries; b = -1: one that does not turn
@@ -648,36 +667,45 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_pairs_kernel(const __g
 }
 
 // Weights' gradients: a block adds up 8 columns of the partial sums of a tensor (of a head of
-// it, with weights for each head); blocks in the grid's z, heads in its y.
-__global__ void __launch_bounds__(kNormThreads) norm_weights_kernel(const __grid_constant__ NormRopeParams p)
+// it, with weights for each head); blocks in the grid's z, heads in its y.  A thread's sum is held as
+// two fp32, what rounding took from the first in the second: 64-bit additions are slow here, and come
+// last.
+__global__ void __launch_bounds__(kNormSumThreads) norm_weights_kernel(const __grid_constant__ NormRopeParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ double sums[32][8];
+    __shared__ double sums[kNormSumThreads / 32][8];
     const NormTensor &t = p.t[blockIdx.z];
-    const int e = 8 * blockIdx.x + threadIdx.x % 8, r0 = threadIdx.x / 8;
+    const int lane = threadIdx.x & 31, e = 8 * blockIdx.x + lane % 8, r0 = threadIdx.x / 8;
     const bool heads = t.weight_h != 0;
     if (!t.dweight || (int)blockIdx.y >= (heads ? t.n_heads : 1)) return;  // whole blocks
     const int rows = heads ? t.blocks : t.n_groups * t.blocks;
     const float *from = t.partial + (heads ? (size_t)blockIdx.y * t.blocks * t.d_row : 0) + e;
-    double x = 0.;
+    float hi = 0.f, lo = 0.f;
     if (e < t.d_row) {
-#pragma unroll 4
-        for (int r = r0; r < rows; r += 32) x += from[(size_t)r * t.d_row];
+#pragma unroll 8
+        for (int r = r0; r < rows; r += kNormSumThreads / 8) {
+            const float x = from[(size_t)r * t.d_row], sum = hi + x, back = sum - hi;
+            lo += (hi - (sum - back)) + (x - back);
+            hi = sum;
+        }
     }
-    sums[r0][threadIdx.x % 8] = x;
+    double x = (double)hi + lo;
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    x += __shfl_xor_sync(0xffffffffu, x, 16);
+    if (lane < 8) sums[threadIdx.x / 32][lane] = x;
     __syncthreads();
-    if (r0 == 0 && e < t.d_row) {
-        for (int r = 1; r < 32; ++r) x += sums[r][threadIdx.x];
+    if (threadIdx.x < 8 && e < t.d_row) {
+        for (int r = 1; r < kNormSumThreads / 32; ++r) x += sums[r][lane];
         t.dweight[(heads ? (size_t)blockIdx.y * t.d_row : 0) + e] = (float)x;
     }
 }
 
 template <typename K, typename... A>
-cudaError_t launch_grid(K kernel, dim3 grid, int smem, cudaStream_t stream, const A &...args)
+cudaError_t launch_grid(K kernel, dim3 grid, int threads, int smem, cudaStream_t stream, const A &...args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kNormThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -703,15 +731,14 @@ template <int L>
 cudaError_t launch_rows(const NormRopeParams &p, bool half, bool grad, cudaStream_t stream)
 {
     const dim3 grid(grid_of(p));
-    if (grad) {
-        constexpr int ring = kGradStages * kGradStage;
-        static KernelSetup setup[2];
-        const auto kernel = half ? norm_grad_rows_kernel<L, true> : norm_grad_rows_kernel<L, false>;
-        const cudaError_t err = setup[half](kernel, ring);
-        return err != cudaSuccess ? err : launch_grid(kernel, grid, ring, stream, p);
-    }
-    return half ? launch_grid(norm_rows_kernel<L, true>, grid, 0, stream, p)
-                : launch_grid(norm_rows_kernel<L, false>, grid, 0, stream, p);
+    if (!grad)
+        return half ? launch_grid(norm_rows_kernel<L, true>, grid, kNormThreads, 0, stream, p)
+                    : launch_grid(norm_rows_kernel<L, false>, grid, kNormThreads, 0, stream, p);
+    constexpr int ring = Feed<L, false>::kBytes;
+    static KernelSetup setup[2];
+    const auto kernel = half ? norm_grad_rows_kernel<L, true> : norm_grad_rows_kernel<L, false>;
+    const cudaError_t err = setup[half](kernel, ring);
+    return err != cudaSuccess ? err : launch_grid(kernel, grid, kNormThreads, ring, stream, p);
 }
 
 cudaError_t launch_lanes(const NormRopeParams &p, bool half, bool grad, int lanes, cudaStream_t stream)
@@ -727,7 +754,7 @@ cudaError_t launch_lanes(const NormRopeParams &p, bool half, bool grad, int lane
 cudaError_t launch_norm_rope(const NormRopeParams &p, bool half, int lanes, cudaStream_t stream)
 {
     return lanes ? launch_lanes(p, half, false, lanes, stream)
-                 : launch_grid(norm_pairs_kernel, dim3(grid_of(p)), 0, stream, p, half);
+                 : launch_grid(norm_pairs_kernel, dim3(grid_of(p)), kNormThreads, 0, stream, p, half);
 }
 
 cudaError_t launch_norm_rope_grad(const NormRopeParams &p, bool half, int lanes, cudaStream_t stream)
@@ -741,9 +768,10 @@ cudaError_t launch_norm_rope_grad(const NormRopeParams &p, bool half, int lanes,
     }
     const cudaError_t err =
         lanes ? launch_lanes(p, half, true, lanes, stream)
-              : launch_grid(norm_grad_pairs_kernel, dim3(grid_of(p)), kNormThreads / 32 * width * (int)sizeof(float), stream, p, half);
+              : launch_grid(norm_grad_pairs_kernel, dim3(grid_of(p)), kNormThreads,
+                            kNormThreads / 32 * width * (int)sizeof(float), stream, p, half);
     if (err != cudaSuccess || !weights) return err;
-    return launch_grid(norm_weights_kernel, dim3((width + 7) / 8, heads, p.n_tensors), 0, stream, p);
+    return launch_grid(norm_weights_kernel, dim3((width + 7) / 8, heads, p.n_tensors), kNormSumThreads, 0, stream, p);
 }
 
 }  // namespace apex

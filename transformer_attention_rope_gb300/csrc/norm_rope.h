@@ -11,10 +11,12 @@
 
 namespace apex {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 128, kNormSumThreads = 256;
+constexpr int kNormCtas = 5, kNormGradCtas = 4;  // of an SM, where rows go 16 bytes at a time
+constexpr int kNormBatch = 4;                    // heads of a token that a lane takes, whose loads are in flight together
 constexpr int kNormFastRow = 512;      // widest row of the kernels that go 16 bytes at a time
 constexpr int kNormHeads = 128;        // heads with weights of their own that a block takes, times lanes of a row
-constexpr int kNormGradBlocks = 512;   // blocks of a gradient at most (but for one of each group),
+constexpr int kNormGradBlocks = 1024;  // blocks of a gradient at most (but for one of each group),
 constexpr int kNormGradHeads = 8;      // and partial sums of weights of each at most
 
 // Rows at x + b * x_b + h * x_h + s * x_s, likewise dy (gradients) and out (the result, or x's gradient).
