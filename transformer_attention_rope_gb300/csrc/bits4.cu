@@ -9,8 +9,9 @@
 // no tie is further from one than this is off (x has 8 significant bits, the scale 4).
 //
 // Bound: HBM, 2.56 bytes an entry either way.  32767 tokens of 8 heads of 128 written and read back (344
-// MB): 68 us, 39 and 28 (84 with 16 bytes of a row at a time, as half sectors go twice); writing is near the
-// issue of its instructions as well.  One token for each of 16 sequences, both ways: 3.5 us.
+// MB): 60 us, 32.5 and 27.6 (67 in blocks of 256 threads with two rows of a thread and more blocks, 84
+// with 16 bytes of a row at a time, as half sectors go twice); writing is near the issue of its
+// instructions as well.  One token for each of 16 sequences, both ways: 3.5 us.
 #include <algorithm>
 
 #include "bits4.cuh"
@@ -20,7 +21,7 @@
 namespace apex {
 namespace {
 
-constexpr int kRows = 2;  // of a thread, in turn
+constexpr int kRows = 4;  // of a thread, whose loads are in flight together
 
 // A block's rows: `per` at a time of head blockIdx.x of tensor blockIdx.z % 2 and sequence
 // blockIdx.z / 2, and of those a grid's width behind.  Blocks of the same tokens run side by side, as
@@ -135,7 +136,7 @@ __device__ __forceinline__ void append_rows(const Bits4Params &p, const Bits4Ten
     }
 }
 
-__global__ void __launch_bounds__(kBits4Threads, 5) append4_kernel(const __grid_constant__ Bits4Params p)
+__global__ void __launch_bounds__(kBits4Threads, 6) append4_kernel(const __grid_constant__ Bits4Params p)
 {
     // launched as a programmatic dependent: inputs may be the previous kernel's output
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -186,7 +187,7 @@ __device__ __forceinline__ void unpack_rows(const Bits4Params &p, const Bits4Ten
     }
 }
 
-__global__ void __launch_bounds__(kBits4Threads, 5) unpack4_kernel(const __grid_constant__ Bits4Params p)
+__global__ void __launch_bounds__(kBits4Threads, 6) unpack4_kernel(const __grid_constant__ Bits4Params p)
 {
     // launched as a programmatic dependent: inputs may be the previous kernel's output
     asm volatile("griddepcontrol.wait;" ::: "memory");

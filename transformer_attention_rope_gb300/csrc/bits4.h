@@ -15,7 +15,7 @@
 
 namespace apex {
 
-constexpr int kBits4Threads = 256;
+constexpr int kBits4Threads = 128;
 constexpr int kBits4Block = 16;    // entries of a scale
 constexpr int kBits4MaxRow = 512;  // widest row that is written and read back
 
