@@ -205,12 +205,12 @@ __device__ __forceinline__ void rope_q_tile(uint8_t *tile, int rt, const float2 
 // One work item: (batch, kv head) unit and a block of 2P query rows.
 struct Item {
     int unit, b, hk, r0, j_lo, n_kt, zq;
-    int sink;  // of the n_kt key tiles, how many are the first ones of the sequence
-    // the j-th key tile
+    int near;  // of the n_kt key tiles, how many are the window's; the others are the first of the sequence
+    // the j-th key tile: the sinks' come last, when the running maximum stands
     template <bool SINK>
     __device__ __forceinline__ int tile(int j) const
     {
-        return SINK && j < sink ? j : j_lo + j;
+        return SINK && j >= near ? j - near : j_lo + j;
     }
 };
 
@@ -232,13 +232,8 @@ __device__ __forceinline__ Item make_item(const PrefillParams &p, int w)
     const int key_lo = (m_first < p.prefix_len || p.window <= 0) ? 0 : max(0, m_first - p.window + 1);
     const int key_hi = (m_first < p.prefix_len) ? max(m_last, p.prefix_len - 1) : m_last;
     it.j_lo = key_lo / 128;
-    it.n_kt = key_hi / 128 - it.j_lo + 1;
-    it.sink = 0;
-    if (SINK) {  // the tiles of the sinks that lie before the window's
-        it.sink = min(it.j_lo, (p.n_sink + 127) / 128);
-        it.j_lo -= it.sink;
-        it.n_kt += it.sink;
-    }
+    it.n_kt = it.near = key_hi / 128 - it.j_lo + 1;
+    if (SINK) it.n_kt += min(it.j_lo, (p.n_sink + 127) / 128);  // the tiles of the sinks that lie before the window's
     it.zq = it.b * p.H_q + it.hk * p.G;
     return it;
 }
@@ -252,7 +247,7 @@ __device__ __forceinline__ int item_index(int k)
 }
 
 // SINK: the first n_sink keys stay visible behind the window; a work item then visits
-// their tiles before the window's.
+// their tiles after the window's.
 template <int D, bool SINK>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -475,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int ch = 0; ch < 4; ++ch)
                     tmem_ld32(s_addr + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * ch]));
                 tmem_wait_ld();
-                if (SINK && j < it.sink)  // before every row's window: the sinks alone, the same for all rows
+                if (SINK && j >= it.near)  // before every row's window: the sinks alone, the same for all rows
                     mask_row128_from(v, p.n_sink - kstart);
                 else if (SINK && !all_full && kstart < p.n_sink)
                     mask_row128_sink(v, lo_c, hi_c, p.n_sink - kstart);

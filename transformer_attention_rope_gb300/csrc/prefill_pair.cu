@@ -267,12 +267,12 @@ __device__ __forceinline__ int q_heads_softmax(int G) { return G - G / 4; }
 // tile T = 2 rank + t of the pair covers rows r0 + T P .. r0 + T P + P - 1.
 struct Item {
     int unit, r0, j_lo, n_kt, zq;
-    int sink;  // of the n_kt key tiles, how many are the first ones of the sequence
-    // the j-th key tile
+    int near;  // of the n_kt key tiles, how many are the window's; the others are the first of the sequence
+    // the j-th key tile: the sinks' come last, when the running maximum stands
     template <bool SINK>
     __device__ __forceinline__ int tile(int j) const
     {
-        return SINK && j < sink ? j : j_lo + j;
+        return SINK && j >= near ? j - near : j_lo + j;
     }
 };
 
@@ -291,13 +291,8 @@ __device__ __forceinline__ Item make_item(const PrefillParams &p, int w)
     const int key_lo = (m_first < p.prefix_len || p.window <= 0) ? 0 : max(0, m_first - p.window + 1);
     const int key_hi = (m_first < p.prefix_len) ? max(m_last, p.prefix_len - 1) : m_last;
     it.j_lo = key_lo / 128;
-    it.n_kt = key_hi / 128 - it.j_lo + 1;
-    it.sink = 0;
-    if (SINK) {  // the tiles of the sinks that lie before the window's
-        it.sink = min(it.j_lo, (p.n_sink + 127) / 128);
-        it.j_lo -= it.sink;
-        it.n_kt += it.sink;
-    }
+    it.n_kt = it.near = key_hi / 128 - it.j_lo + 1;
+    if (SINK) it.n_kt += min(it.j_lo, (p.n_sink + 127) / 128);  // the tiles of the sinks that lie before the window's
     it.zq = b * p.H_q + hk * p.G;
     return it;
 }
@@ -512,13 +507,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (lane == 0) arrive_leader(bar(kBarQReady + t));
                 }
             }
-            if (KROT) kr.load_seed(p.rope.cs, min(128 * it.tile<SINK>(0) + half0 + r0, max_row), c);
+            int row = 128 * it.j_lo + half0 + r0;
+            if (KROT) kr.load_seed(p.rope.cs, min(row, max_row), c);
             for (int j = 0; j < it.n_kt; ++j, ++kc) {
                 const int ks = kc % kKStages;
                 pair_wait(bar(kBarKFull + ks), (kc / kKStages) & 1, p.wait, abort);
                 if (KROT && !p.keys_prerotated) kr.rotate(smem + kKOff + ks * kKTile, rt);
-                if (KROT && j + 1 < it.n_kt)
-                    kr.load_seed(p.rope.cs, min(128 * it.tile<SINK>(j + 1) + half0 + r0, max_row), c);
+                row += 128;
+                if (SINK && j + 1 == it.near) row = half0 + r0;
+                if (KROT && j + 1 < it.n_kt) kr.load_seed(p.rope.cs, min(row, max_row), c);
                 // K(j) ready also means V(j) has landed: the MMA thread waits for
                 // KReady(j) before QK(j), which precedes PV(j)
                 pair_wait(bar(kBarVFull + kc % kVStages), (kc / kVStages) & 1, p.wait, abort);
@@ -583,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int ch = 0; ch < 4; ++ch)
                     tmem_ld32(s_addr + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * ch]));
                 tmem_wait_ld();
-                if (SINK && j < it.sink)  // before every row's window: the sinks alone, the same for all rows
+                if (SINK && j >= it.near)  // before every row's window: the sinks alone, the same for all rows
                     mask_row128_from(v, p.n_sink - kstart);
                 else if (SINK && !all_full && kstart < p.n_sink)
                     mask_row128_sink(v, lo_c, hi_c, p.n_sink - kstart);
