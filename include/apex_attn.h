@@ -212,8 +212,9 @@ apex_status apex_attn_mla_fwd_ws(const void *q, const void *k, const void *v, vo
  * and for everything else apex_attn_fwd_ws (d_r = 0) or apex_attn_mla_fwd_ws (d_r > 0:
  * q and k rows of d_h + d_r entries): layouts, options (a query inside a prefix sees the
  * prefix alone), workspaces, supported sizes and errors.  n_sink >= 0; 0, or no window, is
- * the call without sinks.  A work item visits the key tiles of the sinks and those of its
- * window, whatever lies between.
+ * the call without sinks.  A work item visits the key tiles of its window and those of the
+ * sinks, whatever lies between.  As for the calls without, k and v hold no infinities or NaN, at
+ * masked keys either: a weight of 0 does not hide them.
  */
 apex_status apex_attn_sink_fwd(const void *q, const void *k, const void *v, void *out,
                                int B, int H_q, int H_kv, int S_q, int S_k, int d_h, int d_r, int n_sink,
@@ -226,7 +227,8 @@ size_t apex_attn_sink_fwd_workspace_bytes(int B, int H_q, int H_kv, int S_q, int
 
 /*
  * Decode under the same rule: apex_attn_decode_ex (d_r = 0) or apex_attn_mla_decode (d_r > 0)
- * with the first n_sink keys visible behind opt->window; workspace as for them.
+ * with the first n_sink keys visible behind opt->window; workspace as for them, and caches without
+ * infinities or NaN.
  */
 apex_status apex_attn_sink_decode(const void *q, const void *k_cache, const void *v_cache, void *out,
                                   int B, int H_q, int H_kv, int S_k, int d_h, int d_r, int n_sink,

@@ -299,6 +299,9 @@ int max_stages_for(int S_k) { return (S_k + kDecodeKeysPerStage - 1) / kDecodeKe
 // and about 1 us for its launch (the prefill, a programmatic dependent, sets up
 // during the pass); decoupled-RoPE rows (128 + 64, only the 64-entry rope part
 // turned): about 1.1 ns per visit against 15 ns per tile (1.5 times the bytes).
+// With sinks the pair kernel that rotates plain rows is short of registers: 4.4 to 6.2
+// ns per visit (B4 H_q32 S4096 W1024 at 4096 of 8192 keys: 344 us, 295 and the pass's 21
+// with it).
 // The pass is used when it costs less than the visits it saves.
 struct PrerotatePlan {
     bool use;
@@ -311,6 +314,12 @@ struct PrerotateCost {
 };
 constexpr PrerotateCost kCostPlain{17, 100};
 constexpr PrerotateCost kCostDecoupled{11, 150};
+constexpr PrerotateCost kCostSinks{45, 100};
+
+PrerotateCost prerotate_cost(bool mla, bool pair, int n_sink)
+{
+    return mla ? kCostDecoupled : pair && n_sink > 0 ? kCostSinks : kCostPlain;
+}
 
 PrerotatePlan plan_prerotate(int units, int S_q, int S_k, int q_pos0, int window, int n_sink, int P, int block_rows,
                              PrerotateCost cost)
@@ -563,7 +572,7 @@ apex_status prefill_launch(const void *q, const void *k, const void *v, void *ou
     PrerotatePlan pre{false, 0};
     if (workspace && !opt->keys_prerotated)
         pre = plan_prerotate(B * H_kv, S_q, S_k, q_pos0, window > 0 ? window : 0, n_sink, P,
-                             (pair ? 4 : 2) * rows_per_head, mla ? kCostDecoupled : kCostPlain);
+                             (pair ? 4 : 2) * rows_per_head, prerotate_cost(mla, pair, n_sink));
     PrefillLaunch L;
     memset(&L, 0, sizeof L);
     if (!make_map(&L.tm_q, q, d_qk, S_q, B * H_q, rows_per_head, G) ||
@@ -644,7 +653,7 @@ static size_t prefill_workspace_bytes(int B, int H_q, int H_kv, int S_q, int S_k
     const bool pair = d_r != 0 || use_pair_prefill(d_h, 2);
     const int block_rows = (pair ? 4 : 2) * (128 / (H_q / H_kv));
     const PrerotatePlan pr = plan_prerotate(B * H_kv, S_q, S_k, q_pos0, opt->window > 0 ? opt->window : 0, n_sink,
-                                            P, block_rows, d_r ? kCostDecoupled : kCostPlain);
+                                            P, block_rows, prerotate_cost(d_r != 0, pair, n_sink));
     return pr.use ? (size_t)B * H_kv * (size_t)S_k * (d_h + d_r) * 2 : 0;
 }
 
@@ -774,17 +783,19 @@ apex_status apex_attn_mla_rope_keys(const void *k_in, void *k_out, int n_heads, 
 
 // ----------------------------------------------------------------- windows with sinks
 
-// Sinks that a call has: none without a window, behind which they would stay visible.
-static int sinks_of(const apex_attn_options *opt, int n_sink, int S_k)
+// Sinks that a call has whose last query is at position `last`: none without a window that leaves
+// something behind.
+static int sinks_of(const apex_attn_options *opt, int n_sink, int S_k, long long last)
 {
-    return opt->window > 0 ? std::min(n_sink, S_k) : 0;
+    return opt->window > 0 && last >= opt->window ? std::min(n_sink, S_k) : 0;
 }
 
 size_t apex_attn_sink_fwd_workspace_bytes(int B, int H_q, int H_kv, int S_q, int S_k, int d_h, int d_r, int n_sink,
                                           const apex_attn_options *opt)
 {
     if (!opt || n_sink < 0 || d_r < 0) return 0;
-    return prefill_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, d_r, opt, sinks_of(opt, n_sink, S_k));
+    return prefill_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, d_r, opt,
+                                   sinks_of(opt, n_sink, S_k, (long long)opt->q_pos + S_q - 1));
 }
 
 apex_status apex_attn_sink_fwd(const void *q, const void *k, const void *v, void *out, int B, int H_q, int H_kv,
@@ -803,7 +814,7 @@ apex_status apex_attn_sink_fwd(const void *q, const void *k, const void *v, void
                       workspace_bytes < apex_attn_sink_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, d_r, n_sink, opt)))
         return APEX_ERR_INVALID_ARG;
     return prefill_launch(q, k, v, out, B, H_q, H_kv, S_q, S_k, d_h + d_r, d_h, d_r ? d_r : d_h, opt, f, stream,
-                          workspace, sinks_of(opt, n_sink, S_k));
+                          workspace, sinks_of(opt, n_sink, S_k, (long long)opt->q_pos + S_q - 1));
 }
 
 apex_status apex_attn_sink_decode(const void *q, const void *k_cache, const void *v_cache, void *out, int B, int H_q,
@@ -820,7 +831,7 @@ apex_status apex_attn_sink_decode(const void *q, const void *k_cache, const void
     if (s != APEX_OK) return s;
     if (d_r != 0 && (d_h != 128 || d_r != 64)) return APEX_ERR_UNSUPPORTED;
     return decode_launch(q, k_cache, v_cache, out, B, H_q, H_kv, S_k, d_h + d_r, d_h, d_r ? d_r : d_h, opt, f, workspace,
-                         workspace_bytes, stream, sinks_of(opt, n_sink, S_k));
+                         workspace_bytes, stream, sinks_of(opt, n_sink, S_k, opt->q_pos));
 }
 
 }  // extern "C"
