@@ -248,8 +248,17 @@ apex_status apex_attn_norm_rope(const apex_norm_tensor *q, const apex_norm_tenso
         // 3.5 blocks an SM of the 5 that run at once: 1026 tokens of 32 + 8 heads 6.4 us (8.5 with 2 asked
         // for), 1000 of 128 + 8 10.5 us (14.4 with 4, which makes it a wave and a half)
         cut_rows(plan, 16, false, kNormHeads / plan.lanes, 7 * plan.sm_count / 2);
-        for (int i = 0; i < p.n_tensors; ++i)
-            p.t[i].blocks = (int)std::min<long long>((long long)B * p.t[i].tiles, 1 << 16);
+        // a tile for each block; with weights for each head, which a block fetches first, and tiles for
+        // three waves or more, as many blocks as run at once (8191 tokens of 128 + 8 heads 126 us, 136 with a
+        // tile each; 4096 of 32 + 8, just a wave, 24.5 and 22.2)
+        const long long wave = kNormCtas * plan.sm_count;
+        long long n = 0;
+        for (int i = 0; i < p.n_tensors; ++i) n += (long long)p.t[i].n_groups * B * p.t[i].tiles;
+        for (int i = 0; i < p.n_tensors; ++i) {
+            NormTensor &a = p.t[i];
+            const long long room = a.weight_h && n >= 3 * wave ? wave * a.n_heads / plan.heads / a.n_groups : 1 << 16;
+            a.blocks = (int)std::max(1ll, std::min((long long)B * a.tiles, room));
+        }
     } else {
         // up to 8 heads with four blocks an SM
         const long long bx = ((long long)B * S + plan.slots - 1) / plan.slots;

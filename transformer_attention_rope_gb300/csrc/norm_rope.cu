@@ -254,23 +254,8 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_rows_kernel(cons
             const bool in = my.a >= 0 && tok < n, two = my.b >= 0, out = in && row0 + tok >= 0 && row0 + tok < rows;
             const uint16_t *from = src;
             uint16_t *to = dst;
-            // u = a ca + b nsb, w = a sa + b cb: sines, times weights
+            // u = a ca + b nsb, w = a sa + b cb: sines, times the weights that all heads share
             uint64_t ca[4], sa[4], cb[4], nsb[4];
-            auto factors = [&](int h) {
-                uint64_t wa[4], wb[4], c[4], s[4], ns[4];
-                Shared<L>::get(sh.c[min(tok, n - 1)], my.u, c);
-                Shared<L>::get(sh.s[min(tok, n - 1)], my.u, s);
-                Shared<L>::get(sh.ns[min(tok, n - 1)], my.u, ns);
-                Shared<L>::get(sh.wa[h], my.u, wa);
-                Shared<L>::get(sh.wb[h], my.u, wb);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    ca[e] = f2_mul(wa[e], c[e]);
-                    sa[e] = f2_mul(wa[e], s[e]);
-                    cb[e] = f2_mul(wb[e], c[e]);
-                    nsb[e] = f2_mul(wb[e], ns[e]);
-                }
-            };
             for (int h = my.h0, j = 0; j < my.per_token; j += kNormBatch) {
                 uint4 x[kNormBatch], y[kNormBatch];
 #pragma unroll
@@ -287,12 +272,28 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_rows_kernel(cons
                     __syncthreads();
                     made = true;
                 }
-                if (t.norm && j == 0 && shared) factors(0);
+                if (t.norm && j == 0) {
+                    Shared<L>::get(sh.c[min(tok, n - 1)], my.u, ca);
+                    Shared<L>::get(sh.s[min(tok, n - 1)], my.u, sa);
+                    Shared<L>::get(sh.c[min(tok, n - 1)], my.u, cb);
+                    Shared<L>::get(sh.ns[min(tok, n - 1)], my.u, nsb);
+                    if (shared) {
+                        uint64_t wa[4], wb[4];
+                        Shared<L>::get(sh.wa[0], my.u, wa);
+                        Shared<L>::get(sh.wb[0], my.u, wb);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            ca[e] = f2_mul(wa[e], ca[e]);
+                            sa[e] = f2_mul(wa[e], sa[e]);
+                            cb[e] = f2_mul(wb[e], cb[e]);
+                            nsb[e] = f2_mul(wb[e], nsb[e]);
+                        }
+                    }
+                }
 #pragma unroll
                 for (int k = 0; k < kNormBatch; ++k, h += my.wide, to += out_step) {
                     if (j + k >= my.per_token) break;
                     if (t.norm) {
-                        if (!shared) factors(min(h, heads - 1));
                         uint64_t A[4], B[4];
                         unpack<HALF>(x[k], y[k], A, B);
                         uint64_t s2 = 0, s3 = 0;  // +0
@@ -303,6 +304,16 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_rows_kernel(cons
                         }
                         const float rs = rsqrtf(fmaf(sum_lanes<L>(sum2(f2_add(s2, s3))), t.inv_d, p.eps));
                         const uint64_t rs2 = f2_pack(rs, rs);
+                        if (!shared) {  // weights of the head's own
+                            uint64_t wa[4], wb[4];
+                            Shared<L>::get(sh.wa[min(h, heads - 1)], my.u, wa);
+                            Shared<L>::get(sh.wb[min(h, heads - 1)], my.u, wb);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                A[e] = f2_mul(A[e], wa[e]);
+                                B[e] = f2_mul(B[e], wb[e]);
+                            }
+                        }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const uint64_t u = f2_fma(B[e], nsb[e], f2_mul(A[e], ca[e]));
