@@ -489,3 +489,44 @@ def test_conveniences_refuse_what_does_not_fit():
         apex.norm_rope(q, positions=pos, eps=-1.0)
     with pytest.raises(apex.ApexError):
         apex.norm_rope_grad(q, q, positions=pos, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
+
+
+# ------------------------------------------------------------------------------------------------- many tokens
+@pytest.mark.gpu
+@pytest.mark.parametrize("half,each", [(True, True), (False, True), (True, False)])
+def test_many_tokens_are_their_parts(half, each):
+    """Blocks that go over several tiles, over the ends of sequences: rows as those of a call over a part of
+    the tokens, bit for bit, and sums of weights as those of the parts."""
+    dev = _gpu()
+    g = _gen(dev, 31)
+    B, S, H, d, part = 3, 6301, 16, 128, 997
+    q, k = _normal(g, dev, B, S, H, d).transpose(1, 2), _normal(g, dev, B, S, H, d).transpose(1, 2)
+    dq, dk = _normal(g, dev, B, H, S, d), _normal(g, dev, B, H, S, d)
+    w = [1 + 0.1 * torch.randn(*((H, d) if each else (d,)), generator=g, device=dev) for _ in range(2)]
+    pos = torch.randint(0, 1 << 20, (B, S), generator=g, device=dev, dtype=torch.int32)
+    how = dict(q_weight=w[0], k_weight=w[1], layout="half" if half else "interleaved")
+    whole = apex.norm_rope(q, k, positions=pos, **how)
+    gq, gk, gqw, gkw = apex.norm_rope_grad(dq, q, dk, k, positions=pos, **how)
+    sums = [torch.zeros_like(x, dtype=torch.float64) for x in (gqw, gkw)]
+    sizes = [torch.zeros_like(x) for x in sums]
+    for lo in range(0, S, part):
+        at = slice(lo, lo + part)
+        p = pos[:, at].contiguous()
+        a = [x[:, :, at] for x in (q, k, dq, dk)]
+        rows = apex.norm_rope(a[0], a[1], positions=p, **how)
+        assert torch.equal(rows[0], whole[0][:, :, at]) and torch.equal(rows[1], whole[1][:, :, at])
+        grads = apex.norm_rope_grad(a[2], a[0], a[3], a[1], positions=p, **how)
+        assert torch.equal(grads[0], gq[:, :, at]) and torch.equal(grads[1], gk[:, :, at])
+        for i in range(2):
+            sums[i] += grads[2 + i].double()
+            # magnitudes of the terms: a turned gradient's entry is at most its pair's, a normed one at most sqrt(d)
+            x = a[i].float()
+            x = x * torch.rsqrt((x * x).mean(-1, keepdim=True))
+            y = a[2 + i].float()
+            far = (y.unflatten(-1, (2, -1)) if half else y.unflatten(-1, (-1, 2))).norm(dim=-2 if half else -1)
+            far = torch.cat([far, far], -1) if half else far.repeat_interleave(2, -1)
+            sizes[i] += (far * x.abs()).double().sum((0, 2) if each else (0, 1, 2))
+    # both ways sums of the same fp32 terms: threads' runs of at most n / 8 + 32 terms, as above, twice
+    n = B * S * (1 if each else H)
+    for got, ref, size in zip((gqw, gkw), sums, sizes):
+        assert ((got.double() - ref).abs() <= 2 * (n / 8 + 32) * 2.0 ** -24 * size).all()
