@@ -422,3 +422,36 @@ def test_on_another_stream(d, d_r):
         _close(out, ref, tol)
         assert ((one.double() - ref[:, :, -1:]).abs() <= tol[:, :, -1:]).all()
         del junk
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,d_r,S", [(128, 0, 2100), (128, 64, 2100), (128, 64, 6000)])
+def test_a_workspace_of_the_callers(d, d_r, S):
+    """Keys rotated once into a caller's workspace of the bytes that are asked for, in a captured call."""
+    dev = _gpu()
+    B, Hq, Hkv, window, sinks = 1, 32, 2, 700, 4
+    q, k, v = _inputs(dev, 14, B, Hq, Hkv, S, S, d, d_r)
+    if d_r:
+        need = apex.mla_fwd_workspace_bytes(B, Hq, Hkv, S, S, d, d_r, window=window, n_sink=sinks)
+        call = lambda ws: apex.mla_fwd(q, k, v, d_r, window=window, n_sink=sinks, workspace=ws)  # noqa: E731
+    else:
+        need = apex.fwd_workspace_bytes(B, Hq, Hkv, S, S, d, window=window, n_sink=sinks)
+        call = lambda ws: apex.fwd(q, k, v, window=window, n_sink=sinks, workspace=ws)  # noqa: E731
+    # short prompts of decoupled rows are cheaper without the pass
+    assert need == (0 if d_r and S < 3000 else B * Hkv * S * (d + d_r) * 2)
+    assert apex.fwd_workspace_bytes(B, Hq, Hkv, S, S, d, window=0, n_sink=sinks) == \
+        apex.fwd_workspace_bytes(B, Hq, Hkv, S, S, d)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=dev) if need else False
+    ref, tol = _ref(q, k, v, 0, window, sinks, d_r)
+    _close(call(ws), ref, tol)
+    if need:
+        with pytest.raises(apex.ApexError):
+            call(ws[:-16])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(ws)
+    k.normal_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, call(None))

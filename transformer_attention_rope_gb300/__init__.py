@@ -495,10 +495,14 @@ def _sink_shapes(q, k, v, d_r):
 
 def fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, *, window: int = 0, q_pos0: int = 0,
                         rope_base: float = 10000.0, yarn_scale: float = 1.0, yarn_beta_fast: float = 32.0,
-                        yarn_beta_slow: float = 1.0, prefix_len: int = 0, keys_prerotated: bool = False) -> int:
+                        yarn_beta_slow: float = 1.0, prefix_len: int = 0, keys_prerotated: bool = False,
+                        n_sink: int = 0) -> int:
     """Workspace bytes a prefill with these arguments uses (0: none; see apex_attn_fwd_workspace_bytes)."""
     opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                    keys_prerotated)
+    n_sink = _sinks(n_sink, window)
+    if n_sink:
+        return int(apex_attn_sink_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, 0, n_sink, opt))
     return int(apex_attn_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, opt))
 
 
@@ -555,11 +559,15 @@ def fwd(q, k, v, *, window: int = 0, q_pos0: int = 0, rope_base: float = 10000.0
 
 def mla_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, d_r, *, window: int = 0, q_pos0: int = 0,
                             rope_base: float = 10000.0, yarn_scale: float = 1.0, yarn_beta_fast: float = 32.0,
-                            yarn_beta_slow: float = 1.0, prefix_len: int = 0, keys_prerotated: bool = False) -> int:
+                            yarn_beta_slow: float = 1.0, prefix_len: int = 0, keys_prerotated: bool = False,
+                            n_sink: int = 0) -> int:
     """Workspace bytes a decoupled-RoPE prefill with these arguments uses (0: none; see
     apex_attn_mla_fwd_workspace_bytes)."""
     opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                    keys_prerotated)
+    n_sink = _sinks(n_sink, window)
+    if n_sink:
+        return int(apex_attn_sink_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, int(d_r), n_sink, opt))
     return int(apex_attn_mla_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, int(d_r), opt))
 
 
