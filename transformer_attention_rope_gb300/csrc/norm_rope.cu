@@ -83,7 +83,9 @@ __device__ __forceinline__ int tensor_of(const NormRopeParams &p, int &group, in
 }
 
 // The two chunks of 8 entries that lane u of a row holds (-1: none).  Half layout: those whose
-// entries pair up, then the others two by two; interleaved: neighbours.
+// entries pair up; of the others, and of interleaved rows all, one of each half, so that
+// neighbouring lanes' accesses are neighbours (side by side in a lane they went as half sectors: the
+// gradient of 16384 tokens of 64 + 8 heads, 64 of 128 entries turned, interleaved, 158 us and 245).
 template <bool HALF>
 __device__ __forceinline__ void chunks_of(const NormRopeParams &p, int d_row, bool turns, int u, int &a, int &b)
 {
@@ -93,14 +95,15 @@ __device__ __forceinline__ void chunks_of(const NormRopeParams &p, int d_row, bo
         b = a + np;
         return;
     }
-    a = 2 * (u - np);
-    b = a + 1;
+    const int rest = n - nrot, lanes = (rest + 1) >> 1;
+    a = u - np;
+    b = a + lanes;
+    if (a >= lanes) a = -1;
+    if (b >= rest) b = -1;
     if (nrot > 0) {  // past the turned part
         if (a >= c0) a += nrot;
         if (b >= c0) b += nrot;
     }
-    if (a >= n) a = -1;
-    if (b >= n) b = -1;
 }
 
 // Two chunks as pairs of fp32: A the first entries of the lane's pairs, B the second ones.
