@@ -290,7 +290,8 @@ apex_status apex_attn_norm_rope_grad(const apex_norm_tensor *q, const apex_norm_
     const apex_status s = make_plan(t, true, B, S, positions, pos_stride, nullptr, 0, opt, eps, &plan);
     if (s != APEX_OK) return s;
     NormRopeParams &p = plan.p;
-    const int room = std::min(kNormGradBlocks, kNormGradCtas * plan.sm_count);  // as many blocks as run at once
+    // as many blocks as run at once (2 bytes at a time: as there may be)
+    const int room = std::min(kNormGradBlocks, (plan.lanes ? kNormGradCtas : 16) * plan.sm_count);
     if (plan.lanes) {
         cut_rows(plan, 8, true, std::min({kNormGradHeads, plan.slots, kNormHeads / plan.lanes}), room);
     } else {

@@ -26,7 +26,7 @@
 // tokens of 32 + 8 heads (503 MB): 96 us, 5.2 TB/s, with two rows in shared memory on their way (111 with
 // one in registers, 125 with three copied beside three blocks an SM), where the issue of some 320
 // instructions for a row of four warps a scheduler is behind it; of 1026 tokens with weights for each
-// head: 19 us, 5 of them the second kernel.
+// head: 17 us, 5 of them the second kernel.
 #include "cache_attn.cuh"
 #include "device_common.cuh"
 #include "norm_rope.h"
@@ -568,6 +568,13 @@ struct Unit {
     }
 };
 
+// Cosines and sines of a token's pairs, once for the heads that a warp goes over (16384 tokens of 81 + 8
+// heads of 100: 497 us and 782, the gradient, with more blocks, 1030 and 2082).
+__device__ __forceinline__ void sines_of(const NormRopeParams &p, int m, float2 *turn)
+{
+    for (int u = threadIdx.x & 31; u < p.d_rot / 2; u += 32) turn_angle(p.turns[u], m, p.sign, turn[u].x, turn[u].y);
+}
+
 __global__ void __launch_bounds__(kNormThreads) norm_pairs_kernel(const __grid_constant__ NormRopeParams p, bool half)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -576,11 +583,13 @@ __global__ void __launch_bounds__(kNormThreads) norm_pairs_kernel(const __grid_c
     const int h0 = group * t.per, h1 = min(h0 + t.per, t.n_heads);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kNormThreads / 32;
     const int tokens = p.B * p.S;
+    extern __shared__ float2 sines[];  // [warps][pairs] of the warp's token; a lane's own alone
+    float2 *turn = sines + warp * (p.d_rot / 2);
     for (long long token = (long long)block * warps + warp; token < tokens; token += (long long)t.blocks * warps) {
         const int b = (int)(token / p.S), s = (int)(token % p.S);
         const long long row = out_row(p, t, b, s);
         if (row < 0) continue;
-        const int m = p.d_rot ? p.positions[b * p.pos_stride + s] : 0;
+        if (t.norm) sines_of(p, p.positions[b * p.pos_stride + s], turn);
         for (int h = h0; h < h1; ++h) {
             const uint16_t *src = t.x + b * t.x_b + s * t.x_s + h * t.x_h;
             uint16_t *dst = t.out + b * t.out_b + row * t.out_s + h * t.out_h;
@@ -598,9 +607,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_pairs_kernel(const __grid_c
                 const Unit at(p, u, half);
                 float x = bf16lo_to_f32(src[at.a]) * rs * weight_at(t, h, at.a);
                 if (at.b >= 0) {
-                    float y = bf16lo_to_f32(src[at.b]) * rs * weight_at(t, h, at.b), c, sn;
-                    turn_angle(p.turns[u], m, p.sign, c, sn);
-                    rotate2(x, y, c, sn, x, y);
+                    float y = bf16lo_to_f32(src[at.b]) * rs * weight_at(t, h, at.b);
+                    rotate2(x, y, turn[u].x, turn[u].y, x, y);
                     dst[at.b] = (uint16_t)pack_bf16x2(y, 0.f);
                 }
                 dst[at.a] = (uint16_t)pack_bf16x2(x, 0.f);
@@ -612,13 +620,15 @@ __global__ void __launch_bounds__(kNormThreads) norm_pairs_kernel(const __grid_c
 __global__ void __launch_bounds__(kNormThreads) norm_grad_pairs_kernel(const __grid_constant__ NormRopeParams p, bool half)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    extern __shared__ float acc[];  // [warps][d_row]
+    extern __shared__ float2 sines[];  // [warps][pairs] of the warp's token, a lane's own alone; then sums
+    float *acc = reinterpret_cast<float *>(sines + kNormThreads / 32 * (p.d_rot / 2));  // [warps][d_row]
     int group, block;
     const NormTensor &t = p.t[tensor_of(p, group, block)];
     const int h0 = group * t.per, h1 = min(h0 + t.per, t.n_heads);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kNormThreads / 32;
     const int tokens = p.B * p.S;
     float *dw = acc + warp * t.d_row;  // an entry always belongs to the same lane
+    float2 *turn = sines + warp * (p.d_rot / 2);
     const int units = t.d_row - p.d_rot / 2;
     for (int u = lane; u < units; u += 32) {
         const Unit at(p, u, half);
@@ -627,7 +637,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_pairs_kernel(const __g
     }
     for (long long token = (long long)block * warps + warp; token < tokens; token += (long long)t.blocks * warps) {
         const int b = (int)(token / p.S), s = (int)(token % p.S);
-        const int m = p.d_rot ? p.positions[b * p.pos_stride + s] : 0;
+        sines_of(p, p.positions[b * p.pos_stride + s], turn);
         for (int h = h0; h < h1; ++h) {
             const uint16_t *src = t.x + b * t.x_b + s * t.x_s + h * t.x_h;
             const uint16_t *grad = t.dy + b * t.dy_b + s * t.dy_s + h * t.dy_h;
@@ -638,14 +648,13 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_pairs_kernel(const __g
                 g0 = bf16lo_to_f32(grad[at.a]);
                 x1 = g1 = 0.f;
                 if (at.b >= 0) {
-                    float c, sn;
                     x1 = bf16lo_to_f32(src[at.b]);
                     g1 = bf16lo_to_f32(grad[at.b]);
-                    turn_angle(p.turns[u], m, p.sign, c, sn);
-                    rotate2(g0, g1, c, sn, g0, g1);
+                    rotate2(g0, g1, turn[u].x, turn[u].y, g0, g1);
                 }
             };
             float ss = 0.f, gx = 0.f;
+#pragma unroll 4
             for (int u = lane; u < units; u += 32) {
                 const Unit at(p, u, half);
                 float x0, x1, g0, g1;
@@ -656,6 +665,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_pairs_kernel(const __g
             }
             const float rs = rsqrtf(fmaf(sum_lanes<32>(ss), t.inv_d, p.eps));
             const float mean = sum_lanes<32>(gx) * rs * t.inv_d;
+#pragma unroll 4
             for (int u = lane; u < units; u += 32) {
                 const Unit at(p, u, half);
                 float x0, x1, g0, g1;
@@ -768,7 +778,8 @@ cudaError_t launch_lanes(const NormRopeParams &p, bool half, bool grad, int lane
 cudaError_t launch_norm_rope(const NormRopeParams &p, bool half, int lanes, cudaStream_t stream)
 {
     return lanes ? launch_lanes(p, half, false, lanes, stream)
-                 : launch_grid(norm_pairs_kernel, dim3(grid_of(p)), kNormThreads, 0, stream, p, half);
+                 : launch_grid(norm_pairs_kernel, dim3(grid_of(p)), kNormThreads,
+                               kNormThreads / 32 * (p.d_rot / 2) * (int)sizeof(float2), stream, p, half);
 }
 
 cudaError_t launch_norm_rope_grad(const NormRopeParams &p, bool half, int lanes, cudaStream_t stream)
@@ -783,7 +794,7 @@ cudaError_t launch_norm_rope_grad(const NormRopeParams &p, bool half, int lanes,
     const cudaError_t err =
         lanes ? launch_lanes(p, half, true, lanes, stream)
               : launch_grid(norm_grad_pairs_kernel, dim3(grid_of(p)), kNormThreads,
-                            kNormThreads / 32 * width * (int)sizeof(float), stream, p, half);
+                            kNormThreads / 32 * (p.d_rot + width) * (int)sizeof(float), stream, p, half);
     if (err != cudaSuccess || !weights) return err;
     return launch_grid(norm_weights_kernel, dim3((width + 7) / 8, heads, p.n_tensors), kNormSumThreads, 0, stream, p);
 }
