@@ -663,3 +663,58 @@ def test_conveniences_refuse_what_does_not_fit():
     ws = torch.empty(16, dtype=torch.uint8, device=dev)
     with pytest.raises(apex.ApexError):
         apex.decode4(q, *c, ln, workspace=ws)
+
+
+# Sizes past 2 GiB of codes: B x 8 heads x cap rows of 128 entries (64 bytes of codes, 8 of scales).
+@pytest.mark.parametrize("B,cap", [(32, 65536), (80, 65536), (96, 65536), (160, 65536), (7, 1000003), (1, 3)])
+def test_packed_tensors_end_where_they_end(lib, B, cap):
+    """Tensors right behind one another share nothing; one that starts a byte sooner does."""
+    if torch.cuda.is_available():
+        pytest.skip("calls that pass the checks would run on addresses that hold nothing")
+    codes, scales = B * 8 * cap * 64, B * 8 * cap * 8
+    rows = B * 8 * 2 * 256  # two tokens of each sequence
+
+    def call(f, **moved):
+        at, end = {}, 1 << 32
+        for name, size in (("k4", codes), ("ks", scales), ("v4", codes), ("vs", scales), ("k", rows), ("v", rows)):
+            at[name] = end
+            end += size
+        at.update((n, at[n] - by) for n, by in moved.items())
+        t = [_tensor(rows=at[n], bytes=at[n + "4"], scales=at[n + "s"], b=2048, h=256, s=128) for n in ("k", "v")]
+        return f(*t, B, 8, 2, cap, None, None)
+    for f in (apex.apex_attn_append4, apex.apex_attn_unpack4):
+        assert call(f) not in (BAD, UNSUPPORTED)
+        assert call(f, k=2) == BAD  # the first rows on the last scale
+    # one packed tensor on the end of another: refused where they are written
+    for n in ("ks", "v4", "vs"):
+        assert call(apex.apex_attn_append4, **{n: 16}) == BAD
+
+
+@pytest.mark.gpu
+def test_packed_tensors_right_behind_one_another():
+    """2.5 GiB of codes with what is next in memory: the calls run and keep to their rows."""
+    dev = _gpu()
+    B, H, d, cap, n = 80, 8, 128, 65536, 3
+    codes, scales, rows = B * H * cap * d // 2, B * H * cap * d // 16, B * H * n * d * 2
+    sizes = [codes, scales, codes, scales, rows, rows]
+    try:
+        buf = torch.zeros(sum(sizes), dtype=torch.uint8, device=dev)
+    except torch.OutOfMemoryError:
+        pytest.skip("needs 6 GB")
+    k4, ks, v4, vs, k, v = torch.split(buf, sizes)
+    f8 = torch.float8_e4m3fn
+    cache = (k4.view(B, H, cap, d // 2), ks.view(f8).view(B, H, cap, d // 16), v4.view(B, H, cap, d // 2),
+             vs.view(f8).view(B, H, cap, d // 16))
+    k, v = (x.view(torch.bfloat16).view(B, H, n, d) for x in (k, v))
+    g = _gen(dev, 31)
+    k.copy_(_normal(g, dev, B, H, n, d))
+    v.copy_(_normal(g, dev, B, H, n, d))
+    row0 = torch.full((B,), cap - n, dtype=torch.int32, device=dev)
+    apex.append4(k, v, *cache, row0=row0)
+    for x, (x4, s) in ((k, cache[:2]), (v, cache[2:])):
+        code, sb, _ = _pack_ref(x, None)
+        assert torch.equal(_codes(x4[:, :, -n:]), code) and torch.equal(_bits(s)[:, :, -n:].cpu(), sb)
+        assert int(x4[:, :, -n - 1].count_nonzero()) == 0 and int(_bits(s)[:, :, -n - 1].count_nonzero()) == 0
+    want = [_pack_ref(x, None)[2] for x in (k, v)]
+    apex.unpack4(*cache, row0=row0, n_rows=n, k_out=k, v_out=v)
+    assert torch.equal(k.double().cpu(), want[0]) and torch.equal(v.double().cpu(), want[1])

@@ -14,13 +14,14 @@ namespace {
 size_t cache_bytes(int B, int H, int S_cap, int d) { return (size_t)B * H * S_cap * (d / 2); }
 size_t scale_bytes(int B, int H, int S_cap, int d) { return (size_t)B * H * S_cap * (d / kBits4Block); }
 
-RowSet bytes_of(const void *at, size_t bytes)  // as 2-byte elements, whole ones
+// `bytes` at an address as 2-byte elements, in rows of about 2^30 that end with the last of them: equal
+// steps, each row as long as what the steps leave.
+RowSet bytes_of(const void *at, size_t bytes)
 {
     const uintptr_t a = reinterpret_cast<uintptr_t>(at);
-    // in rows of at most 2^30 elements, the last of which may reach a little far
     const long long first = (long long)(a / 2), n = (long long)((a + bytes + 1) / 2) - first;
-    const long long row = std::min<long long>(n, 1 << 30);
-    return RowSet{(__int128)first, {0, 0, row}, {1, 1, (int)((n + row - 1) / row)}, (int)row};
+    const long long count = (n >> 30) + 1, step = n / count;
+    return RowSet{(__int128)first, {0, 0, step}, {1, 1, (int)count}, (int)(n - (count - 1) * step)};
 }
 
 // Rows of bf16 in and packed rows out (append), or the other way round (unpack).
@@ -39,17 +40,22 @@ apex_status move_rows(const apex_bits4_tensor *const (&t)[2], bool append, int B
         (__int128)B * H * S_cap > (1ll << 40))
         return APEX_ERR_UNSUPPORTED;
     // an output lies on no input and on no other output
-    RowSet rows[2], held[4];
+    RowSet rows[2];
+    const void *packed[4];
+    size_t size[4];
     for (int i = 0; i < 2; ++i) {
         rows[i] = RowSet{(__int128)(reinterpret_cast<uintptr_t>(t[i]->rows) / 2), {t[i]->b, t[i]->h, t[i]->s}, {B, H, S}, t[i]->d};
-        held[2 * i] = bytes_of(t[i]->bytes, cache_bytes(B, H, S_cap, t[i]->d));
-        held[2 * i + 1] = bytes_of(t[i]->scales, scale_bytes(B, H, S_cap, t[i]->d));
+        packed[2 * i] = t[i]->bytes;
+        size[2 * i] = cache_bytes(B, H, S_cap, t[i]->d);
+        packed[2 * i + 1] = t[i]->scales;
+        size[2 * i + 1] = scale_bytes(B, H, S_cap, t[i]->d);
     }
     for (int i = 0; i < 4; ++i) {
+        const RowSet held = bytes_of(packed[i], size[i]);
         for (int k = 0; k < 2; ++k)
-            if (share_elements(held[i], rows[k])) return APEX_ERR_INVALID_ARG;
+            if (share_elements(held, rows[k])) return APEX_ERR_INVALID_ARG;
         for (int k = 0; append && k < i; ++k)
-            if (share_elements(held[i], held[k])) return APEX_ERR_INVALID_ARG;
+            if (overlap(packed[i], size[i], packed[k], size[k])) return APEX_ERR_INVALID_ARG;
     }
     if (!append && (share_elements(rows[0], rows[0]) || share_elements(rows[1], rows[1]) || share_elements(rows[0], rows[1])))
         return APEX_ERR_INVALID_ARG;
