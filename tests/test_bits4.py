@@ -718,3 +718,29 @@ def test_packed_tensors_right_behind_one_another():
     want = [_pack_ref(x, None)[2] for x in (k, v)]
     apex.unpack4(*cache, row0=row0, n_rows=n, k_out=k, v_out=v)
     assert torch.equal(k.double().cpu(), want[0]) and torch.equal(v.double().cpu(), want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 4, 16])  # 4, 16 and 64 query rows of a KV head
+@pytest.mark.parametrize("power", [-90, 90])
+def test_factors_at_both_ends_of_their_range(T, power):
+    dev = _gpu()
+    f = torch.full((1,), 2.0 ** power, device=dev)
+    # equal scores, all values the largest there are: sums over a long cut cache are 2^17 of them
+    cap, d = 130000, 128
+    k4, ks = _cache(dev, 1, 1, cap, d)
+    v4, vs = _cache(dev, 1, 1, cap, d, fill=0x77)
+    _bits(vs).fill_(0x7E)
+    ln = torch.tensor([cap - T], dtype=torch.int32, device=dev)
+    q = torch.ones(1, 4, T, d, dtype=torch.bfloat16, device=dev)
+    got = apex.decode4(q, k4, ks, v4, vs, ln, k_factor=f, v_factor=f)
+    # weights are powers of two here, sums of them whole numbers times one: exact but for the division
+    assert (got.double() / (6 * 448 * 2.0 ** power) - 1).abs().max() <= U
+    # other values, whole and cut; queries that bring the scores back
+    for cap in (200, 3000):
+        lens = [cap - T, 77]
+        _, cache, ln, _, vals = _attn_inputs(dev, cap, 4, 1, T, d, d, cap, lens)
+        q = _normal(_gen(dev, cap), dev, 2, 4, T, d)
+        out = apex.decode4((q.double() * 2.0 ** -power).to(torch.bfloat16), *cache, ln, k_factor=f, v_factor=f)
+        ref, tol = _attn_ref(q, *vals, lens)
+        _close(out.double() * 2.0 ** -power, ref, tol)

@@ -45,7 +45,7 @@ struct Decode4Params {
     CacheAttnParams c;  // sizes, lengths, masks, schedule and workspace, as for bf16 caches
     const uint16_t *q;
     const uint8_t *k, *v, *k_scale, *v_scale;
-    const float *k_factor, *v_factor;
+    const float *k_factor;  // the values': c.v_factor
 };
 
 // Rows of a KV head's queries that are worked on together: they share each key's conversion.  Up

@@ -178,7 +178,7 @@ apex_status apex_attn_decode4(const void *q, const void *k4, const void *k_scale
     p.k_scale = static_cast<const uint8_t *>(k_scale);
     p.v_scale = static_cast<const uint8_t *>(v_scale);
     p.k_factor = k_factor;
-    p.v_factor = v_factor;
+    c.v_factor = v_factor;
     c.wait = dev.wait;
     if (launch_decode4(p, dev.sm_count, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return APEX_ERR_CUDA;
     return APEX_OK;

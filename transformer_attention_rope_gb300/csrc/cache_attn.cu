@@ -328,6 +328,7 @@ __device__ __forceinline__ void join_rows(const CacheAttnParams &p, int blocks_p
     const int2 c = p.units[unit];
     if (c.x == c.y) return;
     const int n = c.y - c.x + 1, first = SPLIT == 1 ? 0 : warp;
+    const float factor = p.v_factor ? p.v_factor[unit / p.n_groups % p.H_kv] : 1.f;
     auto slot = [&](int i) { return (size_t)(2 * (c.x + i) + (i == 0 ? 1 : 0)) * p.rows_cap; };
     float M = -INFINITY, L = 0.f, acc[8];
 #pragma unroll
@@ -392,7 +393,7 @@ __device__ __forceinline__ void join_rows(const CacheAttnParams &p, int blocks_p
         }
     }
     if (!ok) return;
-    const float inv = (L > 0.f) ? 1.f / L : 0.f;
+    const float inv = (L > 0.f) ? factor / L : 0.f;
     uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)(unit / p.n_groups) * p.R + r) * DV) + chunk;
     *dst = make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
                       pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));

@@ -414,14 +414,14 @@ __device__ __forceinline__ float row_max(float m_run, float l_run)
     return (m_run == -INFINITY && !(l_run == 0.f)) ? 0.f : m_run;
 }
 
-// The finished row (index `row` over all query rows), or its part of a cut unit's result:
-// row rc of the slot.  Partial outputs lie four entries at a time, rows adjacent, so that
+// The finished row (index `row` over all query rows) times `factor`, or its part of a cut unit's
+// result: row rc of the slot.  Partial outputs lie four entries at a time, rows adjacent, so that
 // the lanes' rows are written and read side by side.
 template <int DV, bool WEIGHTS>
 __device__ __forceinline__ void write_row(const CacheAttnParams &p, uint32_t o_addr, bool whole, bool row_ok,
-                                          size_t row, int slot, int rc, float m_run, float l_run)
+                                          size_t row, int slot, int rc, float m_run, float l_run, float factor = 1.f)
 {
-    const float inv = (l_run > 0.f) ? 1.f / l_run : 0.f;
+    const float inv = (l_run > 0.f) ? factor / l_run : 0.f;
     if (row_ok && !whole) p.ws_ml[(size_t)slot * p.rows_cap + rc] = make_float2(row_max(m_run, l_run), l_run);
     if (WEIGHTS && row_ok && whole) p.lse[row] = m_run + log2f(l_run);
     uint4 *dst16 = reinterpret_cast<uint4 *>(p.out + row * DV);

@@ -28,6 +28,7 @@ struct CacheAttnParams {
     int drafts;  // draft rows behind lens[b]: T, or 0 for the decode
     float *acc;  // [B, H_kv, S_cap], or NULL
     float scale_log2;
+    const float *v_factor;  // [H_kv] of the values, for the rows once they are joined, or NULL: 1
     WaitCtl wait;
     int R;          // query rows of a KV head, G * T
     int group;      // rows of a row group

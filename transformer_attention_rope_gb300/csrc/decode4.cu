@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, decode4_ctas(8 * NT)) decode4_kernel
             for (int e = 0; e < 2; ++e) factor[nt][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + e));
         }
         const float kf = (p.k_factor ? p.k_factor[f.hk] : 1.f) * pc.scale_log2;
-        const float vf = p.v_factor ? p.v_factor[f.hk] : 1.f;
+        const float vf = pc.v_factor ? pc.v_factor[f.hk] : 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -506,14 +506,15 @@ __global__ void __launch_bounds__(kThreads, decode4_ctas(8 * NT)) decode4_kernel
                 x.z = fmaf(y.z, k, x.z);
                 x.w = fmaf(y.w, k, x.w);
             }
+            // the values' factor comes last, when a row is whole: sums of weights up to 2^15 times values up to
+            // 2688 would leave fp32 with the largest factors
             if (f.head && f.tail) {
-                const float inv = (L == 0.f ? 0.f : 1.f / L) * vf;
+                const float inv = L == 0.f ? 0.f : vf / L;
                 *reinterpret_cast<uint2 *>(pc.out + (kv * pc.R + r) * DV + 4 * c) =
                     make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
             } else {
                 if (c == 0) pc.ws_ml[(size_t)slot * pc.rows_cap + rc] = make_float2(top, L);
-                reinterpret_cast<float4 *>(pc.ws_o + (size_t)slot * pc.rows_cap * DV)[(size_t)c * pc.rows_cap + rc] =
-                    make_float4(x.x * vf, x.y * vf, x.z * vf, x.w * vf);
+                reinterpret_cast<float4 *>(pc.ws_o + (size_t)slot * pc.rows_cap * DV)[(size_t)c * pc.rows_cap + rc] = x;
             }
         }
         __syncthreads();  // the rings are filled again

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_wide_kernel(const __grid_
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::kBarQReady));
-            const float kf = p.k_factor ? p.k_factor[f.hk] : 1.f, vf = p.v_factor ? p.v_factor[f.hk] : 1.f;
+            const float kf = p.k_factor ? p.k_factor[f.hk] : 1.f, vf = pc.v_factor ? pc.v_factor[f.hk] : 1.f;
             const float scale = fmaxf(up * kf * pc.scale_log2, 1e-37f);  // not 0: masked scores stay -inf
 
             const int m = f.s.len + r % pc.T;  // position
@@ -342,11 +342,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_wide_kernel(const __grid_
                 if (lane == 0) mbar_arrive(bar(C::kBarPReady + (g & 1)));
             }
 
-            // ---- the finished row, or this fragment's part of it; the values' factor goes into the sum
+            // ---- the finished row, or this fragment's part of it
             mbar_wait(bar(C::kBarPV), (g - 1) & 1, p.c.wait);
             tc_fence_after();
             write_row<DV, false>(pc, o_addr, f.head && f.tail, row_ok, row, 2 * blockIdx.x + (f.head ? 1 : 0), i, m_run,
-                                 l_run / vf);
+                                 l_run, vf);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::kBarOEmpty));
