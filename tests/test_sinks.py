@@ -455,3 +455,28 @@ def test_a_workspace_of_the_callers(d, d_r, S):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, call(None))
+
+
+@pytest.mark.gpu
+def test_sinks_and_drafts_past_the_capacity():
+    """Drafts stand at positions of any size; those below n_sink stay visible, whatever rows the cache has."""
+    dev = _gpu()
+    T, cap, window = 5, 200, 4
+    q, k, v = _inputs(dev, 15, 2, 8, 2, T, cap, 128)
+    ln = torch.tensor([0, 150], dtype=torch.int32, device=dev)
+    at = torch.tensor([1000, 1010, 1020, 1021, 1 << 25], dtype=torch.int32)
+    for sinks in (3, 190, 1010, 1021, 2 ** 25, 2 ** 31 - 1, 2 ** 40):
+        got = apex.tree_decode(q, k, v, ln, positions=at.expand(2, T).contiguous().to(dev), window=window, n_sink=sinks)
+        for b, n in enumerate(ln.tolist()):
+            pos = torch.cat([torch.arange(n), at.long()]).to(dev)  # of the rows: cached ones, drafts
+            m = at.long().to(dev)[:, None]
+            row = torch.arange(n + T, device=dev)
+            seen = (row <= n + torch.arange(T, device=dev)[:, None]) & ((m - pos < window) | (pos < sinks))
+            for h in range(8):
+                x, kk, vv = q[b, h].double(), k[b, h // 4, :n + T].double(), v[b, h // 4, :n + T].double()
+                s = (x @ kk.T / math.sqrt(128)).masked_fill(~seen, -math.inf)
+                p = torch.softmax(s, -1)
+                e = (2.0 ** -17 / math.sqrt(128) * (x.abs() @ kk.abs().T)).masked_fill(~seen, 0).amax(-1, keepdim=True)
+                o, A = p @ vv, p @ vv.abs()
+                err = (got[b, h].double() - o).abs()
+                assert (err <= U * o.abs() + A * (U + 2 * e + 2.0 ** -13)).all(), sinks

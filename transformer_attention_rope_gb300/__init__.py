@@ -432,7 +432,7 @@ def _sinks(n_sink, window) -> int:
     """Sinks of a call: none without a window."""
     if n_sink < 0:
         raise ValueError("n_sink must not be negative")
-    return min(int(n_sink), 2 ** 24) if window > 0 else 0
+    return min(int(n_sink), _INT_MAX) if window > 0 else 0
 
 
 def _sink_fwd(q, k, v, d_r, n_sink, opt, out, workspace, stream):

@@ -530,7 +530,8 @@ cudaError_t launch_cache_attn(CacheAttnLaunch &L, int sm_count, cudaStream_t str
     const int n_units = p.B * p.H_kv * p.n_groups, room = pairs ? sm_count / 2 : sm_count;
     int shares = std::min(room, cache_attn_shares(p.B, p.H_kv, p.n_groups, p.S_cap, pairs));
     // keys that a unit can reach: a window bounds them, the drafts and a tile's slack beside it
-    const int reach = p.window > 0 ? (int)std::min<long long>(p.S_cap, (long long)p.window + p.drafts + kKeys + (p.n_sink ? p.n_sink + kKeys : 0)) : p.S_cap;
+    const long long sinks = p.n_sink > 0 ? (long long)p.n_sink + kKeys : 0;
+    const int reach = p.window > 0 ? (int)std::min<long long>(p.S_cap, p.window + sinks + p.drafts + kKeys) : p.S_cap;
     p.whole = !p.acc && cache_attn_whole(n_units, reach, room);
     if (p.whole) shares = std::min(shares, n_units);
     cudaError_t err;

@@ -416,7 +416,7 @@ static apex_status cache_attn(const void *q, const void *k_cache, const void *v_
     p.mask_stride = mask_stride;
     p.positions = positions;
     p.window = window > 0 ? window : 0;
-    p.n_sink = window > 0 ? std::min(n_sink, S_cap) : 0;  // without a window every key stays visible
+    p.n_sink = window > 0 ? n_sink : 0;  // without a window every key stays visible; drafts may stand past S_cap
     p.drafts = weights ? 0 : T;
     p.acc = acc;
     p.scale_log2 = (float)(1.4426950408889634 * (scale == 0.f ? 1.0 / sqrt((double)d_qk) : (double)scale));
