@@ -681,7 +681,7 @@ apex_status apex_attn_unpack4(const apex_bits4_tensor *k, const apex_bits4_tenso
  *
  * Row lengths, groups and limits as for apex_attn_tree_decode (1 <= T <= 64).  A row that sees no
  * key gives zeros.  Cache rows that no token of the sequence sees may hold anything; the values of
- * the others must be finite, and factors from 2^-90 to 2^90.  Queries are held in fp16 relative to
+ * the others and the scores (in fp32) must be finite, and factors from 2^-90 to 2^90.  Queries are held in fp16 relative to
  * their row's largest entry, where entries below 2^-21 of it lose precision; scores, statistics
  * and sums are fp32, weights are rounded to fp16 for the tensor cores.  Equal inputs give equal bits.
  */

@@ -744,3 +744,45 @@ def test_factors_at_both_ends_of_their_range(T, power):
         out = apex.decode4((q.double() * 2.0 ** -power).to(torch.bfloat16), *cache, ln, k_factor=f, v_factor=f)
         ref, tol = _attn_ref(q, *vals, lens)
         _close(out.double() * 2.0 ** -power, ref, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 4, 16])
+@pytest.mark.parametrize("power", [12, 18, 24, 70])
+def test_scores_of_any_size(T, power):
+    """Scores of which one key's is the largest by far, or two keys' are, of either sign: that key's value, or
+    the mean of the two."""
+    dev = _gpu()
+    cap, d = 3000, 128
+    g = _gen(dev, power + T)
+    q, cache, ln, _, vals = _attn_inputs(dev, power, 4, 1, T, d, d, cap, [cap - T])
+    q = q[:, :, :1].expand(1, 4, T, d).contiguous()  # the tokens of a head alike
+    f = torch.full((1,), 2.0 ** power, device=dev)
+    vv = vals[1][0, 0]
+    twin = torch.randperm(cap - T, generator=torch.Generator().manual_seed(T))
+    for sign in (1, -1):
+        x = sign * q.abs()
+        s = (x[0, :, 0].double().cpu() @ vals[0][0, 0].T) / math.sqrt(d) * 2.0 ** power
+        s = s[:, :cap - T]  # a prompt's keys: all tokens see them
+        best = s.argmax(-1)
+        c = [y.clone() for y in cache]
+        for i in (0, 1):  # tokens' own keys score nothing like the best: the first key's negative codes
+            c[i].view(torch.uint8)[:, :, cap - T:] = c[i].view(torch.uint8)[:, :, best[0]:best[0] + 1]
+        c[0][:, :, cap - T:] ^= 0x88
+        other = int(twin[0]) if int(twin[0]) not in best.tolist() else int(twin[1])
+        for y in c:  # a twin of head 0's best key and of its value
+            z = y.view(torch.uint8)
+            z[:, :, other] = z[:, :, best[0]]
+        got = apex.decode4(x, *c, ln, k_factor=f).double().cpu()
+        assert torch.isfinite(got).all()
+        s[:, other] = s[:, best[0]]
+        for h in range(4):
+            # the next one is far below, by more than 2^-20 of the scores' size: scores of fp32 tell them apart
+            order = s[h].sort(descending=True)
+            low = 2 if int(order.indices[0]) in (int(best[0]), other) else 1
+            gap = (order.values[0] - order.values[low]) - 2.0 ** -20 * s[h].abs().max()
+            if gap < 40:
+                continue
+            want = vv[best[h]] if int(best[h]) != other else vv[best[0]]
+            rest = cap * math.exp(-40) * vv.abs().max()  # the formula's weights of all other keys
+            assert ((got[0, h] - want).abs() <= (U + 2.0 ** -11) * want.abs() + rest).all()

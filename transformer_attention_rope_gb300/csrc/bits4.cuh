@@ -16,6 +16,11 @@ __device__ __forceinline__ void e2m1_bytes_to_f16x2(uint32_t w, uint32_t (&o)[4]
         : "r"(w));
 }
 
+// References of scores from here on in magnitude are rounded by up to 2^-4 and more: a score less its reference as
+// one fused operation would be the product's rounding error, not what lies between two scores, and from 2^27 on more
+// than fp16 weights hold.  The product is then rounded first, as the reference was.
+constexpr float kLargeScore = 0x1p20f;
+
 // Two e4m3 values as an fp16 pair.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)
 {

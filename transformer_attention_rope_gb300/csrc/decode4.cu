@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, decode4_ctas(8 * NT)) decode4_kernel
             ref[nt][0] = ref[nt][1] = kUnseen;
             sum[nt][0] = sum[nt][1] = 0.f;
         }
+        bool large = false;  // some reference is: scores are rounded before they are compared with it
 
         constexpr int U = kSlice / kStep;  // steps whose scores are there together
         const uint8_t *at = smem + warp * kStages * C::kStage;
@@ -362,19 +363,26 @@ __global__ void __launch_bounds__(kThreads, decode4_ctas(8 * NT)) decode4_kernel
                     for (int e = 0; e < 4; ++e) x[u][nt][e] = fmaf(s[u][nt][e], factor[nt][e & 1], -ref[nt][e & 1]);
                     most = fmax3(most, fmaxf(x[u][nt][0], x[u][nt][1]), fmaxf(x[u][nt][2], x[u][nt][3]));
                 }
-            if (__any_sync(0xffffffffu, most > kSlack)) {
+            if (__any_sync(0xffffffffu, large || most > kSlack)) {
+                bool grown = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = kUnseen;
+                        float y[U][2], top = kUnseen;
 #pragma unroll
-                        for (int u = 0; u < U; ++u)
-                            top = fmax3(top, s[u][nt][e] * factor[nt][e], s[u][nt][e + 2] * factor[nt][e]);
+                        for (int u = 0; u < U; ++u) {
+                            y[u][0] = __fmul_rn(s[u][nt][e], factor[nt][e]);
+                            y[u][1] = __fmul_rn(s[u][nt][e + 2], factor[nt][e]);
+                            top = fmax3(top, y[u][0], y[u][1]);
+                        }
 #pragma unroll
                         for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
                         if (top - ref[nt][e] > kSlack) {
-                            const float now = top - kHeadroom, keep = fast_exp2(ref[nt][e] - now);
+                            // a large one as it is: less the headroom it could be rounded to 16 below itself, and
+                            // weights end at 2^16
+                            const float now = top - (fabsf(top) > kLargeScore ? 0.f : kHeadroom);
+                            const float keep = fast_exp2(ref[nt][e] - now);
                             ref[nt][e] = now;
                             sum[nt][e] *= keep;
 #pragma unroll
@@ -382,13 +390,15 @@ __global__ void __launch_bounds__(kThreads, decode4_ctas(8 * NT)) decode4_kernel
                                 o[nt][i][e] *= keep;
                                 o[nt][i][e + 2] *= keep;
                             }
-#pragma unroll
-                            for (int u = 0; u < U; ++u) {
-                                x[u][nt][e] = fmaf(s[u][nt][e], factor[nt][e], -now);
-                                x[u][nt][e + 2] = fmaf(s[u][nt][e + 2], factor[nt][e], -now);
-                            }
                         }
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            x[u][nt][e] = __fsub_rn(y[u][0], ref[nt][e]);
+                            x[u][nt][e + 2] = __fsub_rn(y[u][1], ref[nt][e]);
+                        }
+                        grown |= fabsf(ref[nt][e]) > kLargeScore - kHeadroom && ref[nt][e] != kUnseen;
                     }
+                large = __any_sync(0xffffffffu, grown);
             }
             uint32_t pb[U][NT][2];
 #pragma unroll

@@ -292,10 +292,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_wide_kernel(const __grid_
                 for (int a = 0; a < 8; ++a) acc[a] = fmaxf(acc[a], __uint_as_float(v[120 + a]));
                 const float mx = fmax3(fmax3(acc[0], acc[1], acc[2]), fmax3(acc[3], acc[4], acc[5]), fmaxf(acc[6], acc[7]));
                 const float m_new = fmaxf(m_run, mx * scale);
-                const bool need = (m_run != -INFINITY) && (m_new > m_run + 8.f);
+                const bool large = fabsf(m_new) > kLargeScore && m_new != -INFINITY;
+                const bool need = (m_run != -INFINITY && m_new - m_run > 8.f) || large;
                 // the last tile's product must be done before O is touched, and is waited for in every
                 // tile, so that no phase of its barrier is skipped
                 if (g > 0) mbar_wait(bar(C::kBarPV), (g - 1) & 1, p.c.wait);
+                float factor = scale, base = 0.f;  // of the scores from here on, where they are large
                 if (__any_sync(0xffffffffu, need)) {
                     tc_fence_after();
                     const float alpha = (m_new == -INFINITY) ? 1.f : fast_exp2(m_run - m_new);
@@ -310,11 +312,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode4_wide_kernel(const __grid_
                         for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                         tmem_st16(o_addr + 16 * ch, o);
                     }
+                    if (__any_sync(0xffffffffu, large)) {
+                        base = m_run == -INFINITY ? 0.f : m_run;
+                        factor = 1.f;
+#pragma unroll
+                        for (int e = 0; e < 128; ++e)
+                            v[e] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(v[e]), scale), base));
+                    }
                 } else if (m_run == -INFINITY) {
                     m_run = m_new;
                 }
-                const float m_use = kBias - (m_run == -INFINITY ? 0.f : m_run);
-                const uint64_t SC = f2_pack(scale, scale), NM = f2_pack(m_use, m_use);
+                const float m_use = kBias - (m_run == -INFINITY ? 0.f : m_run - base);
+                const uint64_t SC = f2_pack(factor, factor), NM = f2_pack(m_use, m_use);
                 uint64_t lacc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
                 for (int q4 = 0; q4 < 4; ++q4) {
