@@ -480,3 +480,35 @@ def test_sinks_and_drafts_past_the_capacity():
                 o, A = p @ vv, p @ vv.abs()
                 err = (got[b, h].double() - o).abs()
                 assert (err <= U * o.abs() + A * (U + 2 * e + 2.0 ** -13)).all(), sinks
+
+
+@pytest.mark.gpu
+def test_without_sinks_a_window_past_32_bits_is_none_too():
+    dev = _gpu()
+    for d, d_r in ((128, 0), (128, 64)):
+        q, k, v = _inputs(dev, 16, 1, 4, 2, 300, 300, d, d_r)
+        one = q[:, :, -1:].contiguous()
+        call = (lambda **o: apex.mla_fwd(q, k, v, d_r, **o)) if d_r else lambda **o: apex.fwd(q, k, v, **o)
+        dec = (lambda **o: apex.mla_decode(one, k, v, 299, d_r, **o)) if d_r else lambda **o: apex.decode(one, k, v, 299, **o)
+        for window in (2 ** 32 + 5, 2 ** 31, 5 - 2 ** 32, -1):
+            for f in (call, dec):
+                assert torch.equal(f(window=window), f()), window
+                assert torch.equal(f(window=window, n_sink=3), f()), window
+        with pytest.raises(ValueError):
+            call(q_pos0=2 ** 32)
+        with pytest.raises(ValueError):
+            call(prefix_len=2 ** 32, window=8, n_sink=2)
+    with pytest.raises(ValueError):
+        apex.decode(one[..., :128].contiguous(), k[..., :128].contiguous(), v, 2 ** 32 + 5)
+    with pytest.raises(ValueError):
+        apex.rope_keys(v, pos0=2 ** 32)
+
+
+def test_integers_past_32_bits_are_refused(lib):
+    with pytest.raises(ValueError):
+        apex.fwd_workspace_bytes(1, 16, 1, 6000, 6000, 128, q_pos0=2 ** 32)
+    with pytest.raises(ValueError):
+        apex.mla_fwd_workspace_bytes(1, 16, 1, 6000, 6000, 128, 64, prefix_len=2 ** 32, window=100, n_sink=3)
+    for window in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1, 5 - 2 ** 32):
+        assert apex.fwd_workspace_bytes(1, 16, 1, 6000, 6000, 128, window=window) == \
+            apex.fwd_workspace_bytes(1, 16, 1, 6000, 6000, 128)

@@ -424,8 +424,20 @@ def _stream_handle(stream):
 
 def _options(window=0, q_pos=0, rope_base=10000.0, yarn_scale=1.0, yarn_beta_fast=32.0, yarn_beta_slow=1.0,
              prefix_len=0, keys_prerotated=False) -> Options:
-    return Options(min(int(window), _INT_MAX), int(q_pos), float(rope_base), float(yarn_scale), float(yarn_beta_fast),
-                   float(yarn_beta_slow), int(prefix_len), 1 if keys_prerotated else 0)
+    return Options(_window(window), _int32(q_pos, "q_pos"), float(rope_base), float(yarn_scale), float(yarn_beta_fast),
+                   float(yarn_beta_slow), _int32(prefix_len, "prefix_len"), 1 if keys_prerotated else 0)
+
+
+def _window(window) -> int:
+    """A window as the C interface takes it: positions are int32, so a wider one is none, as one below 1 is."""
+    return int(window) if 0 < window <= _INT_MAX else 0
+
+
+def _int32(x, name) -> int:
+    x = int(x)
+    if not _INT_MIN <= x <= _INT_MAX:
+        raise ValueError("%s must fit 32 bits" % name)
+    return x
 
 
 def _sinks(n_sink, window) -> int:
@@ -546,7 +558,7 @@ def fwd(q, k, v, *, window: int = 0, q_pos0: int = 0, rope_base: float = 10000.0
                               _stream_handle(stream))
     elif plain:
         st = apex_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, H_q, H_kv, S_q, S_k, d,
-                           int(window), int(q_pos0), float(rope_base), _stream_handle(stream))
+                           _window(window), _int32(q_pos0, "q_pos0"), float(rope_base), _stream_handle(stream))
     else:
         opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                        keys_prerotated)
@@ -647,8 +659,8 @@ def decode(q, k_cache, v_cache, q_pos: int, *, window: int = 0, rope_base: float
     plain = yarn_scale <= 1.0 and prefix_len == 0 and not keys_prerotated
     if plain:
         st = apex_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
-                              S_k, d, int(window), int(q_pos), float(rope_base), workspace.data_ptr(), ws_bytes,
-                              _stream_handle(stream))
+                              S_k, d, _window(window), _int32(q_pos, "q_pos"), float(rope_base), workspace.data_ptr(),
+                              ws_bytes, _stream_handle(stream))
     else:
         opt = _options(window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                        keys_prerotated)
@@ -707,7 +719,7 @@ def rope_keys(k, *, pos0: int = 0, out=None, rope_base: float = 10000.0, yarn_sc
     if out.shape != k.shape:
         raise ValueError("out must have the shape of k")
     opt = _options(0, 0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow)
-    st = apex_attn_rope_keys(k.data_ptr(), out.data_ptr(), B * H, S, d, int(pos0), S * d, S * d, opt,
+    st = apex_attn_rope_keys(k.data_ptr(), out.data_ptr(), B * H, S, d, _int32(pos0, "pos0"), S * d, S * d, opt,
                              _stream_handle(stream))
     if st != APEX_OK:
         raise ApexError(st, "apex_attn_rope_keys")
@@ -727,7 +739,8 @@ def mla_rope_keys(k, d_r: int, *, pos0: int = 0, out=None, rope_base: float = 10
     if out.shape != k.shape:
         raise ValueError("out must have the shape of k")
     opt = _options(0, 0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow)
-    st = apex_attn_mla_rope_keys(k.data_ptr(), out.data_ptr(), B * H, S, d - int(d_r), int(d_r), int(pos0), S * d,
+    d_r = _int32(d_r, "d_r")
+    st = apex_attn_mla_rope_keys(k.data_ptr(), out.data_ptr(), B * H, S, d - d_r, d_r, _int32(pos0, "pos0"), S * d,
                                  S * d, opt, _stream_handle(stream))
     if st != APEX_OK:
         raise ApexError(st, "apex_attn_mla_rope_keys")
@@ -1106,8 +1119,7 @@ def tree_decode(q, k_cache, v_cache, lens, *, tree_mask=None, positions=None, wi
     torch = _torch or _load_torch()
     B, H_q, T, d_qk, H_kv, S_cap, d_v, device, pq, pk, pv = _cache_shapes(q, k_cache, v_cache)
     plens = _fit(lens, "lens", torch.int32, (B,), device)
-    if not 0 < window <= _INT_MAX:  # positions are int32: a wider window is none
-        window = 0
+    window = _window(window)
     n_sink = _sinks(n_sink, window)
     pmask = ppos = None
     stride = 0
@@ -1189,8 +1201,7 @@ def evict(k_cache, v_cache, acc, lens, budget: int, *, n_sink: int = 0, n_recent
     that tree_decode takes no window over the cache from then on."""
     torch = _torch or _load_torch()
     for n, x in (("budget", budget), ("n_sink", n_sink), ("n_recent", n_recent)):
-        if not _INT_MIN <= x <= _INT_MAX:
-            raise ValueError("%s must fit 32 bits" % n)
+        _int32(x, n)
     B, H_kv, S_cap, d_k = _rows4(k_cache, "k_cache")
     if B > _INT_MAX or H_kv > _INT_MAX or S_cap > _INT_MAX:
         raise ValueError("more sequences, heads or rows than evict takes")
@@ -1348,8 +1359,7 @@ def decode4(q, k4, k_scale, v4, v_scale, lens, *, window: int = 0, n_sink: int =
         raise ValueError("more heads or tokens than decode4 takes")
     pq = _fit(q, "q", torch.bfloat16, shape, device)
     plens = _fit(lens, "lens", torch.int32, (B,), device)
-    if not 0 < window <= _INT_MAX:  # rows are int32: a wider window is none
-        window = 0
+    window = _window(window)
     if n_sink < 0:
         raise ValueError("n_sink must not be negative")
     fk, fv = _factor4(k_factor, "k", H_kv, device), _factor4(v_factor, "v", H_kv, device)
