@@ -512,3 +512,33 @@ def test_integers_past_32_bits_are_refused(lib):
     for window in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1, 5 - 2 ** 32):
         assert apex.fwd_workspace_bytes(1, 16, 1, 6000, 6000, 128, window=window) == \
             apex.fwd_workspace_bytes(1, 16, 1, 6000, 6000, 128)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,d_r", [(128, 0), (128, 64)])
+@pytest.mark.parametrize("sinks", [0, 4])
+def test_a_call_on_another_stream_keeps_off_the_current_ones_memory(d, d_r, sinks):
+    """Outputs and workspaces of a call that waits on its stream: what the current stream allocates and writes
+    meanwhile stays as it is, and so do they."""
+    dev = _gpu()
+    S, window = 6000, 3000
+    q, k, v = _inputs(dev, 17, 1, 16, 1, S, S, d, d_r)
+    q1 = q[:, :, -1:].contiguous()
+    how = dict(window=window, n_sink=sinks)
+
+    def calls(**at):
+        if d_r:
+            return [apex.mla_fwd(q, k, v, d_r, **how, **at), apex.mla_decode(q1, k, v, S - 1, d_r, **how, **at),
+                    apex.mla_rope_keys(k, d_r, **at)]
+        return [apex.fwd(q, k, v, **how, **at), apex.decode(q1, k, v, S - 1, **how, **at), apex.rope_keys(k, **at)]
+    want = calls()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+    got = calls(stream=side)
+    junk = [torch.full((n,), 7, dtype=torch.uint8, device=dev) for n in (k.numel() * 2, 1 << 20, 1 << 21, 1 << 22) for _ in "ab"]
+    side.synchronize()
+    assert all(bool((x == 7).all()) for x in junk)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)

@@ -422,6 +422,19 @@ def _stream_handle(stream):
     return s.cuda_stream
 
 
+def _new(like, shape, dtype, stream):
+    """A tensor from torch's allocator on the device of `like`: the launch stream's memory, as that of the
+    current one may still be in use there, kept until the current stream is done with it too."""
+    torch = _torch or _load_torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    now = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(now)
+    return t
+
+
 def _options(window=0, q_pos=0, rope_base=10000.0, yarn_scale=1.0, yarn_beta_fast=32.0, yarn_beta_slow=1.0,
              prefix_len=0, keys_prerotated=False) -> Options:
     return Options(_window(window), _int32(q_pos, "q_pos"), float(rope_base), float(yarn_scale), float(yarn_beta_fast),
@@ -540,7 +553,7 @@ def fwd(q, k, v, *, window: int = 0, q_pos0: int = 0, rope_base: float = 10000.0
     B, H_q, S_q, d = q.shape
     _, H_kv, S_k, _ = k.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q, q.shape, torch.bfloat16, stream)
     _check(out, "out", 4)
     if workspace is None:
         need = fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d, window=window, q_pos0=q_pos0, rope_base=rope_base,
@@ -548,7 +561,7 @@ def fwd(q, k, v, *, window: int = 0, q_pos0: int = 0, rope_base: float = 10000.0
                                    yarn_beta_slow=yarn_beta_slow, prefix_len=prefix_len,
                                    keys_prerotated=keys_prerotated)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _new(q, need, torch.uint8, stream)
     plain = yarn_scale <= 1.0 and prefix_len == 0 and not keys_prerotated
     if workspace is not None and workspace is not False:
         opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
@@ -607,12 +620,12 @@ def mla_fwd(q, k, v, d_r: int, *, window: int = 0, q_pos0: int = 0, rope_base: f
     if n_sink:
         return _sink_fwd(q, k, v, int(d_r), n_sink, opt, out, workspace, stream)
     if out is None:
-        out = torch.empty((B, H_q, S_q, d_h), dtype=torch.bfloat16, device=q.device)
+        out = _new(q, (B, H_q, S_q, d_h), torch.bfloat16, stream)
     _check(out, "out", 4)
     if workspace is None:
         need = int(apex_attn_mla_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, int(d_r), opt))
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _new(q, need, torch.uint8, stream)
     if workspace is not None and workspace is not False:
         st = apex_attn_mla_fwd_ws(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, H_q, H_kv, S_q,
                                   S_k, d_h, int(d_r), opt, workspace.data_ptr(),
@@ -650,11 +663,11 @@ def decode(q, k_cache, v_cache, q_pos: int, *, window: int = 0, rope_base: float
                        keys_prerotated)
         return _sink_decode(q, k_cache, v_cache, 0, n_sink, opt, out, workspace, stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q, q.shape, torch.bfloat16, stream)
     _check(out, "out", 4)
     need = decode_workspace_bytes(B, H_q, H_kv, S_k, d)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(q, max(need, 16), torch.uint8, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     plain = yarn_scale <= 1.0 and prefix_len == 0 and not keys_prerotated
     if plain:
@@ -694,11 +707,11 @@ def mla_decode(q, k_cache, v_cache, q_pos: int, d_r: int, *, window: int = 0, ro
     if n_sink:
         return _sink_decode(q, k_cache, v_cache, int(d_r), n_sink, opt, out, workspace, stream)
     if out is None:
-        out = torch.empty((B, H_q, 1, d_h), dtype=torch.bfloat16, device=q.device)
+        out = _new(q, (B, H_q, 1, d_h), torch.bfloat16, stream)
     _check(out, "out", 4)
     need = decode_workspace_bytes(B, H_q, H_kv, S_k, d_h)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(q, max(need, 16), torch.uint8, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     st = apex_attn_mla_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
                               S_k, d_h, int(d_r), opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
@@ -714,7 +727,7 @@ def rope_keys(k, *, pos0: int = 0, out=None, rope_base: float = 10000.0, yarn_sc
     _check(k, "k", 4)
     B, H, S, d = k.shape
     if out is None:
-        out = torch.empty_like(k)
+        out = _new(k, k.shape, torch.bfloat16, stream)
     _check(out, "out", 4)
     if out.shape != k.shape:
         raise ValueError("out must have the shape of k")
@@ -734,7 +747,7 @@ def mla_rope_keys(k, d_r: int, *, pos0: int = 0, out=None, rope_base: float = 10
     _check(k, "k", 4)
     B, H, S, d = k.shape
     if out is None:
-        out = torch.empty_like(k)
+        out = _new(k, k.shape, torch.bfloat16, stream)
     _check(out, "out", 4)
     if out.shape != k.shape:
         raise ValueError("out must have the shape of k")
@@ -812,15 +825,7 @@ class _Launch:
             self.guard.__exit__(None, None, None)
 
     def new(self, like, shape, dtype):
-        """A tensor from torch's allocator: the launch stream's memory, as that of the current
-        one may still be in use there, kept until the current stream is done with it too."""
-        if self.stream is None:
-            return _torch.empty(shape, dtype=dtype, device=like.device)
-        now = _torch.cuda.current_stream(self.device)
-        with _torch.cuda.stream(self.stream):
-            t = _torch.empty(shape, dtype=dtype, device=like.device)
-        t.record_stream(now)
-        return t
+        return _new(like, shape, dtype, self.stream)
 
     def workspace(self, given, like, need):
         if given is None:
