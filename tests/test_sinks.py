@@ -542,3 +542,34 @@ def test_a_call_on_another_stream_keeps_off_the_current_ones_memory(d, d_r, sink
     assert all(bool((x == 7).all()) for x in junk)
     for x, y in zip(got, want):
         assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sinks", [0, 2])
+def test_tensors_that_do_not_belong_together_are_refused(sinks):
+    """Nothing is launched; without sinks as with them."""
+    dev = _gpu()
+    how = dict(window=8, n_sink=sinks)
+    for d, d_r in ((128, 0), (128, 64)):
+        q, k, v = _inputs(dev, 18, 2, 4, 2, 64, 64, d, d_r)
+        one = q[:, :, :1].contiguous()
+        fwd = (lambda *a, **o: apex.mla_fwd(*a, d_r, **how, **o)) if d_r else lambda *a, **o: apex.fwd(*a, **how, **o)
+        dec = (lambda q, k, v, **o: apex.mla_decode(q, k, v, 63, d_r, **how, **o)) if d_r else \
+            lambda q, k, v, **o: apex.decode(q, k, v, 63, **how, **o)
+        k1, v1, k_long, v_long = k[:, :1].contiguous(), v[:, :1].contiguous(), torch.cat([k, k], 2), torch.cat([v, v], 2)
+        for bad in ((k1, v), (k, v1), (k[:1], v), (k, v[:1]), (k_long, v), (k, v_long), (k, v[..., :64].contiguous()),
+                    (k[..., :64].contiguous(), v)):
+            with pytest.raises(ValueError):
+                fwd(q, *bad)
+            with pytest.raises(ValueError):
+                dec(one, *bad)
+        with pytest.raises(ValueError):
+            fwd(q, k, v, out=torch.empty_like(v))
+        with pytest.raises(ValueError):
+            dec(one, k, v, out=torch.empty(2, 4, 1, 64, dtype=torch.bfloat16, device=dev))
+        for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, 2, dtype=torch.uint8, device=dev)[:, 0]):
+            with pytest.raises(ValueError):
+                dec(one, k, v, workspace=ws)
+            if not sinks:
+                with pytest.raises(ValueError):
+                    fwd(q, k, v, workspace=ws)

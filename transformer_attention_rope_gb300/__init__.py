@@ -416,6 +416,29 @@ def _check(t, name, ndim):
         raise ValueError("%s must be a contiguous %d-D tensor" % (name, ndim))
 
 
+def _check_together(q, k, v, d_r=0):
+    """Keys and values of one length for q's sequences, rows of d entries (keys and queries: d + d_r), one device."""
+    B, _, _, d_qk = q.shape
+    _, H_kv, S_k, d = v.shape
+    if k.shape != (B, H_kv, S_k, d_qk) or v.shape[0] != B or d_qk != d + d_r:
+        raise ValueError("queries, keys and values must have the same sequences and row lengths, keys and values the "
+                         "same heads and length")
+    if not q.get_device() == k.get_device() == v.get_device():
+        raise ValueError("queries, keys and values must be on one device")
+
+
+def _check_out(out, shape, like):
+    _check(out, "out", 4)
+    if out.shape != shape or out.get_device() != like.get_device():
+        raise ValueError("out must be of shape %s, on the device of the other tensors" % (tuple(shape),))
+
+
+def _check_workspace(given, like):
+    if not given.is_cuda or given.get_device() != like.get_device() or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of the other tensors")
+    return given
+
+
 def _stream_handle(stream):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
@@ -550,11 +573,12 @@ def fwd(q, k, v, *, window: int = 0, q_pos0: int = 0, rope_base: float = 10000.0
         opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                        keys_prerotated)
         return _sink_fwd(q, k, v, 0, n_sink, opt, out, workspace, stream)
+    _check_together(q, k, v)
     B, H_q, S_q, d = q.shape
     _, H_kv, S_k, _ = k.shape
     if out is None:
         out = _new(q, q.shape, torch.bfloat16, stream)
-    _check(out, "out", 4)
+    _check_out(out, q.shape, q)
     if workspace is None:
         need = fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d, window=window, q_pos0=q_pos0, rope_base=rope_base,
                                    yarn_scale=yarn_scale, yarn_beta_fast=yarn_beta_fast,
@@ -564,6 +588,7 @@ def fwd(q, k, v, *, window: int = 0, q_pos0: int = 0, rope_base: float = 10000.0
             workspace = _new(q, need, torch.uint8, stream)
     plain = yarn_scale <= 1.0 and prefix_len == 0 and not keys_prerotated
     if workspace is not None and workspace is not False:
+        _check_workspace(workspace, q)
         opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                        keys_prerotated)
         st = apex_attn_fwd_ws(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, H_q, H_kv, S_q, S_k,
@@ -619,14 +644,16 @@ def mla_fwd(q, k, v, d_r: int, *, window: int = 0, q_pos0: int = 0, rope_base: f
     n_sink = _sinks(n_sink, window)
     if n_sink:
         return _sink_fwd(q, k, v, int(d_r), n_sink, opt, out, workspace, stream)
+    _check_together(q, k, v, d_r)
     if out is None:
         out = _new(q, (B, H_q, S_q, d_h), torch.bfloat16, stream)
-    _check(out, "out", 4)
+    _check_out(out, (B, H_q, S_q, d_h), q)
     if workspace is None:
         need = int(apex_attn_mla_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, int(d_r), opt))
         if need > 0:
             workspace = _new(q, need, torch.uint8, stream)
     if workspace is not None and workspace is not False:
+        _check_workspace(workspace, q)
         st = apex_attn_mla_fwd_ws(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, H_q, H_kv, S_q,
                                   S_k, d_h, int(d_r), opt, workspace.data_ptr(),
                                   workspace.numel() * workspace.element_size(), _stream_handle(stream))
@@ -662,12 +689,14 @@ def decode(q, k_cache, v_cache, q_pos: int, *, window: int = 0, rope_base: float
         opt = _options(window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
                        keys_prerotated)
         return _sink_decode(q, k_cache, v_cache, 0, n_sink, opt, out, workspace, stream)
+    _check_together(q, k_cache, v_cache)
     if out is None:
         out = _new(q, q.shape, torch.bfloat16, stream)
-    _check(out, "out", 4)
+    _check_out(out, q.shape, q)
     need = decode_workspace_bytes(B, H_q, H_kv, S_k, d)
     if workspace is None:
         workspace = _new(q, max(need, 16), torch.uint8, stream)
+    _check_workspace(workspace, q)
     ws_bytes = workspace.numel() * workspace.element_size()
     plain = yarn_scale <= 1.0 and prefix_len == 0 and not keys_prerotated
     if plain:
@@ -706,12 +735,14 @@ def mla_decode(q, k_cache, v_cache, q_pos: int, d_r: int, *, window: int = 0, ro
     n_sink = _sinks(n_sink, window)
     if n_sink:
         return _sink_decode(q, k_cache, v_cache, int(d_r), n_sink, opt, out, workspace, stream)
+    _check_together(q, k_cache, v_cache, d_r)
     if out is None:
         out = _new(q, (B, H_q, 1, d_h), torch.bfloat16, stream)
-    _check(out, "out", 4)
+    _check_out(out, (B, H_q, 1, d_h), q)
     need = decode_workspace_bytes(B, H_q, H_kv, S_k, d_h)
     if workspace is None:
         workspace = _new(q, max(need, 16), torch.uint8, stream)
+    _check_workspace(workspace, q)
     ws_bytes = workspace.numel() * workspace.element_size()
     st = apex_attn_mla_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
                               S_k, d_h, int(d_r), opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
@@ -830,9 +861,7 @@ class _Launch:
     def workspace(self, given, like, need):
         if given is None:
             return self.new(like, need if need > 16 else 16, _torch.uint8)
-        if not given.is_cuda or given.get_device() != self.device or not given.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the device of the other tensors")
-        return given
+        return _check_workspace(given, like)
 
 
 # apex_rope_tensor and apex_rope_options as bytes: quicker to make than ctypes structs
