@@ -530,3 +530,58 @@ def test_many_tokens_are_their_parts(half, each):
     n = B * S * (1 if each else H)
     for got, ref, size in zip((gqw, gkw), sums, sizes):
         assert ((got.double() - ref).abs() <= 2 * (n / 8 + 32) * 2.0 ** -24 * size).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("half,weights", [(True, "bf16"), (False, "heads")])
+def test_batches_of_single_tokens(half, weights):
+    """More sequences of a token than blocks run at once, appended to caches of their own rows."""
+    dev = _gpu()
+    B, Hq, Hkv, d, cap = 1100, 24, 6, 128, 5
+    g, q, k, pos, (qw, kw) = _inputs(dev, B, 1, Hq, Hkv, d, weights, 41)
+    v = _normal(g, dev, B, Hkv, 1, d)
+    row0 = torch.randint(-1, cap + 1, (B,), generator=g, device=dev, dtype=torch.int32)
+    kc, vc = (torch.full((B, Hkv, cap, d), 3.0, dtype=torch.bfloat16, device=dev) for _ in "kv")
+    o = dict(half=half)
+    got = apex.norm_rope(q, k, v, positions=pos, q_weight=qw, k_weight=kw, eps=1e-5, k_out=kc, v_out=vc, row0=row0, **_options(o))
+    ref, slack = _norm_ref(q, qw, pos, 1e-5, o)
+    _close(got[0], ref, U * ref.abs() + slack)
+    rk, sk = _norm_ref(k, kw, pos, 1e-5, o)
+    rows = torch.arange(cap)[None] == row0.cpu()[:, None]
+    keep = ~rows[:, None, :, None]
+    ref = torch.where(keep, torch.full((1,), 3.0, dtype=torch.float64), rk)
+    _close(kc, ref, torch.where(keep, torch.zeros(1, dtype=torch.float64), U * rk.abs() + sk))
+    assert torch.equal(vc.cpu(), torch.where(keep, torch.full((1,), 3.0, dtype=torch.bfloat16), v.cpu()))
+    dq, dk = _normal(g, dev, B, Hq, 1, d), _normal(g, dev, B, Hkv, 1, d)
+    grads = apex.norm_rope_grad(dq, q, dk, k, positions=pos, q_weight=qw, k_weight=kw, eps=1e-5, **_options(o))
+    for x, w, dy, dx, dw in ((q, qw, dq, grads[0], grads[2]), (k, kw, dk, grads[1], grads[3])):
+        ref, slack, rw, ew, terms, n = _grad_ref(dy, x, w, pos, 1e-5, o)
+        _close(dx, ref, U * ref.abs() + slack, "dx")
+        if w.dim() == 1:
+            rw, ew, terms, n = rw.sum(0), ew.sum(0), terms.sum(0), n * x.shape[1]
+        _close(dw, rw, ew + terms * (n / 8 + 32) * 2.0 ** -24, "dw")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("weights", ["fp32", "heads"])
+def test_many_rows_two_bytes_at_a_time(weights):
+    """More tokens than warps: the pass past 2^18 of them, the gradient past its 1024 blocks of four."""
+    dev = _gpu()
+    o = dict(half=True, rot_start=2, d_rot=14)
+    for B, S, Hq, Hkv, grad in ((2, 150001, 1, 1, False), (3, 3333, 5, 2, True)):
+        d = 18
+        g, q, k, pos, (qw, kw) = _inputs(dev, B, S, Hq, Hkv, d, weights, S)
+        got = apex.norm_rope(q, k, positions=pos, q_weight=qw, k_weight=kw, eps=1e-5, **_options(o))
+        for x, w, y in ((q, qw, got[0]), (k, kw, got[1])):
+            ref, slack = _norm_ref(x, w, pos, 1e-5, o)
+            _close(y, ref, U * ref.abs() + slack)
+        if not grad:
+            continue
+        dq, dk = _normal(g, dev, B, Hq, S, d), _normal(g, dev, B, Hkv, S, d)
+        grads = apex.norm_rope_grad(dq, q, dk, k, positions=pos, q_weight=qw, k_weight=kw, eps=1e-5, **_options(o))
+        for x, w, dy, dx, dw in ((q, qw, dq, grads[0], grads[2]), (k, kw, dk, grads[1], grads[3])):
+            ref, slack, rw, ew, terms, n = _grad_ref(dy, x, w, pos, 1e-5, o)
+            _close(dx, ref, U * ref.abs() + slack, "dx")
+            if w.dim() == 1:
+                rw, ew, terms, n = rw.sum(0), ew.sum(0), terms.sum(0), n * x.shape[1]
+            _close(dw, rw, ew + terms * (n / 8 + 32) * 2.0 ** -24, "dw")

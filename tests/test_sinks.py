@@ -573,3 +573,18 @@ def test_tensors_that_do_not_belong_together_are_refused(sinks):
             if not sinks:
                 with pytest.raises(ValueError):
                     fwd(q, k, v, workspace=ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,d_r,Hq,Hkv,S,window", [(64, 0, 32, 2, 2100, 700), (128, 0, 32, 2, 2100, 700), (128, 64, 16, 1, 6000, 3000)])
+def test_the_pass_that_rotates_keys_matches_the_formula(d, d_r, Hq, Hkv, S, window):
+    """Sizes at which the pass runs, with it and without."""
+    dev = _gpu()
+    sinks = 5
+    assert apex.apex_attn_sink_fwd_workspace_bytes(1, Hq, Hkv, S, S, d, d_r, sinks, apex.Options(window=window)) == \
+        Hkv * S * (d + d_r) * 2
+    q, k, v = _inputs(dev, 19, 1, Hq, Hkv, S, S, d, d_r)
+    ref = _ref(q, k, v, 0, window, sinks, d_r)
+    for ws in (None, False):
+        how = dict(window=window, n_sink=sinks, workspace=ws)
+        _close(apex.mla_fwd(q, k, v, d_r, **how) if d_r else apex.fwd(q, k, v, **how), *ref)
