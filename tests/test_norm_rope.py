@@ -585,3 +585,33 @@ def test_many_rows_two_bytes_at_a_time(weights):
             if w.dim() == 1:
                 rw, ew, terms, n = rw.sum(0), ew.sum(0), terms.sum(0), n * x.shape[1]
             _close(dw, rw, ew + terms * (n / 8 + 32) * 2.0 ** -24, "dw")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [128, 126])  # 16 bytes and 2 bytes at a time
+def test_rows_past_32_bit_offsets(d):
+    """Entries past 2^31 of a tensor, its output, a cache and the gradients: as a call over those tokens alone."""
+    dev = _gpu()
+    g = _gen(dev, 51)
+    H, S, n = 64, 280000, 37  # 2.3e9 entries
+    try:
+        q = torch.empty(1, H, S, d, dtype=torch.bfloat16, device=dev)
+        dq, out, cache = (torch.empty_like(q) for _ in range(3))
+    except torch.OutOfMemoryError:
+        pytest.skip("needs 20 GB")
+    for x in (q, dq):
+        for h in range(H):
+            x[0, h].normal_(generator=g)
+    pos = torch.arange(S, dtype=torch.int32, device=dev)
+    w = torch.ones(d, dtype=torch.bfloat16, device=dev)
+    last = slice(S - n, S)
+    apex.norm_rope(q, positions=pos, q_weight=w, q_out=out)
+    few = apex.norm_rope(q[:, :, last], positions=pos[last], q_weight=w)
+    assert torch.equal(out[:, :, last], few)
+    # appended behind, at rows of a cache whose last heads lie past 2^31
+    row0 = torch.full((1,), S - n, dtype=torch.int32, device=dev)
+    apex.norm_rope(q[:, :1, last], q[:, :, last], positions=pos[last], k_weight=w, k_out=cache, row0=row0)
+    assert torch.equal(cache[:, :, last], few)
+    apex.norm_rope_grad(dq, q, positions=pos, q_weight=w, q_out=out)
+    few, _ = apex.norm_rope_grad(dq[:, :, last], q[:, :, last], positions=pos[last], q_weight=w)
+    assert torch.equal(out[:, :, last], few)
