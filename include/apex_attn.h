@@ -477,7 +477,9 @@ typedef struct apex_norm_tensor {
  *   y = R_m (x / sqrt(mean(x^2) + eps) * weight)
  * with R_m the rotation of apex_attn_rope (the whole row is normed, the part that *opt names is
  * turned), in fp32, rounded once to bf16.  Positions, row0, out_rows, layouts and limits are
- * those of apex_attn_rope; opt->inverse is not used.  q may not be NULL, k and v may be.
+ * those of apex_attn_rope; opt->inverse is not used.  q may not be NULL, k and v may be.  The sum of
+ * squares is fp32 too: a row whose sum passes 2^128 comes out as zeros, and under an eps of 0 one whose
+ * sum is below 2^-126 loses precision, a row of zeros giving NaN.
  *
  * An out may be its own x with the same strides (of k and v only without row0); otherwise no
  * out may share an element with any x, weight or other out, nor hold one twice.
@@ -681,9 +683,10 @@ apex_status apex_attn_unpack4(const apex_bits4_tensor *k, const apex_bits4_tenso
  *
  * Row lengths, groups and limits as for apex_attn_tree_decode (1 <= T <= 64).  A row that sees no
  * key gives zeros.  Cache rows that no token of the sequence sees may hold anything; the values of
- * the others and the scores (in fp32) must be finite, and factors from 2^-90 to 2^90.  Queries are held in fp16 relative to
- * their row's largest entry, where entries below 2^-21 of it lose precision; scores, statistics
- * and sums are fp32, weights are rounded to fp16 for the tensor cores.  Equal inputs give equal bits.
+ * the others and the scores, in fp32, must be finite, and factors from 2^-90 to 2^90.  Queries are
+ * held in fp16 relative to their row's largest entry, where entries below 2^-21 of it lose precision;
+ * scores, statistics and sums are fp32, weights are rounded to fp16 for the tensor cores, where those
+ * below 2^-36 of the largest (with more than 16 rows G * T: 2^-32) vanish.  Equal inputs give equal bits.
  */
 apex_status apex_attn_decode4(const void *q, const void *k4, const void *k_scale, const void *v4, const void *v_scale,
                               void *out, int B, int H_q, int H_kv, int T, int S_cap, int d_qk, int d_v, const int *lens,

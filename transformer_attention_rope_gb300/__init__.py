@@ -28,6 +28,8 @@ Over caches of rotated keys (int32 lengths and positions on the device; the tens
 Over caches held in 4 bits:
     append4(k, v, k4, k_scale, v4, v_scale, row0=...), unpack4(k4, k_scale, v4, v_scale, row0=..., n_rows=...),
     decode4(q, k4, k_scale, v4, v_scale, lens, ...)
+No call is recorded by autograd: results do not require gradients, whatever their inputs do.  The gradient of
+rope is rope with inverse=True, that of norm_rope is norm_rope_grad.
 """
 from __future__ import annotations
 
@@ -1015,7 +1017,8 @@ def norm_rope(q, k=None, v=None, *, positions, q_weight=None, k_weight=None, eps
 
     A row x becomes R(x / sqrt(mean(x^2) + eps) * weight): the whole row is normed, the d_rot entries from
     rot_start on are turned.  q_weight, k_weight: bf16 or fp32, [d] or, for each head its own, [H,d] (None: ones).
-    Layouts, frequencies, outputs and row0 (appending k and v to caches) as for rope."""
+    Layouts, frequencies, outputs and row0 (appending k and v to caches) as for rope.  Not recorded by autograd:
+    norm_rope_grad gives the gradients."""
     torch = _torch or _load_torch()
     if k is None and (v is not None or k_out is not None or k_weight is not None) or v is None and v_out is not None:
         raise ValueError("k_out and k_weight go with k, and v and v_out with k")

@@ -65,8 +65,8 @@ inline int decode4_shares(long long units, int S_cap, int ctas)
 }
 
 // Whether short caches are better not cut: without cuts the joining kernel is not launched (3 us), but
-// few units leave SMs idle, where a tile takes 0.8 us (1.2 with groups of 128 rows).  Decided on full
-// caches.  Measured cut / whole at d = 128, 32/8 heads, one token: 1 cache of 500 keys 7.5 / 6.8 us, of
+// few units leave SMs idle, where a tile takes 0.8 us (1.2 with groups of 128 rows).  `keys`: what a unit of
+// a full cache can reach, under a window the window, the sinks and two tiles beside them.  Measured cut / whole at d = 128, 32/8 heads, one token: 1 cache of 500 keys 7.5 / 6.8 us, of
 // 760 7.5 / 8.5; 8 of 1020 10.6 / 10.3, of 1500 11.0 / 13.4; 32 of 1000 15.9 / 13.0, of 2000 21.3 /
 // 21.2; 128 of 1000 40.0 / 38.0, of 2000 63.5 / 65.7; four tokens: 1 of 500 9.5 / 9.0, of 1000 9.6 /
 // 13.0, 32 of 1000 22.1 / 16.7; sixteen: 1 of 250 11.8 / 11.4, of 500 12.1 / 14.3, 8 of 1000 18.4 / 17.6.

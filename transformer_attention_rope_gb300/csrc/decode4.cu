@@ -14,7 +14,7 @@
 // scores' scale.  Weights are taken relative to a reference 2^11 below the running
 // maximum, as fp16 up to 2^15 is: those of 2^-25 of the largest keep 11 bits, and what is lost
 // lies below 2^-36 of it.  The reference moves only when a score outgrows it, so a slice costs one
-// vote and no exchange of maxima.
+// vote and no exchange of maxima; past 2^20 it is the maximum itself (kLargeScore).
 //
 // Keys: lane 4g + t holds bytes 16t .. 16t + 15 of key g's row, 32 neighbouring entries, as the
 // order of the sum over entries is free; queries are laid out alike.  Values: lane 4g + t holds
@@ -26,7 +26,7 @@
 // keys takes some 290 instructions a warp, 64 of them conversions and 64 scales.  64 caches of 9001 to
 // 32767 keys, 32/8 heads of 128 (1.54 GB): 251 us, 6.1 TB/s; with slices of 16 keys for 8 warps 279, and 303
 // with addresses and masks made anew for each.  16 rows over 8 such caches (193 MB): 56 us, where the
-// conversions are the same and the products twice as many.  One cache under a window of 1024: 6.5 us.
+// conversions are the same and the products twice as many.  One cache under a window of 1024: 6.7 us.
 #include <math.h>
 
 #include "bits4.cuh"

@@ -12,7 +12,7 @@
 //
 // Bound: the softmax of a tile (0.9 us beside the conversions' instructions) and the products (0.6) in
 // turn, 1.3 us a tile of 128 keys and SM whatever the rows; its bytes take 0.4.  8 caches of 9001 to
-// 32768 keys, 8 KV heads of 128: 32 rows 92 us, 64 rows 94, 128 rows 98 (142 with the four warps of one
+// 32768 keys, 8 KV heads of 128: 32 rows 92 us, 64 rows 93, 128 rows 100 (142 with the four warps of one
 // warpgroup for the conversions), where groups of 16 rows take 56 each.
 #include <math.h>
 

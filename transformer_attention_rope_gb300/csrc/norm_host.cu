@@ -181,10 +181,10 @@ apex_status make_plan(const apex_norm_tensor *const (&t)[3], bool grad, int B, i
 
 // Cuts the work for rows that go 16 bytes at a time, into `blocks` (group, tile)s if there is so
 // much.  A block makes the sines of its tile for all heads of its group, and so has `rows` rows for each
-// of its slots, of as many heads and then tokens as there are; a slot takes two heads of a token, whose
-// loads are in flight together.  Where that leaves SMs without blocks, a block has fewer rows, and
-// at last one for each slot.  Weights of each head's own are held for `most` heads of a block; a
-// gradient's slot has one head then, whose sums it makes.
+// of its slots, of as many heads and then tokens as there are; a slot takes up to kNormBatch heads of a token,
+// whose loads are in flight together (a gradient's slot two, one by one from its ring).  Where that leaves SMs
+// without blocks, a block has fewer rows, and at last one for each slot.  Weights of each head's own are
+// held for `most` heads of a block; a gradient's slot has one head then, whose sums it makes.
 void cut_rows(Plan &plan, int rows, bool grad, int most, long long blocks)
 {
     NormRopeParams &p = plan.p;
@@ -249,7 +249,7 @@ apex_status apex_attn_norm_rope(const apex_norm_tensor *q, const apex_norm_tenso
         // for), 1000 of 128 + 8 10.5 us (14.4 with 4, which makes it a wave and a half)
         cut_rows(plan, 16, false, kNormHeads / plan.lanes, 7 * plan.sm_count / 2);
         // a tile for each block; with weights for each head, which a block fetches first, and tiles for
-        // three waves or more, as many blocks as run at once (8191 tokens of 128 + 8 heads 126 us, 136 with a
+        // three waves or more, as many blocks as run at once (8191 tokens of 128 + 8 heads 124 us, 136 with a
         // tile each; 4096 of 32 + 8, just a wave, 24.5 and 22.2)
         const long long wave = kNormCtas * plan.sm_count;
         long long n = 0;
