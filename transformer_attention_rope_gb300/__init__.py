@@ -18,7 +18,7 @@ Raw C-ABI names (pointers and sizes):
     apex_attn_evict_workspace_bytes, apex_attn_norm_rope and apex_attn_norm_rope_grad (with NormTensor structs),
     apex_attn_norm_rope_grad_workspace_bytes, apex_attn_append4 and apex_attn_unpack4 (with Bits4Tensor structs),
     apex_attn_decode4, apex_attn_decode4_workspace_bytes
-Tensor conveniences (torch, bf16, contiguous, on the current CUDA device):
+Tensor conveniences (torch, bf16, contiguous, on their own CUDA device):
     fwd(q, k, v, ...), decode(q, k_cache, v_cache, q_pos, ...), rope_keys(k, ...), mla_fwd(q, k, v, d_r, ...),
     mla_decode(q, k_cache, v_cache, q_pos, d_r, ...), mla_rope_keys(k, d_r, ...)
 Over caches of rotated keys (int32 lengths and positions on the device; the tensors' own device):
@@ -410,56 +410,6 @@ def apex_attn_status_string(status: int) -> str:
 
 
 # ------------------------------------------------------------------ torch conveniences
-def _check(t, name, ndim):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
-        raise TypeError("%s must be a CUDA bf16 tensor" % name)
-    if t.dim() != ndim or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %d-D tensor" % (name, ndim))
-
-
-def _check_together(q, k, v, d_r=0):
-    """Keys and values of one length for q's sequences, rows of d entries (keys and queries: d + d_r), one device."""
-    B, _, _, d_qk = q.shape
-    _, H_kv, S_k, d = v.shape
-    if k.shape != (B, H_kv, S_k, d_qk) or v.shape[0] != B or d_qk != d + d_r:
-        raise ValueError("queries, keys and values must have the same sequences and row lengths, keys and values the "
-                         "same heads and length")
-    if not q.get_device() == k.get_device() == v.get_device():
-        raise ValueError("queries, keys and values must be on one device")
-
-
-def _check_out(out, shape, like):
-    _check(out, "out", 4)
-    if out.shape != shape or out.get_device() != like.get_device():
-        raise ValueError("out must be of shape %s, on the device of the other tensors" % (tuple(shape),))
-
-
-def _check_workspace(given, like):
-    if not given.is_cuda or given.get_device() != like.get_device() or not given.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the device of the other tensors")
-    return given
-
-
-def _stream_handle(stream):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
-
-
-def _new(like, shape, dtype, stream):
-    """A tensor from torch's allocator on the device of `like`: the launch stream's memory, as that of the
-    current one may still be in use there, kept until the current stream is done with it too."""
-    torch = _torch or _load_torch()
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    now = torch.cuda.current_stream(like.device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=like.device)
-    t.record_stream(now)
-    return t
-
-
 def _options(window=0, q_pos=0, rope_base=10000.0, yarn_scale=1.0, yarn_beta_fast=32.0, yarn_beta_slow=1.0,
              prefix_len=0, keys_prerotated=False) -> Options:
     return Options(_window(window), _int32(q_pos, "q_pos"), float(rope_base), float(yarn_scale), float(yarn_beta_fast),
@@ -485,51 +435,89 @@ def _sinks(n_sink, window) -> int:
     return min(int(n_sink), _INT_MAX) if window > 0 else 0
 
 
-def _sink_fwd(q, k, v, d_r, n_sink, opt, out, workspace, stream):
-    """Prefill with sinks on q's device (apex_attn_sink_fwd), its workspace as for the calls without."""
+def _prefill(q, k, v, d_r, n_sink, how, out, workspace, stream):
+    """Prefill on q's device; how: arguments of _options."""
     torch = _torch or _load_torch()
-    B, H_q, S_q, S_k, H_kv, d, device, pq, pk, pv = _sink_shapes(q, k, v, d_r)
-    sizes = (B, H_q, H_kv, S_q, S_k, d, d_r, n_sink)
+    B, H_q, S_q, S_k, H_kv, d, device, pq, pk, pv = _shapes(q, k, v, d_r)
+    n_sink = _sinks(n_sink, how[0])
+    sizes = (B, H_q, H_kv, S_q, S_k, d)
+    lib, opt = _lib or load_library(), None
+    if n_sink:
+        need, run, sizes, name = lib.apex_attn_sink_fwd_workspace_bytes, lib.apex_attn_sink_fwd, sizes + (d_r, n_sink), \
+            "apex_attn_sink_fwd"
+    elif d_r:
+        need, run, sizes, name = lib.apex_attn_mla_fwd_workspace_bytes, lib.apex_attn_mla_fwd_ws, sizes + (d_r,), \
+            "apex_attn_mla_fwd"
+    else:
+        need, run, name = lib.apex_attn_fwd_workspace_bytes, lib.apex_attn_fwd_ws, "apex_attn_fwd"
+    plain = not d_r and not n_sink and _plain(how)
+    if workspace is not False or not plain:
+        opt = _options(*how)
     at = _Launch(device, stream)
     try:
         if out is None:
             out = at.new(q, (B, H_q, S_q, d), torch.bfloat16)
-        pout = _fit(out, "out", torch.bfloat16, (B, H_q, S_q, d), device)
-        lib, pws, size = _lib or load_library(), None, 0
-        if workspace is None:
-            size = lib.apex_attn_sink_fwd_workspace_bytes(*sizes, opt)
+            pout = out.data_ptr()
+        else:
+            pout = _fit(out, "out", torch.bfloat16, (B, H_q, S_q, d), device)
+        pws, size = None, need(*sizes, opt) if workspace is None else 0
         if workspace is not None and workspace is not False or size:
             ws = at.workspace(workspace, q, size)
             pws, size = ws.data_ptr(), ws.nbytes
-        status = lib.apex_attn_sink_fwd(pq, pk, pv, pout, *sizes, opt, pws, size, at.handle)
+        if plain and pws is None:
+            status = lib.apex_attn_fwd(pq, pk, pv, pout, *sizes, _window(how[0]), _int32(how[1], "q_pos0"), how[2],
+                                       at.handle)
+        else:
+            status = run(pq, pk, pv, pout, *sizes, opt, pws, size, at.handle)
         if status:
-            raise ApexError(status, "apex_attn_sink_fwd")
+            raise ApexError(status, name)
     finally:
         at.leave()
     return out
 
 
-def _sink_decode(q, k_cache, v_cache, d_r, n_sink, opt, out, workspace, stream):
-    """Decode with sinks on q's device (apex_attn_sink_decode)."""
+def _decode(q, k_cache, v_cache, d_r, n_sink, how, out, workspace, stream):
+    """Decode on q's device; how: arguments of _options."""
     torch = _torch or _load_torch()
-    B, H_q, _, S_k, H_kv, d, device, pq, pk, pv = _sink_shapes(q, k_cache, v_cache, d_r)
+    B, H_q, one, S_k, H_kv, d, device, pq, pk, pv = _shapes(q, k_cache, v_cache, d_r)
+    if one != 1:
+        raise ValueError("decode takes one query per sequence")
+    n_sink = _sinks(n_sink, how[0])
+    lib, sizes = _lib or load_library(), (B, H_q, H_kv, S_k, d)
+    plain = not d_r and not n_sink and _plain(how)
+    opt = None if plain else _options(*how)
     at = _Launch(device, stream)
     try:
         if out is None:
             out = at.new(q, (B, H_q, 1, d), torch.bfloat16)
-        pout = _fit(out, "out", torch.bfloat16, (B, H_q, 1, d), device)
-        lib = _lib or load_library()
-        ws = at.workspace(workspace, q, lib.apex_attn_decode_workspace_bytes(B, H_q, H_kv, S_k, d))
-        status = lib.apex_attn_sink_decode(pq, pk, pv, pout, B, H_q, H_kv, S_k, d, d_r, n_sink, opt, ws.data_ptr(),
-                                           ws.nbytes, at.handle)
+            pout = out.data_ptr()
+        else:
+            pout = _fit(out, "out", torch.bfloat16, (B, H_q, 1, d), device)
+        ws = at.workspace(workspace, q, lib.apex_attn_decode_workspace_bytes(*sizes) if workspace is None else 0)
+        tail = (ws.data_ptr(), ws.nbytes, at.handle)
+        if plain:
+            name, status = "apex_attn_decode", lib.apex_attn_decode(
+                pq, pk, pv, pout, *sizes, _window(how[0]), _int32(how[1], "q_pos"), how[2], *tail)
+        elif n_sink:
+            name, status = "apex_attn_sink_decode", lib.apex_attn_sink_decode(pq, pk, pv, pout, *sizes, d_r, n_sink, opt,
+                                                                              *tail)
+        elif d_r:
+            name, status = "apex_attn_mla_decode", lib.apex_attn_mla_decode(pq, pk, pv, pout, *sizes, d_r, opt, *tail)
+        else:
+            name, status = "apex_attn_decode", lib.apex_attn_decode_ex(pq, pk, pv, pout, *sizes, opt, *tail)
         if status:
-            raise ApexError(status, "apex_attn_sink_decode")
+            raise ApexError(status, name)
     finally:
         at.leave()
     return out
 
 
-def _sink_shapes(q, k, v, d_r):
+def _plain(how) -> bool:
+    """Whether of the arguments of _options only window, position and base count."""
+    return how[3] <= 1.0 and how[6] == 0 and not how[7]
+
+
+def _shapes(q, k, v, d_r):
     """Sizes of queries, keys and values, their device and addresses."""
     bf16 = _torch.bfloat16
     B, H_q, S_q, d_qk = _rows4(q, "q")
@@ -567,46 +555,8 @@ def fwd(q, k, v, *, window: int = 0, q_pos0: int = 0, rope_base: float = 10000.0
     prefill (fwd_workspace_bytes > 0), a buffer for them is taken from torch's
     allocator and apex_attn_fwd_ws runs; a uint8 CUDA tensor -- that buffer;
     False -- no workspace (apex_attn_fwd / apex_attn_fwd_ex)."""
-    import torch
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _check(t, n, 4)
-    n_sink = _sinks(n_sink, window)
-    if n_sink:
-        opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
-                       keys_prerotated)
-        return _sink_fwd(q, k, v, 0, n_sink, opt, out, workspace, stream)
-    _check_together(q, k, v)
-    B, H_q, S_q, d = q.shape
-    _, H_kv, S_k, _ = k.shape
-    if out is None:
-        out = _new(q, q.shape, torch.bfloat16, stream)
-    _check_out(out, q.shape, q)
-    if workspace is None:
-        need = fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d, window=window, q_pos0=q_pos0, rope_base=rope_base,
-                                   yarn_scale=yarn_scale, yarn_beta_fast=yarn_beta_fast,
-                                   yarn_beta_slow=yarn_beta_slow, prefix_len=prefix_len,
-                                   keys_prerotated=keys_prerotated)
-        if need > 0:
-            workspace = _new(q, need, torch.uint8, stream)
-    plain = yarn_scale <= 1.0 and prefix_len == 0 and not keys_prerotated
-    if workspace is not None and workspace is not False:
-        _check_workspace(workspace, q)
-        opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
-                       keys_prerotated)
-        st = apex_attn_fwd_ws(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, H_q, H_kv, S_q, S_k,
-                              d, opt, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                              _stream_handle(stream))
-    elif plain:
-        st = apex_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, H_q, H_kv, S_q, S_k, d,
-                           _window(window), _int32(q_pos0, "q_pos0"), float(rope_base), _stream_handle(stream))
-    else:
-        opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
-                       keys_prerotated)
-        st = apex_attn_fwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, H_q, H_kv, S_q, S_k,
-                              d, opt, _stream_handle(stream))
-    if st != APEX_OK:
-        raise ApexError(st, "apex_attn_fwd")
-    return out
+    return _prefill(q, k, v, 0, n_sink, (window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow,
+                                         prefix_len, keys_prerotated), out, workspace, stream)
 
 
 def mla_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, d_r, *, window: int = 0, q_pos0: int = 0,
@@ -634,39 +584,8 @@ def mla_fwd(q, k, v, d_r: int, *, window: int = 0, q_pos0: int = 0, rope_base: f
     workspace: None -- a buffer from torch's allocator when the library would rotate
     the keys' rope parts once before the prefill (mla_fwd_workspace_bytes > 0); a
     uint8 CUDA tensor -- that buffer; False -- no workspace (apex_attn_mla_fwd)."""
-    import torch
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _check(t, n, 4)
-    B, H_q, S_q, d_qk = q.shape
-    _, H_kv, S_k, d_h = v.shape
-    if d_qk != d_h + d_r or k.shape[-1] != d_qk:
-        raise ValueError("q / k rows must hold d_h + d_r entries")
-    opt = _options(window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
-                   keys_prerotated)
-    n_sink = _sinks(n_sink, window)
-    if n_sink:
-        return _sink_fwd(q, k, v, int(d_r), n_sink, opt, out, workspace, stream)
-    _check_together(q, k, v, d_r)
-    if out is None:
-        out = _new(q, (B, H_q, S_q, d_h), torch.bfloat16, stream)
-    _check_out(out, (B, H_q, S_q, d_h), q)
-    if workspace is None:
-        need = int(apex_attn_mla_fwd_workspace_bytes(B, H_q, H_kv, S_q, S_k, d_h, int(d_r), opt))
-        if need > 0:
-            workspace = _new(q, need, torch.uint8, stream)
-    if workspace is not None and workspace is not False:
-        _check_workspace(workspace, q)
-        st = apex_attn_mla_fwd_ws(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, H_q, H_kv, S_q,
-                                  S_k, d_h, int(d_r), opt, workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _stream_handle(stream))
-        name = "apex_attn_mla_fwd_ws"
-    else:
-        st = apex_attn_mla_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, H_q, H_kv, S_q, S_k,
-                               d_h, int(d_r), opt, _stream_handle(stream))
-        name = "apex_attn_mla_fwd"
-    if st != APEX_OK:
-        raise ApexError(st, name)
-    return out
+    return _prefill(q, k, v, int(d_r), n_sink, (window, q_pos0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow,
+                                                prefix_len, keys_prerotated), out, workspace, stream)
 
 
 def decode_workspace_bytes(B, H_q, H_kv, S_k, d_h) -> int:
@@ -679,40 +598,8 @@ def decode(q, k_cache, v_cache, q_pos: int, *, window: int = 0, rope_base: float
     """Decode. q [B,H_q,1,d], caches [B,H_kv,S_k,d] (bf16, CUDA) -> out [B,H_q,1,d].
 
     n_sink: the first keys, which stay visible behind a window (sinks)."""
-    import torch
-    for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check(t, n, 4)
-    B, H_q, one, d = q.shape
-    _, H_kv, S_k, _ = k_cache.shape
-    if one != 1:
-        raise ValueError("decode takes one query per sequence")
-    n_sink = _sinks(n_sink, window)
-    if n_sink:
-        opt = _options(window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
-                       keys_prerotated)
-        return _sink_decode(q, k_cache, v_cache, 0, n_sink, opt, out, workspace, stream)
-    _check_together(q, k_cache, v_cache)
-    if out is None:
-        out = _new(q, q.shape, torch.bfloat16, stream)
-    _check_out(out, q.shape, q)
-    need = decode_workspace_bytes(B, H_q, H_kv, S_k, d)
-    if workspace is None:
-        workspace = _new(q, max(need, 16), torch.uint8, stream)
-    _check_workspace(workspace, q)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    plain = yarn_scale <= 1.0 and prefix_len == 0 and not keys_prerotated
-    if plain:
-        st = apex_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
-                              S_k, d, _window(window), _int32(q_pos, "q_pos"), float(rope_base), workspace.data_ptr(),
-                              ws_bytes, _stream_handle(stream))
-    else:
-        opt = _options(window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
-                       keys_prerotated)
-        st = apex_attn_decode_ex(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q,
-                                 H_kv, S_k, d, opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
-    if st != APEX_OK:
-        raise ApexError(st, "apex_attn_decode")
-    return out
+    return _decode(q, k_cache, v_cache, 0, n_sink, (window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow,
+                                                    prefix_len, keys_prerotated), out, workspace, stream)
 
 
 def mla_decode(q, k_cache, v_cache, q_pos: int, d_r: int, *, window: int = 0, rope_base: float = 10000.0,
@@ -723,73 +610,47 @@ def mla_decode(q, k_cache, v_cache, q_pos: int, d_r: int, *, window: int = 0, ro
     (bf16, CUDA; rows [content | rope part]) -> out [B,H_q,1,d_h].
 
     n_sink: the first keys, which stay visible behind a window (sinks)."""
-    import torch
-    for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check(t, n, 4)
-    B, H_q, one, d_qk = q.shape
-    _, H_kv, S_k, d_h = v_cache.shape
-    if one != 1:
-        raise ValueError("decode takes one query per sequence")
-    if d_qk != d_h + d_r or k_cache.shape[-1] != d_qk:
-        raise ValueError("q / k_cache rows must hold d_h + d_r entries")
-    opt = _options(window, q_pos, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow, prefix_len,
-                   keys_prerotated)
-    n_sink = _sinks(n_sink, window)
-    if n_sink:
-        return _sink_decode(q, k_cache, v_cache, int(d_r), n_sink, opt, out, workspace, stream)
-    _check_together(q, k_cache, v_cache, d_r)
-    if out is None:
-        out = _new(q, (B, H_q, 1, d_h), torch.bfloat16, stream)
-    _check_out(out, (B, H_q, 1, d_h), q)
-    need = decode_workspace_bytes(B, H_q, H_kv, S_k, d_h)
-    if workspace is None:
-        workspace = _new(q, max(need, 16), torch.uint8, stream)
-    _check_workspace(workspace, q)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    st = apex_attn_mla_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), B, H_q, H_kv,
-                              S_k, d_h, int(d_r), opt, workspace.data_ptr(), ws_bytes, _stream_handle(stream))
-    if st != APEX_OK:
-        raise ApexError(st, "apex_attn_mla_decode")
-    return out
+    return _decode(q, k_cache, v_cache, int(d_r), n_sink, (window, q_pos, rope_base, yarn_scale, yarn_beta_fast,
+                                                           yarn_beta_slow, prefix_len, keys_prerotated), out,
+                   workspace, stream)
 
 
 def rope_keys(k, *, pos0: int = 0, out=None, rope_base: float = 10000.0, yarn_scale: float = 1.0,
               yarn_beta_fast: float = 32.0, yarn_beta_slow: float = 1.0, stream=None):
     """Rotate keys k [B,H,S,d] (bf16, CUDA) to positions pos0 + s: out = RoPE(k) (pre-rotated cache)."""
-    import torch
-    _check(k, "k", 4)
-    B, H, S, d = k.shape
-    if out is None:
-        out = _new(k, k.shape, torch.bfloat16, stream)
-    _check(out, "out", 4)
-    if out.shape != k.shape:
-        raise ValueError("out must have the shape of k")
-    opt = _options(0, 0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow)
-    st = apex_attn_rope_keys(k.data_ptr(), out.data_ptr(), B * H, S, d, _int32(pos0, "pos0"), S * d, S * d, opt,
-                             _stream_handle(stream))
-    if st != APEX_OK:
-        raise ApexError(st, "apex_attn_rope_keys")
-    return out
+    return _turn_keys(k, None, pos0, out, (rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow), stream)
 
 
 def mla_rope_keys(k, d_r: int, *, pos0: int = 0, out=None, rope_base: float = 10000.0, yarn_scale: float = 1.0,
                   yarn_beta_fast: float = 32.0, yarn_beta_slow: float = 1.0, stream=None):
     """Decoupled-RoPE key rows k [B,H,S,d_h+d_r] (bf16, CUDA; [content | rope part]) with the
     rope part rotated to positions pos0 + s and the content part copied (pre-rotated cache)."""
-    import torch
-    _check(k, "k", 4)
-    B, H, S, d = k.shape
-    if out is None:
-        out = _new(k, k.shape, torch.bfloat16, stream)
-    _check(out, "out", 4)
-    if out.shape != k.shape:
-        raise ValueError("out must have the shape of k")
-    opt = _options(0, 0, rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow)
-    d_r = _int32(d_r, "d_r")
-    st = apex_attn_mla_rope_keys(k.data_ptr(), out.data_ptr(), B * H, S, d - d_r, d_r, _int32(pos0, "pos0"), S * d,
-                                 S * d, opt, _stream_handle(stream))
-    if st != APEX_OK:
-        raise ApexError(st, "apex_attn_mla_rope_keys")
+    return _turn_keys(k, _int32(d_r, "d_r"), pos0, out, (rope_base, yarn_scale, yarn_beta_fast, yarn_beta_slow), stream)
+
+
+def _turn_keys(k, d_r, pos0, out, freq, stream):
+    """Rows of k turned, or with a d_r their last d_r entries."""
+    torch = _torch or _load_torch()
+    shape = B, H, S, d = _rows4(k, "k")
+    device = k.get_device()
+    pk = _fit(k, "k", torch.bfloat16, shape, device)
+    _int32(B * H, "sequences times heads"), _int32(S, "tokens"), _int32(d, "row length")
+    lib, opt, pos0 = _lib or load_library(), _options(0, 0, *freq), _int32(pos0, "pos0")
+    at = _Launch(device, stream)
+    try:
+        if out is None:
+            out = at.new(k, shape, torch.bfloat16)
+        pout = _fit(out, "out", torch.bfloat16, shape, device)
+        if d_r is None:
+            name, status = "apex_attn_rope_keys", lib.apex_attn_rope_keys(pk, pout, B * H, S, d, pos0, S * d, S * d, opt,
+                                                                          at.handle)
+        else:
+            name, status = "apex_attn_mla_rope_keys", lib.apex_attn_mla_rope_keys(pk, pout, B * H, S, d - d_r, d_r, pos0,
+                                                                                  S * d, S * d, opt, at.handle)
+        if status:
+            raise ApexError(status, name)
+    finally:
+        at.leave()
     return out
 
 
@@ -858,12 +719,22 @@ class _Launch:
             self.guard.__exit__(None, None, None)
 
     def new(self, like, shape, dtype):
-        return _new(like, shape, dtype, self.stream)
+        """A tensor from torch's allocator: the launch stream's memory, as that of the current
+        one may still be in use there, kept until the current stream is done with it too."""
+        if self.stream is None:
+            return _torch.empty(shape, dtype=dtype, device=like.device)
+        now = _torch.cuda.current_stream(self.device)
+        with _torch.cuda.stream(self.stream):
+            t = _torch.empty(shape, dtype=dtype, device=like.device)
+        t.record_stream(now)
+        return t
 
     def workspace(self, given, like, need):
         if given is None:
             return self.new(like, need if need > 16 else 16, _torch.uint8)
-        return _check_workspace(given, like)
+        if not given.is_cuda or given.get_device() != self.device or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the device of the other tensors")
+        return given
 
 
 # apex_rope_tensor and apex_rope_options as bytes: quicker to make than ctypes structs
